@@ -1,0 +1,206 @@
+// C ABI of the operators around the expert layer (residual norm, paged MX cache,
+// attention): argument checks and workspace carving (see include/mxmoe.h).
+#include <cuda_runtime.h>
+#include <climits>
+#include <cstdint>
+
+#include "../../include/mxmoe.h"
+#include "internal.h"
+
+using namespace mxk;
+
+namespace {
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline size_t al256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? MX_OK : MX_ERR_CUDA; }
+bool type_ok(int t) { return t == MX_BF16 || t == MX_F32; }
+bool finite_positive(float v) { return v > 0.0f && v <= 3.402823466e38f; }
+
+// The cache and the batch's sizes, as all three cache calls take them.
+int check_cache(const mx_kv_cache* c, int n_seqs, int max_pages, int T) {
+  if (!c || T < 0 || n_seqs < 0 || max_pages <= 0) return MX_ERR_INVALID_ARG;
+  if (c->num_pages <= 0 || c->page_size <= 0 || c->n_kv_heads <= 0 || c->head_dim <= 0) return MX_ERR_INVALID_ARG;
+  if (c->fmt != MX_E4M3 && c->fmt != MX_E2M1) return MX_ERR_INVALID_ARG;
+  if (c->head_dim % 32) return MX_ERR_UNSUPPORTED;
+  // positions, heads x elements and grid sizes are ints
+  if (static_cast<int64_t>(max_pages) * c->page_size > INT_MAX / 2) return MX_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(c->n_kv_heads) * c->head_dim > (1 << 20) || T > INT_MAX / 2) return MX_ERR_UNSUPPORTED;
+  return MX_OK;
+}
+
+int check_cache_pointers(const mx_kv_cache* c, const void* block_table, const void* kv_lens, const void* q_starts,
+                         const void* ws, size_t ws_bytes) {
+  if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales || !block_table || !kv_lens || !q_starts || !ws)
+    return MX_ERR_INVALID_ARG;
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4) ||
+      !aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(q_starts, 4) || !aligned(ws, 256))
+    return MX_ERR_ALIGNMENT;
+  return ws_bytes < 256 ? MX_ERR_WORKSPACE : MX_OK;
+}
+
+KvArgs kv_args(const mx_kv_cache* c, const int32_t* block_table, const int32_t* kv_lens, const int32_t* q_starts,
+               int n_seqs, int max_pages, int T, void* ws) {
+  KvArgs a{};
+  a.k_codes = c->k_codes;
+  a.k_scales = c->k_scales;
+  a.v_codes = c->v_codes;
+  a.v_scales = c->v_scales;
+  a.num_pages = c->num_pages;
+  a.page_size = c->page_size;
+  a.n_heads = c->n_kv_heads;
+  a.head_dim = c->head_dim;
+  a.e2m1 = c->fmt == MX_E2M1 ? 1 : 0;
+  a.block_table = block_table;
+  a.kv_lens = kv_lens;
+  a.q_starts = q_starts;
+  a.n_seqs = n_seqs;
+  a.max_pages = max_pages;
+  a.T = T;
+  a.status = static_cast<int*>(ws);
+  return a;
+}
+
+// Attention workspace: the status word, the segments' arrival counters, then
+// the split segments' partial results.
+constexpr size_t kArrivedOffset = 256;
+constexpr size_t kArrivedBytes = sizeof(unsigned) * kAttnMaxCtas;
+
+int check_attention(int T, int n_seqs, int n_heads, int n_kv_heads, int head_dim, int max_q_len) {
+  if (T < 0 || n_seqs < 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || max_q_len < 0) return MX_ERR_INVALID_ARG;
+  if (n_heads % n_kv_heads) return MX_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return MX_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(T) * n_heads > (1 << 30) || n_heads > (1 << 14)) return MX_ERR_UNSUPPORTED;
+  return MX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mx_add_rmsnorm(const void* x, int x_type, const void* residual, int residual_type, const void* weight,
+                   int weight_type, int T, int H, float eps, void* residual_out, void* y, int fmt, uint8_t* codes,
+                   uint8_t* scales, mx_stream_t stream) {
+  if (T < 0 || H <= 0 || !type_ok(x_type) || !type_ok(weight_type) || (residual && !type_ok(residual_type)) ||
+      !finite_positive(eps))
+    return MX_ERR_INVALID_ARG;
+  if (codes && fmt != MX_E4M3 && fmt != MX_E2M1) return MX_ERR_INVALID_ARG;
+  if (T == 0) return MX_OK;
+  if (!x || !weight || (!y && !codes) || !codes != !scales || !residual != !residual_out) return MX_ERR_INVALID_ARG;
+  if (H % 32 || H > 32768) return MX_ERR_UNSUPPORTED;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
+      !aligned(y, 16) || !aligned(codes, 16))
+    return MX_ERR_ALIGNMENT;
+  NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.x_f32 = x_type == MX_F32;
+  a.residual_f32 = residual_type == MX_F32;
+  a.weight_f32 = weight_type == MX_F32;
+  a.T = T;
+  a.H = H;
+  a.eps = eps;
+  a.residual_out = residual_out;
+  a.y = y;
+  a.e2m1 = fmt == MX_E2M1 ? 1 : 0;
+  a.codes = codes;
+  a.scales = scales;
+  return cuda_status(launch_add_rmsnorm(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int mx_kv_append(const mx_kv_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                 const int32_t* block_table, const int32_t* kv_lens, const int32_t* q_starts, int n_seqs,
+                 int max_pages, int T, void* ws, size_t ws_bytes, mx_stream_t stream) {
+  int st = check_cache(cache, n_seqs, max_pages, T);
+  if (st != MX_OK) return st;
+  const int64_t row = static_cast<int64_t>(cache->n_kv_heads) * cache->head_dim;
+  if (k_stride < row || v_stride < row) return MX_ERR_INVALID_ARG;
+  if (T == 0 || n_seqs == 0) return MX_OK;
+  if (!k || !v) return MX_ERR_INVALID_ARG;
+  st = check_cache_pointers(cache, block_table, kv_lens, q_starts, ws, ws_bytes);
+  if (st != MX_OK) return st;
+  if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 || v_stride % 8) return MX_ERR_ALIGNMENT;
+  KvArgs a = kv_args(cache, block_table, kv_lens, q_starts, n_seqs, max_pages, T, ws);
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  return cuda_status(launch_kv_append(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int mx_kv_read(const mx_kv_cache* cache, const int32_t* block_table, const int32_t* kv_lens, const int32_t* q_starts,
+               int n_seqs, int max_pages, int T, void* k_out, void* v_out, void* ws, size_t ws_bytes,
+               mx_stream_t stream) {
+  int st = check_cache(cache, n_seqs, max_pages, T);
+  if (st != MX_OK) return st;
+  if (T == 0 || n_seqs == 0) return MX_OK;
+  if (!k_out || !v_out) return MX_ERR_INVALID_ARG;
+  st = check_cache_pointers(cache, block_table, kv_lens, q_starts, ws, ws_bytes);
+  if (st != MX_OK) return st;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return MX_ERR_ALIGNMENT;
+  KvArgs a = kv_args(cache, block_table, kv_lens, q_starts, n_seqs, max_pages, T, ws);
+  a.k_out = k_out;
+  a.v_out = v_out;
+  return cuda_status(launch_kv_read(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mx_paged_attention_workspace_size(int T, int n_seqs, int n_heads, int n_kv_heads, int head_dim, int max_q_len) {
+  if (check_attention(T, n_seqs, n_heads, n_kv_heads, head_dim, max_q_len) != MX_OK) return 0;
+  return kArrivedOffset + al256(kArrivedBytes) + attn_rows_part_bytes(head_dim);
+}
+
+int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride, int n_heads,
+                       const int32_t* block_table, const int32_t* kv_lens, const int32_t* q_starts, int n_seqs,
+                       int max_pages, int T, int max_q_len, float scale, int causal, int window, void* out, float* lse,
+                       void* ws, size_t ws_bytes, mx_stream_t stream) {
+  int st = check_cache(cache, n_seqs, max_pages, T);
+  if (st != MX_OK) return st;
+  st = check_attention(T, n_seqs, n_heads, cache->n_kv_heads, cache->head_dim, max_q_len);
+  if (st != MX_OK) return st;
+  if (!finite_positive(scale) || window < 0 || (window > 0 && !causal)) return MX_ERR_INVALID_ARG;
+  if (q_stride < static_cast<int64_t>(n_heads) * cache->head_dim) return MX_ERR_INVALID_ARG;
+  if (cache->page_size % 16) return MX_ERR_UNSUPPORTED;
+  if (T == 0 || n_seqs == 0 || max_q_len == 0) return MX_OK;
+  if (!q || !out) return MX_ERR_INVALID_ARG;
+  st = check_cache_pointers(cache, block_table, kv_lens, q_starts, ws, ws_bytes);
+  if (st != MX_OK) return st;
+  if (!aligned(q, 16) || q_stride % 8 || !aligned(out, 16) || !aligned(lse, 4)) return MX_ERR_ALIGNMENT;
+  if (ws_bytes < mx_paged_attention_workspace_size(T, n_seqs, n_heads, cache->n_kv_heads, cache->head_dim, max_q_len))
+    return MX_ERR_WORKSPACE;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  AttnArgs a{};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k_codes = cache->k_codes;
+  a.k_scales = cache->k_scales;
+  a.v_codes = cache->v_codes;
+  a.v_scales = cache->v_scales;
+  a.num_pages = cache->num_pages;
+  a.page_size = cache->page_size;
+  a.n_kv_heads = cache->n_kv_heads;
+  a.head_dim = cache->head_dim;
+  a.e2m1 = cache->fmt == MX_E2M1 ? 1 : 0;
+  a.block_table = block_table;
+  a.kv_lens = kv_lens;
+  a.q_starts = q_starts;
+  a.n_seqs = n_seqs;
+  a.max_pages = max_pages;
+  a.T = T;
+  a.group = n_heads / cache->n_kv_heads;
+  a.max_q_len = max_q_len;
+  a.causal = causal != 0;
+  a.window = window;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.out = out;
+  a.lse = lse;
+  a.status = static_cast<int*>(ws);
+  a.arrived = reinterpret_cast<unsigned*>(w + kArrivedOffset);
+  a.part_ml = reinterpret_cast<float2*>(w + kArrivedOffset + al256(kArrivedBytes));
+  a.rows_above = 0;
+  a.rows_upto = INT_MAX;
+  a.min_units = 4;
+  return cuda_status(launch_attn_rows(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -94,6 +94,64 @@ cudaError_t launch_prepare_weights(const uint8_t* codes, const uint8_t* scales,
 
 cudaError_t launch_zero(void* p, size_t bytes, cudaStream_t s);
 
+// ---- norm.cu
+struct NormArgs {
+  const void* x;           // [T, H] bf16 or fp32
+  const void* residual;    // [T, H] bf16 or fp32, or null
+  const void* weight;      // [H] bf16 or fp32
+  int x_f32, residual_f32, weight_f32;
+  int T, H;
+  float eps;
+  void* residual_out;      // the residual's type (with residual)
+  void* y;                 // [T, H] bf16, or null
+  int e2m1;                // codes as MXFP4 instead of MXFP8
+  uint8_t* codes;          // or null
+  uint8_t* scales;
+};
+cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s);
+
+// ---- kvcache.cu
+struct KvArgs {
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;  // [num_pages, n_heads, page_size, row]
+  int num_pages, page_size, n_heads, head_dim, e2m1;
+  const int32_t* block_table;                        // [n_seqs, max_pages]
+  const int32_t* kv_lens;                            // [n_seqs]
+  const int32_t* q_starts;                           // [n_seqs + 1]
+  int n_seqs, max_pages, T;
+  const void *k, *v;                                 // append: bf16 [T, n_heads, head_dim]
+  int64_t k_stride, v_stride;                        // elements between tokens
+  void *k_out, *v_out;                               // read: bf16 [T, n_heads, head_dim], dense
+  int* status;
+};
+cudaError_t launch_kv_append(const KvArgs& a, cudaStream_t s);
+cudaError_t launch_kv_read(const KvArgs& a, cudaStream_t s);
+
+// ---- attn_rows.cu, attn_chunk.cu
+constexpr int kAttnMaxCtas = 608;                    // 152 SMs x 4: partial slots and counters of the workspace
+struct AttnArgs {
+  const void* q;                                     // bf16 [T, n_heads, head_dim]
+  int64_t q_stride;                                  // elements between tokens
+  const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  int num_pages, page_size, n_kv_heads, head_dim, e2m1;
+  const int32_t* block_table;
+  const int32_t* kv_lens;
+  const int32_t* q_starts;
+  int n_seqs, max_pages, T, group;                   // group: query heads of one KV head
+  int max_q_len, causal, window;
+  float scale_log2;                                  // softmax scale * log2(e)
+  int rows_above, rows_upto;                         // the sequences (by rows) this launch handles
+  int min_units;                                     // least units of a CTA's stretch
+  void* out;                                         // bf16 [T, n_heads, head_dim], dense
+  float* lse;                                        // [T, n_heads] or null
+  int* status;
+  unsigned* arrived;                                 // [kAttnMaxCtas], zero between launches
+  float2* part_ml;                                   // [2 * CTAs][tile rows] maximum and sum
+  float* part_o;                                     // [2 * CTAs][tile rows][head_dim]
+  uint64_t wait_limit_ns;
+};
+size_t attn_rows_part_bytes(int head_dim);           // part_ml and part_o of the few-rows kernel
+cudaError_t launch_attn_rows(AttnArgs a, cudaStream_t s);
+
 // ---- router.cu
 struct RouterArgs {
   const void* x;         // bf16 [T, H]

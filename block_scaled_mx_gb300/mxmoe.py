@@ -28,10 +28,19 @@ MX_ERR_DEVICE_ARG = 7
 MX_E4M3 = 0
 MX_E2M1 = 1
 FORMATS = {"e4m3": MX_E4M3, "e2m1": MX_E2M1}
+MX_BF16 = 0
+MX_F32 = 1
 MX_ACT_SWIGLU = 0
 MX_ACT_SWIGLU_OAI = 1
 MX_SHARED_FOLDED = 0
 MX_SHARED_DENSE = 1
+
+
+class KVCacheTables(ctypes.Structure):
+    """mx_kv_cache of include/mxmoe.h (field order and types as declared)."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("fmt", ctypes.c_int)]
 
 
 class LayerOpts(ctypes.Structure):
@@ -48,6 +57,7 @@ def layer_opts(activation="swiglu", alpha=1.0, limit=7.0, shared="folded", act_f
 
 # every entry point of the C ABI: name -> (restype, argtypes)
 _P, _I, _I64, _SZ, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_uint64
+_F = ctypes.c_float
 SIGNATURES = {
     "mx_status_string": (ctypes.c_char_p, [_I]),
     "mx_quantize_act": (_I, [_P, _I, _I, _P, _P, _P]),
@@ -70,6 +80,11 @@ SIGNATURES = {
     "moe_grouped_gemm_swiglu_ex": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P, _P]),
     "moe_forward_launches_ex": (_I, [_I, _I, _I, _I, _I, _I, _P]),
     "moe_forward_launches": (_I, [_I, _I, _I, _I, _I, _I]),
+    "mx_add_rmsnorm": (_I, [_P, _I, _P, _I, _P, _I, _I, _I, _F, _P, _P, _I, _P, _P, _P]),
+    "mx_kv_append": (_I, [_P, _P, _I64, _P, _I64, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
+    "mx_kv_read": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _SZ, _P]),
+    "mx_paged_attention_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "mx_paged_attention": (_I, [_P, _P, _I64, _I, _P, _P, _P, _I, _I, _I, _I, _F, _I, _I, _P, _P, _P, _SZ, _P]),
     "moe_get_status": (_I, [_P, _P, _P]),
     "mx_debug_set_wait_limit_ns": (None, [_U64]),
     "mx_debug_time_gemms": (None, [_I]),
@@ -270,6 +285,156 @@ def moe_forward_ex(x, logits, w1_prep, w2_prep, fmt, I, k, out, ws, opts=None, s
 def moe_forward_launches_ex(T, H, I, E, k, fmt, opts=None) -> int:
     """Kernel launches moe_forward_ex enqueues for this shape and these options (host only)."""
     return lib().moe_forward_launches_ex(T, H, I, E, k, _fmt(fmt), _opts_ptr(opts))
+
+
+# ------------------------------------------------------------------ around the expert layer
+_TYPES = {torch.bfloat16: MX_BF16, torch.float32: MX_F32}
+
+
+def _type(t) -> int:
+    """The MX_BF16 / MX_F32 code of a tensor's dtype."""
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"expected a bf16 or fp32 tensor, got {t.dtype}")
+    return code
+
+
+def _expect(t, dtype, shape, what):
+    if t.dtype is not dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+def mx_add_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, codes=None, scales=None, fmt="e4m3",
+                   stream=None):
+    """z = x + residual; residual_out = z; y = RMSNorm(z) * weight; codes, scales = MX(y),
+    written where tensors are given (x, residual, weight: bf16 or fp32; y bf16;
+    codes [T, H] or, for "e2m1", [T, H/2] and scales [T, H/32] uint8)."""
+    T, H = x.shape
+    f = _fmt(fmt)
+    if weight.shape != (H,):
+        raise ValueError(f"weight: expected shape {(H,)}, got {tuple(weight.shape)}")
+    rt = MX_BF16
+    if residual is not None:
+        rt = _type(residual)
+        _expect(residual, residual.dtype, (T, H), "residual")
+        if residual_out is not None:
+            _expect(residual_out, residual.dtype, (T, H), "residual_out")
+    if y is not None:
+        _expect(y, torch.bfloat16, (T, H), "y")
+    if codes is not None:
+        _expect(codes, torch.uint8, (T, H // 2 if f == MX_E2M1 else H), "codes")
+    if scales is not None:
+        _expect(scales, torch.uint8, (T, H // 32), "scales")
+    _check(lib().mx_add_rmsnorm(_ptr(x), _type(x), _ptr(residual), rt, _ptr(weight), _type(weight), T, H, eps,
+                                _ptr(residual_out), _ptr(y), f, _ptr(codes), _ptr(scales), _stream(stream)),
+           "mx_add_rmsnorm")
+
+
+class KVCache:
+    """A paged key/value cache in MX form (mx_kv_cache): ``num_pages`` pages of
+    ``page_size`` tokens, "e4m3" (MXFP8) or "e2m1" (MXFP4) with an E8M0 scale for
+    each 32 elements of a head.  The four tables are tensors of uint8,
+    [num_pages, n_kv_heads, page_size, bytes of a row]."""
+
+    def __init__(self, num_pages, page_size, n_kv_heads, head_dim, fmt="e4m3", device="cuda"):
+        f = _fmt(fmt)
+        shape = (num_pages, n_kv_heads, page_size)
+
+        def table(row):
+            return torch.zeros(*shape, row, dtype=torch.uint8, device=device)
+
+        row = head_dim // 2 if f == MX_E2M1 else head_dim
+        self._hold(table(row), table(head_dim // 32), table(row), table(head_dim // 32), head_dim, f)
+
+    @classmethod
+    def of(cls, k_codes, k_scales, v_codes, v_scales, head_dim, fmt="e4m3"):
+        """A cache over tables that the caller holds."""
+        c = cls.__new__(cls)
+        c._hold(k_codes, k_scales, v_codes, v_scales, head_dim, _fmt(fmt))
+        return c
+
+    def _hold(self, k_codes, k_scales, v_codes, v_scales, head_dim, fmt):
+        pages, heads, size, _ = k_codes.shape
+        row = head_dim // 2 if fmt == MX_E2M1 else head_dim
+        for t, r, what in ((k_codes, row, "k_codes"), (k_scales, head_dim // 32, "k_scales"), (v_codes, row, "v_codes"),
+                           (v_scales, head_dim // 32, "v_scales")):
+            _expect(t, torch.uint8, (pages, heads, size, r), what)
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.num_pages, self.page_size, self.n_kv_heads, self.head_dim, self.fmt = pages, size, heads, head_dim, fmt
+        self._tables = KVCacheTables(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), pages, size, heads,
+                                     head_dim, fmt)
+        self._address = ctypes.addressof(self._tables)
+
+
+def _batch(block_table, kv_lens, q_starts):
+    """Checked sizes (n_seqs, max_pages) of a batch's int32 tensors."""
+    n, pages = block_table.shape
+    if not (block_table.dtype is kv_lens.dtype is q_starts.dtype is torch.int32):
+        raise ValueError("block_table, kv_lens and q_starts are int32 tensors")
+    if kv_lens.shape != (n,) or q_starts.shape != (n + 1,):
+        raise ValueError(f"expected kv_lens [{n}] and q_starts [{n + 1}] beside block_table {tuple(block_table.shape)}")
+    return n, pages
+
+
+def _rows(t, heads, dim, what):
+    """Address and token stride of a bf16 [T, heads, dim] tensor whose tokens may
+    lie apart (a slice of a wider projection)."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{what}: expected bf16 [T, {heads}, {dim}], got {t.dtype} {tuple(t.shape)}")
+    st = t.stride()
+    if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
+        raise ValueError(f"{what}: a token's heads are dense, got strides {st}")
+    if not t.is_cuda:
+        raise ValueError(f"expected a CUDA tensor, got one on {t.device}")
+    # one token has no stride of its own
+    return t.data_ptr(), st[0] if t.shape[0] > 1 else heads * dim
+
+
+def mx_kv_append(cache, k, v, block_table, kv_lens, q_starts, ws, stream=None):
+    """Quantise new keys and values (bf16 [T, n_kv_heads, head_dim], token stride
+    free) into their places in the cache: the last ones of each sequence."""
+    n, pages = _batch(block_table, kv_lens, q_starts)
+    if v.shape != k.shape:
+        raise ValueError(f"k and v differ in shape: {tuple(k.shape)}, {tuple(v.shape)}")
+    kp, ks = _rows(k, cache.n_kv_heads, cache.head_dim, "k")
+    vp, vs = _rows(v, cache.n_kv_heads, cache.head_dim, "v")
+    _check(lib().mx_kv_append(cache._address, kp, ks, vp, vs, _ptr(block_table), _ptr(kv_lens), _ptr(q_starts), n,
+                              pages, k.shape[0], _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "mx_kv_append")
+
+
+def mx_kv_read(cache, block_table, kv_lens, q_starts, k_out, v_out, ws, stream=None):
+    """The last q_starts[b+1] - q_starts[b] tokens of each sequence as bf16."""
+    n, pages = _batch(block_table, kv_lens, q_starts)
+    shape = (k_out.shape[0], cache.n_kv_heads, cache.head_dim)
+    _expect(k_out, torch.bfloat16, shape, "k_out")
+    _expect(v_out, torch.bfloat16, shape, "v_out")
+    _check(lib().mx_kv_read(cache._address, _ptr(block_table), _ptr(kv_lens), _ptr(q_starts), n, pages, shape[0],
+                            _ptr(k_out), _ptr(v_out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "mx_kv_read")
+
+
+def mx_paged_attention_workspace_size(T, n_seqs, n_heads, n_kv_heads, head_dim, max_q_len=None) -> int:
+    return lib().mx_paged_attention_workspace_size(T, n_seqs, n_heads, n_kv_heads, head_dim,
+                                                   T if max_q_len is None else max_q_len)
+
+
+def mx_paged_attention(q, cache, block_table, kv_lens, q_starts, out, ws, scale=None, causal=True, window=0,
+                       max_q_len=None, lse=None, stream=None):
+    """Attention of new tokens (bf16 q [T, n_heads, head_dim], token stride free)
+    over the cache; out bf16 and lse fp32 [T, n_heads] are dense.  scale defaults
+    to head_dim ** -0.5; max_q_len (default T) bounds a sequence's new tokens."""
+    n, pages = _batch(block_table, kv_lens, q_starts)
+    T, heads, dim = q.shape
+    qp, qs = _rows(q, heads, cache.head_dim, "q")
+    _expect(out, torch.bfloat16, (T, heads, dim), "out")
+    if lse is not None:
+        _expect(lse, torch.float32, (T, heads), "lse")
+    _check(lib().mx_paged_attention(cache._address, qp, qs, heads, _ptr(block_table), _ptr(kv_lens), _ptr(q_starts), n,
+                                    pages, T, T if max_q_len is None else max_q_len,
+                                    dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, _ptr(out),
+                                    _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "mx_paged_attention")
 
 
 def moe_get_status(ws, stream=None) -> int:

@@ -335,6 +335,113 @@ MX_API int moe_grouped_gemm_down_combine_ex(const uint8_t* h_codes, const uint8_
  * (host only; -1 for a rejected shape or option). */
 MX_API int moe_forward_launches_ex(int T, int H, int I, int E, int k, int fmt, const mx_layer_opts* opts);
 
+/* ---- the operators around the expert layer ---- */
+
+/* element types of plain (unquantised) tensors */
+#define MX_BF16 0
+#define MX_F32 1
+
+/* Residual addition, root-mean-square norm and MX quantisation in one pass:
+ *   z = x + residual,  residual_out = z,
+ *   y = z / sqrt(mean(z^2) + eps) * weight,  (codes, scales) = MX(y)
+ * in fp32; residual_out, y and the codes are each rounded once from fp32 (the
+ * codes by mx_quantize_act's rule, applied to the fp32 y: next to a rounding
+ * border they may differ from the codes of the bf16 y).
+ *   x [T, H] of x_type, residual [T, H] of residual_type or NULL (none),
+ *   weight [H] of weight_type (each MX_BF16 or MX_F32).
+ *   residual_out [T, H] of residual_type, given exactly where residual is; it
+ *     may be residual itself, or x where the types are equal.
+ *   y [T, H] bf16 or NULL.  codes [T, H] bytes (MX_E4M3) or [T, H/2]
+ *     (MX_E2M1), scales [T, H/32]: both or neither.  y or codes is given.
+ * Errors: MX_ERR_INVALID_ARG (null, T < 0, H <= 0, eps not positive and
+ * finite, an unknown type or format), MX_ERR_UNSUPPORTED (H % 32, H > 32768),
+ * MX_ERR_ALIGNMENT (a tensor other than scales not 16-byte aligned). */
+MX_API int mx_add_rmsnorm(const void* x, int x_type, const void* residual, int residual_type, const void* weight,
+                          int weight_type, int T, int H, float eps, void* residual_out, void* y, int fmt,
+                          uint8_t* codes, uint8_t* scales, mx_stream_t stream);
+
+/* A paged cache of keys and values in MX form.  Each of the four tables is
+ * dense, [num_pages, n_kv_heads, page_size, row] with row = head_dim bytes of
+ * codes (MX_E4M3; head_dim / 2 for MX_E2M1, element 2i in the low nibble) or
+ * head_dim / 32 scale bytes: a page holds page_size tokens of one sequence,
+ * head by head.  Codes are 16-byte aligned, scales 4-byte aligned. */
+typedef struct mx_kv_cache {
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  int num_pages;
+  int page_size;
+  int n_kv_heads;
+  int head_dim;
+  int fmt; /* MX_E4M3 or MX_E2M1 */
+} mx_kv_cache;
+
+/* The three cache calls describe a batch in the same way, on the device:
+ *   kv_lens [n_seqs]: tokens of each sequence in the cache, the new ones among
+ *     them (they are its last);
+ *   q_starts [n_seqs + 1]: new tokens q_starts[b] .. q_starts[b+1] - 1 of the
+ *     [T, ...] tensors belong to sequence b (ascending from 0; a sequence may
+ *     have none; rows from q_starts[n_seqs] on are padding);
+ *   block_table [n_seqs, max_pages]: the page of each page_size tokens.
+ * A length, start or page out of range sets MX_ERR_DEVICE_ARG in the workspace
+ * status; nothing is read or written through it (see each call).  ws is a
+ * 256-byte aligned, zero-filled workspace of at least 256 bytes, its first
+ * word the status word. */
+
+/* Quantises T new keys and values and writes them to their places in the cache:
+ * token t of sequence b goes to position kv_lens[b] - q_starts[b+1] + t.
+ *   k, v: bf16, token t's [n_kv_heads, head_dim] at t * stride elements.
+ * The codes are mx_quantize_act's of the same row, bit for bit.  Tokens with a
+ * bad length, start or page are skipped.  Two tokens with the same place leave
+ * either one.
+ * Errors: MX_ERR_INVALID_ARG (null, negative or zero sizes, unknown format, a
+ * stride below n_kv_heads * head_dim), MX_ERR_UNSUPPORTED (head_dim % 32),
+ * MX_ERR_ALIGNMENT (k, v or a stride not a multiple of 16 bytes, a table),
+ * MX_ERR_WORKSPACE. */
+MX_API int mx_kv_append(const mx_kv_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                        const int32_t* block_table, const int32_t* kv_lens, const int32_t* q_starts, int n_seqs,
+                        int max_pages, int T, void* ws, size_t ws_bytes, mx_stream_t stream);
+
+/* The reverse: the last q_starts[b+1] - q_starts[b] tokens of each sequence
+ * (all of them where q_starts counts kv_lens) as bf16 [T, n_kv_heads, head_dim],
+ * dense.  A code's value times its scale is exact in bf16 (but for overflow
+ * and bf16's subnormals, rounded to nearest even).  Rows of padding and of bad
+ * lengths, starts or pages are zero.  Errors as mx_kv_append. */
+MX_API int mx_kv_read(const mx_kv_cache* cache, const int32_t* block_table, const int32_t* kv_lens,
+                      const int32_t* q_starts, int n_seqs, int max_pages, int T, void* k_out, void* v_out, void* ws,
+                      size_t ws_bytes, mx_stream_t stream);
+
+/* Bytes of workspace mx_paged_attention needs for at most T tokens, n_seqs
+ * sequences and max_q_len new tokens in one of them (0 for a shape that it
+ * rejects). */
+MX_API size_t mx_paged_attention_workspace_size(int T, int n_seqs, int n_heads, int n_kv_heads, int head_dim,
+                                                int max_q_len);
+
+/* Attention of new tokens over the cache (which holds their keys and values
+ * already): for new token i of n of a sequence with kv keys, and query head h,
+ *   s_j = scale * q . k_j,  o = sum_j softmax(s)_j v_j,  lse = log sum_j exp s_j
+ * over its visible keys j: j < kv; with causal != 0, j <= kv - n + i; with
+ * window > 0 (causal only), also j > kv - n + i - window.  A row with no
+ * visible key gets o = 0 and lse = -inf.
+ *   q: bf16, token t's [n_heads, head_dim] at t * q_stride elements; query
+ *     heads h * (n_heads / n_kv_heads) .. share KV head h.
+ *   out [T, n_heads, head_dim] bf16, lse [T, n_heads] fp32 or NULL, dense.
+ *   max_q_len: no sequence has more new tokens (one that has is reported and
+ *     its rows are not written).
+ * Scores, softmax statistics and sums are fp32.  Rows of padding and of bad
+ * metadata are not written; a bad page's keys are left out.  Cache places that
+ * no row sees may hold anything, also pages behind the window may be gone.
+ * Deterministic: the same call gives the same bits.
+ * Errors: MX_ERR_INVALID_ARG (null, sizes, n_heads % n_kv_heads, scale not
+ * positive and finite, window < 0 or without causal, stride),
+ * MX_ERR_UNSUPPORTED (head_dim other than 64 and 128, page_size % 16, more
+ * than 2^30 rows), MX_ERR_ALIGNMENT, MX_ERR_WORKSPACE, MX_ERR_CUDA. */
+MX_API int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride, int n_heads,
+                              const int32_t* block_table, const int32_t* kv_lens, const int32_t* q_starts, int n_seqs,
+                              int max_pages, int T, int max_q_len, float scale, int causal, int window, void* out,
+                              float* lse, void* ws, size_t ws_bytes, mx_stream_t stream);
+
 /* Copy the workspace status word to *host_status (synchronising `stream`) and
  * clear it.  0 = no device-side error; otherwise an MX_ERR_* code. */
 MX_API int moe_get_status(void* ws, mx_stream_t stream, int* host_status);

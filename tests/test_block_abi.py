@@ -1,0 +1,130 @@
+"""Host-side argument checks of the operators around the expert layer: every
+call below is refused before any device work (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def L():
+    from block_scaled_mx_gb300 import build as B
+    from block_scaled_mx_gb300 import mxmoe as mx
+
+    B.build()
+    return mx.lib()
+
+
+P = ctypes.c_void_p
+fake = P(4096)   # never dereferenced
+odd = P(4098)
+
+
+def _norm(L, x=fake, xt=0, res=fake, rt=0, w=fake, wt=0, T=4, H=64, eps=1e-6, ro=fake, y=fake, fmt=0, codes=fake,
+          scales=fake):
+    return L.mx_add_rmsnorm(x, xt, res, rt, w, wt, T, H, eps, ro, y, fmt, codes, scales, None)
+
+
+def test_norm_refusals(L):
+    assert _norm(L, T=0) == 0
+    for bad in (dict(x=None), dict(w=None), dict(T=-1), dict(H=0), dict(xt=2), dict(wt=-1), dict(rt=3), dict(eps=0.0),
+                dict(eps=float("nan")), dict(eps=float("inf")), dict(fmt=2), dict(ro=None), dict(res=None),
+                dict(scales=None), dict(codes=None), dict(y=None, codes=None, scales=None)):
+        assert _norm(L, **bad) == 1, bad
+    for bad in (dict(H=48), dict(H=32800)):
+        assert _norm(L, **bad) == 2, bad
+    for bad in (dict(x=odd), dict(res=odd), dict(w=odd), dict(ro=odd), dict(y=odd), dict(codes=odd)):
+        assert _norm(L, **bad) == 3, bad
+
+
+def _cache(**kw):
+    from block_scaled_mx_gb300 import mxmoe as mx
+
+    f = dict(k_codes=4096, k_scales=4096, v_codes=4096, v_scales=4096, num_pages=8, page_size=16, n_kv_heads=2,
+             head_dim=64, fmt=0)
+    f.update(kw)
+    return mx.KVCacheTables(*(f[n] for n, _ in mx.KVCacheTables._fields_))
+
+
+BAD_CACHE = [(dict(num_pages=0), 1), (dict(page_size=-16), 1), (dict(n_kv_heads=0), 1), (dict(head_dim=0), 1),
+             (dict(fmt=2), 1), (dict(head_dim=80), 2), (dict(k_codes=0), 1), (dict(v_scales=0), 1), (dict(k_codes=4104), 3),
+             (dict(v_scales=4098), 3), (dict(page_size=2 ** 30), 2)]
+
+
+def test_cache_refusals(L):
+    def append(c=None, k=fake, ks=128, v=fake, vs=128, bt=fake, kv=fake, qs=fake, n=2, mp=4, T=4, ws=fake, wb=256):
+        c = _cache() if c is None else c
+        return L.mx_kv_append(ctypes.addressof(c), k, ks, v, vs, bt, kv, qs, n, mp, T, ws, wb, None)
+
+    def read(c=None, bt=fake, kv=fake, qs=fake, n=2, mp=4, T=4, ko=fake, vo=fake, ws=fake, wb=256):
+        c = _cache() if c is None else c
+        return L.mx_kv_read(ctypes.addressof(c), bt, kv, qs, n, mp, T, ko, vo, ws, wb, None)
+
+    assert L.mx_kv_append(None, fake, 128, fake, 128, fake, fake, fake, 2, 4, 4, fake, 256, None) == 1
+    assert L.mx_kv_read(None, fake, fake, fake, 2, 4, 4, fake, fake, fake, 256, None) == 1
+    assert append(T=0) == 0 and append(n=0) == 0 and read(T=0) == 0
+    for kw, want in BAD_CACHE:
+        assert append(_cache(**kw), ks=4096, vs=4096) == want, kw
+        assert read(_cache(**kw)) == want, kw
+    for f in (append, read):
+        for bad in (dict(bt=None), dict(kv=None), dict(qs=None), dict(ws=None), dict(T=-1), dict(n=-1), dict(mp=0)):
+            assert f(**bad) == 1, bad
+        assert f(ws=P(4112)) == 3 and f(bt=odd) == 3 and f(wb=255) == 4
+    assert append(k=None) == 1 and append(v=None) == 1 and append(ks=127) == 1 and append(vs=64) == 1
+    assert append(k=odd) == 3 and append(ks=132) == 3
+    assert read(ko=None) == 1 and read(vo=odd) == 3
+
+
+def test_attention_refusals(L):
+    size = L.mx_paged_attention_workspace_size(4, 2, 8, 2, 64, 4)
+    assert size > 256
+
+    def attend(c=None, q=fake, qs=512, h=8, bt=fake, kv=fake, st=fake, n=2, mp=4, T=4, mq=4, scale=0.1, causal=1, win=0,
+               out=fake, lse=fake, ws=fake, wb=size):
+        c = _cache() if c is None else c
+        return L.mx_paged_attention(ctypes.addressof(c), q, qs, h, bt, kv, st, n, mp, T, mq, scale, causal, win, out,
+                                    lse, ws, wb, None)
+
+    assert attend(T=0) == 0 and attend(n=0) == 0 and attend(mq=0) == 0
+    for kw, want in BAD_CACHE:
+        assert attend(_cache(**kw), qs=4096) == want, kw
+    for bad in (dict(q=None), dict(out=None), dict(bt=None), dict(kv=None), dict(st=None), dict(ws=None), dict(h=0),
+                dict(h=7), dict(qs=511), dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf")),
+                dict(scale=-1.0), dict(win=-1), dict(win=4, causal=0), dict(mq=-1), dict(T=-2)):
+        assert attend(**bad) == 1, bad
+    assert attend(_cache(head_dim=96), qs=4096) == 2 and attend(_cache(page_size=24)) == 2
+    assert attend(T=2 ** 28) == 2
+    for bad in (dict(q=odd), dict(qs=516), dict(out=odd), dict(lse=odd), dict(ws=P(4352 + 16))):
+        assert attend(**bad) == 3, bad
+    assert attend(wb=size - 1) == 4 and attend(wb=100) == 4
+
+
+def test_workspace_size_is_host_only(L):
+    f = L.mx_paged_attention_workspace_size
+    assert f(4, 2, 8, 3, 64, 4) == 0 and f(4, 2, 8, 2, 96, 4) == 0 and f(-1, 2, 8, 2, 64, 4) == 0
+    assert f(4096, 2, 32, 8, 128, 4096) >= f(1, 1, 32, 8, 128, 1)
+
+
+def test_binding_checks_tensors(L):
+    from block_scaled_mx_gb300 import mxmoe as mx
+
+    meta = dict(device="meta")
+    x = torch.empty(4, 64, dtype=torch.float16, **meta)
+    with pytest.raises(ValueError, match="weight"):
+        mx.mx_add_rmsnorm(x, torch.empty(32, **meta), 1e-6)
+    with pytest.raises(ValueError, match="codes"):
+        mx.mx_add_rmsnorm(x, torch.empty(64, **meta), 1e-6, codes=torch.empty(4, 64, dtype=torch.uint8, **meta), fmt="e2m1")
+    with pytest.raises(ValueError, match="CUDA"):
+        mx.KVCache(4, 16, 2, 64, device="cpu")
+    with pytest.raises(ValueError, match="k_scales"):
+        t = torch.empty(4, 2, 16, 64, dtype=torch.uint8)
+        mx.KVCache.of(t, t, t, t, 64)
+    with pytest.raises(ValueError, match="int32"):
+        mx._batch(torch.zeros(2, 3), torch.zeros(2), torch.zeros(3))
+    with pytest.raises(ValueError, match="kv_lens"):
+        i = torch.int32
+        mx._batch(torch.zeros(2, 3, dtype=i), torch.zeros(2, dtype=i), torch.zeros(2, dtype=i))
+    with pytest.raises(ValueError, match="dense"):
+        mx._rows(torch.empty(4, 64, 8, dtype=torch.bfloat16, **meta).transpose(1, 2), 8, 64, "q")
+    with pytest.raises(ValueError, match="bf16"):
+        mx._rows(torch.empty(4, 8, 64, **meta), 8, 64, "q")

@@ -1,0 +1,212 @@
+"""GPU parity of mx_paged_attention against a plain fp64 reference: ragged
+batches, head layouts, page sizes, windows, rows that see nothing, garbage in
+places that no row sees, and refusals on the device."""
+import math
+
+import pytest
+import torch
+
+from block_scaled_mx_gb300 import mxmoe as mx
+
+import block_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__ as g
+
+    g.build()
+    torch.cuda.set_device(0)
+    yield
+    torch.cuda.synchronize()
+
+
+def _setup(n, kv, heads, kv_heads, dim, page, fmt, seed=1, spread=0.5, garbage=True):
+    """Batch, q (a strided slice) and a cache whose unused places hold NaN codes and scales."""
+    batch = ref.make_batch(n, kv, page, seed)
+    g = torch.Generator().manual_seed(seed + 100)
+    q = torch.randn(max(batch.T, 1), heads * dim + 64, generator=g).to(torch.bfloat16)[: batch.T, : heads * dim]
+    cache = mx.KVCache(batch.pages, page, kv_heads, dim, fmt)
+    full = ref.Batch(list(kv), list(kv), page, batch.pages, batch.table)
+    if full.T:
+        k = torch.randn(full.T, kv_heads, dim, generator=g) * torch.exp(spread * torch.randn(1, kv_heads, dim, generator=g))
+        v = torch.randn(full.T, kv_heads, dim, generator=g) * torch.exp(spread * torch.randn(full.T, kv_heads, 1, generator=g))
+        if garbage:
+            for t in (cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales):
+                t.fill_(0x7F if t.shape[-1] > 4 else 0xFF)
+        ws = mx.alloc_workspace(256)
+        mx.mx_kv_append(cache, k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda(), *full.device(), ws)
+        assert mx.moe_get_status(ws) == 0
+    return batch, q.cuda().view(batch.T, heads, dim), cache
+
+
+def _call(batch, q, cache, dev=None, **kw):
+    T, heads, dim = q.shape
+    out = torch.full((T, heads, dim), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, heads), 3.0, dtype=torch.float32, device="cuda")
+    mq = kw.get("max_q_len", max(batch.n))
+    ws = mx.alloc_workspace(mx.mx_paged_attention_workspace_size(T, len(batch.n), heads, cache.n_kv_heads, dim, mq))
+    mx.mx_paged_attention(q, cache, *(dev or batch.device()), out, ws, lse=lse, **{"max_q_len": mq, **kw})
+    return out, lse, mx.moe_get_status(ws), ws
+
+
+def _compare(batch, q, cache, out, lse, fmt, scale, causal, window):
+    tables = [t.cpu() for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)]
+    o, l, tol, tol_l = ref.attention(q.cpu(), *tables, fmt, batch, scale, causal, window)
+    got, got_l = out.cpu().double(), lse.cpu().double()
+    assert torch.equal(torch.isinf(got_l), torch.isinf(l))
+    assert torch.all(torch.isfinite(got))
+    bad = (got - o).abs() - tol
+    assert float(bad.max()) <= 0, f"out: worst {float(bad.max())} over its bound at {bad.argmax()}"
+    seen = ~torch.isinf(l)
+    assert torch.all((got_l - l).abs()[seen] <= tol_l[seen])
+    assert torch.all(got[~seen] == 0)
+
+
+def _check(n, kv, heads, kv_heads, dim, page, fmt="e4m3", causal=True, window=0, scale=None, **kw):
+    batch, q, cache = _setup(n, kv, heads, kv_heads, dim, page, fmt, **kw)
+    out, lse, status, _ = _call(batch, q, cache, causal=causal, window=window, scale=scale)
+    assert status == 0
+    _compare(batch, q, cache, out, lse, fmt, dim ** -0.5 if scale is None else scale, causal, window)
+
+
+SHAPES = [
+    # one token, one key; one token, many
+    ([1], [1], 1, 1, 64, 16), ([1], [1], 8, 1, 128, 64), ([1, 1, 1], [17, 64, 65], 8, 2, 128, 16),
+    ([1], [700], 16, 1, 128, 128), ([1] * 5, [300, 1, 64, 33, 129], 13, 1, 64, 32),
+    # drafts; a batch that mixes lengths, with an empty sequence and an empty cache
+    ([6], [70], 16, 2, 128, 64), ([2, 0, 5, 1], [2, 0, 90, 200], 4, 4, 64, 48),
+    # chunks
+    ([40], [40], 8, 2, 128, 16), ([100, 1, 37], [150, 30, 37], 10, 2, 64, 16), ([65], [300], 5, 1, 128, 64),
+    ([130, 3], [131, 259], 6, 3, 128, 32),
+]
+
+
+@pytest.mark.parametrize("n,kv,heads,kv_heads,dim,page", SHAPES)
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_causal(n, kv, heads, kv_heads, dim, page, fmt):
+    _check(n, kv, heads, kv_heads, dim, page, fmt)
+
+
+@pytest.mark.parametrize("n,kv,heads,kv_heads,dim,page", SHAPES[2:])
+def test_all_keys(n, kv, heads, kv_heads, dim, page):
+    _check(n, kv, heads, kv_heads, dim, page, causal=False, seed=4)
+
+
+@pytest.mark.parametrize("window", [1, 7, 64, 65, 1000, 2 ** 31 - 1])
+@pytest.mark.parametrize("n,kv,heads,kv_heads,dim,page", [([1, 1], [300, 5], 8, 1, 128, 16), ([50, 3], [200, 100], 4, 2, 64, 32),
+                                                          ([140], [400], 8, 8, 128, 64)])
+def test_window(n, kv, heads, kv_heads, dim, page, window):
+    _check(n, kv, heads, kv_heads, dim, page, window=window, seed=6)
+
+
+def test_rows_that_see_nothing():
+    """More new tokens than keys: the first ones' rows see no key; a sequence
+    without keys; rows are zero with lse -inf, never NaN."""
+    _check([5, 1, 20, 64], [2, 0, 0, 30], 8, 2, 128, 16)
+    _check([5, 1, 20], [2, 0, 0], 8, 2, 64, 16, causal=False)
+
+
+def test_long_split_segments():
+    """Long contexts of few heads: every segment is split over many CTAs."""
+    _check([1, 2], [20000, 3001], 2, 1, 128, 64, seed=8)
+    _check([1], [9000], 8, 1, 64, 16, fmt="e2m1", seed=9)
+    _check([9], [6000], 8, 1, 128, 32, seed=10)
+
+
+def test_scale_and_peaked_scores():
+    """Large scores: one key takes nearly all of a row's weight."""
+    _check([3, 40], [80, 100], 4, 2, 128, 16, scale=4.0, seed=12)
+
+
+@pytest.mark.parametrize("n,kv", [([1, 3], [200, 150]), ([70], [260])])
+def test_values_of_far_apart_sizes(n, kv):
+    """Tokens whose keys and values differ by 2^60, later (masked) ones among
+    them: a row's result depends on what it sees alone."""
+    heads, kv_heads, dim, page = 8, 2, 128, 16
+    batch = ref.make_batch(n, kv, page, 21)
+    g = torch.Generator().manual_seed(22)
+    full = ref.Batch(list(kv), list(kv), page, batch.pages, batch.table)
+    k = torch.randn(full.T, kv_heads, dim, generator=g)
+    v = torch.randn(full.T, kv_heads, dim, generator=g) * torch.pow(2.0, torch.randint(-30, 31, (full.T, kv_heads, 1), generator=g).float())
+    last = torch.tensor(full.starts[1:]) - 1
+    v[last] *= 2.0 ** 40        # the newest token: only its own row sees it
+    k[last] *= 2.0 ** 20
+    q = torch.randn(batch.T, heads, dim, generator=g).to(torch.bfloat16)
+    q[torch.tensor(batch.starts[1:]) - 1] *= 2.0 ** -20   # whose scores stay ordinary
+    for fmt in ("e4m3", "e2m1"):
+        cache = mx.KVCache(batch.pages, page, kv_heads, dim, fmt)
+        ws = mx.alloc_workspace(256)
+        mx.mx_kv_append(cache, k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda(), *full.device(), ws)
+        out, lse, status, _ = _call(batch, q.cuda(), cache)
+        assert status == 0
+        _compare(batch, q.cuda(), cache, out, lse, fmt, dim ** -0.5, True, 0)
+
+
+def test_pages_behind_the_window_may_be_gone():
+    batch, q, cache = _setup([1, 20], [500, 400], 8, 2, 128, 16, "e4m3", seed=31)
+    window = 50
+    want, want_l, status, _ = _call(batch, q, cache, window=window)
+    assert status == 0
+    table, kv, starts = batch.device()
+    table = table.clone()
+    table[0, : (500 - window) // 16] = -1
+    table[1, : (400 - 20 - window) // 16] = 2 ** 30
+    out, lse, status, _ = _call(batch, q, cache, dev=(table, kv, starts), window=window)
+    assert status == 0
+    assert torch.equal(out, want) and torch.equal(lse, want_l)
+
+
+def test_bad_metadata_is_reported():
+    """A bad page's keys are left out; a bad length or more new tokens than
+    max_q_len leave the sequence's rows unwritten; padding rows too."""
+    batch, q, cache = _setup([1, 2, 1, 4], [64, 40, 33, 50], 8, 2, 128, 16, "e4m3", seed=41)
+    pad = torch.cat([q, q[:2]]).contiguous()
+    table, kv, starts = (t.clone() for t in batch.device())
+    table[0, 2] = -7            # keys 32 .. 47 of sequence 0
+    kv[2] = 10 ** 9
+    out, lse, status, ws = _call(batch, pad, cache, dev=(table, kv, starts), max_q_len=2)
+    assert status == mx.MX_ERR_DEVICE_ARG
+    assert mx.moe_get_status(ws) == 0
+    assert torch.all(out[3:] == 3.0) and torch.all(lse[3:] == 3.0)
+    # sequence 0 without the page's keys, from a batch that has only the others
+    less = ref.Batch([1], [48], 16, batch.pages, torch.cat([batch.table[:1, :2], batch.table[:1, 3:4]], 1))
+    tables = [t.cpu() for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)]
+    o, l, tol, tol_l = ref.attention(q[:1].cpu(), *tables, "e4m3", less, 128 ** -0.5, True, 0)
+    assert torch.all((out[:1].cpu().double() - o).abs() <= tol) and torch.all((lse[:1].cpu().double() - l).abs() <= tol_l)
+
+
+@pytest.mark.parametrize("n,kv", [([1] * 9, [900] * 9), ([90, 30], [700, 333])])
+def test_same_bits_again_and_on_another_stream_and_in_a_graph(n, kv):
+    batch, q, cache = _setup(n, kv, 8, 2, 128, 16, "e4m3", seed=51)
+    want, want_l, status, ws = _call(batch, q, cache)
+    assert status == 0
+    dev = batch.device()
+    out, lse = torch.empty_like(want), torch.empty_like(want_l)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(3):
+            mx.mx_paged_attention(q, cache, *dev, out, ws, max_q_len=max(n), lse=lse)
+    s.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_l)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mx.mx_paged_attention(q, cache, *dev, out, ws, max_q_len=max(n), lse=lse)
+    out.zero_()
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_l)
+    assert mx.moe_get_status(ws) == 0
+
+
+def test_many_sequences():
+    """More sequences than a block has threads."""
+    n = [b % 3 for b in range(300)]
+    kv = [t + (7 * b) % 50 for b, t in enumerate(n)]
+    _check(n, kv, 4, 2, 64, 16, seed=61)
