@@ -269,6 +269,8 @@ int run_gemm2(const uint8_t* h_codes, const uint8_t* h_scales, const int32_t* of
 
 }  // namespace
 
+uint64_t mxk::wait_limit_ns() { return g_wait_limit_ns; }
+
 extern "C" {
 
 const char* mx_status_string(int status) {

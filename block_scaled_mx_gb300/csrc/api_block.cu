@@ -66,6 +66,11 @@ KvArgs kv_args(const mx_kv_cache* c, const int32_t* block_table, const int32_t* 
 constexpr size_t kArrivedOffset = 256;
 constexpr size_t kArrivedBytes = sizeof(unsigned) * kAttnMaxCtas;
 
+// Sequences of up to kFewRows rows (new tokens x query heads of a KV head) are
+// the few-rows kernel's, others the chunk kernel's.
+constexpr int kFewRows = 16;
+bool has_chunks(int group, int max_q_len) { return static_cast<int64_t>(max_q_len) * group > kFewRows; }
+
 int check_attention(int T, int n_seqs, int n_heads, int n_kv_heads, int head_dim, int max_q_len) {
   if (T < 0 || n_seqs < 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || max_q_len < 0) return MX_ERR_INVALID_ARG;
   if (n_heads % n_kv_heads) return MX_ERR_INVALID_ARG;
@@ -147,7 +152,9 @@ int mx_kv_read(const mx_kv_cache* cache, const int32_t* block_table, const int32
 
 size_t mx_paged_attention_workspace_size(int T, int n_seqs, int n_heads, int n_kv_heads, int head_dim, int max_q_len) {
   if (check_attention(T, n_seqs, n_heads, n_kv_heads, head_dim, max_q_len) != MX_OK) return 0;
-  return kArrivedOffset + al256(kArrivedBytes) + attn_rows_part_bytes(head_dim);
+  size_t part = attn_rows_part_bytes(head_dim);
+  if (has_chunks(n_heads / n_kv_heads, max_q_len) && attn_chunk_part_bytes(head_dim) > part) part = attn_chunk_part_bytes(head_dim);
+  return kArrivedOffset + al256(kArrivedBytes) + part;
 }
 
 int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride, int n_heads,
@@ -161,6 +168,8 @@ int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride
   if (!finite_positive(scale) || window < 0 || (window > 0 && !causal)) return MX_ERR_INVALID_ARG;
   if (q_stride < static_cast<int64_t>(n_heads) * cache->head_dim) return MX_ERR_INVALID_ARG;
   if (cache->page_size % 16) return MX_ERR_UNSUPPORTED;
+  // cache rows are counted in ints
+  if (static_cast<int64_t>(cache->num_pages) * cache->page_size > INT_MAX / cache->n_kv_heads) return MX_ERR_UNSUPPORTED;
   if (T == 0 || n_seqs == 0 || max_q_len == 0) return MX_OK;
   if (!q || !out) return MX_ERR_INVALID_ARG;
   st = check_cache_pointers(cache, block_table, kv_lens, q_starts, ws, ws_bytes);
@@ -197,10 +206,20 @@ int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride
   a.status = static_cast<int*>(ws);
   a.arrived = reinterpret_cast<unsigned*>(w + kArrivedOffset);
   a.part_ml = reinterpret_cast<float2*>(w + kArrivedOffset + al256(kArrivedBytes));
+  a.wait_limit_ns = wait_limit_ns();
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   a.rows_above = 0;
   a.rows_upto = INT_MAX;
-  a.min_units = 4;
-  return cuda_status(launch_attn_rows(a, reinterpret_cast<cudaStream_t>(stream)));
+  if (!has_chunks(a.group, max_q_len)) return cuda_status(launch_attn_rows(a, cs));
+  // Where all sequences are as long as the longest (T has room for it), one
+  // launch takes them all; a shorter one among them is right there too.
+  if (T >= static_cast<int64_t>(n_seqs) * max_q_len) return cuda_status(launch_attn_chunk(a, cs));
+  a.rows_upto = kFewRows;
+  st = cuda_status(launch_attn_rows(a, cs));
+  if (st != MX_OK) return st;
+  a.rows_above = kFewRows;
+  a.rows_upto = INT_MAX;
+  return cuda_status(launch_attn_chunk(a, cs));
 }
 
 }  // extern "C"

@@ -72,101 +72,184 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnArgs& a, const AttnSeq& 
   return t;
 }
 
-// Units of one KV head of a sequence.
-template <int kRows, int kUnit>
+// Units of one KV head of a sequence; kWarp: the lanes of a warp (all with the
+// same sequence) take the tiles in turn.
+template <int kRows, int kUnit, bool kWarp>
 __device__ __forceinline__ int attn_seq_units(const AttnArgs& a, const AttnSeq& s) {
   int u = 0;
-  for (int t = 0; t < s.tiles; ++t) u += attn_tile<kRows, kUnit>(a, s, t).units;
-  return u;
+  for (int t = kWarp ? threadIdx.x & 31 : 0; t < s.tiles; t += kWarp ? 32 : 1) u += attn_tile<kRows, kUnit>(a, s, t).units;
+  return kWarp ? __reduce_add_sync(0xffffffffu, u) : u;
 }
-
-// A CTA's stretch [u, end) of the line and the sequence that holds u, with u's
-// place inside that sequence.
-struct AttnShare {
-  int64_t total;
-  int ctas;        // CTAs that have a stretch
-  int64_t u, end;
-  int seq;
-  int64_t in_seq;
-};
 
 // The CTA whose stretch holds unit u: the largest c with total * c / ctas <= u.
 __device__ __forceinline__ int attn_cta_of(int64_t u, int64_t total, int ctas) {
   return static_cast<int>(((u + 1) * ctas - 1) / total);
 }
-__device__ __forceinline__ int64_t attn_start_of(int c, int64_t total, int ctas) { return total * c / ctas; }
 
-// Block-wide; kThreads threads call it, scratch holds kThreads / 32 + 4 words.
-template <int kRows, int kUnit, int kThreads>
-__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int64_t* scratch) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kW = kThreads / 32;
+// A CTA's stretch [u, end) of the line.
+struct AttnShare {
+  int64_t total;
+  int ctas;        // CTAs that have a stretch
+  int64_t u, end;
+  int seq;         // the sequence that holds u,
+  int64_t in_seq;  // and u's place in it
+};
+
+constexpr int kAttnScan = 128;  // sequences looked at together
+
+// Block-wide (kThreads threads); `units` holds kAttnScan words.  kWarp: a warp
+// counts a sequence (long ones have hundreds of tiles), else a thread.
+template <int kRows, int kUnit, int kThreads, bool kWarp>
+__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int64_t* units) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  auto count = [&](int b0, bool report) {
+    for (int i = kWarp ? tid / 32 : tid; i < kAttnScan; i += kWarp ? kThreads / 32 : kThreads) {
+      int64_t u = 0;
+      if (b0 + i < a.n_seqs) {
+        const AttnSeq s = attn_seq<kRows>(a, b0 + i, report && blockIdx.x == 0);
+        u = static_cast<int64_t>(attn_seq_units<kRows, kUnit, kWarp>(a, s)) * a.n_kv_heads;
+      }
+      if (!kWarp || lane == 0) units[i] = u;
+    }
+    __syncthreads();
+  };
+  constexpr int kPer = kAttnScan / 32;
   AttnShare r;
-  // the line's length
-  int64_t mine = 0, first_units = 0;
-  for (int b = tid; b < a.n_seqs; b += kThreads) {
-    const AttnSeq s = attn_seq<kRows>(a, b, blockIdx.x == 0);
-    const int64_t u = static_cast<int64_t>(attn_seq_units<kRows, kUnit>(a, s)) * a.n_kv_heads;
-    if (b == tid) first_units = u;
-    mine += u;
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-  if (lane == 0) scratch[warp] = mine;
-  __syncthreads();
   r.total = 0;
+  int64_t v[kPer], mine = 0;
+  for (int b0 = 0; b0 < a.n_seqs; b0 += kAttnScan) {
+    count(b0, true);
+    mine = 0;
 #pragma unroll
-  for (int w = 0; w < kW; ++w) r.total += scratch[w];
-  __syncthreads();
-  int64_t n = (r.total + a.min_units - 1) / a.min_units;
+    for (int i = 0; i < kPer; ++i) mine += v[i] = units[lane * kPer + i];
+    int64_t all = mine;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+    r.total += all;
+    __syncthreads();
+  }
+  const int64_t n = (r.total + a.min_units - 1) / a.min_units;
   r.ctas = static_cast<int>(n < gridDim.x ? n : gridDim.x);
   r.seq = 0;
-  r.in_seq = 0;
-  r.u = r.end = 0;
+  r.in_seq = r.u = r.end = 0;
   if (static_cast<int>(blockIdx.x) >= r.ctas) return r;
-  r.u = attn_start_of(blockIdx.x, r.total, r.ctas);
-  r.end = attn_start_of(blockIdx.x + 1, r.total, r.ctas);
-  // the sequence that holds u: inclusive scans of kThreads sequences at a time
+  r.u = r.total * blockIdx.x / r.ctas;
+  r.end = r.total * (blockIdx.x + 1) / r.ctas;
   int64_t before = 0;
-  for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
-    const int b = b0 + tid;
-    int64_t v = first_units;
-    if (b0 > 0) {
-      v = 0;
-      if (b < a.n_seqs) {
-        const AttnSeq s = attn_seq<kRows>(a, b, false);
-        v = static_cast<int64_t>(attn_seq_units<kRows, kUnit>(a, s)) * a.n_kv_heads;
-      }
+  for (int b0 = 0; b0 < a.n_seqs; b0 += kAttnScan) {
+    if (a.n_seqs > kAttnScan) {
+      count(b0, false);
+      mine = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) mine += v[i] = units[lane * kPer + i];
+      __syncthreads();
     }
-    int64_t incl = v;
+    int64_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += o;
     }
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    int64_t all = 0, below = before;
+    int64_t from = before + incl - mine;
+    int at = -1;
+    int64_t in = 0;
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      if (w < warp) below += scratch[w];
-      all += scratch[w];
+    for (int i = 0; i < kPer; ++i) {
+      if (r.u >= from && r.u < from + v[i]) {
+        at = b0 + lane * kPer + i;
+        in = r.u - from;
+      }
+      from += v[i];
     }
-    const int64_t from = below + incl - v;
-    if (v > 0 && from <= r.u && r.u < from + v) {
-      scratch[kW] = b;
-      scratch[kW + 1] = r.u - from;
+    before += __shfl_sync(0xffffffffu, incl, 31);
+    const unsigned hit = __ballot_sync(0xffffffffu, at >= 0);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      r.seq = __shfl_sync(0xffffffffu, at, src);
+      r.in_seq = __shfl_sync(0xffffffffu, in, src);
+      break;
     }
-    before += all;
-    const bool found = r.u < before;
-    __syncthreads();
-    if (found) break;
   }
-  r.seq = static_cast<int>(scratch[kW]);
-  r.in_seq = scratch[kW + 1];
-  __syncthreads();
   return r;
 }
+
+// Where a CTA is on the line: a segment (one row tile of one KV head of one
+// sequence) and the unit `place` of it.
+template <int kRows, int kUnit>
+struct AttnCursor {
+  int b, head, tile, place;
+  AttnSeq s;
+  AttnTile t;
+
+  // At the share's first unit; whole warps call it.
+  template <bool kWarp>
+  __device__ __forceinline__ void start(const AttnArgs& a, const AttnShare& share) {
+    b = share.seq;
+    s = attn_seq<kRows>(a, b, false);
+    const int per_head = attn_seq_units<kRows, kUnit, kWarp>(a, s);
+    head = static_cast<int>(share.in_seq / max(per_head, 1));
+    place = static_cast<int>(share.in_seq - static_cast<int64_t>(head) * per_head);
+    tile = 0;
+    if (kWarp) {
+      const int lane = threadIdx.x & 31;
+      for (; tile < s.tiles; tile += 32) {
+        const int u = tile + lane < s.tiles ? attn_tile<kRows, kUnit>(a, s, tile + lane).units : 0;
+        int incl = u;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += o;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, place < incl);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          place -= __shfl_sync(0xffffffffu, incl - u, src);
+          tile += src;
+          break;
+        }
+        place -= __shfl_sync(0xffffffffu, incl, 31);
+      }
+      t = attn_tile<kRows, kUnit>(a, s, tile);
+    } else {
+      t = attn_tile<kRows, kUnit>(a, s, 0);
+      while (place >= t.units && tile + 1 < s.tiles) {
+        place -= t.units;
+        t = attn_tile<kRows, kUnit>(a, s, ++tile);
+      }
+    }
+  }
+
+  // To the next segment's first unit (there is one: the caller's stretch goes on).
+  __device__ __forceinline__ void next(const AttnArgs& a) {
+    place = 0;
+    if (++tile == s.tiles) {
+      tile = 0;
+      if (++head == a.n_kv_heads) {
+        head = 0;
+        do {
+          if (++b >= a.n_seqs) return;
+          s = attn_seq<kRows>(a, b, false);
+        } while (s.tiles == 0);
+      }
+    }
+    t = attn_tile<kRows, kUnit>(a, s, tile);
+  }
+};
+
+// How a segment of `units` units from `seg` on is shared out: its parts lie
+// with CTAs first .. first + parts - 1.
+struct AttnParts {
+  int first, parts;
+};
+__device__ __forceinline__ AttnParts attn_parts(const AttnShare& sh, int64_t seg, int units) {
+  AttnParts p;
+  p.first = attn_cta_of(seg, sh.total, sh.ctas);
+  p.parts = attn_cta_of(seg + units - 1, sh.total, sh.ctas) - p.first + 1;
+  return p;
+}
+// The workspace slot of a CTA's part: the part that begins a segment and those
+// that continue one lie apart (a CTA has at most one of each that is not whole).
+__device__ __forceinline__ int attn_slot(int cta, bool begins) { return 2 * cta + (begins ? 1 : 0); }
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;

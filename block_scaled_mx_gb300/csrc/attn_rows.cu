@@ -36,6 +36,7 @@ constexpr int kUnit = 64;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 3;
+constexpr int kMinUnits = 4;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -102,32 +103,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
   using Sh = RowsShape<D, E2M1>;
   __shared__ __align__(16) float s_o[kWarps][kRows][D];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
-  __shared__ int64_t s_scratch[kWarps + 4];
+  __shared__ int64_t s_units[kAttnScan];
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const AttnShare share = attn_share<kRows, kUnit, kThreads>(a, s_scratch);
-  int64_t u = share.u;
-  int b = share.seq;
-  int64_t in_seq = share.in_seq;
+  const AttnShare share = attn_share<kRows, kUnit, kThreads, false>(a, s_units);
   const int n_heads = a.n_kv_heads * a.group;
+  int64_t u = share.u;
+  AttnCursor<kRows, kUnit> cur;
+  if (u < share.end) cur.template start<false>(a, share);
 
-  while (u < share.end && b < a.n_seqs) {
-    // ---------------------------------------------------------------- the segment that holds u
-    const AttnSeq s = attn_seq<kRows>(a, b, false);
-    const int per_head = attn_seq_units<kRows, kUnit>(a, s);
-    if (in_seq >= static_cast<int64_t>(per_head) * a.n_kv_heads) {  // on to the next sequence
-      ++b;
-      in_seq = 0;
-      continue;
-    }
-    const int head = static_cast<int>(in_seq / per_head);
-    int place = static_cast<int>(in_seq - static_cast<int64_t>(head) * per_head);
-    int tile = 0;
-    AttnTile t = attn_tile<kRows, kUnit>(a, s, 0);
-    while (place >= t.units) {
-      place -= t.units;
-      t = attn_tile<kRows, kUnit>(a, s, ++tile);
-    }
+  while (u < share.end && cur.b < a.n_seqs) {
+    const AttnSeq& s = cur.s;
+    const AttnTile& t = cur.t;
+    const int head = cur.head, tile = cur.tile, place = cur.place;
     const int take = static_cast<int>(min(static_cast<int64_t>(t.units - place), share.end - u));
     const int rows = s.n * a.group;
     const int base = s.kv - s.n;
@@ -186,18 +174,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
     for (int i = 0; i < Sh::kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
-    const int32_t* table = a.block_table + static_cast<int64_t>(b) * a.max_pages;
+    const int32_t* table = a.block_table + static_cast<int64_t>(cur.b) * a.max_pages;
     // Row index of 16 keys from `key` (a page holds a multiple of 16): or -1
     // where there is nothing to read.
     auto find_row = [&](int key) -> int64_t {
       if (key >= t.hi || key + 16 <= t.lo) return -1;
-      const int p = key / a.page_size;
-      const int page = __ldg(table + p);
+      const int entry = key / a.page_size;
+      const int page = __ldg(table + entry);
       if (page < 0 || page >= a.num_pages) {
         if (lane == 0) set_status(a.status, MX_ERR_DEVICE_ARG);
         return -1;
       }
-      return (static_cast<int64_t>(page) * a.n_kv_heads + head) * a.page_size + (key - p * a.page_size);
+      return (static_cast<int64_t>(page) * a.n_kv_heads + head) * a.page_size + (key - entry * a.page_size);
     };
     uint32_t kw[2][Sh::kPieces][Sh::kPieceWords], ks[2], vw[4][Sh::kVWords], vs[4];
     auto load_k = [&](int64_t row) {
@@ -386,10 +374,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
     __syncthreads();
 
     const bool whole = take == t.units;
-    const int64_t seg = u - place;  // the segment's first unit on the line
-    const int first_cta = attn_cta_of(seg, share.total, share.ctas);
-    const int parts = attn_cta_of(seg + t.units - 1, share.total, share.ctas) - first_cta + 1;
-    const int slot = 2 * static_cast<int>(blockIdx.x) + (place == 0 ? 1 : 0);
+    const AttnParts p = attn_parts(share, u - place, t.units);
+    const int slot = attn_slot(blockIdx.x, place == 0);
 
     // writes a finished row: four elements a lane
     auto finish = [&](int r, int d4, float4 acc, float M, float L) {
@@ -433,21 +419,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
       // ---------------------------------------------------------------- join the CTAs
       __threadfence();
       __syncthreads();
-      if (tid == 0) s_last = atomicAdd(&a.arrived[first_cta], 1u) == static_cast<unsigned>(parts - 1);
+      if (tid == 0) s_last = atomicAdd(&a.arrived[p.first], 1u) == static_cast<unsigned>(p.parts - 1);
       __syncthreads();
       if (s_last) {
         __threadfence();
-        // part i's slot: the first part began the segment, the others continue it
-        auto slot_of = [&](int i) { return 2 * (first_cta + i) + (i == 0 ? 1 : 0); };
+        auto slot_of = [&](int i) { return attn_slot(p.first + i, i == 0); };
         for (int r = warp; r < kRows && tile * kRows + r < rows; r += kWarps) {
           float M = -INFINITY;
-          for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(&a.part_ml[slot_of(i) * kRows + r]).x);
+          for (int i = lane; i < p.parts; i += 32) M = fmaxf(M, __ldcg(&a.part_ml[slot_of(i) * kRows + r]).x);
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
           float L = 0.0f;
           float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-          for (int i = 0; i < parts; ++i) {
+          for (int i = 0; i < p.parts; ++i) {
             const int sl = slot_of(i);
             const float2 ml = __ldcg(&a.part_ml[sl * kRows + r]);
             const float f = M == -INFINITY ? 0.0f : exp2_approx(ml.x - M);
@@ -460,12 +445,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
           }
           if (lane < kLanes) finish(r, lane, acc, M, L);
         }
-        if (tid == 0) a.arrived[first_cta] = 0u;  // ready for the next launch
+        if (tid == 0) a.arrived[p.first] = 0u;  // ready for the next launch
       }
     }
     __syncthreads();  // the warps' parts are read before the next segment overwrites them
     u += take;
-    in_seq += take;
+    if (u < share.end) cur.next(a);
   }
 }
 
@@ -488,6 +473,7 @@ size_t attn_rows_part_bytes(int head_dim) {
 }
 
 cudaError_t launch_attn_rows(AttnArgs a, cudaStream_t s) {
+  a.min_units = kMinUnits;
   a.part_o = reinterpret_cast<float*>(a.part_ml + static_cast<size_t>(2) * kAttnMaxCtas * kRows);
   if (a.head_dim == 128) return a.e2m1 ? launch<128, true>(a, s) : launch<128, false>(a, s);
   return a.e2m1 ? launch<64, true>(a, s) : launch<64, false>(a, s);

@@ -94,6 +94,9 @@ cudaError_t launch_prepare_weights(const uint8_t* codes, const uint8_t* scales,
 
 cudaError_t launch_zero(void* p, size_t bytes, cudaStream_t s);
 
+// ---- api.cu
+uint64_t wait_limit_ns();  // mx_debug_set_wait_limit_ns
+
 // ---- norm.cu
 struct NormArgs {
   const void* x;           // [T, H] bf16 or fp32
@@ -151,6 +154,8 @@ struct AttnArgs {
 };
 size_t attn_rows_part_bytes(int head_dim);           // part_ml and part_o of the few-rows kernel
 cudaError_t launch_attn_rows(AttnArgs a, cudaStream_t s);
+size_t attn_chunk_part_bytes(int head_dim);          // the same of the chunk kernel
+cudaError_t launch_attn_chunk(AttnArgs a, cudaStream_t s);
 
 // ---- router.cu
 struct RouterArgs {

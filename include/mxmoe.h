@@ -432,11 +432,12 @@ MX_API size_t mx_paged_attention_workspace_size(int T, int n_seqs, int n_heads, 
  * Scores, softmax statistics and sums are fp32.  Rows of padding and of bad
  * metadata are not written; a bad page's keys are left out.  Cache places that
  * no row sees may hold anything, also pages behind the window may be gone.
- * Deterministic: the same call gives the same bits.
+ * Deterministic: the same call gives the same bits.  Two launches at most: one
+ * for sequences with few rows, one for chunks.
  * Errors: MX_ERR_INVALID_ARG (null, sizes, n_heads % n_kv_heads, scale not
  * positive and finite, window < 0 or without causal, stride),
  * MX_ERR_UNSUPPORTED (head_dim other than 64 and 128, page_size % 16, more
- * than 2^30 rows), MX_ERR_ALIGNMENT, MX_ERR_WORKSPACE, MX_ERR_CUDA. */
+ * than 2^30 rows of q or 2^31 of a cache table), MX_ERR_ALIGNMENT, MX_ERR_WORKSPACE, MX_ERR_CUDA. */
 MX_API int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride, int n_heads,
                               const int32_t* block_table, const int32_t* kv_lens, const int32_t* q_starts, int n_seqs,
                               int max_pages, int T, int max_q_len, float scale, int causal, int window, void* out,

@@ -210,3 +210,22 @@ def test_many_sequences():
     n = [b % 3 for b in range(300)]
     kv = [t + (7 * b) % 50 for b, t in enumerate(n)]
     _check(n, kv, 4, 2, 64, 16, seed=61)
+
+
+def test_wait_that_runs_out_is_reported_and_the_next_call_is_right():
+    """The chunk kernel's waits are bounded; a limit of zero makes them run out,
+    which is reported and leaves the workspace ready."""
+    n, kv = [90, 300], [700, 333]
+    batch, q, cache = _setup(n, kv, 8, 2, 128, 16, "e4m3", seed=71)
+    want, want_l, status, ws = _call(batch, q, cache)
+    assert status == 0
+    out, lse = torch.empty_like(want), torch.empty_like(want_l)
+    try:
+        mx.mx_debug_set_wait_limit_ns(0)
+        mx.mx_paged_attention(q, cache, *batch.device(), out, ws, max_q_len=max(n), lse=lse)
+        assert mx.moe_get_status(ws) == mx.MX_ERR_TIMEOUT
+    finally:
+        mx.mx_debug_set_wait_limit_ns(2_000_000_000)
+    mx.mx_paged_attention(q, cache, *batch.device(), out, ws, max_q_len=max(n), lse=lse)
+    assert mx.moe_get_status(ws) == 0
+    assert torch.equal(out, want) and torch.equal(lse, want_l)
