@@ -4,26 +4,36 @@
 //
 // A tile is 256 rows (new tokens x the query heads of one KV head) as two MMA
 // tiles of 128, A and B, that take turns: while the tensor cores work for one,
-// the softmax of the other runs.  Keys come in units of 128.  Roles (13 warps):
+// the softmax of the other runs.  Roles (sixteen warps, registers moved to the
+// softmax's):
 //   0-3, 4-7  softmax of A and of B, one row a thread; also its queries, the
 //             rescaling of its accumulator and its output
-//   8-11      reading the cache: codes and scales through registers into the
-//             16-bit operands in shared memory (two stages of K and of V)
+//   8-11      V: codes and scales through registers into the 16-bit operand in
+//             shared memory; K's scales into tensor memory
 //   12        issuing MMAs
-// For each unit, S = Q K^T goes to tensor memory, its softmax weights P
+//   13        K's codes, by TMA
+// For each unit of keys, S = Q K^T goes to tensor memory, its softmax weights P
 // overwrite it there, and O += P V reads P from tensor memory.
 //
-// Arithmetic.  Q and K are bf16: every code times its scale is exact there,
-// relative to the unit's largest K scale, which multiplies the score in fp32.
-// V is exact in f16 relative to the unit's largest V scale e as long as the
-// unit's scales lie within 2^15; P is then rounded to f16 (2^-11).  A unit with
-// a wider spread takes bf16 for both (V exact, P 2^-8).  As in the few-rows
+// Arithmetic.  S is a block-scaled MMA on the cache's own codes and scales, so K
+// is never widened.  A query row is split into two MXFP8 operands, q = hi + lo:
+// hi is q on a grid of 4 significant bits, lo the rest (at most 5 bits) at a
+// scale 2^-5 of hi's.  Together they hold bf16's 8 bits of every element down
+// to 2^-13 of its block's largest, and 2^-21 of the largest below; two MMAs at
+// the 8-bit rate cost what one bf16 MMA would.
+// V varies its scale along N, which the block-scaled MMA cannot take, so V is
+// widened: exactly, to f16 relative to the unit's largest V scale e, as long as
+// the unit's scales lie within 2^15; P is then rounded to f16 (2^-11).  A unit
+// with a wider spread takes bf16 for both (V exact, P 2^-8).  As in the few-rows
 // kernel e joins the softmax's exponent: P = 2^(x + e - M) with M the running
 // maximum of x + e, and the sum adds (sum of P) 2^-e.  M moves only when it
 // would grow by more than 2^8, so O is seldom rescaled.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -36,41 +46,64 @@ namespace mxk {
 namespace {
 
 constexpr int kRows = 256;
-constexpr int kUnit = 128;
-constexpr int kThreads = 416;
+constexpr int kThreads = 512;
 constexpr int kMaxCtas = 152;
 constexpr int kMinUnits = 2;
-constexpr uint32_t kPanel = 128 * 128;  // 128 rows of 64 16-bit elements
-constexpr int kMetaRing = 4;
+constexpr int kStages = 3;    // of K and of V
+constexpr int kMetaRing = 8;  // more units than can be between their scales' arrival and their softmax
+// Registers a thread by warpgroup; the launch's 128 x 4 are shared out.
+constexpr int kLaunchRegs = 128;
+constexpr int kSoftmaxRegs = 168, kValueRegs = 112, kIssueRegs = 64;
+static_assert(2 * kSoftmaxRegs + kValueRegs + kIssueRegs <= 4 * kLaunchRegs, "setmaxnreg would wait for ever");
 
 // What the softmax and the MMA issuer need to know of a unit.
 struct UnitMeta {
-  float k_scale;  // 2^e of the unit's largest K scale
-  int v_exp;      // e of its largest V scale
-  int wide;       // V and P in bf16
+  int v_exp;  // exponent of its largest V scale
+  int wide;   // V and P in bf16
 };
 
 template <int D>
-struct Layout {
-  static constexpr uint32_t kTile = D / 64 * kPanel;  // one 128-row operand
-  static constexpr uint32_t kQ = 0;                   // A, B
-  static constexpr uint32_t kK = 2 * kTile;           // two stages
-  static constexpr uint32_t kV = 4 * kTile;
-  static constexpr uint32_t kBytes = 6 * kTile;
+struct Shape {
+  // Keys of a unit.  Tensor memory has 512 columns: two S (one a key), two O
+  // (one an element) and the scales' 28; with 128 elements that leaves 112 keys.
+  static constexpr int kUnit = D == 128 ? 112 : 128;
+  static constexpr uint32_t kQTile = 128 * D;                // one 8-bit operand
+  static constexpr uint32_t kKStage = kUnit * D;
+  static constexpr uint32_t kVPanel = kUnit * 128;           // 64 16-bit elements of each key
+  static constexpr uint32_t kVStage = kVPanel * (D / 64);
+  static constexpr uint32_t kQ = 0;                          // A hi, A lo, B hi, B lo
+  static constexpr uint32_t kK = 4 * kQTile;
+  static constexpr uint32_t kV = kK + kStages * kKStage;
+  static constexpr uint32_t kBytes = kV + kStages * kVStage;
+  static_assert(kKStage % 1024 == 0 && kVPanel % 1024 == 0, "swizzle atoms");
   // tensor memory columns
-  static constexpr uint32_t kS = 0;    // A, then B 128 on
-  static constexpr uint32_t kO = 256;  // A, then B D on
+  static constexpr uint32_t kS = 0, kSNext = D == 128 ? 112 : 128;
+  static constexpr uint32_t kO = 256;                        // A, then B D on
+  static constexpr uint32_t kScales = D == 128 ? 224 : 384;  // Q: A hi, A lo, B hi, B lo, then K's stages, four each
 };
 constexpr uint32_t kTmemColumns = 512;
 
 struct Shared {
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], drain;
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], drain;
   uint32_t tmem;
   volatile int failed;
   int last[2];
   UnitMeta meta[kMetaRing];
-  int scale_max[2][4][3];  // by parity and warp: largest K scale, largest and smallest V scale
+  int v_range[2][4][2];      // by parity and warp: largest and smallest V scale
+  uint32_t q_scale[2][128];  // a row's scale bytes
   int64_t units[kAttnScan];
+};
+
+// A stage of a ring and the parity of its current round.
+struct Ring {
+  uint32_t stage = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
 };
 
 // A wait that runs out sets the status word and makes every later wait of the
@@ -90,8 +123,15 @@ __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity,
   return true;
 }
 
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+__device__ __forceinline__ void named_barrier(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+template <int kRegs>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -110,6 +150,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
 
 // 2^d twice, as f16 (subnormal below -14, 0 below -24; d <= 15) and as bf16
 // times 2^112 (0 below the type's range).
@@ -119,17 +178,23 @@ __device__ __forceinline__ uint32_t f16_pow2x2(int d) {
 __device__ __forceinline__ uint32_t bf16_pow2x2_112(int d) {
   return (d >= -238 ? static_cast<uint32_t>(127 + 112 + d) << 7 : 0u) * 0x10001u;
 }
-
 // An f16 pair that holds codes' values (no f16 subnormals but 0) as bf16 times
 // 2^-112: the f16 exponent and mantissa moved to bf16's places.
 __device__ __forceinline__ uint32_t bf16x2_of_f16x2(uint32_t h) {
   return ((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u);
 }
+// Four E2M1 codes (16 bits) as E4M3 codes: the magnitudes by a byte table.
+__device__ __forceinline__ uint32_t e4m3_of_e2m1x4(uint32_t c) {
+  const uint32_t mag = __byte_perm(0x3C383000u, 0x4C484440u, c & 0x7777u);
+  const uint32_t twice = __byte_perm(c, 0u, 0x1100u);  // each byte next to itself
+  return mag | ((twice << 4) & 0x00800080u) | (twice & 0x80008000u);
+}
 
 // Sixteen codes of one key, a lane's share.
 template <bool E2M1>
 struct Codes {
-  uint32_t w[E2M1 ? 2 : 4];
+  static constexpr int kWords = E2M1 ? 2 : 4;
+  uint32_t w[kWords];
   __device__ __forceinline__ void load(const uint8_t* p) {
     if constexpr (E2M1) {
       const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
@@ -141,7 +206,7 @@ struct Codes {
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < (E2M1 ? 2 : 4); ++i) w[i] = 0u;
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
   }
   // elements 2i, 2i + 1
   __device__ __forceinline__ uint32_t pair(int i) const {
@@ -150,9 +215,19 @@ struct Codes {
   }
 };
 
+// n columns (a multiple of 8) of a lane from tensor memory, not yet waited for.
+template <int kN>
+__device__ __forceinline__ void tmem_load(uint32_t col, uint32_t (&v)[kN]) {
+  static_assert(kN % 16 == 0, "");
+#pragma unroll
+  for (int c = 0; c + 32 <= kN; c += 32) tmem_ld_32x32b_x32(col + c, reinterpret_cast<uint32_t(&)[32]>(v[c]));
+  if constexpr (kN % 32 != 0) tmem_ld_32x32b_x16(col + kN / 32 * 32, reinterpret_cast<uint32_t(&)[16]>(v[kN / 32 * 32]));
+}
+
 template <int D, bool E2M1>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a) {
-  using L = Layout<D>;
+__global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, const __grid_constant__ CUtensorMap k_map) {
+  using Sh = Shape<D>;
+  constexpr int kUnit = Sh::kUnit;
   using Cursor = AttnCursor<kRows, kUnit>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
@@ -164,7 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a) {
       mbar_init(smem_u32(&sh.s_full[i]), 1);
       mbar_init(smem_u32(&sh.p_full[i]), 128);
       mbar_init(smem_u32(&sh.o_full[i]), 1);
-      mbar_init(smem_u32(&sh.k_full[i]), 128);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&sh.k_full[i]), E2M1 ? 128 : 129);  // the scales' warps, and the TMA's issuer
       mbar_init(smem_u32(&sh.k_empty[i]), 1);
       mbar_init(smem_u32(&sh.v_full[i]), 128);
       mbar_init(smem_u32(&sh.v_empty[i]), 1);
@@ -185,40 +262,104 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a) {
   int64_t u = share.u;
   Cursor cur;
   if (u < share.end) cur.template start<true>(a, share);
-  uint32_t unit = 0;  // units so far, over all segments: stages and phases
+  // Where the 16-key group `group` of the unit at key0 lies: its first cache
+  // row, or -1 where no row sees it or its page is bad.
+  auto group_row = [&](const Cursor& c, int key0, int group) {
+    const int key = key0 + 16 * group;
+    if (key >= c.t.hi || key + 16 <= c.t.lo) return -1;
+    const int entry = key / a.page_size;
+    const int page = __ldg(a.block_table + static_cast<int64_t>(c.b) * a.max_pages + entry);
+    if (page < 0 || page >= a.num_pages) {
+      set_status(a.status, MX_ERR_DEVICE_ARG);
+      return -1;
+    }
+    return (page * a.n_kv_heads + c.head) * a.page_size + (key - entry * a.page_size);
+  };
 
   if (warp < 8) {
     // ================================================================ softmax
+    take_registers<kSoftmaxRegs>();
     const int x = warp >> 2;                       // tile A or B
     const int row = tid & 127;                     // the thread's row of it
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t s_col = tmem + lanes + L::kS + 128u * x, o_col = tmem + lanes + L::kO + D * static_cast<uint32_t>(x);
+    const uint32_t s_col = tmem + lanes + Sh::kS + Sh::kSNext * x, o_col = tmem + lanes + Sh::kO + D * static_cast<uint32_t>(x);
     const int n_heads = a.n_kv_heads * a.group;
-    uint32_t s_phase = 0, o_phase = 0;
+    uint32_t unit = 0, s_phase = 0, o_phase = 0;
     bool ok = true;
+
+    // The tile's queries as two MXFP8 operands.  Eight elements a lane at a
+    // time, four lanes a block.
+    auto load_queries = [&](const Cursor& c) {
+      constexpr int kPieces = D / 8;
+      const int rows = c.s.n * a.group, row0 = c.tile * kRows + 128 * x;
+      uint8_t* hi_base = base + Sh::kQ + 2 * x * Sh::kQTile;
+#pragma unroll 2
+      for (int i = row; i < 128 * kPieces; i += 128) {
+        const int r = i / kPieces, p = i - r * kPieces;
+        const int R = row0 + r;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (R < rows) {
+          const int tok = R / a.group;
+          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                   static_cast<int64_t>(c.s.q0 + tok) * a.q_stride +
+                                                   static_cast<int64_t>(c.head * a.group + (R - tok * a.group)) * D) + p);
+        }
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t amax = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // the block's largest element lands in [2^7, 2^8): hi's rounding error
+        // is then at most 2^3 and 2^5 times it stays below E4M3's 448
+        const int s = max(static_cast<int>(amax >> 7) - 127 - 7, -122);
+        const float down = pow2_neg(s);
+        uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x0 = __uint_as_float(w[k] << 16) * down, x1 = __uint_as_float(w[k] & 0xFFFF0000u) * down;
+          const uint32_t h = enc_e4m3x2(x0, x1);
+          const uint32_t back = f16x2_of_e4m3x2(h);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+          hi[k >> 1] |= h << ((k & 1) * 16);
+          lo[k >> 1] |= enc_e4m3x2((x0 - f.x) * 32.0f, (x1 - f.y) * 32.0f) << ((k & 1) * 16);
+        }
+        const uint32_t at = D == 128 ? r * 128 + (((p >> 1) ^ (r & 7)) << 4) + (p & 1) * 8
+                                     : r * 64 + (((p >> 1) ^ ((r >> 1) & 3)) << 4) + (p & 1) * 8;
+        *reinterpret_cast<uint2*>(hi_base + at) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(hi_base + Sh::kQTile + at) = make_uint2(lo[0], lo[1]);
+        if ((p & 3) == 0) reinterpret_cast<uint8_t*>(&sh.q_scale[x][r])[p >> 2] = static_cast<uint8_t>(s + 127);
+      }
+      fence_proxy_async_shared();
+      named_barrier(1 + x);
+      // scales: row 32 j + lane in column j, the same in every lane quarter
+      const uint32_t col = tmem + lanes + Sh::kScales + 8u * x;
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = sh.q_scale[x][32 * j + lane];
+      tmem_st_32x32b_x4(col, w[0], w[1], w[2], w[3]);
+      constexpr uint32_t kFive = D == 128 ? 0x05050505u : 0x0505u;
+      tmem_st_32x32b_x4(col + 4, w[0] - kFive, w[1] - kFive, w[2] - kFive, w[3] - kFive);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&sh.q_full[x]));
+    };
+
+    sh.q_scale[x][row] = 0u;
+    named_barrier(1 + x);
+    if (u < share.end && cur.tile * kRows + 128 * x < cur.s.n * a.group) load_queries(cur);
     while (u < share.end && cur.b < a.n_seqs) {
       const int take = static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), share.end - u));
       const int rows = cur.s.n * a.group;
       const int row0 = cur.tile * kRows + 128 * x;
+      Cursor ahead;
+      auto to_next = [&]() {  // and its queries
+        ahead = cur;
+        if (u + take >= share.end) return;
+        ahead.next(a);
+        if (ahead.b < a.n_seqs && ahead.tile * kRows + 128 * x < ahead.s.n * a.group) load_queries(ahead);
+      };
       if (row0 < rows) {
-        // queries: sixteen-byte pieces, D / 8 of them a row, swizzled
-        constexpr int kPieces = D / 8;
-#pragma unroll 4
-        for (int i = row; i < 128 * kPieces; i += 128) {
-          const int r = i / kPieces, p = i - r * kPieces;
-          const int R = row0 + r;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (R < rows) {
-            const int tok = R / a.group;
-            v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                     static_cast<int64_t>(cur.s.q0 + tok) * a.q_stride +
-                                                     static_cast<int64_t>(cur.head * a.group + (R - tok * a.group)) * D) + p);
-          }
-          *reinterpret_cast<uint4*>(base + L::kQ + x * L::kTile + (p / 8) * kPanel + r * 128 + (((p & 7) ^ (r & 7)) << 4)) = v;
-        }
-        fence_proxy_async_shared();
-        mbar_arrive(smem_u32(&sh.q_full[x]));
-
         const int R = row0 + row;
         const bool valid = R < rows;
         const int tok = valid ? R / a.group : 0;
@@ -228,34 +369,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a) {
         const int lo = valid && a.window > 0 ? max(at - a.window + 1, 0) : 0;
         const int all_hi = __reduce_min_sync(0xffffffffu, hi), all_lo = __reduce_max_sync(0xffffffffu, lo);
         const bool warp_valid = row0 + 32 * (warp & 3) < rows;
+        const float scale = a.scale_log2;
         float m = -INFINITY, l = 0.0f;
         for (int j = 0; j < take; ++j) {
           if (ok) ok = wait(sh, &sh.s_full[x], s_phase, a);
           s_phase ^= 1u;
-          tc_fence_after();
           ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
           if (ok && warp_valid) {
+            uint32_t v[kUnit];
+            tmem_load<kUnit>(s_col, v);
             const UnitMeta meta = sh.meta[(unit + j) % kMetaRing];
             const int key0 = cur.t.first + (cur.place + j) * kUnit;
-            const bool masked = key0 + kUnit > all_hi || key0 < all_lo;
-            const float scale = a.scale_log2 * meta.k_scale;
-            // the columns that the row sees
-            const int c_hi = hi - key0, c_lo = lo - key0;
-            float top = -INFINITY;
+            tmem_ld_wait();
+            if (key0 + kUnit > all_hi || key0 < all_lo) {
+              const int c_hi = hi - key0, c_lo = lo - key0;  // the columns that the row sees
 #pragma unroll
-            for (int c = 0; c < kUnit; c += 32) {
-              uint32_t v[32];
-              tmem_ld_32x32b_x32(s_col + c, v);
-              tmem_ld_wait();
-              if (masked) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (c + i < c_hi && c + i >= c_lo) top = fmaxf(top, __uint_as_float(v[i]));
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
-              }
+              for (int i = 0; i < kUnit; ++i)
+                if (i >= c_hi || i < c_lo) v[i] = 0xFF800000u;
             }
+            float t4[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t4[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[4 + k]));
+#pragma unroll
+            for (int i = 8; i < kUnit; i += 8) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) t4[k] = fmaxf(t4[k], fmaxf(__uint_as_float(v[i + k]), __uint_as_float(v[i + 4 + k])));
+            }
+            const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
             const float e = static_cast<float>(meta.v_exp);
             const float joint = fmaf(top, scale, e);
             if (__any_sync(0xffffffffu, joint > m + 8.0f)) {
@@ -264,46 +405,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a) {
               m = to;
               l *= f;
               if (j > 0) {  // the MMA that S waited for was issued behind the last one that writes O
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                  uint32_t v[32];
-                  tmem_ld_32x32b_x32(o_col + c, v);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld_32x32b_x16(o_col + c, o);
                   tmem_ld_wait();
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                  tmem_st_32x32b_x32(o_col + c, v);
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st_32x32b_x16(o_col + c, o);
                 }
               }
             }
             const float off = m == -INFINITY ? 0.0f : e - m;
-            float sum = 0.0f;
+            const float2 scale2 = make_float2(scale, scale), off2 = make_float2(off, off);
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-            for (int c = 0; c < kUnit; c += 32) {
-              uint32_t v[32];
-              tmem_ld_32x32b_x32(s_col + c, v);
-              tmem_ld_wait();
-              float w[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) w[i] = exp2_approx(fmaf(__uint_as_float(v[i]), scale, off));
-              if (masked) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (!(c + i < c_hi && c + i >= c_lo)) w[i] = 0.0f;
-              }
-              uint32_t p[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                sum += w[2 * i] + w[2 * i + 1];
-                p[i] = meta.wide ? pack_bf16(w[2 * i], w[2 * i + 1]) : pack_f16(w[2 * i], w[2 * i + 1]);
-              }
-              tmem_st_32x32b_x16(s_col + c / 2, p);  // behind the columns read so far
+            for (int i = 0; i < kUnit; i += 2) {
+              const float2 z = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), scale2, off2);
+              const float2 w = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+              v[i] = __float_as_uint(w.x), v[i + 1] = __float_as_uint(w.y);
+              sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], w);
             }
-            l = fmaf(sum, __uint_as_float(static_cast<uint32_t>(127 - meta.v_exp) << 23), l);
+            if (meta.wide) {
+#pragma unroll
+              for (int i = 0; i < kUnit / 2; ++i) v[i] = pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < kUnit / 2; ++i) v[i] = pack_f16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            }
+            tmem_st_32x32b_x32(s_col, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+            tmem_st_32x32b_x16(s_col + 32, reinterpret_cast<uint32_t(&)[16]>(v[32]));
+            if constexpr (kUnit == 128) tmem_st_32x32b_x16(s_col + 48, reinterpret_cast<uint32_t(&)[16]>(v[48]));
+            else tmem_st_32x32b_x8(s_col + 48, reinterpret_cast<uint32_t(&)[8]>(v[48]));
+            const float2 all = add2(sum[0], sum[1]);
+            l = fmaf(all.x + all.y, __uint_as_float(static_cast<uint32_t>(127 - meta.v_exp) << 23), l);
             tmem_st_wait();
           }
           tc_fence_before();
           mbar_arrive(smem_u32(&sh.p_full[x]));
         }
+        // the last scores are done: the next segment's queries may come
+        to_next();
 
         // ---------------------------------------------------------------- output
         if (ok) ok = wait(sh, &sh.o_full[x], o_phase, a);
@@ -312,38 +454,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a) {
         tc_fence_after();
         const bool whole = take == cur.t.units;
         const int64_t oh = static_cast<int64_t>(cur.s.q0 + tok) * n_heads + cur.head * a.group + (R - tok * a.group);
-        // 32 finished elements of the row
-        auto put = [&](int c, const float (&v)[32], float inv) {
+        // sixteen finished elements of the row
+        auto put = [&](int c, const float (&v)[16], float inv) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + oh * D + c);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 2; ++i)
             dst[i] = make_uint4(pack_bf16(v[8 * i] * inv, v[8 * i + 1] * inv), pack_bf16(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
                                 pack_bf16(v[8 * i + 4] * inv, v[8 * i + 5] * inv), pack_bf16(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
         };
         auto put_lse = [&](float M, float Lsum) {
           if (a.lse) a.lse[oh] = Lsum > 0.0f ? (M + log2f(Lsum)) * 0.69314718055994531f : -INFINITY;
         };
-        const AttnParts parts = attn_parts(share, u - cur.place, cur.t.units);
         // a part's row lies with float4s of the same elements of all rows side by side
         auto part_at = [&](int slot, int d4) {
           return reinterpret_cast<float4*>(a.part_o) + (static_cast<int64_t>(slot) * (D / 4) + d4) * kRows + 128 * x + row;
         };
         const int slot = attn_slot(blockIdx.x, cur.place == 0);
         if (ok && warp_valid) {
-#pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(o_col + c, v);
+          const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll 2
+          for (int c = 0; c < D; c += 16) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(o_col + c, v);
             tmem_ld_wait();
-            float f[32];
+            float f[16];
             // a row without a visible key never had its accumulator's weights defined
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = l > 0.0f ? __uint_as_float(v[i]) : 0.0f;
+            for (int i = 0; i < 16; ++i) f[i] = l > 0.0f ? __uint_as_float(v[i]) : 0.0f;
             if (valid && whole) {
-              put(c, f, l > 0.0f ? 1.0f / l : 0.0f);
+              put(c, f, inv);
             } else if (valid) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) *part_at(slot, c / 4 + i) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+              for (int i = 0; i < 4; ++i) *part_at(slot, c / 4 + i) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
             }
             __syncwarp();
           }
@@ -353,15 +495,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a) {
           }
         }
         if (!whole) {
+          const AttnParts parts = attn_parts(share, u - cur.place, cur.t.units);
           // also after a wait that ran out: the counters are zero for the next call
           __threadfence();
-          named_barrier(1 + x, 128);
+          named_barrier(1 + x);
           unsigned* counter = &a.arrived[2 * parts.first + x];
           if (row == 0) {
             sh.last[x] = atomicAdd(counter, 1u) == static_cast<unsigned>(parts.parts - 1);
             if (sh.last[x]) *counter = 0u;
           }
-          named_barrier(1 + x, 128);
+          named_barrier(1 + x);
           if (sh.last[x] && ok && valid) {
             __threadfence();
             float M = -INFINITY;
@@ -373,16 +516,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a) {
               Lsum += ml.y * (M == -INFINITY ? 0.0f : exp2_approx(ml.x - M));
             }
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float f[32];
+            for (int c = 0; c < D; c += 16) {
+              float f[16];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) f[i] = 0.0f;
-#pragma unroll 1
+              for (int i = 0; i < 16; ++i) f[i] = 0.0f;
+#pragma unroll 2
               for (int i = 0; i < parts.parts; ++i) {
                 const int sl = attn_slot(parts.first + i, i == 0);
                 const float w = M == -INFINITY ? 0.0f : exp2_approx(__ldcg(&a.part_ml[sl * kRows + 128 * x + row]).x - M);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                   const float4 v = __ldcg(part_at(sl, c / 4 + k));
                   f[4 * k] = fmaf(v.x, w, f[4 * k]), f[4 * k + 1] = fmaf(v.y, w, f[4 * k + 1]);
                   f[4 * k + 2] = fmaf(v.z, w, f[4 * k + 2]), f[4 * k + 3] = fmaf(v.w, w, f[4 * k + 3]);
@@ -393,202 +536,219 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a) {
             put_lse(M, Lsum);
           }
         }
+      } else {
+        to_next();  // this segment has no tile B
       }
       unit += take;
       u += take;
-      if (u < share.end) cur.next(a);
+      cur = ahead;
     }
   } else if (warp < 12) {
-    // ================================================================ reading the cache
-    constexpr int kShares = D / 16;             // lanes of a key: sixteen elements each
-    constexpr int kIts = kShares;               // a lane's keys of a unit
-    constexpr int kKeysPerIt = 128 / kShares;   // over the four warps
+    // ================================================================ V, and K's scales
+    give_registers<kValueRegs>();
+    constexpr int kShares = D / 16;                 // lanes of a key: sixteen elements each
+    constexpr int kKeysPerIt = 128 / kShares;       // over the four warps
+    constexpr int kIts = kUnit / kKeysPerIt;        // a lane's keys of a unit
+    constexpr int kRowBytes = E2M1 ? D / 2 : D;
+    constexpr int kBlocks = D / 32;
     const int dw = warp - 8;
     const int part = lane % kShares;
     const int r0 = dw * (32 / kShares) + lane / kShares;
-    constexpr int kRowBytes = E2M1 ? D / 2 : D;
-    constexpr int kBlocks = D / 32;
-    Codes<E2M1> kc[kIts], vc[kIts];
-    int ks[kIts], vs[kIts];  // scale bytes; -1: nothing there
-    // the lane's keys of the unit at key0: cache row of each, or -1
-    auto find_rows = [&](int key0, int (&rows)[kIts]) {
-      int mine = -1;  // of the 16-key group `lane`
-      if (lane < 8) {
-        const int key = key0 + 16 * lane;
-        if (key < cur.t.hi && key + 16 > cur.t.lo) {
-          const int entry = key / a.page_size;
-          const int page = __ldg(a.block_table + static_cast<int64_t>(cur.b) * a.max_pages + entry);
-          if (page < 0 || page >= a.num_pages) set_status(a.status, MX_ERR_DEVICE_ARG);
-          else mine = (page * a.n_kv_heads + cur.head) * a.page_size + (key - entry * a.page_size);
-        }
-      }
+    struct Unit {
+      Codes<E2M1> v[kIts];
+      int vs[kIts];        // scale bytes; -1: nothing there
+      uint32_t ks[4];      // keys 32 j + lane: a row's K scale bytes
+      Codes<E2M1> k[E2M1 ? kIts : 1];
+    };
+    auto load = [&](const Cursor& c, int key0, Unit& w) {
+      const int mine = lane < kUnit / 16 ? group_row(c, key0, lane) : -1;
 #pragma unroll
       for (int i = 0; i < kIts; ++i) {
         const int r = i * kKeysPerIt + r0;
         const int g = __shfl_sync(0xffffffffu, mine, r / 16);
-        const int key = key0 + r;
-        rows[i] = g >= 0 && key < cur.t.hi && key >= cur.t.lo ? g + r % 16 : -1;
+        const bool there = g >= 0 && key0 + r < c.t.hi && key0 + r >= c.t.lo;
+        const int64_t at = there ? g + r % 16 : 0;
+        w.vs[i] = -1;
+        w.v[i].clear();
+        if (E2M1) w.k[i].clear();
+        if (there) {
+          w.v[i].load(a.v_codes + at * kRowBytes + part * (kRowBytes / kShares));
+          w.vs[i] = __ldg(a.v_scales + at * kBlocks + part / 2);
+          if (E2M1) w.k[i].load(a.k_codes + at * kRowBytes + part * (kRowBytes / kShares));
+        }
       }
-    };
-    auto load = [&](const uint8_t* codes, const uint8_t* scales, const int (&rows)[kIts], Codes<E2M1> (&c)[kIts], int (&s)[kIts]) {
 #pragma unroll
-      for (int i = 0; i < kIts; ++i) {
-        if (rows[i] >= 0) {
-          const int64_t r = rows[i];
-          c[i].load(codes + r * kRowBytes + part * (kRowBytes / kShares));
-          s[i] = __ldg(scales + r * kBlocks + part / 2);
-        } else {
-          c[i].clear();
-          s[i] = -1;
+      for (int j = 0; j < 4; ++j) {
+        const int r = 32 * j + lane;
+        const int g = __shfl_sync(0xffffffffu, mine, min(r / 16, kUnit / 16 - 1));
+        w.ks[j] = 0x7F7F7F7Fu;
+        if (r < kUnit && g >= 0) {
+          const int64_t at = g + r % 16;
+          if constexpr (kBlocks == 4) w.ks[j] = __ldg(reinterpret_cast<const uint32_t*>(a.k_scales) + at);
+          else w.ks[j] = __ldg(reinterpret_cast<const uint16_t*>(a.k_scales) + at);
         }
       }
     };
-    // sixteen elements as two 16-byte pieces of the swizzled operand; the
-    // second panel's lanes write theirs in the other order, so that eight lanes
-    // of a store touch all banks
-    auto store = [&](uint32_t operand, int i, const uint32_t (&o)[8]) {
+    // where a lane's two 16-byte pieces of a V row go: the second panel's
+    // lanes write theirs in the other order, so that eight lanes of a store
+    // touch all banks
+    auto store = [&](uint32_t stage, int i, const uint32_t (&o)[8]) {
       const int r = i * kKeysPerIt + r0;
-      uint8_t* line = base + operand + (part / 4) * kPanel + r * 128;
+      uint8_t* line = base + Sh::kV + stage * Sh::kVStage + (part / 4) * Sh::kVPanel + r * 128;
       const int p = (part % 4) * 2;
       const bool swap = part >= 4;
       const uint4 first = make_uint4(o[0], o[1], o[2], o[3]), second = make_uint4(o[4], o[5], o[6], o[7]);
       *reinterpret_cast<uint4*>(line + (((p + (swap ? 1 : 0)) ^ (r & 7)) << 4)) = swap ? second : first;
       *reinterpret_cast<uint4*>(line + (((p + (swap ? 0 : 1)) ^ (r & 7)) << 4)) = swap ? first : second;
     };
-    bool ok = true;
-    while (ok && u < share.end && cur.b < a.n_seqs) {
-      const int take = static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), share.end - u));
-      const int first = cur.t.first + cur.place * kUnit;
-      int rows[kIts];
-      find_rows(first, rows);
-      load(a.k_codes, a.k_scales, rows, kc, ks);
-      load(a.v_codes, a.v_scales, rows, vc, vs);
-      for (int j = 0; j < take && ok; ++j, ++unit) {
-        const uint32_t stage = unit & 1u, phase = (unit >> 1) & 1u;
-        // the unit's largest scales, and V's smallest of a block that is not zero
-        int k_max = -1, v_max = -1, v_min = 255;
-#pragma unroll
-        for (int i = 0; i < kIts; ++i) {
-          k_max = max(k_max, ks[i]);
-          v_max = max(v_max, vs[i]);
-          v_min = min(v_min, vs[i] > 0 ? vs[i] : 255);
+    const int n = static_cast<int>(share.end - share.u);
+    int left = n > 0 ? static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), static_cast<int64_t>(n))) : 0;
+    Ring ring;
+    Unit now, then;
+    if (n > 0) load(cur, cur.t.first + cur.place * kUnit, now);
+    for (int i = 0; i < n; ++i) {
+      // the next unit's loads have this unit's time to arrive
+      if (i + 1 < n) {
+        if (--left == 0) {
+          cur.next(a);
+          if (cur.b >= a.n_seqs) break;
+          left = cur.t.units;
+        } else {
+          ++cur.place;
         }
-        k_max = __reduce_max_sync(0xffffffffu, k_max);
-        v_max = __reduce_max_sync(0xffffffffu, v_max);
-        v_min = __reduce_min_sync(0xffffffffu, v_min);
-        int(*seen)[3] = sh.scale_max[stage];
-        if (lane == 0) seen[dw][0] = k_max, seen[dw][1] = v_max, seen[dw][2] = v_min;
-        named_barrier(3, 128);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          k_max = max(k_max, seen[w][0]);
-          v_max = max(v_max, seen[w][1]);
-          v_min = min(v_min, seen[w][2]);
-        }
-        const int k_exp = min(max(k_max - 127, -100), 126), v_exp = min(max(v_max - 127, -100), 126);
-        const bool wide = v_exp - (v_min - 127) > 15;
-        if (dw == 0 && lane == 0) {
-          UnitMeta meta;
-          meta.k_scale = __uint_as_float(static_cast<uint32_t>(127 + k_exp) << 23);
-          meta.v_exp = v_exp;
-          meta.wide = wide;
-          sh.meta[unit % kMetaRing] = meta;
-        }
-        const bool more = j + 1 < take;
-        if (more) find_rows(first + (j + 1) * kUnit, rows);
-
-        ok = wait(sh, &sh.k_empty[stage], phase ^ 1u, a);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-#pragma unroll
-        for (int i = 0; i < kIts; ++i) {
-          const uint32_t f = bf16_pow2x2_112(ks[i] - 127 - k_exp);
-          uint32_t o[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) o[q] = mul_bf16x2(bf16x2_of_f16x2(kc[i].pair(q)), f);
-          store(L::kK + stage * L::kTile, i, o);
-        }
-        fence_proxy_async_shared();
-        mbar_arrive(smem_u32(&sh.k_full[stage]));
-        if (more) load(a.k_codes, a.k_scales, rows, kc, ks);
-
-        ok = wait(sh, &sh.v_empty[stage], phase ^ 1u, a);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-#pragma unroll
-        for (int i = 0; i < kIts; ++i) {
-          uint32_t o[8];
-          if (wide) {
-            const uint32_t f = bf16_pow2x2_112(vs[i] - 127 - v_exp);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) o[q] = mul_bf16x2(bf16x2_of_f16x2(vc[i].pair(q)), f);
-          } else {
-            const uint32_t f = f16_pow2x2(vs[i] - 127 - v_exp);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) o[q] = mul_f16x2(vc[i].pair(q), f);
-          }
-          store(L::kV + stage * L::kTile, i, o);
-        }
-        fence_proxy_async_shared();
-        mbar_arrive(smem_u32(&sh.v_full[stage]));
-        if (more) load(a.v_codes, a.v_scales, rows, vc, vs);
+        load(cur, cur.t.first + cur.place * kUnit, then);
       }
-      u += take;
-      if (ok && u < share.end) cur.next(a);
+      // V's largest scale, and the smallest of a block that is not zero
+      int v_max = -1, v_min = 255;
+#pragma unroll
+      for (int k = 0; k < kIts; ++k) {
+        v_max = max(v_max, now.vs[k]);
+        v_min = min(v_min, now.vs[k] > 0 ? now.vs[k] : 255);
+      }
+      v_max = __reduce_max_sync(0xffffffffu, v_max);
+      v_min = __reduce_min_sync(0xffffffffu, v_min);
+      int(*seen)[2] = sh.v_range[i & 1];
+      if (lane == 0) seen[dw][0] = v_max, seen[dw][1] = v_min;
+      named_barrier(3);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        v_max = max(v_max, seen[w][0]);
+        v_min = min(v_min, seen[w][1]);
+      }
+      const int v_exp = min(max(v_max - 127, -100), 126);
+      const bool wide = v_exp - (v_min - 127) > 15;
+      if (dw == 0 && lane == 0) {
+        sh.meta[i % kMetaRing].v_exp = v_exp;
+        sh.meta[i % kMetaRing].wide = wide;
+      }
+
+      bool ok = wait(sh, &sh.k_empty[ring.stage], ring.phase ^ 1u, a);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      if (E2M1) {
+#pragma unroll
+        for (int k = 0; k < kIts; ++k) {
+          const int r = k * kKeysPerIt + r0;
+          const uint32_t c0 = now.k[E2M1 ? k : 0].w[0], c1 = now.k[E2M1 ? k : 0].w[1];
+          const uint32_t at = D == 128 ? r * 128 + ((part ^ (r & 7)) << 4) : r * 64 + ((part ^ ((r >> 1) & 3)) << 4);
+          *reinterpret_cast<uint4*>(base + Sh::kK + ring.stage * Sh::kKStage + at) =
+              make_uint4(e4m3_of_e2m1x4(c0), e4m3_of_e2m1x4(c0 >> 16), e4m3_of_e2m1x4(c1), e4m3_of_e2m1x4(c1 >> 16));
+        }
+        fence_proxy_async_shared();
+      }
+      tmem_st_32x32b_x4(tmem + (static_cast<uint32_t>(32 * dw) << 16) + Sh::kScales + 16u + 4u * ring.stage, now.ks[0],
+                        now.ks[1], now.ks[2], now.ks[3]);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&sh.k_full[ring.stage]));
+
+      ok = wait(sh, &sh.v_empty[ring.stage], ring.phase ^ 1u, a);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (wide) {
+#pragma unroll
+        for (int k = 0; k < kIts; ++k) {
+          const uint32_t f = bf16_pow2x2_112(now.vs[k] - 127 - v_exp);
+          uint32_t o[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) o[q] = mul_bf16x2(bf16x2_of_f16x2(now.v[k].pair(q)), f);
+          store(ring.stage, k, o);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kIts; ++k) {
+          const uint32_t f = f16_pow2x2(now.vs[k] - 127 - v_exp);
+          uint32_t o[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) o[q] = mul_f16x2(now.v[k].pair(q), f);
+          store(ring.stage, k, o);
+        }
+      }
+      fence_proxy_async_shared();
+      mbar_arrive(smem_u32(&sh.v_full[ring.stage]));
+      ring.next();
+      now = then;
     }
   } else {
-    // ================================================================ MMAs
-    if (lane == 0) {
-      const uint32_t q_lo = desc_lo_sw128(smem_u32(base + L::kQ)), k_lo = desc_lo_sw128(smem_u32(base + L::kK));
-      // V is MN-major: 64-element panels along N lie kPanel apart (leading
+    give_registers<kIssueRegs>();
+    if (warp == 12 && lane == 0) {
+      // ================================================================ MMAs
+      // V is MN-major: 64-element panels along N lie kVPanel apart (leading
       // offset), eight-key groups 1024 bytes (stride)
-      const uint32_t v_lo = ((smem_u32(base + L::kV) >> 4) & 0x3FFFu) | ((kPanel >> 4) << 16);
-      const uint32_t qk_idesc = idesc_f16(true, false, 128, kUnit);
+      const uint32_t q_lo = desc_lo_sw128(smem_u32(base + Sh::kQ)), k_lo = desc_lo_sw128(smem_u32(base + Sh::kK));
+      const uint32_t v_lo = ((smem_u32(base + Sh::kV) >> 4) & 0x3FFFu) | ((Sh::kVPanel >> 4) << 16);
+      constexpr uint32_t kQkHi = D == 128 ? kDescHiSw128 : kDescHiSw64;
       uint32_t q_phase = 0, p_phase = 0;
       bool ok = true;
       auto scores = [&](uint32_t x, uint32_t stage) {
+        const uint32_t d = tmem + Sh::kS + Sh::kSNext * x;
+        const uint32_t q_sf = tmem + Sh::kScales + 8u * x, k_sf = tmem + Sh::kScales + 16u + 4u * stage;
+        const uint32_t q = q_lo + ((2 * x * Sh::kQTile) >> 4), k = k_lo + ((stage * Sh::kKStage) >> 4);
 #pragma unroll
-        for (uint32_t p = 0; p < D / 64; ++p) {
+        for (uint32_t part = 0; part < 2; ++part) {
 #pragma unroll
-          for (uint32_t k = 0; k < 4; ++k)
-            mma_f16_ss(tmem + L::kS + 128u * x, q_lo + ((x * L::kTile + p * kPanel) >> 4) + 2u * k,
-                       k_lo + ((stage * L::kTile + p * kPanel) >> 4) + 2u * k, kDescHiSw128, qk_idesc, (p | k) != 0);
+          for (uint32_t b = 0; b < D / 32; ++b)
+            mma_mxf8f6f4_lo(d, q + ((part * Sh::kQTile) >> 4) + 2u * b, k + 2u * b, kQkHi,
+                            idesc_mx(kFmtE4M3, kFmtE4M3, 128, kUnit, b, b), q_sf + 4u * part, k_sf, (part | b) != 0);
         }
         mma_commit(smem_u32(&sh.s_full[x]));
       };
       auto values = [&](uint32_t x, uint32_t stage, uint32_t idesc, bool first) {
 #pragma unroll
         for (uint32_t k = 0; k < kUnit / 16; ++k)
-          mma_f16_ts(tmem + L::kO + D * x, tmem + L::kS + 128u * x + 8u * k, v_lo + ((stage * L::kTile + k * 2048u) >> 4),
-                     kDescHiSw128, idesc, !first || k != 0);
+          mma_f16_ts(tmem + Sh::kO + D * x, tmem + Sh::kS + Sh::kSNext * x + 8u * k,
+                     v_lo + ((stage * Sh::kVStage + k * 2048u) >> 4), kDescHiSw128, idesc, !first || k != 0);
       };
+      uint32_t unit = 0;
+      Ring kr, vr;  // the next stage to take
       while (ok && u < share.end && cur.b < a.n_seqs) {
         const int take = static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), share.end - u));
         const bool two = cur.s.n * a.group - cur.tile * kRows > 128;
         ok = wait(sh, &sh.q_full[0], q_phase & 1u, a);
         if (ok && two) ok = wait(sh, &sh.q_full[1], (q_phase >> 1) & 1u, a);
         q_phase ^= two ? 3u : 1u;
-        if (ok) ok = wait(sh, &sh.k_full[unit & 1u], (unit >> 1) & 1u, a);
+        if (ok) ok = wait(sh, &sh.k_full[kr.stage], kr.phase, a);
         if (!ok) break;
         tc_fence_after();
-        scores(0, unit & 1u);
-        if (two) scores(1, unit & 1u);
-        mma_commit(smem_u32(&sh.k_empty[unit & 1u]));
+        scores(0, kr.stage);
+        if (two) scores(1, kr.stage);
+        mma_commit(smem_u32(&sh.k_empty[kr.stage]));
+        kr.next();
         for (int j = 0; j < take; ++j, ++unit) {
-          const uint32_t stage = unit & 1u, next = stage ^ 1u;
           const bool more = j + 1 < take;
-          ok = wait(sh, &sh.v_full[stage], (unit >> 1) & 1u, a);
+          ok = wait(sh, &sh.v_full[vr.stage], vr.phase, a);
           if (ok) ok = wait(sh, &sh.p_full[0], p_phase & 1u, a);
           if (!ok) break;
           tc_fence_after();
           const uint32_t idesc = idesc_f16(sh.meta[unit % kMetaRing].wide != 0, true, 128, D);
-          values(0, stage, idesc, j == 0);
+          values(0, vr.stage, idesc, j == 0);
           if (more) {
             // P lies in S: this MMA is issued behind the ones that read it
-            ok = wait(sh, &sh.k_full[next], ((unit + 1) >> 1) & 1u, a);
+            ok = wait(sh, &sh.k_full[kr.stage], kr.phase, a);
             if (!ok) break;
             tc_fence_after();
-            scores(0, next);
+            scores(0, kr.stage);
           } else {
             mma_commit(smem_u32(&sh.o_full[0]));
           }
@@ -596,13 +756,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a) {
             ok = wait(sh, &sh.p_full[1], (p_phase >> 1) & 1u, a);
             if (!ok) break;
             tc_fence_after();
-            values(1, stage, idesc, j == 0);
+            values(1, vr.stage, idesc, j == 0);
           }
           p_phase ^= two ? 3u : 1u;
-          mma_commit(smem_u32(&sh.v_empty[stage]));
+          mma_commit(smem_u32(&sh.v_empty[vr.stage]));
+          vr.next();
           if (more) {
-            if (two) scores(1, next);
-            mma_commit(smem_u32(&sh.k_empty[next]));
+            if (two) scores(1, kr.stage);
+            mma_commit(smem_u32(&sh.k_empty[kr.stage]));
+            kr.next();
           } else if (two) {
             mma_commit(smem_u32(&sh.o_full[1]));
           }
@@ -613,6 +775,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a) {
       // every MMA issued has completed before tensor memory is released
       mma_commit(smem_u32(&sh.drain));
       mbar_wait(smem_u32(&sh.drain), 0, 100000000ull);
+    } else if (warp == 13 && !E2M1) {
+      // ================================================================ K's codes
+      // sixteen keys a box, each by its own lane; a group that is not there is
+      // read past the table's end, which fills zeros
+      const int n = static_cast<int>(share.end - share.u);
+      const int none = a.num_pages * a.n_kv_heads * a.page_size;
+      int left = n > 0 ? static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), static_cast<int64_t>(n))) : 0;
+      Ring ring;
+      bool ok = true;
+      int issued = 0;
+      if (lane == 0) prefetch_tensormap(&k_map);
+      for (int i = 0; i < n; ++i) {
+        int at = none;
+        if (lane < kUnit / 16) at = group_row(cur, cur.t.first + cur.place * kUnit, lane);
+        if (at < 0) at = none;
+        ok = wait(sh, &sh.k_empty[ring.stage], ring.phase ^ 1u, a);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t bar = smem_u32(&sh.k_full[ring.stage]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, Sh::kKStage);
+        __syncwarp();
+        if (lane < kUnit / 16)
+          tma_load_2d(smem_u32(base + Sh::kK + ring.stage * Sh::kKStage + lane * 16 * D), &k_map, 0, at, bar);
+        ++issued;
+        ring.next();
+        if (i + 1 < n) {
+          if (--left == 0) {
+            cur.next(a);
+            if (cur.b >= a.n_seqs) break;
+            left = cur.t.units;
+          } else {
+            ++cur.place;
+          }
+        }
+      }
+      // the last fills have landed before the CTA exits, also where a wait of
+      // the others ran out
+      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+        mbar_wait(smem_u32(&sh.k_full[i % kStages]), (i / kStages) & 1u, 100000000ull);
+      __syncwarp();
     }
     __syncwarp();
   }
@@ -622,17 +824,50 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a) {
   if (warp == 12) tmem_dealloc(tmem, kTmemColumns);
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }
+  return fn;
+}
+
 template <int D, bool E2M1>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
-  constexpr int kSmem = Layout<D>::kBytes + 1024;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  constexpr int kSmem = Shape<D>::kBytes + 1024;
+  constexpr int kMaxDevices = 64;
+  static std::atomic<bool> ready[kMaxDevices];
+  int sms = 0, dev = 0;
+  cudaError_t e = attn_sm_count(&sms);
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(k_attn_chunk<D, E2M1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  k_attn_chunk<D, E2M1><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, kSmem, s>>>(a);
+  if (dev < 0 || dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
+    // the register split counts on the launch's 128 a thread
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, k_attn_chunk<D, E2M1>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(k_attn_chunk<D, E2M1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
+  }
+  CUtensorMap k_map{};
+  if (!E2M1) {
+    auto encode = encode_fn();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t rows = static_cast<cuuint64_t>(a.num_pages) * a.n_kv_heads * a.page_size;
+    cuuint64_t dims[2] = {D, rows}, strides[1] = {D};
+    cuuint32_t box[2] = {D, 16}, es[2] = {1, 1};
+    if (encode(&k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.k_codes), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  k_attn_chunk<D, E2M1><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, kSmem, s>>>(a, k_map);
   return cudaGetLastError();
 }
 

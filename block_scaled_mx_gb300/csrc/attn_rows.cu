@@ -456,17 +456,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
 
 template <int D, bool E2M1>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  int sms = 0;
+  const cudaError_t e = attn_sm_count(&sms);
   if (e != cudaSuccess) return e;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  const int grid = sms * kCtasPerSm < kAttnMaxCtas ? sms * kCtasPerSm : kAttnMaxCtas;
-  k_attn_rows<D, E2M1><<<grid, kThreads, 0, s>>>(a);
+  k_attn_rows<D, E2M1><<<sms * kCtasPerSm < kAttnMaxCtas ? sms * kCtasPerSm : kAttnMaxCtas, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+cudaError_t attn_sm_count(int* sms) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) : e;
+}
 
 size_t attn_rows_part_bytes(int head_dim) {
   return static_cast<size_t>(2) * kAttnMaxCtas * kRows * (sizeof(float2) + sizeof(float) * head_dim);

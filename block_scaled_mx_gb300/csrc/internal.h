@@ -152,6 +152,7 @@ struct AttnArgs {
   float* part_o;                                     // [2 * CTAs][tile rows][head_dim]
   uint64_t wait_limit_ns;
 };
+cudaError_t attn_sm_count(int* sms);                 // of the current device
 size_t attn_rows_part_bytes(int head_dim);           // part_ml and part_o of the few-rows kernel
 cudaError_t launch_attn_rows(AttnArgs a, cudaStream_t s);
 size_t attn_chunk_part_bytes(int head_dim);          // the same of the chunk kernel

@@ -113,7 +113,9 @@ def test_binding_checks_tensors(L):
     with pytest.raises(ValueError, match="weight"):
         mx.mx_add_rmsnorm(x, torch.empty(32, **meta), 1e-6)
     with pytest.raises(ValueError, match="codes"):
-        mx.mx_add_rmsnorm(x, torch.empty(64, **meta), 1e-6, codes=torch.empty(4, 64, dtype=torch.uint8, **meta), fmt="e2m1")
+        mx._dense(torch.empty(4, 64, dtype=torch.uint8, **meta), torch.uint8, (4, 32), "codes")
+    with pytest.raises(ValueError, match="residual_out"):
+        mx._dense(x, torch.bfloat16, (4, 64), "residual_out")
     with pytest.raises(ValueError, match="CUDA"):
         mx.KVCache(4, 16, 2, 64, device="cpu")
     with pytest.raises(ValueError, match="k_scales"):
@@ -122,8 +124,9 @@ def test_binding_checks_tensors(L):
     with pytest.raises(ValueError, match="int32"):
         mx._batch(torch.zeros(2, 3), torch.zeros(2), torch.zeros(3))
     with pytest.raises(ValueError, match="kv_lens"):
-        i = torch.int32
-        mx._batch(torch.zeros(2, 3, dtype=i), torch.zeros(2, dtype=i), torch.zeros(2, dtype=i))
+        mx._dense(torch.zeros(2, dtype=torch.int64), torch.int32, (2,), "kv_lens")
+    with pytest.raises(ValueError, match="q_starts"):
+        mx._dense(torch.zeros(2, dtype=torch.int32), torch.int32, (3,), "q_starts")
     with pytest.raises(ValueError, match="dense"):
         mx._rows(torch.empty(4, 64, 8, dtype=torch.bfloat16, **meta).transpose(1, 2), 8, 64, "q")
     with pytest.raises(ValueError, match="bf16"):
