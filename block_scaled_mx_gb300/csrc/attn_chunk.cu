@@ -65,8 +65,9 @@ struct UnitMeta {
 template <int D>
 struct Shape {
   // Keys of a unit.  Tensor memory has 512 columns: two S (one a key), two O
-  // (one an element) and the scales' 28; with 128 elements that leaves 112 keys.
-  static constexpr int kUnit = D == 128 ? 112 : 128;
+  // (one an element) and the scales' 28; with 128 elements that leaves 96 keys in
+  // steps of 32 columns.
+  static constexpr int kUnit = D == 128 ? 96 : 128;
   static constexpr uint32_t kQTile = 128 * D;                // one 8-bit operand
   static constexpr uint32_t kKStage = kUnit * D;
   static constexpr uint32_t kVPanel = kUnit * 128;           // 64 16-bit elements of each key
@@ -77,9 +78,9 @@ struct Shape {
   static constexpr uint32_t kBytes = kV + kStages * kVStage;
   static_assert(kKStage % 1024 == 0 && kVPanel % 1024 == 0, "swizzle atoms");
   // tensor memory columns
-  static constexpr uint32_t kS = 0, kSNext = D == 128 ? 112 : 128;
+  static constexpr uint32_t kS = 0, kSNext = kUnit;
   static constexpr uint32_t kO = 256;                        // A, then B D on
-  static constexpr uint32_t kScales = D == 128 ? 224 : 384;  // Q: A hi, A lo, B hi, B lo, then K's stages, four each
+  static constexpr uint32_t kScales = D == 128 ? 192 : 384;  // Q: A hi, A lo, B hi, B lo, then K's stages, four each
 };
 constexpr uint32_t kTmemColumns = 512;
 
@@ -232,7 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same for the warp, and known to be
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.q_full[i]), 128);
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  constexpr uint32_t tmem = 0;  // all of tensor memory is this CTA's
   int64_t u = share.u;
   Cursor cur;
   if (u < share.end) cur.template start<true>(a, share);
@@ -377,17 +379,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
           ok = __all_sync(0xffffffffu, ok);
           tc_fence_after();
           if (ok && warp_valid) {
-            uint32_t v[kUnit];
-            tmem_load<kUnit>(s_col, v);
             const UnitMeta meta = sh.meta[(unit + j) % kMetaRing];
             const int key0 = cur.t.first + (cur.place + j) * kUnit;
-            tmem_ld_wait();
             if (key0 + kUnit > all_hi || key0 < all_lo) {
               const int c_hi = hi - key0, c_lo = lo - key0;  // the columns that the row sees
+#pragma unroll 1
+              for (int c = 0; c < kUnit; c += 16) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(s_col + c, v);
+                tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < kUnit; ++i)
-                if (i >= c_hi || i < c_lo) v[i] = 0xFF800000u;
+                for (int i = 0; i < 16; ++i)
+                  if (c + i >= c_hi || c + i < c_lo) v[i] = 0xFF800000u;
+                tmem_st_32x32b_x16(s_col + c, v);
+              }
+              tmem_st_wait();
             }
+            // The code that runs for every unit is kept short: the warps' roles
+            // differ, and together they have to fit the instruction cache.
+            uint32_t v[kUnit];
+            tmem_load<kUnit>(s_col, v);
+            tmem_ld_wait();
             float t4[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) t4[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[4 + k]));
@@ -419,24 +431,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
             const float off = m == -INFINITY ? 0.0f : e - m;
             const float2 scale2 = make_float2(scale, scale), off2 = make_float2(off, off);
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            if (!meta.wide) {
 #pragma unroll
-            for (int i = 0; i < kUnit; i += 2) {
-              const float2 z = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), scale2, off2);
-              const float2 w = make_float2(exp2_approx(z.x), exp2_approx(z.y));
-              v[i] = __float_as_uint(w.x), v[i + 1] = __float_as_uint(w.y);
-              sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], w);
-            }
-            if (meta.wide) {
+              for (int i = 0; i < kUnit; i += 2) {
+                const float2 z = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), scale2, off2);
+                const float2 w = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+                sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], w);
+                v[i / 2] = pack_f16(w.x, w.y);
+              }
 #pragma unroll
-              for (int i = 0; i < kUnit / 2; ++i) v[i] = pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+              for (int c = 0; c < kUnit / 2; c += 16) tmem_st_32x32b_x16(s_col + c, reinterpret_cast<uint32_t(&)[16]>(v[c]));
             } else {
+#pragma unroll 1
+              for (int c = 0; c < kUnit; c += 32) {
+                uint32_t z[32], p[16];
+                tmem_ld_32x32b_x32(s_col + c, z);
+                tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < kUnit / 2; ++i) v[i] = pack_f16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                for (int i = 0; i < 32; i += 2) {
+                  const float2 y = fma2(make_float2(__uint_as_float(z[i]), __uint_as_float(z[i + 1])), scale2, off2);
+                  const float2 w = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                  sum[0] = add2(sum[0], w);
+                  p[i / 2] = pack_bf16(w.x, w.y);
+                }
+                tmem_st_32x32b_x16(s_col + c / 2, p);  // behind the columns read so far
+              }
             }
-            tmem_st_32x32b_x32(s_col, reinterpret_cast<uint32_t(&)[32]>(v[0]));
-            tmem_st_32x32b_x16(s_col + 32, reinterpret_cast<uint32_t(&)[16]>(v[32]));
-            if constexpr (kUnit == 128) tmem_st_32x32b_x16(s_col + 48, reinterpret_cast<uint32_t(&)[16]>(v[48]));
-            else tmem_st_32x32b_x8(s_col + 48, reinterpret_cast<uint32_t(&)[8]>(v[48]));
             const float2 all = add2(sum[0], sum[1]);
             l = fmaf(all.x + all.y, __uint_as_float(static_cast<uint32_t>(127 - meta.v_exp) << 23), l);
             tmem_st_wait();
@@ -552,74 +572,112 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
     constexpr int kRowBytes = E2M1 ? D / 2 : D;
     constexpr int kBlocks = D / 32;
     const int dw = warp - 8;
-    const int part = lane % kShares;
-    const int r0 = dw * (32 / kShares) + lane / kShares;
+    // Lanes 0-15 take the first 64 elements of their keys and, with 128, lanes
+    // 16-31 the second: eight lanes of a store then lie in two rows of one
+    // panel, which touches all banks.
+    const int part = lane % 4 + (D == 128 ? lane / 16 * 4 : 0);
+    const int r0 = dw * (32 / kShares) + (D == 128 ? lane % 16 / 4 : lane / 4);
     struct Unit {
       Codes<E2M1> v[kIts];
-      int vs[kIts];        // scale bytes; -1: nothing there
+      int vs[kIts];        // scale bytes
+      uint32_t there;      // bit i: key i is one that some row sees (others hold what lies first in the cache)
       uint32_t ks[4];      // keys 32 j + lane: a row's K scale bytes
       Codes<E2M1> k[E2M1 ? kIts : 1];
     };
-    auto load = [&](const Cursor& c, int key0, Unit& w) {
-      const int mine = lane < kUnit / 16 ? group_row(c, key0, lane) : -1;
+    // Where a unit lies: looked up one unit before its loads, those one unit
+    // before their use.
+    struct Place {
+      int page;          // of the lane's 16-key group, as the table has it
+      int head, offset;  // the group's first place in the page; -1: no row sees it
+      int key0, lo, hi;  // the unit's first key, and the keys to read
+    };
+    auto look_up = [&](const Cursor& c) {
+      Place p;
+      p.key0 = c.t.first + c.place * kUnit;
+      p.lo = c.t.lo;
+      p.hi = c.t.hi;
+      p.head = c.head;
+      p.page = -1;
+      const int key = p.key0 + 16 * lane;
+      const int entry = key / a.page_size;
+      p.offset = key - entry * a.page_size;
+      if (lane < kUnit / 16 && key < p.hi && key + 16 > p.lo)
+        p.page = __ldg(a.block_table + static_cast<int64_t>(c.b) * a.max_pages + entry);
+      else
+        p.offset = -1;
+      return p;
+    };
+    auto load = [&](const Place& c, Unit& w) {
+      const int key0 = c.key0;
+      int mine = -1;
+      if (c.offset >= 0) {
+        if (c.page < 0 || c.page >= a.num_pages) set_status(a.status, MX_ERR_DEVICE_ARG);
+        else mine = (c.page * a.n_kv_heads + c.head) * a.page_size + c.offset;
+      }
+      // no load's result is touched here, not even to choose between it and a
+      // constant: that would wait for it
+      w.there = 0;
 #pragma unroll
       for (int i = 0; i < kIts; ++i) {
         const int r = i * kKeysPerIt + r0;
         const int g = __shfl_sync(0xffffffffu, mine, r / 16);
-        const bool there = g >= 0 && key0 + r < c.t.hi && key0 + r >= c.t.lo;
+        const bool there = g >= 0 && key0 + r < c.hi && key0 + r >= c.lo;
         const int64_t at = there ? g + r % 16 : 0;
-        w.vs[i] = -1;
-        w.v[i].clear();
-        if (E2M1) w.k[i].clear();
-        if (there) {
-          w.v[i].load(a.v_codes + at * kRowBytes + part * (kRowBytes / kShares));
-          w.vs[i] = __ldg(a.v_scales + at * kBlocks + part / 2);
-          if (E2M1) w.k[i].load(a.k_codes + at * kRowBytes + part * (kRowBytes / kShares));
-        }
+        w.there |= (there ? 1u : 0u) << i;
+        w.v[i].load(a.v_codes + at * kRowBytes + part * (kRowBytes / kShares));
+        w.vs[i] = __ldg(a.v_scales + at * kBlocks + part / 2);
+        if (E2M1) w.k[E2M1 ? i : 0].load(a.k_codes + at * kRowBytes + part * (kRowBytes / kShares));
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int r = 32 * j + lane;
         const int g = __shfl_sync(0xffffffffu, mine, min(r / 16, kUnit / 16 - 1));
-        w.ks[j] = 0x7F7F7F7Fu;
-        if (r < kUnit && g >= 0) {
-          const int64_t at = g + r % 16;
-          if constexpr (kBlocks == 4) w.ks[j] = __ldg(reinterpret_cast<const uint32_t*>(a.k_scales) + at);
-          else w.ks[j] = __ldg(reinterpret_cast<const uint16_t*>(a.k_scales) + at);
-        }
+        const int64_t at = r < kUnit && g >= 0 ? g + r % 16 : 0;
+        if constexpr (kBlocks == 4) w.ks[j] = __ldg(reinterpret_cast<const uint32_t*>(a.k_scales) + at);
+        else w.ks[j] = __ldg(reinterpret_cast<const uint16_t*>(a.k_scales) + at);
       }
     };
-    // where a lane's two 16-byte pieces of a V row go: the second panel's
-    // lanes write theirs in the other order, so that eight lanes of a store
-    // touch all banks
-    auto store = [&](uint32_t stage, int i, const uint32_t (&o)[8]) {
-      const int r = i * kKeysPerIt + r0;
-      uint8_t* line = base + Sh::kV + stage * Sh::kVStage + (part / 4) * Sh::kVPanel + r * 128;
-      const int p = (part % 4) * 2;
-      const bool swap = part >= 4;
-      const uint4 first = make_uint4(o[0], o[1], o[2], o[3]), second = make_uint4(o[4], o[5], o[6], o[7]);
-      *reinterpret_cast<uint4*>(line + (((p + (swap ? 1 : 0)) ^ (r & 7)) << 4)) = swap ? second : first;
-      *reinterpret_cast<uint4*>(line + (((p + (swap ? 0 : 1)) ^ (r & 7)) << 4)) = swap ? first : second;
+    // a lane's two 16-byte pieces of a V row; kKeysPerIt is a multiple of 8, so
+    // the swizzle is the same for all its keys
+    const uint32_t v_at = (part / 4) * Sh::kVPanel + r0 * 128;
+    const uint32_t v_at0 = v_at + (((part % 4 * 2) ^ (r0 & 7)) << 4), v_at1 = v_at + (((part % 4 * 2 + 1) ^ (r0 & 7)) << 4);
+    auto store = [&](uint8_t* stage, int i, const uint32_t (&o)[8]) {
+      *reinterpret_cast<uint4*>(stage + v_at0 + i * kKeysPerIt * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(stage + v_at1 + i * kKeysPerIt * 128) = make_uint4(o[4], o[5], o[6], o[7]);
     };
     const int n = static_cast<int>(share.end - share.u);
     int left = n > 0 ? static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), static_cast<int64_t>(n))) : 0;
     Ring ring;
     Unit now, then;
-    if (n > 0) load(cur, cur.t.first + cur.place * kUnit, now);
+    Place at;
+    auto advance = [&]() {  // to the unit after the one in `at`
+      if (--left == 0) {
+        cur.next(a);
+        left = cur.t.units;
+      } else {
+        ++cur.place;
+      }
+      at = look_up(cur);
+    };
+    if (n > 0) {
+      at = look_up(cur);
+      load(at, now);
+      if (n > 1) advance();
+    }
     for (int i = 0; i < n; ++i) {
-      // the next unit's loads have this unit's time to arrive
-      if (i + 1 < n) {
-        if (--left == 0) {
-          cur.next(a);
-          if (cur.b >= a.n_seqs) break;
-          left = cur.t.units;
-        } else {
-          ++cur.place;
+      if (i + 1 < n) load(at, then);
+      if (i + 2 < n) advance();
+      if (now.there != (1u << kIts) - 1) {
+#pragma unroll
+        for (int k = 0; k < kIts; ++k) {
+          if (now.there >> k & 1) continue;
+          now.v[k].clear();
+          now.vs[k] = 0;
+          if (E2M1) now.k[E2M1 ? k : 0].clear();
         }
-        load(cur, cur.t.first + cur.place * kUnit, then);
       }
       // V's largest scale, and the smallest of a block that is not zero
-      int v_max = -1, v_min = 255;
+      int v_max = 0, v_min = 255;
 #pragma unroll
       for (int k = 0; k < kIts; ++k) {
         v_max = max(v_max, now.vs[k]);
@@ -666,6 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
       ok = wait(sh, &sh.v_empty[ring.stage], ring.phase ^ 1u, a);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
+      uint8_t* v_stage = base + Sh::kV + ring.stage * Sh::kVStage;
       if (wide) {
 #pragma unroll
         for (int k = 0; k < kIts; ++k) {
@@ -673,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
           uint32_t o[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) o[q] = mul_bf16x2(bf16x2_of_f16x2(now.v[k].pair(q)), f);
-          store(ring.stage, k, o);
+          store(v_stage, k, o);
         }
       } else {
 #pragma unroll
@@ -682,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
           uint32_t o[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) o[q] = mul_f16x2(now.v[k].pair(q), f);
-          store(ring.stage, k, o);
+          store(v_stage, k, o);
         }
       }
       fence_proxy_async_shared();
@@ -692,7 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
     }
   } else {
     give_registers<kIssueRegs>();
-    if (warp == 12 && lane == 0) {
+    if (warp == 12) {
+      if (elect_one()) {
       // ================================================================ MMAs
       // V is MN-major: 64-element panels along N lie kVPanel apart (leading
       // offset), eight-key groups 1024 bytes (stride)
@@ -724,49 +784,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
       Ring kr, vr;  // the next stage to take
       while (ok && u < share.end && cur.b < a.n_seqs) {
         const int take = static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), share.end - u));
-        const bool two = cur.s.n * a.group - cur.tile * kRows > 128;
-        ok = wait(sh, &sh.q_full[0], q_phase & 1u, a);
-        if (ok && two) ok = wait(sh, &sh.q_full[1], (q_phase >> 1) & 1u, a);
-        q_phase ^= two ? 3u : 1u;
-        if (ok) ok = wait(sh, &sh.k_full[kr.stage], kr.phase, a);
-        if (!ok) break;
-        tc_fence_after();
-        scores(0, kr.stage);
-        if (two) scores(1, kr.stage);
-        mma_commit(smem_u32(&sh.k_empty[kr.stage]));
-        kr.next();
-        for (int j = 0; j < take; ++j, ++unit) {
+        const uint32_t tiles = cur.s.n * a.group - cur.tile * kRows > 128 ? 2 : 1;
+        for (uint32_t x = 0; x < tiles && ok; ++x) ok = wait(sh, &sh.q_full[x], (q_phase >> x) & 1u, a);
+        q_phase ^= tiles == 2 ? 3u : 1u;
+        // step j: O += P V of unit j, then S of unit j + 1, tile by tile
+        for (int j = -1; j < take && ok; ++j) {
           const bool more = j + 1 < take;
-          ok = wait(sh, &sh.v_full[vr.stage], vr.phase, a);
-          if (ok) ok = wait(sh, &sh.p_full[0], p_phase & 1u, a);
+          uint32_t idesc = 0;
+          if (j >= 0) {
+            ok = wait(sh, &sh.v_full[vr.stage], vr.phase, a);
+            if (!ok) break;
+            idesc = idesc_f16(sh.meta[unit % kMetaRing].wide != 0, true, 128, D);
+            ++unit;
+          }
+#pragma unroll 1
+          for (uint32_t x = 0; x < tiles; ++x) {
+            if (j >= 0) {
+              ok = wait(sh, &sh.p_full[x], (p_phase >> x) & 1u, a);
+              if (!ok) break;
+              tc_fence_after();
+              values(x, vr.stage, idesc, j == 0);
+            }
+            if (more) {
+              // P lies in S: these MMAs are issued behind the ones that read it
+              if (x == 0) {
+                ok = wait(sh, &sh.k_full[kr.stage], kr.phase, a);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              scores(x, kr.stage);
+            } else {
+              mma_commit(smem_u32(&sh.o_full[x]));
+            }
+          }
           if (!ok) break;
-          tc_fence_after();
-          const uint32_t idesc = idesc_f16(sh.meta[unit % kMetaRing].wide != 0, true, 128, D);
-          values(0, vr.stage, idesc, j == 0);
-          if (more) {
-            // P lies in S: this MMA is issued behind the ones that read it
-            ok = wait(sh, &sh.k_full[kr.stage], kr.phase, a);
-            if (!ok) break;
-            tc_fence_after();
-            scores(0, kr.stage);
-          } else {
-            mma_commit(smem_u32(&sh.o_full[0]));
+          if (j >= 0) {
+            p_phase ^= tiles == 2 ? 3u : 1u;
+            mma_commit(smem_u32(&sh.v_empty[vr.stage]));
+            vr.next();
           }
-          if (two) {
-            ok = wait(sh, &sh.p_full[1], (p_phase >> 1) & 1u, a);
-            if (!ok) break;
-            tc_fence_after();
-            values(1, vr.stage, idesc, j == 0);
-          }
-          p_phase ^= two ? 3u : 1u;
-          mma_commit(smem_u32(&sh.v_empty[vr.stage]));
-          vr.next();
           if (more) {
-            if (two) scores(1, kr.stage);
             mma_commit(smem_u32(&sh.k_empty[kr.stage]));
             kr.next();
-          } else if (two) {
-            mma_commit(smem_u32(&sh.o_full[1]));
           }
         }
         u += take;
@@ -775,6 +834,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
       // every MMA issued has completed before tensor memory is released
       mma_commit(smem_u32(&sh.drain));
       mbar_wait(smem_u32(&sh.drain), 0, 100000000ull);
+      }
+      __syncwarp();
     } else if (warp == 13 && !E2M1) {
       // ================================================================ K's codes
       // sixteen keys a box, each by its own lane; a group that is not there is
@@ -821,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, kTmemColumns);
+  if (warp == 12) tmem_dealloc(sh.tmem, kTmemColumns);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
