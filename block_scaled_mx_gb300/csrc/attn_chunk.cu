@@ -225,8 +225,123 @@ __device__ __forceinline__ void tmem_load(uint32_t col, uint32_t (&v)[kN]) {
   if constexpr (kN % 32 != 0) tmem_ld_32x32b_x16(col + kN / 32 * 32, reinterpret_cast<uint32_t(&)[16]>(v[kN / 32 * 32]));
 }
 
+// Sixteen finished elements of row oh of the output, and its lse.
+template <int D>
+__device__ __forceinline__ void put(const AttnArgs& a, int64_t oh, int c, const float (&v)[16], float inv) {
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + oh * D + c);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    dst[i] = make_uint4(pack_bf16(v[8 * i] * inv, v[8 * i + 1] * inv), pack_bf16(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
+                        pack_bf16(v[8 * i + 4] * inv, v[8 * i + 5] * inv), pack_bf16(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+}
+__device__ __forceinline__ void put_lse(const AttnArgs& a, int64_t oh, float M, float L) {
+  if (a.lse) a.lse[oh] = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+}
+// Four elements of a row of a part: the same elements of all rows side by side.
+template <int D>
+__device__ __forceinline__ float4* part_at(const AttnArgs& a, int slot, int d4, int row) {
+  return reinterpret_cast<float4*>(a.part_o) + (static_cast<int64_t>(slot) * (D / 4) + d4) * kRows + row;
+}
+
+// A tile's queries as two MXFP8 operands and their scales, by the 128 threads of
+// its softmax: eight elements a lane at a time, four lanes a block.  Not inlined
+// (nor is join_parts): once a segment, and it would push the unit loops out of
+// the instruction cache.
+template <int D>
+__device__ __noinline__ void load_queries(const AttnArgs& a, Shared& sh, uint8_t* base, int x, int q0, int head, int row0,
+                                          int rows) {
+  using Sh = Shape<D>;
+  constexpr uint32_t tmem = 0;
+  const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
+  const uint32_t lanes = static_cast<uint32_t>(threadIdx.x & 96) << 16;
+        constexpr int kPieces = D / 8;
+              uint8_t* hi_base = base + Sh::kQ + 2 * x * Sh::kQTile;
+#pragma unroll 2
+        for (int i = row; i < 128 * kPieces; i += 128) {
+          const int r = i / kPieces, p = i - r * kPieces;
+          const int R = row0 + r;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (R < rows) {
+            const int tok = R / a.group;
+            v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                     static_cast<int64_t>(q0 + tok) * a.q_stride +
+                                                     static_cast<int64_t>(head * a.group + (R - tok * a.group)) * D) + p);
+          }
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t amax = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          // the block's largest element lands in [2^7, 2^8): hi's rounding error
+          // is then at most 2^3 and 2^5 times it stays below E4M3's 448
+          const int s = max(static_cast<int>(amax >> 7) - 127 - 7, -122);
+          const float down = pow2_neg(s);
+          uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x0 = __uint_as_float(w[k] << 16) * down, x1 = __uint_as_float(w[k] & 0xFFFF0000u) * down;
+            const uint32_t h = enc_e4m3x2(x0, x1);
+            const uint32_t back = f16x2_of_e4m3x2(h);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+            hi[k >> 1] |= h << ((k & 1) * 16);
+            lo[k >> 1] |= enc_e4m3x2((x0 - f.x) * 32.0f, (x1 - f.y) * 32.0f) << ((k & 1) * 16);
+          }
+          const uint32_t at = D == 128 ? r * 128 + (((p >> 1) ^ (r & 7)) << 4) + (p & 1) * 8
+                                       : r * 64 + (((p >> 1) ^ ((r >> 1) & 3)) << 4) + (p & 1) * 8;
+          *reinterpret_cast<uint2*>(hi_base + at) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(hi_base + Sh::kQTile + at) = make_uint2(lo[0], lo[1]);
+          if ((p & 3) == 0) reinterpret_cast<uint8_t*>(&sh.q_scale[x][r])[p >> 2] = static_cast<uint8_t>(s + 127);
+        }
+        fence_proxy_async_shared();
+        named_barrier(1 + x);
+        // scales: row 32 j + lane in column j, the same in every lane quarter
+        const uint32_t col = tmem + lanes + Sh::kScales + 8u * x;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = sh.q_scale[x][32 * j + lane];
+        tmem_st_32x32b_x4(col, w[0], w[1], w[2], w[3]);
+        constexpr uint32_t kFive = D == 128 ? 0x05050505u : 0x0505u;
+        tmem_st_32x32b_x4(col + 4, w[0] - kFive, w[1] - kFive, w[2] - kFive, w[3] - kFive);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sh.q_full[x]));
+}
+
+// A row of a split segment from its parts, in key order.
+template <int D>
+__device__ __noinline__ void join_parts(const AttnArgs& a, AttnParts p, int row, int64_t oh) {
+  auto ml_of = [&](int i) { return __ldcg(&a.part_ml[attn_slot(p.first + i, i == 0) * kRows + row]); };
+  float M = -INFINITY;
+  for (int i = 0; i < p.parts; ++i) M = fmaxf(M, ml_of(i).x);
+  const float from = M == -INFINITY ? 0.0f : M;
+  float L = 0.0f;
+  for (int i = 0; i < p.parts; ++i) {
+    const float2 ml = ml_of(i);
+    L = fmaf(ml.y, exp2_approx(ml.x - from), L);
+  }
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    float f[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = 0.0f;
+#pragma unroll 2
+    for (int i = 0; i < p.parts; ++i) {
+      const float w = exp2_approx(ml_of(i).x - from);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = __ldcg(part_at<D>(a, attn_slot(p.first + i, i == 0), c / 4 + k, row));
+        f[4 * k] = fmaf(v.x, w, f[4 * k]), f[4 * k + 1] = fmaf(v.y, w, f[4 * k + 1]);
+        f[4 * k + 2] = fmaf(v.z, w, f[4 * k + 2]), f[4 * k + 3] = fmaf(v.w, w, f[4 * k + 3]);
+      }
+    }
+    put<D>(a, oh, c, f, L > 0.0f ? 1.0f / L : 0.0f);
+  }
+  put_lse(a, oh, M, L);
+}
+
 template <int D, bool E2M1>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, const __grid_constant__ CUtensorMap k_map) {
+__global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap k_map) {
   using Sh = Shape<D>;
   constexpr int kUnit = Sh::kUnit;
   using Cursor = AttnCursor<kRows, kUnit>;
@@ -289,67 +404,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
     uint32_t unit = 0, s_phase = 0, o_phase = 0;
     bool ok = true;
 
-    // The tile's queries as two MXFP8 operands.  Eight elements a lane at a
-    // time, four lanes a block.
-    auto load_queries = [&](const Cursor& c) {
-      constexpr int kPieces = D / 8;
-      const int rows = c.s.n * a.group, row0 = c.tile * kRows + 128 * x;
-      uint8_t* hi_base = base + Sh::kQ + 2 * x * Sh::kQTile;
-#pragma unroll 2
-      for (int i = row; i < 128 * kPieces; i += 128) {
-        const int r = i / kPieces, p = i - r * kPieces;
-        const int R = row0 + r;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (R < rows) {
-          const int tok = R / a.group;
-          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                   static_cast<int64_t>(c.s.q0 + tok) * a.q_stride +
-                                                   static_cast<int64_t>(c.head * a.group + (R - tok * a.group)) * D) + p);
-        }
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t amax = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // the block's largest element lands in [2^7, 2^8): hi's rounding error
-        // is then at most 2^3 and 2^5 times it stays below E4M3's 448
-        const int s = max(static_cast<int>(amax >> 7) - 127 - 7, -122);
-        const float down = pow2_neg(s);
-        uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float x0 = __uint_as_float(w[k] << 16) * down, x1 = __uint_as_float(w[k] & 0xFFFF0000u) * down;
-          const uint32_t h = enc_e4m3x2(x0, x1);
-          const uint32_t back = f16x2_of_e4m3x2(h);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
-          hi[k >> 1] |= h << ((k & 1) * 16);
-          lo[k >> 1] |= enc_e4m3x2((x0 - f.x) * 32.0f, (x1 - f.y) * 32.0f) << ((k & 1) * 16);
-        }
-        const uint32_t at = D == 128 ? r * 128 + (((p >> 1) ^ (r & 7)) << 4) + (p & 1) * 8
-                                     : r * 64 + (((p >> 1) ^ ((r >> 1) & 3)) << 4) + (p & 1) * 8;
-        *reinterpret_cast<uint2*>(hi_base + at) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(hi_base + Sh::kQTile + at) = make_uint2(lo[0], lo[1]);
-        if ((p & 3) == 0) reinterpret_cast<uint8_t*>(&sh.q_scale[x][r])[p >> 2] = static_cast<uint8_t>(s + 127);
-      }
-      fence_proxy_async_shared();
-      named_barrier(1 + x);
-      // scales: row 32 j + lane in column j, the same in every lane quarter
-      const uint32_t col = tmem + lanes + Sh::kScales + 8u * x;
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = sh.q_scale[x][32 * j + lane];
-      tmem_st_32x32b_x4(col, w[0], w[1], w[2], w[3]);
-      constexpr uint32_t kFive = D == 128 ? 0x05050505u : 0x0505u;
-      tmem_st_32x32b_x4(col + 4, w[0] - kFive, w[1] - kFive, w[2] - kFive, w[3] - kFive);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(smem_u32(&sh.q_full[x]));
-    };
-
     sh.q_scale[x][row] = 0u;
     named_barrier(1 + x);
-    if (u < share.end && cur.tile * kRows + 128 * x < cur.s.n * a.group) load_queries(cur);
+    auto queries_of = [&](const Cursor& c) {
+      const int rows = c.s.n * a.group, row0 = c.tile * kRows + 128 * x;
+      if (row0 < rows) load_queries<D>(a, sh, base, x, c.s.q0, c.head, row0, rows);
+    };
+    if (u < share.end) queries_of(cur);
     while (u < share.end && cur.b < a.n_seqs) {
       const int take = static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), share.end - u));
       const int rows = cur.s.n * a.group;
@@ -359,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
         ahead = cur;
         if (u + take >= share.end) return;
         ahead.next(a);
-        if (ahead.b < a.n_seqs && ahead.tile * kRows + 128 * x < ahead.s.n * a.group) load_queries(ahead);
+        if (ahead.b < a.n_seqs) queries_of(ahead);
       };
       if (row0 < rows) {
         const int R = row0 + row;
@@ -373,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
         const bool warp_valid = row0 + 32 * (warp & 3) < rows;
         const float scale = a.scale_log2;
         float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
         for (int j = 0; j < take; ++j) {
           if (ok) ok = wait(sh, &sh.s_full[x], s_phase, a);
           s_phase ^= 1u;
@@ -414,9 +476,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
             if (__any_sync(0xffffffffu, joint > m + 8.0f)) {
               const float to = fmaxf(m, joint);
               const float f = to == -INFINITY ? 1.0f : exp2_approx(m - to);
+              // O holds something but zeros once a row has seen a key; the MMA
+              // that S waited for was issued behind the last one that writes O
+              const bool rescale = __any_sync(0xffffffffu, m != -INFINITY);
               m = to;
               l *= f;
-              if (j > 0) {  // the MMA that S waited for was issued behind the last one that writes O
+              if (rescale) {
 #pragma unroll 1
                 for (int c = 0; c < D; c += 16) {
                   uint32_t o[16];
@@ -431,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
             const float off = m == -INFINITY ? 0.0f : e - m;
             const float2 scale2 = make_float2(scale, scale), off2 = make_float2(off, off);
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-            if (!meta.wide) {
+            if (__builtin_expect(meta.wide == 0, 1)) {
 #pragma unroll
               for (int i = 0; i < kUnit; i += 2) {
                 const float2 z = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), scale2, off2);
@@ -474,21 +539,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
         tc_fence_after();
         const bool whole = take == cur.t.units;
         const int64_t oh = static_cast<int64_t>(cur.s.q0 + tok) * n_heads + cur.head * a.group + (R - tok * a.group);
-        // sixteen finished elements of the row
-        auto put = [&](int c, const float (&v)[16], float inv) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + oh * D + c);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            dst[i] = make_uint4(pack_bf16(v[8 * i] * inv, v[8 * i + 1] * inv), pack_bf16(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
-                                pack_bf16(v[8 * i + 4] * inv, v[8 * i + 5] * inv), pack_bf16(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
-        };
-        auto put_lse = [&](float M, float Lsum) {
-          if (a.lse) a.lse[oh] = Lsum > 0.0f ? (M + log2f(Lsum)) * 0.69314718055994531f : -INFINITY;
-        };
-        // a part's row lies with float4s of the same elements of all rows side by side
-        auto part_at = [&](int slot, int d4) {
-          return reinterpret_cast<float4*>(a.part_o) + (static_cast<int64_t>(slot) * (D / 4) + d4) * kRows + 128 * x + row;
-        };
         const int slot = attn_slot(blockIdx.x, cur.place == 0);
         if (ok && warp_valid) {
           const float inv = l > 0.0f ? 1.0f / l : 0.0f;
@@ -502,15 +552,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
 #pragma unroll
             for (int i = 0; i < 16; ++i) f[i] = l > 0.0f ? __uint_as_float(v[i]) : 0.0f;
             if (valid && whole) {
-              put(c, f, inv);
+              put<D>(a, oh, c, f, inv);
             } else if (valid) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) *part_at(slot, c / 4 + i) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+              for (int i = 0; i < 4; ++i) *part_at<D>(a, slot, c / 4 + i, 128 * x + row) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
             }
             __syncwarp();
           }
           if (valid) {
-            if (whole) put_lse(m, l);
+            if (whole) put_lse(a, oh, m, l);
             else a.part_ml[slot * kRows + 128 * x + row] = make_float2(m, l);
           }
         }
@@ -527,33 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
           named_barrier(1 + x);
           if (sh.last[x] && ok && valid) {
             __threadfence();
-            float M = -INFINITY;
-            for (int i = 0; i < parts.parts; ++i)
-              M = fmaxf(M, __ldcg(&a.part_ml[attn_slot(parts.first + i, i == 0) * kRows + 128 * x + row]).x);
-            float Lsum = 0.0f;
-            for (int i = 0; i < parts.parts; ++i) {
-              const float2 ml = __ldcg(&a.part_ml[attn_slot(parts.first + i, i == 0) * kRows + 128 * x + row]);
-              Lsum += ml.y * (M == -INFINITY ? 0.0f : exp2_approx(ml.x - M));
-            }
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              float f[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) f[i] = 0.0f;
-#pragma unroll 2
-              for (int i = 0; i < parts.parts; ++i) {
-                const int sl = attn_slot(parts.first + i, i == 0);
-                const float w = M == -INFINITY ? 0.0f : exp2_approx(__ldcg(&a.part_ml[sl * kRows + 128 * x + row]).x - M);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float4 v = __ldcg(part_at(sl, c / 4 + k));
-                  f[4 * k] = fmaf(v.x, w, f[4 * k]), f[4 * k + 1] = fmaf(v.y, w, f[4 * k + 1]);
-                  f[4 * k + 2] = fmaf(v.z, w, f[4 * k + 2]), f[4 * k + 3] = fmaf(v.w, w, f[4 * k + 3]);
-                }
-              }
-              put(c, f, Lsum > 0.0f ? 1.0f / Lsum : 0.0f);
-            }
-            put_lse(M, Lsum);
+            join_parts<D>(a, parts, 128 * x + row, oh);
           }
         }
       } else {
@@ -577,62 +601,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
     // panel, which touches all banks.
     const int part = lane % 4 + (D == 128 ? lane / 16 * 4 : 0);
     const int r0 = dw * (32 / kShares) + (D == 128 ? lane % 16 / 4 : lane / 4);
+    // A unit on its way: nothing in it is touched before the unit's turn, not
+    // even to choose between a load's result and a constant, which would wait
+    // for the load.  What no row sees is read as whatever lies in its place and
+    // cleared later.
     struct Unit {
       Codes<E2M1> v[kIts];
       int vs[kIts];        // scale bytes
-      uint32_t there;      // bit i: key i is one that some row sees (others hold what lies first in the cache)
-      uint32_t ks[4];      // keys 32 j + lane: a row's K scale bytes
+      uint32_t ks[kUnit / 32];  // keys 32 j + lane: a row's K scale bytes
       Codes<E2M1> k[E2M1 ? kIts : 1];
+      uint32_t gone;       // bit g: 16-key group g is not there
+      int lo, hi;          // the keys to read, counted from the unit's first
     };
     // Where a unit lies: looked up one unit before its loads, those one unit
     // before their use.
     struct Place {
-      int page;          // of the lane's 16-key group, as the table has it
-      int head, offset;  // the group's first place in the page; -1: no row sees it
-      int key0, lo, hi;  // the unit's first key, and the keys to read
+      int page, head;      // the page of the lane's 16-key group, as the table has it
+      int offset;          // the group's first place in it, or -1: no row sees it
+      int lo, hi;
     };
     auto look_up = [&](const Cursor& c) {
       Place p;
-      p.key0 = c.t.first + c.place * kUnit;
-      p.lo = c.t.lo;
-      p.hi = c.t.hi;
-      p.head = c.head;
-      p.page = -1;
-      const int key = p.key0 + 16 * lane;
+      const int key = c.t.first + c.place * kUnit + 16 * lane;
       const int entry = key / a.page_size;
-      p.offset = key - entry * a.page_size;
-      if (lane < kUnit / 16 && key < p.hi && key + 16 > p.lo)
+      p.lo = c.t.lo - (key - 16 * lane);
+      p.hi = c.t.hi - (key - 16 * lane);
+      p.head = c.head;
+      p.page = 0;
+      p.offset = -1;
+      if (lane < kUnit / 16 && 16 * lane < p.hi && 16 * lane + 16 > p.lo) {
+        p.offset = key - entry * a.page_size;
         p.page = __ldg(a.block_table + static_cast<int64_t>(c.b) * a.max_pages + entry);
-      else
-        p.offset = -1;
+      }
       return p;
     };
+    const uint8_t* v_base = a.v_codes + part * (kRowBytes / kShares);
+    const uint8_t* k_base = a.k_codes + part * (kRowBytes / kShares);
+    const uint8_t* vs_base = a.v_scales + part / 2;
     auto load = [&](const Place& c, Unit& w) {
-      const int key0 = c.key0;
-      int mine = -1;
-      if (c.offset >= 0) {
-        if (c.page < 0 || c.page >= a.num_pages) set_status(a.status, MX_ERR_DEVICE_ARG);
-        else mine = (c.page * a.n_kv_heads + c.head) * a.page_size + c.offset;
-      }
-      // no load's result is touched here, not even to choose between it and a
-      // constant: that would wait for it
-      w.there = 0;
+      const bool bad = c.offset >= 0 && (c.page < 0 || c.page >= a.num_pages);
+      if (bad) set_status(a.status, MX_ERR_DEVICE_ARG);
+      const bool there = c.offset >= 0 && !bad;
+      // the group's first cache row; the table's first where it is not there
+      const int mine = there ? (c.page * a.n_kv_heads + c.head) * a.page_size + c.offset : 0;
+      w.gone = __ballot_sync(0xffffffffu, lane < kUnit / 16 && !there);
+      w.lo = c.lo;
+      w.hi = c.hi;
 #pragma unroll
       for (int i = 0; i < kIts; ++i) {
-        const int r = i * kKeysPerIt + r0;
-        const int g = __shfl_sync(0xffffffffu, mine, r / 16);
-        const bool there = g >= 0 && key0 + r < c.hi && key0 + r >= c.lo;
-        const int64_t at = there ? g + r % 16 : 0;
-        w.there |= (there ? 1u : 0u) << i;
-        w.v[i].load(a.v_codes + at * kRowBytes + part * (kRowBytes / kShares));
-        w.vs[i] = __ldg(a.v_scales + at * kBlocks + part / 2);
-        if (E2M1) w.k[E2M1 ? i : 0].load(a.k_codes + at * kRowBytes + part * (kRowBytes / kShares));
+        const int64_t at = __shfl_sync(0xffffffffu, mine, (i * kKeysPerIt + r0) / 16) + r0 % 16;
+        w.v[i].load(v_base + at * kRowBytes);
+        w.vs[i] = __ldg(vs_base + at * kBlocks);
+        if (E2M1) w.k[E2M1 ? i : 0].load(k_base + at * kRowBytes);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = 32 * j + lane;
-        const int g = __shfl_sync(0xffffffffu, mine, min(r / 16, kUnit / 16 - 1));
-        const int64_t at = r < kUnit && g >= 0 ? g + r % 16 : 0;
+      for (int j = 0; j < kUnit / 32; ++j) {
+        const int64_t at = __shfl_sync(0xffffffffu, mine, 2 * j + lane / 16) + lane % 16;
         if constexpr (kBlocks == 4) w.ks[j] = __ldg(reinterpret_cast<const uint32_t*>(a.k_scales) + at);
         else w.ks[j] = __ldg(reinterpret_cast<const uint16_t*>(a.k_scales) + at);
       }
@@ -650,27 +674,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
     Ring ring;
     Unit now, then;
     Place at;
-    auto advance = [&]() {  // to the unit after the one in `at`
-      if (--left == 0) {
-        cur.next(a);
-        left = cur.t.units;
-      } else {
-        ++cur.place;
+    // one unit is looked up, one loaded and one converted in each turn
+#pragma unroll 1
+    for (int i = -2; i < n; ++i) {
+      if (i >= -1 && i + 1 < n) load(at, then);
+      if (i + 2 < n) {
+        if (i > -2) {
+          if (--left == 0) {
+            cur.next(a);
+            left = cur.t.units;
+          } else {
+            ++cur.place;
+          }
+        }
+        at = look_up(cur);
       }
-      at = look_up(cur);
-    };
-    if (n > 0) {
-      at = look_up(cur);
-      load(at, now);
-      if (n > 1) advance();
-    }
-    for (int i = 0; i < n; ++i) {
-      if (i + 1 < n) load(at, then);
-      if (i + 2 < n) advance();
-      if (now.there != (1u << kIts) - 1) {
+      if (i < 0) {
+        now = then;
+        continue;
+      }
+      if (now.gone != 0 || now.lo > 0 || now.hi < kUnit) {
 #pragma unroll
         for (int k = 0; k < kIts; ++k) {
-          if (now.there >> k & 1) continue;
+          const int r = k * kKeysPerIt + r0;
+          if (r >= now.lo && r < now.hi && !(now.gone >> (r / 16) & 1u)) continue;
           now.v[k].clear();
           now.vs[k] = 0;
           if (E2M1) now.k[E2M1 ? k : 0].clear();
@@ -716,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
         fence_proxy_async_shared();
       }
       tmem_st_32x32b_x4(tmem + (static_cast<uint32_t>(32 * dw) << 16) + Sh::kScales + 16u + 4u * ring.stage, now.ks[0],
-                        now.ks[1], now.ks[2], now.ks[3]);
+                        now.ks[1], now.ks[2], kUnit == 128 ? now.ks[kUnit / 32 - 1] : 0x7F7F7F7Fu);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(smem_u32(&sh.k_full[ring.stage]));
@@ -725,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       uint8_t* v_stage = base + Sh::kV + ring.stage * Sh::kVStage;
-      if (wide) {
+      if (__builtin_expect(wide, 0)) {
 #pragma unroll
         for (int k = 0; k < kIts; ++k) {
           const uint32_t f = bf16_pow2x2_112(now.vs[k] - 127 - v_exp);
@@ -788,6 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
         for (uint32_t x = 0; x < tiles && ok; ++x) ok = wait(sh, &sh.q_full[x], (q_phase >> x) & 1u, a);
         q_phase ^= tiles == 2 ? 3u : 1u;
         // step j: O += P V of unit j, then S of unit j + 1, tile by tile
+#pragma unroll 1
         for (int j = -1; j < take && ok; ++j) {
           const bool more = j + 1 < take;
           uint32_t idesc = 0;
@@ -847,6 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const AttnArgs a, co
       bool ok = true;
       int issued = 0;
       if (lane == 0) prefetch_tensormap(&k_map);
+#pragma unroll 1
       for (int i = 0; i < n; ++i) {
         int at = none;
         if (lane < kUnit / 16) at = group_row(cur, cur.t.first + cur.place * kUnit, lane);
