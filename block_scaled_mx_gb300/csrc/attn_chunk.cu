@@ -8,10 +8,10 @@
 // softmax's):
 //   0-3, 4-7  softmax of A and of B, one row a thread; also its queries, the
 //             rescaling of its accumulator and its output
-//   8-11      V: codes and scales through registers into the 16-bit operand in
-//             shared memory; K's scales into tensor memory
+//   8-11      V: codes through registers into the 16-bit operand in shared memory
+//             (and K's, where they are E2M1)
 //   12        issuing MMAs
-//   13        K's codes, by TMA
+//   13        K's codes by TMA, and all scales
 // For each unit of keys, S = Q K^T goes to tensor memory, its softmax weights P
 // overwrite it there, and O += P V reads P from tensor memory.
 //
@@ -91,8 +91,9 @@ struct Shared {
   volatile int failed;
   int last[2];
   UnitMeta meta[kMetaRing];
-  int v_range[2][4][2];      // by parity and warp: largest and smallest V scale
+  uint64_t meta_full[kMetaRing];
   uint32_t q_scale[2][128];  // a row's scale bytes
+  alignas(128) uint32_t k_scale[kStages][32][4];  // keys 32 j + lane, by lane
   int64_t units[kAttnScan];
 };
 
@@ -113,7 +114,8 @@ __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity,
   const uint32_t b = smem_u32(bar);
   if (mbar_try_wait(b, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(b, parity)) {
+  for (uint32_t n = 1; !mbar_try_wait(b, parity); ++n) {
+    if (n & 15u) continue;
     if (sh.failed) return false;
     if (globaltimer_ns() - t0 > a.wait_limit_ns) {
       sh.failed = 1;
@@ -358,11 +360,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
       mbar_init(smem_u32(&sh.o_full[i]), 1);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&sh.k_full[i]), E2M1 ? 128 : 129);  // the scales' warps, and the TMA's issuer
+      mbar_init(smem_u32(&sh.k_full[i]), E2M1 ? 129 : 1);  // the scales' warp; E2M1 codes come by V's warps
       mbar_init(smem_u32(&sh.k_empty[i]), 1);
       mbar_init(smem_u32(&sh.v_full[i]), 128);
       mbar_init(smem_u32(&sh.v_empty[i]), 1);
     }
+    for (int i = 0; i < kMetaRing; ++i) mbar_init(smem_u32(&sh.meta_full[i]), 1);
     mbar_init(smem_u32(&sh.drain), 1);
     sh.failed = 0;
     fence_mbar_init();
@@ -379,18 +382,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
   int64_t u = share.u;
   Cursor cur;
   if (u < share.end) cur.template start<true>(a, share);
-  // Where the 16-key group `group` of the unit at key0 lies: its first cache
-  // row, or -1 where no row sees it or its page is bad.
-  auto group_row = [&](const Cursor& c, int key0, int group) {
-    const int key = key0 + 16 * group;
-    if (key >= c.t.hi || key + 16 <= c.t.lo) return -1;
+  // Where a unit lies, its 16-key groups by lane: looked up one unit before it
+  // is needed, and the page id left alone until then.
+  struct Place {
+    int page, head;  // as the table has it
+    int offset;      // the group's first place in the page, or -1: no row sees it
+    int lo, hi;      // the keys to read, counted from the unit's first
+  };
+  auto look_up = [&](const Cursor& c) {
+    Place p;
+    const int key = c.t.first + c.place * kUnit + 16 * lane;
     const int entry = key / a.page_size;
-    const int page = __ldg(a.block_table + static_cast<int64_t>(c.b) * a.max_pages + entry);
-    if (page < 0 || page >= a.num_pages) {
+    p.lo = c.t.lo - (key - 16 * lane);
+    p.hi = c.t.hi - (key - 16 * lane);
+    p.head = c.head;
+    const bool seen = lane < kUnit / 16 && 16 * lane < p.hi && 16 * lane + 16 > p.lo;
+    p.offset = seen ? key - entry * a.page_size : -1;
+    p.page = __ldg(a.block_table + static_cast<int64_t>(c.b) * a.max_pages + (seen ? entry : 0));
+    return p;
+  };
+  // The group's first cache row, or -1 where it is not there.
+  auto group_row = [&](const Place& p) {
+    if (p.offset < 0) return -1;
+    if (p.page < 0 || p.page >= a.num_pages) {
       set_status(a.status, MX_ERR_DEVICE_ARG);
       return -1;
     }
-    return (page * a.n_kv_heads + c.head) * a.page_size + (key - entry * a.page_size);
+    return (p.page * a.n_kv_heads + p.head) * a.page_size + p.offset;
   };
 
   if (warp < 8) {
@@ -601,64 +619,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
     // panel, which touches all banks.
     const int part = lane % 4 + (D == 128 ? lane / 16 * 4 : 0);
     const int r0 = dw * (32 / kShares) + (D == 128 ? lane % 16 / 4 : lane / 4);
-    // A unit on its way: nothing in it is touched before the unit's turn, not
-    // even to choose between a load's result and a constant, which would wait
-    // for the load.  What no row sees is read as whatever lies in its place and
-    // cleared later.
-    struct Unit {
-      Codes<E2M1> v[kIts];
-      int vs[kIts];        // scale bytes
-      uint32_t ks[kUnit / 32];  // keys 32 j + lane: a row's K scale bytes
-      Codes<E2M1> k[E2M1 ? kIts : 1];
-      uint32_t gone;       // bit g: 16-key group g is not there
-      int lo, hi;          // the keys to read, counted from the unit's first
-    };
-    // Where a unit lies: looked up one unit before its loads, those one unit
-    // before their use.
-    struct Place {
-      int page, head;      // the page of the lane's 16-key group, as the table has it
-      int offset;          // the group's first place in it, or -1: no row sees it
-      int lo, hi;
-    };
-    auto look_up = [&](const Cursor& c) {
-      Place p;
-      const int key = c.t.first + c.place * kUnit + 16 * lane;
-      const int entry = key / a.page_size;
-      p.lo = c.t.lo - (key - 16 * lane);
-      p.hi = c.t.hi - (key - 16 * lane);
-      p.head = c.head;
-      p.page = 0;
-      p.offset = -1;
-      if (lane < kUnit / 16 && 16 * lane < p.hi && 16 * lane + 16 > p.lo) {
-        p.offset = key - entry * a.page_size;
-        p.page = __ldg(a.block_table + static_cast<int64_t>(c.b) * a.max_pages + entry);
-      }
-      return p;
-    };
     const uint8_t* v_base = a.v_codes + part * (kRowBytes / kShares);
     const uint8_t* k_base = a.k_codes + part * (kRowBytes / kShares);
     const uint8_t* vs_base = a.v_scales + part / 2;
+    // A unit on its way.  What no row sees is read as whatever lies in its place
+    // (the table's first rows where there is none) and cleared later: choosing
+    // between a load's result and a constant here would wait for the load.
+    struct Unit {
+      Codes<E2M1> v[kIts], k[E2M1 ? kIts : 1];
+      int vs[kIts];   // scale bytes
+      uint32_t gone;  // bit g: 16-key group g is not there
+      int lo, hi;     // the keys to read
+    };
     auto load = [&](const Place& c, Unit& w) {
-      const bool bad = c.offset >= 0 && (c.page < 0 || c.page >= a.num_pages);
-      if (bad) set_status(a.status, MX_ERR_DEVICE_ARG);
-      const bool there = c.offset >= 0 && !bad;
-      // the group's first cache row; the table's first where it is not there
-      const int mine = there ? (c.page * a.n_kv_heads + c.head) * a.page_size + c.offset : 0;
-      w.gone = __ballot_sync(0xffffffffu, lane < kUnit / 16 && !there);
+      const int row = group_row(c);
+      const int first_row = max(row, 0);
+      w.gone = __ballot_sync(0xffffffffu, lane < kUnit / 16 && row < 0);
       w.lo = c.lo;
       w.hi = c.hi;
 #pragma unroll
       for (int i = 0; i < kIts; ++i) {
-        const int64_t at = __shfl_sync(0xffffffffu, mine, (i * kKeysPerIt + r0) / 16) + r0 % 16;
+        const int64_t at = __shfl_sync(0xffffffffu, first_row, (i * kKeysPerIt + r0) / 16) + r0 % 16;
         w.v[i].load(v_base + at * kRowBytes);
         w.vs[i] = __ldg(vs_base + at * kBlocks);
         if (E2M1) w.k[E2M1 ? i : 0].load(k_base + at * kRowBytes);
-      }
-#pragma unroll
-      for (int j = 0; j < kUnit / 32; ++j) {
-        const int64_t at = __shfl_sync(0xffffffffu, mine, 2 * j + lane / 16) + lane % 16;
-        if constexpr (kBlocks == 4) w.ks[j] = __ldg(reinterpret_cast<const uint32_t*>(a.k_scales) + at);
-        else w.ks[j] = __ldg(reinterpret_cast<const uint16_t*>(a.k_scales) + at);
       }
     };
     // a lane's two 16-byte pieces of a V row; kKeysPerIt is a multiple of 8, so
@@ -672,11 +656,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
     const int n = static_cast<int>(share.end - share.u);
     int left = n > 0 ? static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), static_cast<int64_t>(n))) : 0;
     Ring ring;
+    Place at{};
     Unit now, then;
-    Place at;
-    // one unit is looked up, one loaded and one converted in each turn
+    // In each turn one unit is looked up, the one before it loaded, and the one
+    // before that, whose loads have had a turn to arrive, converted.
 #pragma unroll 1
     for (int i = -2; i < n; ++i) {
+      if (i >= 0) now = then;
       if (i >= -1 && i + 1 < n) load(at, then);
       if (i + 2 < n) {
         if (i > -2) {
@@ -689,92 +675,61 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
         }
         at = look_up(cur);
       }
-      if (i < 0) {
-        now = then;
-        continue;
-      }
-      if (now.gone != 0 || now.lo > 0 || now.hi < kUnit) {
+      if (i >= 0) {
+        if (now.gone != 0 || now.lo > 0 || now.hi < kUnit) {
 #pragma unroll
-        for (int k = 0; k < kIts; ++k) {
-          const int r = k * kKeysPerIt + r0;
-          if (r >= now.lo && r < now.hi && !(now.gone >> (r / 16) & 1u)) continue;
-          now.v[k].clear();
-          now.vs[k] = 0;
-          if (E2M1) now.k[E2M1 ? k : 0].clear();
+          for (int q = 0; q < kIts; ++q) {
+            const int r = q * kKeysPerIt + r0;
+            if (r >= now.lo && r < now.hi && !(now.gone >> (r / 16) & 1u)) continue;
+            now.v[q].clear();
+            if (E2M1) now.k[E2M1 ? q : 0].clear();
+          }
         }
-      }
-      // V's largest scale, and the smallest of a block that is not zero
-      int v_max = 0, v_min = 255;
+        if (E2M1) {
+          bool ok = wait(sh, &sh.k_empty[ring.stage], ring.phase ^ 1u, a);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
 #pragma unroll
-      for (int k = 0; k < kIts; ++k) {
-        v_max = max(v_max, now.vs[k]);
-        v_min = min(v_min, now.vs[k] > 0 ? now.vs[k] : 255);
-      }
-      v_max = __reduce_max_sync(0xffffffffu, v_max);
-      v_min = __reduce_min_sync(0xffffffffu, v_min);
-      int(*seen)[2] = sh.v_range[i & 1];
-      if (lane == 0) seen[dw][0] = v_max, seen[dw][1] = v_min;
-      named_barrier(3);
+          for (int q = 0; q < kIts; ++q) {
+            const int r = q * kKeysPerIt + r0;
+            const uint32_t c0 = now.k[E2M1 ? q : 0].w[0], c1 = now.k[E2M1 ? q : 0].w[1];
+            const uint32_t to = D == 128 ? r * 128 + ((part ^ (r & 7)) << 4) : r * 64 + ((part ^ ((r >> 1) & 3)) << 4);
+            *reinterpret_cast<uint4*>(base + Sh::kK + ring.stage * Sh::kKStage + to) =
+                make_uint4(e4m3_of_e2m1x4(c0), e4m3_of_e2m1x4(c0 >> 16), e4m3_of_e2m1x4(c1), e4m3_of_e2m1x4(c1 >> 16));
+          }
+          fence_proxy_async_shared();
+          mbar_arrive(smem_u32(&sh.k_full[ring.stage]));
+        }
+        const uint32_t m = static_cast<uint32_t>(i) % kMetaRing;
+        bool ok = wait(sh, &sh.meta_full[m], (static_cast<uint32_t>(i) / kMetaRing) & 1u, a);
+        if (ok) ok = wait(sh, &sh.v_empty[ring.stage], ring.phase ^ 1u, a);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const UnitMeta meta = sh.meta[m];
+        uint8_t* v_stage = base + Sh::kV + ring.stage * Sh::kVStage;
+        if (__builtin_expect(meta.wide, 0)) {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        v_max = max(v_max, seen[w][0]);
-        v_min = min(v_min, seen[w][1]);
-      }
-      const int v_exp = min(max(v_max - 127, -100), 126);
-      const bool wide = v_exp - (v_min - 127) > 15;
-      if (dw == 0 && lane == 0) {
-        sh.meta[i % kMetaRing].v_exp = v_exp;
-        sh.meta[i % kMetaRing].wide = wide;
-      }
-
-      bool ok = wait(sh, &sh.k_empty[ring.stage], ring.phase ^ 1u, a);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      if (E2M1) {
+          for (int q = 0; q < kIts; ++q) {
+            const uint32_t f = bf16_pow2x2_112(min(now.vs[q] - 127 - meta.v_exp, 15));
+            uint32_t o[8];
 #pragma unroll
-        for (int k = 0; k < kIts; ++k) {
-          const int r = k * kKeysPerIt + r0;
-          const uint32_t c0 = now.k[E2M1 ? k : 0].w[0], c1 = now.k[E2M1 ? k : 0].w[1];
-          const uint32_t at = D == 128 ? r * 128 + ((part ^ (r & 7)) << 4) : r * 64 + ((part ^ ((r >> 1) & 3)) << 4);
-          *reinterpret_cast<uint4*>(base + Sh::kK + ring.stage * Sh::kKStage + at) =
-              make_uint4(e4m3_of_e2m1x4(c0), e4m3_of_e2m1x4(c0 >> 16), e4m3_of_e2m1x4(c1), e4m3_of_e2m1x4(c1 >> 16));
+            for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(bf16x2_of_f16x2(now.v[q].pair(e)), f);
+            store(v_stage, q, o);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < kIts; ++q) {
+            const uint32_t f = f16_pow2x2(min(now.vs[q] - 127 - meta.v_exp, 15));
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = mul_f16x2(now.v[q].pair(e), f);
+            store(v_stage, q, o);
+          }
         }
         fence_proxy_async_shared();
+        mbar_arrive(smem_u32(&sh.v_full[ring.stage]));
+        ring.next();
       }
-      tmem_st_32x32b_x4(tmem + (static_cast<uint32_t>(32 * dw) << 16) + Sh::kScales + 16u + 4u * ring.stage, now.ks[0],
-                        now.ks[1], now.ks[2], kUnit == 128 ? now.ks[kUnit / 32 - 1] : 0x7F7F7F7Fu);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(smem_u32(&sh.k_full[ring.stage]));
-
-      ok = wait(sh, &sh.v_empty[ring.stage], ring.phase ^ 1u, a);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      uint8_t* v_stage = base + Sh::kV + ring.stage * Sh::kVStage;
-      if (__builtin_expect(wide, 0)) {
-#pragma unroll
-        for (int k = 0; k < kIts; ++k) {
-          const uint32_t f = bf16_pow2x2_112(now.vs[k] - 127 - v_exp);
-          uint32_t o[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) o[q] = mul_bf16x2(bf16x2_of_f16x2(now.v[k].pair(q)), f);
-          store(v_stage, k, o);
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < kIts; ++k) {
-          const uint32_t f = f16_pow2x2(now.vs[k] - 127 - v_exp);
-          uint32_t o[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) o[q] = mul_f16x2(now.v[k].pair(q), f);
-          store(v_stage, k, o);
-        }
-      }
-      fence_proxy_async_shared();
-      mbar_arrive(smem_u32(&sh.v_full[ring.stage]));
-      ring.next();
-      now = then;
     }
   } else {
     give_registers<kIssueRegs>();
@@ -839,6 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
                 ok = wait(sh, &sh.k_full[kr.stage], kr.phase, a);
                 if (!ok) break;
                 tc_fence_after();
+                tmem_copy_scales(tmem + Sh::kScales + 16u + 4u * kr.stage, smem_u32(&sh.k_scale[kr.stage][0][0]));
               }
               scores(x, kr.stage);
             } else {
@@ -864,45 +820,96 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
       mbar_wait(smem_u32(&sh.drain), 0, 100000000ull);
       }
       __syncwarp();
-    } else if (warp == 13 && !E2M1) {
-      // ================================================================ K's codes
-      // sixteen keys a box, each by its own lane; a group that is not there is
-      // read past the table's end, which fills zeros
+    } else if (warp == 13) {
+      // ================================================================ scales, and K's codes
+      // Sixteen keys a TMA box, each by its own lane; a group that is not there
+      // is read past the table's end, which fills zeros.
+      constexpr int kWords = kUnit / 32, kBlocks = D / 32;
       const int n = static_cast<int>(share.end - share.u);
       const int none = a.num_pages * a.n_kv_heads * a.page_size;
       int left = n > 0 ? static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), static_cast<int64_t>(n))) : 0;
       Ring ring;
       bool ok = true;
       int issued = 0;
-      if (lane == 0) prefetch_tensormap(&k_map);
+      if (!E2M1 && lane == 0) prefetch_tensormap(&k_map);
+      auto scale_word = [&](const uint8_t* p, int64_t row) -> uint32_t {
+        if constexpr (kBlocks == 4) return __ldg(reinterpret_cast<const uint32_t*>(p) + row);
+        else return __ldg(reinterpret_cast<const uint16_t*>(p) + row);
+      };
+      struct Unit {
+        uint32_t ks[kWords], vs[kWords];  // keys 32 j + lane: a row's scale bytes
+        int row, lo, hi;                  // the lane's group's first cache row; the keys to read
+      };
+      Place at{};
+      Unit now, then;
+      // looked up, loaded and passed on a turn apart, as V's units are
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        int at = none;
-        if (lane < kUnit / 16) at = group_row(cur, cur.t.first + cur.place * kUnit, lane);
-        if (at < 0) at = none;
+      for (int i = -2; i < n; ++i) {
+        if (i >= 0) now = then;
+        if (i >= -1 && i + 1 < n) {
+          then.row = group_row(at);
+          then.lo = at.lo;
+          then.hi = at.hi;
+          const int first_row = max(then.row, 0);
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) {
+            const int64_t to = __shfl_sync(0xffffffffu, first_row, 2 * j + lane / 16) + lane % 16;
+            then.ks[j] = scale_word(a.k_scales, to);
+            then.vs[j] = scale_word(a.v_scales, to);
+          }
+        }
+        if (i + 2 < n) {
+          if (i > -2) {
+            if (--left == 0) {
+              cur.next(a);
+              left = cur.t.units;
+            } else {
+              ++cur.place;
+            }
+          }
+          at = look_up(cur);
+        }
+        if (i < 0) continue;
         ok = wait(sh, &sh.k_empty[ring.stage], ring.phase ^ 1u, a);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t bar = smem_u32(&sh.k_full[ring.stage]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, Sh::kKStage);
+        *reinterpret_cast<uint4*>(&sh.k_scale[ring.stage][lane][0]) =
+            make_uint4(now.ks[0], now.ks[1], now.ks[2], kWords == 4 ? now.ks[kWords - 1] : 0x7F7F7F7Fu);
+        // V's largest scale, and the smallest of a block that is not zero
+        const uint32_t gone = __ballot_sync(0xffffffffu, lane < kUnit / 16 && now.row < 0);
+        uint32_t top = 0, low = 0xFFFFFFFFu;
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          const int r = 32 * j + lane;
+          const uint32_t w = r >= now.lo && r < now.hi && !(gone >> (r / 16) & 1u) ? now.vs[j] : 0u;
+          top = __vmaxu4(top, w);
+          low = __vminu4(low, w | __vcmpeq4(w, 0u));
+        }
+        top = max(max(top & 0xFFu, (top >> 8) & 0xFFu), max((top >> 16) & 0xFFu, top >> 24));
+        low = min(min(low & 0xFFu, (low >> 8) & 0xFFu), min((low >> 16) & 0xFFu, low >> 24));
+        top = __reduce_max_sync(0xffffffffu, top);
+        low = __reduce_min_sync(0xffffffffu, low);
+        const int v_exp = min(max(static_cast<int>(top) - 127, -100), 126);
+        const uint32_t m = static_cast<uint32_t>(i) % kMetaRing;
+        fence_proxy_async_shared();
         __syncwarp();
-        if (lane < kUnit / 16)
-          tma_load_2d(smem_u32(base + Sh::kK + ring.stage * Sh::kKStage + lane * 16 * D), &k_map, 0, at, bar);
+        if (lane == 0) {
+          sh.meta[m].v_exp = v_exp;
+          sh.meta[m].wide = v_exp - (static_cast<int>(low) - 127) > 15;
+          mbar_arrive(smem_u32(&sh.meta_full[m]));
+          if (E2M1) mbar_arrive(bar);
+          else mbar_arrive_expect_tx(bar, Sh::kKStage);
+        }
+        __syncwarp();
+        if (!E2M1 && lane < kUnit / 16)
+          tma_load_2d(smem_u32(base + Sh::kK + ring.stage * Sh::kKStage + lane * 16 * D), &k_map, 0, now.row < 0 ? none : now.row, bar);
         ++issued;
         ring.next();
-        if (i + 1 < n) {
-          if (--left == 0) {
-            cur.next(a);
-            if (cur.b >= a.n_seqs) break;
-            left = cur.t.units;
-          } else {
-            ++cur.place;
-          }
-        }
       }
       // the last fills have landed before the CTA exits, also where a wait of
       // the others ran out
-      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+      for (int i = issued > kStages ? issued - kStages : 0; i < issued && !E2M1; ++i)
         mbar_wait(smem_u32(&sh.k_full[i % kStages]), (i / kStages) & 1u, 100000000ull);
       __syncwarp();
     }

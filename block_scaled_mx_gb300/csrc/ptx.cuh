@@ -218,6 +218,18 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(desc_hi));
 }
 
+// 32 rows of 16 bytes (512 bytes of shared memory, 128-byte aligned, unswizzled)
+// to four columns of tensor memory, lane i of every lane quarter from row i:
+// block-scale words, ordered before the MMAs that this thread issues next.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t smem) {
+  const uint32_t lo = ((smem >> 4) & 0x3FFFu) | (8u << 16);
+  asm volatile(
+      "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+      "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+      "r"(lo), "r"((128u >> 4) | (1u << 14))
+      : "memory");
+}
+
 // Arrive (once) on an mbarrier when every previously issued tcgen05 async
 // operation of this thread has completed.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
