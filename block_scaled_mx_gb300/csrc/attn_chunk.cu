@@ -8,10 +8,11 @@
 // softmax's):
 //   0-3, 4-7  softmax of A and of B, one row a thread; also its queries, the
 //             rescaling of its accumulator and its output
-//   8-11      V: codes through registers into the 16-bit operand in shared memory
-//             (and K's, where they are E2M1)
+//   8-11      V: codes into the 16-bit operand, from and to shared memory (and
+//             K's into 8-bit ones, where they are E2M1)
 //   12        issuing MMAs
-//   13        K's codes by TMA, and all scales
+//   13        all codes, by TMA
+//   14        all scales
 // For each unit of keys, S = Q K^T goes to tensor memory, its softmax weights P
 // overwrite it there, and O += P V reads P from tensor memory.
 //
@@ -50,6 +51,7 @@ constexpr int kThreads = 512;
 constexpr int kMaxCtas = 152;
 constexpr int kMinUnits = 2;
 constexpr int kStages = 3;    // of K and of V
+constexpr int kRawStages = 2; // of codes on their way to V
 constexpr int kMetaRing = 8;  // more units than can be between their scales' arrival and their softmax
 // Registers a thread by warpgroup; the launch's 128 x 4 are shared out.
 constexpr int kLaunchRegs = 128;
@@ -60,6 +62,7 @@ static_assert(2 * kSoftmaxRegs + kValueRegs + kIssueRegs <= 4 * kLaunchRegs, "se
 struct UnitMeta {
   int v_exp;  // exponent of its largest V scale
   int wide;   // V and P in bf16
+  int lo, hi; // the keys that some row sees, counted from the unit's first
 };
 
 template <int D>
@@ -75,7 +78,10 @@ struct Shape {
   static constexpr uint32_t kQ = 0;                          // A hi, A lo, B hi, B lo
   static constexpr uint32_t kK = 4 * kQTile;
   static constexpr uint32_t kV = kK + kStages * kKStage;
-  static constexpr uint32_t kBytes = kV + kStages * kVStage;
+  // codes as they come: V's, and K's where they are E2M1
+  static constexpr uint32_t kRaw = kV + kStages * kVStage;
+  static constexpr uint32_t kRawStage = kUnit * D;
+  static constexpr uint32_t kBytes = kRaw + kRawStages * kRawStage;
   static_assert(kKStage % 1024 == 0 && kVPanel % 1024 == 0, "swizzle atoms");
   // tensor memory columns
   static constexpr uint32_t kS = 0, kSNext = kUnit;
@@ -87,21 +93,23 @@ constexpr uint32_t kTmemColumns = 512;
 struct Shared {
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], drain;
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages];
   uint32_t tmem;
   volatile int failed;
   int last[2];
   UnitMeta meta[kMetaRing];
-  uint64_t meta_full[kMetaRing];
   uint32_t q_scale[2][128];  // a row's scale bytes
   alignas(128) uint32_t k_scale[kStages][32][4];  // keys 32 j + lane, by lane
+  uint32_t v_scale[kRawStages][128];
   int64_t units[kAttnScan];
 };
 
 // A stage of a ring and the parity of its current round.
+template <int kN>
 struct Ring {
   uint32_t stage = 0, phase = 0;
   __device__ __forceinline__ void next() {
-    if (++stage == kStages) {
+    if (++stage == kN) {
       stage = 0;
       phase ^= 1u;
     }
@@ -200,10 +208,10 @@ struct Codes {
   uint32_t w[kWords];
   __device__ __forceinline__ void load(const uint8_t* p) {
     if constexpr (E2M1) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
       w[0] = v.x, w[1] = v.y;
     } else {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
       w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     }
   }
@@ -343,7 +351,8 @@ __device__ __noinline__ void join_parts(const AttnArgs& a, AttnParts p, int row,
 }
 
 template <int D, bool E2M1>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap k_map) {
+__global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap k_map,
+                                                              const __grid_constant__ CUtensorMap v_map) {
   using Sh = Shape<D>;
   constexpr int kUnit = Sh::kUnit;
   using Cursor = AttnCursor<kRows, kUnit>;
@@ -360,12 +369,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
       mbar_init(smem_u32(&sh.o_full[i]), 1);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&sh.k_full[i]), E2M1 ? 129 : 1);  // the scales' warp; E2M1 codes come by V's warps
+      mbar_init(smem_u32(&sh.k_full[i]), E2M1 ? 129 : 2);  // scales, and codes by TMA or by V's warps
       mbar_init(smem_u32(&sh.k_empty[i]), 1);
       mbar_init(smem_u32(&sh.v_full[i]), 128);
       mbar_init(smem_u32(&sh.v_empty[i]), 1);
     }
-    for (int i = 0; i < kMetaRing; ++i) mbar_init(smem_u32(&sh.meta_full[i]), 1);
+    for (int i = 0; i < kRawStages; ++i) {
+      mbar_init(smem_u32(&sh.raw_full[i]), 2);  // scales and codes
+      mbar_init(smem_u32(&sh.raw_empty[i]), 128);
+    }
     mbar_init(smem_u32(&sh.drain), 1);
     sh.failed = 0;
     fence_mbar_init();
@@ -389,14 +401,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
     int offset;      // the group's first place in the page, or -1: no row sees it
     int lo, hi;      // the keys to read, counted from the unit's first
   };
-  auto look_up = [&](const Cursor& c) {
+  auto look_up = [&](const Cursor& c, int group) {
     Place p;
-    const int key = c.t.first + c.place * kUnit + 16 * lane;
+    const int key = c.t.first + c.place * kUnit + 16 * group;
     const int entry = key / a.page_size;
-    p.lo = c.t.lo - (key - 16 * lane);
-    p.hi = c.t.hi - (key - 16 * lane);
+    p.lo = c.t.lo - (key - 16 * group);
+    p.hi = c.t.hi - (key - 16 * group);
     p.head = c.head;
-    const bool seen = lane < kUnit / 16 && 16 * lane < p.hi && 16 * lane + 16 > p.lo;
+    const bool seen = group < kUnit / 16 && 16 * group < p.hi && 16 * group + 16 > p.lo;
     p.offset = seen ? key - entry * a.page_size : -1;
     p.page = __ldg(a.block_table + static_cast<int64_t>(c.b) * a.max_pages + (seen ? entry : 0));
     return p;
@@ -608,128 +620,80 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
   } else if (warp < 12) {
     // ================================================================ V, and K's scales
     give_registers<kValueRegs>();
-    constexpr int kShares = D / 16;                 // lanes of a key: sixteen elements each
-    constexpr int kKeysPerIt = 128 / kShares;       // over the four warps
-    constexpr int kIts = kUnit / kKeysPerIt;        // a lane's keys of a unit
+    constexpr int kShares = D / 16;            // lanes of a key: sixteen elements each
+    constexpr int kKeysPerIt = 128 / kShares;  // over the four warps
     constexpr int kRowBytes = E2M1 ? D / 2 : D;
-    constexpr int kBlocks = D / 32;
+    constexpr int kPieceBytes = kRowBytes / kShares;
     const int dw = warp - 8;
     // Lanes 0-15 take the first 64 elements of their keys and, with 128, lanes
     // 16-31 the second: eight lanes of a store then lie in two rows of one
     // panel, which touches all banks.
     const int part = lane % 4 + (D == 128 ? lane / 16 * 4 : 0);
     const int r0 = dw * (32 / kShares) + (D == 128 ? lane % 16 / 4 : lane / 4);
-    const uint8_t* v_base = a.v_codes + part * (kRowBytes / kShares);
-    const uint8_t* k_base = a.k_codes + part * (kRowBytes / kShares);
-    const uint8_t* vs_base = a.v_scales + part / 2;
-    // A unit on its way.  What no row sees is read as whatever lies in its place
-    // (the table's first rows where there is none) and cleared later: choosing
-    // between a load's result and a constant here would wait for the load.
-    struct Unit {
-      Codes<E2M1> v[kIts], k[E2M1 ? kIts : 1];
-      int vs[kIts];   // scale bytes
-      uint32_t gone;  // bit g: 16-key group g is not there
-      int lo, hi;     // the keys to read
-    };
-    auto load = [&](const Place& c, Unit& w) {
-      const int row = group_row(c);
-      const int first_row = max(row, 0);
-      w.gone = __ballot_sync(0xffffffffu, lane < kUnit / 16 && row < 0);
-      w.lo = c.lo;
-      w.hi = c.hi;
-#pragma unroll
-      for (int i = 0; i < kIts; ++i) {
-        const int64_t at = __shfl_sync(0xffffffffu, first_row, (i * kKeysPerIt + r0) / 16) + r0 % 16;
-        w.v[i].load(v_base + at * kRowBytes);
-        w.vs[i] = __ldg(vs_base + at * kBlocks);
-        if (E2M1) w.k[E2M1 ? i : 0].load(k_base + at * kRowBytes);
-      }
-    };
     // a lane's two 16-byte pieces of a V row; kKeysPerIt is a multiple of 8, so
     // the swizzle is the same for all its keys
     const uint32_t v_at = (part / 4) * Sh::kVPanel + r0 * 128;
     const uint32_t v_at0 = v_at + (((part % 4 * 2) ^ (r0 & 7)) << 4), v_at1 = v_at + (((part % 4 * 2 + 1) ^ (r0 & 7)) << 4);
-    auto store = [&](uint8_t* stage, int i, const uint32_t (&o)[8]) {
-      *reinterpret_cast<uint4*>(stage + v_at0 + i * kKeysPerIt * 128) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(stage + v_at1 + i * kKeysPerIt * 128) = make_uint4(o[4], o[5], o[6], o[7]);
-    };
+    const uint32_t k_at = D == 128 ? r0 * 128 + ((part ^ (r0 & 7)) << 4) : r0 * 64 + ((part ^ ((r0 >> 1) & 3)) << 4);
     const int n = static_cast<int>(share.end - share.u);
-    int left = n > 0 ? static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), static_cast<int64_t>(n))) : 0;
-    Ring ring;
-    Place at{};
-    Unit now, then;
-    // In each turn one unit is looked up, the one before it loaded, and the one
-    // before that, whose loads have had a turn to arrive, converted.
+    Ring<kStages> ring;
+    Ring<kRawStages> raw;
 #pragma unroll 1
-    for (int i = -2; i < n; ++i) {
-      if (i >= 0) now = then;
-      if (i >= -1 && i + 1 < n) load(at, then);
-      if (i + 2 < n) {
-        if (i > -2) {
-          if (--left == 0) {
-            cur.next(a);
-            left = cur.t.units;
-          } else {
-            ++cur.place;
-          }
-        }
-        at = look_up(cur);
-      }
-      if (i >= 0) {
-        if (now.gone != 0 || now.lo > 0 || now.hi < kUnit) {
-#pragma unroll
-          for (int q = 0; q < kIts; ++q) {
-            const int r = q * kKeysPerIt + r0;
-            if (r >= now.lo && r < now.hi && !(now.gone >> (r / 16) & 1u)) continue;
-            now.v[q].clear();
-            if (E2M1) now.k[E2M1 ? q : 0].clear();
-          }
-        }
-        if (E2M1) {
-          bool ok = wait(sh, &sh.k_empty[ring.stage], ring.phase ^ 1u, a);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-#pragma unroll
-          for (int q = 0; q < kIts; ++q) {
-            const int r = q * kKeysPerIt + r0;
-            const uint32_t c0 = now.k[E2M1 ? q : 0].w[0], c1 = now.k[E2M1 ? q : 0].w[1];
-            const uint32_t to = D == 128 ? r * 128 + ((part ^ (r & 7)) << 4) : r * 64 + ((part ^ ((r >> 1) & 3)) << 4);
-            *reinterpret_cast<uint4*>(base + Sh::kK + ring.stage * Sh::kKStage + to) =
-                make_uint4(e4m3_of_e2m1x4(c0), e4m3_of_e2m1x4(c0 >> 16), e4m3_of_e2m1x4(c1), e4m3_of_e2m1x4(c1 >> 16));
-          }
-          fence_proxy_async_shared();
-          mbar_arrive(smem_u32(&sh.k_full[ring.stage]));
-        }
-        const uint32_t m = static_cast<uint32_t>(i) % kMetaRing;
-        bool ok = wait(sh, &sh.meta_full[m], (static_cast<uint32_t>(i) / kMetaRing) & 1u, a);
-        if (ok) ok = wait(sh, &sh.v_empty[ring.stage], ring.phase ^ 1u, a);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const UnitMeta meta = sh.meta[m];
-        uint8_t* v_stage = base + Sh::kV + ring.stage * Sh::kVStage;
-        if (__builtin_expect(meta.wide, 0)) {
-#pragma unroll
-          for (int q = 0; q < kIts; ++q) {
-            const uint32_t f = bf16_pow2x2_112(min(now.vs[q] - 127 - meta.v_exp, 15));
-            uint32_t o[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(bf16x2_of_f16x2(now.v[q].pair(e)), f);
-            store(v_stage, q, o);
-          }
-        } else {
-#pragma unroll
-          for (int q = 0; q < kIts; ++q) {
-            const uint32_t f = f16_pow2x2(min(now.vs[q] - 127 - meta.v_exp, 15));
-            uint32_t o[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = mul_f16x2(now.v[q].pair(e), f);
-            store(v_stage, q, o);
-          }
+    for (int i = 0; i < n; ++i) {
+      bool ok = wait(sh, &sh.raw_full[raw.stage], raw.phase, a);
+      if (E2M1 && ok) ok = wait(sh, &sh.k_empty[ring.stage], ring.phase ^ 1u, a);
+      if (ok) ok = wait(sh, &sh.v_empty[ring.stage], ring.phase ^ 1u, a);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const UnitMeta meta = sh.meta[static_cast<uint32_t>(i) % kMetaRing];
+      const uint8_t* codes = base + Sh::kRaw + raw.stage * Sh::kRawStage + r0 * kRowBytes + part * kPieceBytes;
+      const uint8_t* scales = reinterpret_cast<const uint8_t*>(&sh.v_scale[raw.stage][r0]) + part / 2;
+      uint8_t* v_to = base + Sh::kV + ring.stage * Sh::kVStage;
+      const bool cut = meta.lo > 0 || meta.hi < kUnit;
+      if (E2M1) {
+        const uint8_t* k_codes = codes + kUnit * kRowBytes;
+        uint8_t* k_to = base + Sh::kK + ring.stage * Sh::kKStage + k_at;
+#pragma unroll 1
+        for (int r = 0; r < kUnit; r += kKeysPerIt) {
+          const uint2 c = *reinterpret_cast<const uint2*>(k_codes + r * kRowBytes);
+          *reinterpret_cast<uint4*>(k_to + r * D) =
+              make_uint4(e4m3_of_e2m1x4(c.x), e4m3_of_e2m1x4(c.x >> 16), e4m3_of_e2m1x4(c.y), e4m3_of_e2m1x4(c.y >> 16));
         }
         fence_proxy_async_shared();
-        mbar_arrive(smem_u32(&sh.v_full[ring.stage]));
-        ring.next();
+        mbar_arrive(smem_u32(&sh.k_full[ring.stage]));
       }
+      if (__builtin_expect(meta.wide, 0)) {
+#pragma unroll 1
+        for (int r = 0; r < kUnit; r += kKeysPerIt) {
+          Codes<E2M1> v;
+          v.load(codes + r * kRowBytes);
+          if (cut && (r + r0 < meta.lo || r + r0 >= meta.hi)) v.clear();
+          const uint32_t f = bf16_pow2x2_112(min(scales[r * 4] - 127 - meta.v_exp, 15));
+          uint32_t o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(bf16x2_of_f16x2(v.pair(e)), f);
+          *reinterpret_cast<uint4*>(v_to + v_at0 + r * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(v_to + v_at1 + r * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      } else {
+#pragma unroll 2
+        for (int r = 0; r < kUnit; r += kKeysPerIt) {
+          Codes<E2M1> v;
+          v.load(codes + r * kRowBytes);
+          if (cut && (r + r0 < meta.lo || r + r0 >= meta.hi)) v.clear();
+          const uint32_t f = f16_pow2x2(min(scales[r * 4] - 127 - meta.v_exp, 15));
+          uint32_t o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = mul_f16x2(v.pair(e), f);
+          *reinterpret_cast<uint4*>(v_to + v_at0 + r * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(v_to + v_at1 + r * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      }
+      fence_proxy_async_shared();
+      mbar_arrive(smem_u32(&sh.v_full[ring.stage]));
+      mbar_arrive(smem_u32(&sh.raw_empty[raw.stage]));
+      ring.next();
+      raw.next();
     }
   } else {
     give_registers<kIssueRegs>();
@@ -763,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
                      v_lo + ((stage * Sh::kVStage + k * 2048u) >> 4), kDescHiSw128, idesc, !first || k != 0);
       };
       uint32_t unit = 0;
-      Ring kr, vr;  // the next stage to take
+      Ring<kStages> kr, vr;  // the next stage to take
       while (ok && u < share.end && cur.b < a.n_seqs) {
         const int take = static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), share.end - u));
         const uint32_t tiles = cur.s.n * a.group - cur.tile * kRows > 128 ? 2 : 1;
@@ -821,36 +785,99 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
       }
       __syncwarp();
     } else if (warp == 13) {
-      // ================================================================ scales, and K's codes
-      // Sixteen keys a TMA box, each by its own lane; a group that is not there
-      // is read past the table's end, which fills zeros.
-      constexpr int kWords = kUnit / 32, kBlocks = D / 32;
+      // ================================================================ codes
+      // Sixteen keys a TMA box, each by its own lane (K's from lane 0, V's from
+      // lane 16 on); a group that is not there is read past the table's end,
+      // which fills zeros.
       const int n = static_cast<int>(share.end - share.u);
       const int none = a.num_pages * a.n_kv_heads * a.page_size;
+      constexpr uint32_t kCodeBytes = E2M1 ? Sh::kRawStage / 2 : Sh::kRawStage;  // of K or V
+      constexpr uint32_t kGroupBytes = kCodeBytes / (kUnit / 16);
       int left = n > 0 ? static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), static_cast<int64_t>(n))) : 0;
-      Ring ring;
+      Ring<kStages> ring;
+      Ring<kRawStages> raw;
       bool ok = true;
       int issued = 0;
-      if (!E2M1 && lane == 0) prefetch_tensormap(&k_map);
+      if (lane < 2) prefetch_tensormap(lane == 0 ? &k_map : &v_map);
+      const int group = lane & 15;
+      Place at{};
+#pragma unroll 1
+      for (int i = -1; i < n; ++i) {
+        const int found = i >= 0 ? group_row(at) : -1;
+        const int row = found < 0 ? none : found;
+        if (i + 1 < n) {
+          if (i >= 0) {
+            if (--left == 0) {
+              cur.next(a);
+              left = cur.t.units;
+            } else {
+              ++cur.place;
+            }
+          }
+          at = look_up(cur, group);
+        }
+        if (i < 0) continue;
+        if (!E2M1) ok = wait(sh, &sh.k_empty[ring.stage], ring.phase ^ 1u, a);
+        if (ok) ok = wait(sh, &sh.raw_empty[raw.stage], raw.phase ^ 1u, a);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t k_bar = smem_u32(E2M1 ? &sh.raw_full[raw.stage] : &sh.k_full[ring.stage]);
+        const uint32_t v_bar = smem_u32(&sh.raw_full[raw.stage]);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(v_bar, E2M1 ? 2 * kCodeBytes : kCodeBytes);
+          if (!E2M1) mbar_arrive_expect_tx(k_bar, kCodeBytes);
+        }
+        __syncwarp();
+        if (group < kUnit / 16) {
+          const uint32_t v_to = smem_u32(base + Sh::kRaw + raw.stage * Sh::kRawStage) + group * kGroupBytes;
+          const uint32_t k_to = E2M1 ? v_to + kCodeBytes : smem_u32(base + Sh::kK + ring.stage * Sh::kKStage) + group * kGroupBytes;
+          if (lane < 16) tma_load_2d(k_to, &k_map, 0, row, k_bar);
+          else tma_load_2d(v_to, &v_map, 0, row, v_bar);
+        }
+        __syncwarp();
+        ++issued;
+        ring.next();
+        raw.next();
+      }
+      // the last fills have landed before the CTA exits, also where a wait of
+      // the others ran out
+      for (int i = issued > kRawStages ? issued - kRawStages : 0; i < issued; ++i)
+        mbar_wait(smem_u32(&sh.raw_full[i % kRawStages]), (i / kRawStages) & 1u, 100000000ull);
+      for (int i = issued > kStages ? issued - kStages : 0; i < issued && !E2M1; ++i)
+        mbar_wait(smem_u32(&sh.k_full[i % kStages]), (i / kStages) & 1u, 100000000ull);
+      __syncwarp();
+    } else if (warp == 14) {
+      // ================================================================ scales
+      constexpr int kWords = kUnit / 32, kBlocks = D / 32;
+      const int n = static_cast<int>(share.end - share.u);
+      int left = n > 0 ? static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), static_cast<int64_t>(n))) : 0;
+      Ring<kStages> ring;
+      Ring<kRawStages> raw;
       auto scale_word = [&](const uint8_t* p, int64_t row) -> uint32_t {
         if constexpr (kBlocks == 4) return __ldg(reinterpret_cast<const uint32_t*>(p) + row);
         else return __ldg(reinterpret_cast<const uint16_t*>(p) + row);
       };
       struct Unit {
         uint32_t ks[kWords], vs[kWords];  // keys 32 j + lane: a row's scale bytes
-        int row, lo, hi;                  // the lane's group's first cache row; the keys to read
+        uint32_t gone;                    // bit g: 16-key group g is not there
+        int lo, hi;
       };
       Place at{};
       Unit now, then;
-      // looked up, loaded and passed on a turn apart, as V's units are
+      // In each turn one unit is looked up, the one before it loaded, and the one
+      // before that, whose loads have had a turn to arrive, passed on.  What no
+      // row sees is read as whatever lies in its place (the table's first rows
+      // where there is none) and left out later: choosing between a load's
+      // result and a constant would wait for the load.
 #pragma unroll 1
       for (int i = -2; i < n; ++i) {
         if (i >= 0) now = then;
         if (i >= -1 && i + 1 < n) {
-          then.row = group_row(at);
+          const int row = group_row(at);
+          const int first_row = max(row, 0);
+          then.gone = __ballot_sync(0xffffffffu, lane < kUnit / 16 && row < 0);
           then.lo = at.lo;
           then.hi = at.hi;
-          const int first_row = max(then.row, 0);
 #pragma unroll
           for (int j = 0; j < kWords; ++j) {
             const int64_t to = __shfl_sync(0xffffffffu, first_row, 2 * j + lane / 16) + lane % 16;
@@ -867,22 +894,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
               ++cur.place;
             }
           }
-          at = look_up(cur);
+          at = look_up(cur, lane);
         }
         if (i < 0) continue;
-        ok = wait(sh, &sh.k_empty[ring.stage], ring.phase ^ 1u, a);
+        bool ok = wait(sh, &sh.k_empty[ring.stage], ring.phase ^ 1u, a);
+        if (ok) ok = wait(sh, &sh.raw_empty[raw.stage], raw.phase ^ 1u, a);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t bar = smem_u32(&sh.k_full[ring.stage]);
         *reinterpret_cast<uint4*>(&sh.k_scale[ring.stage][lane][0]) =
             make_uint4(now.ks[0], now.ks[1], now.ks[2], kWords == 4 ? now.ks[kWords - 1] : 0x7F7F7F7Fu);
+        fence_proxy_async_shared();
         // V's largest scale, and the smallest of a block that is not zero
-        const uint32_t gone = __ballot_sync(0xffffffffu, lane < kUnit / 16 && now.row < 0);
         uint32_t top = 0, low = 0xFFFFFFFFu;
 #pragma unroll
         for (int j = 0; j < kWords; ++j) {
           const int r = 32 * j + lane;
-          const uint32_t w = r >= now.lo && r < now.hi && !(gone >> (r / 16) & 1u) ? now.vs[j] : 0u;
+          const uint32_t w = r >= now.lo && r < now.hi && !(now.gone >> (r / 16) & 1u) ? now.vs[j] : 0u;
+          sh.v_scale[raw.stage][r] = w;
           top = __vmaxu4(top, w);
           low = __vminu4(low, w | __vcmpeq4(w, 0u));
         }
@@ -890,28 +918,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
         low = min(min(low & 0xFFu, (low >> 8) & 0xFFu), min((low >> 16) & 0xFFu, low >> 24));
         top = __reduce_max_sync(0xffffffffu, top);
         low = __reduce_min_sync(0xffffffffu, low);
-        const int v_exp = min(max(static_cast<int>(top) - 127, -100), 126);
-        const uint32_t m = static_cast<uint32_t>(i) % kMetaRing;
-        fence_proxy_async_shared();
-        __syncwarp();
         if (lane == 0) {
-          sh.meta[m].v_exp = v_exp;
-          sh.meta[m].wide = v_exp - (static_cast<int>(low) - 127) > 15;
-          mbar_arrive(smem_u32(&sh.meta_full[m]));
-          if (E2M1) mbar_arrive(bar);
-          else mbar_arrive_expect_tx(bar, Sh::kKStage);
+          UnitMeta meta;
+          meta.v_exp = min(max(static_cast<int>(top) - 127, -100), 126);
+          meta.wide = meta.v_exp - (static_cast<int>(low) - 127) > 15;
+          meta.lo = now.lo;
+          meta.hi = now.hi;
+          sh.meta[static_cast<uint32_t>(i) % kMetaRing] = meta;
         }
         __syncwarp();
-        if (!E2M1 && lane < kUnit / 16)
-          tma_load_2d(smem_u32(base + Sh::kK + ring.stage * Sh::kKStage + lane * 16 * D), &k_map, 0, now.row < 0 ? none : now.row, bar);
-        ++issued;
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sh.k_full[ring.stage]));
+          mbar_arrive(smem_u32(&sh.raw_full[raw.stage]));
+        }
+        __syncwarp();
         ring.next();
+        raw.next();
       }
-      // the last fills have landed before the CTA exits, also where a wait of
-      // the others ran out
-      for (int i = issued > kStages ? issued - kStages : 0; i < issued && !E2M1; ++i)
-        mbar_wait(smem_u32(&sh.k_full[i % kStages]), (i / kStages) & 1u, 100000000ull);
-      __syncwarp();
     }
     __syncwarp();
   }
@@ -952,19 +975,24 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
   }
-  CUtensorMap k_map{};
-  if (!E2M1) {
-    auto encode = encode_fn();
-    if (!encode) return cudaErrorNotSupported;
-    const cuuint64_t rows = static_cast<cuuint64_t>(a.num_pages) * a.n_kv_heads * a.page_size;
-    cuuint64_t dims[2] = {D, rows}, strides[1] = {D};
-    cuuint32_t box[2] = {D, 16}, es[2] = {1, 1};
-    if (encode(&k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.k_codes), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
-  }
-  k_attn_chunk<D, E2M1><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, kSmem, s>>>(a, k_map);
+  // K's E4M3 rows are an MMA operand as they are, swizzled on their way; the
+  // codes that pass through V's warps keep their order
+  auto encode = encode_fn();
+  if (!encode) return cudaErrorNotSupported;
+  CUtensorMap k_map, v_map;
+  const cuuint64_t row = E2M1 ? D / 2 : D;
+  cuuint64_t dims[2] = {row, static_cast<cuuint64_t>(a.num_pages) * a.n_kv_heads * a.page_size}, strides[1] = {row};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(row), 16}, es[2] = {1, 1};
+  const CUtensorMapSwizzle k_swizzle =
+      E2M1 ? CU_TENSOR_MAP_SWIZZLE_NONE : D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  if (encode(&k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.k_codes), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, k_swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+      encode(&v_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.v_codes), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  k_attn_chunk<D, E2M1><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, kSmem, s>>>(a, k_map, v_map);
   return cudaGetLastError();
 }
 
