@@ -33,7 +33,7 @@ int check_cache_pointers(const mx_kv_cache* c, const void* block_table, const vo
                          const void* ws, size_t ws_bytes) {
   if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales || !block_table || !kv_lens || !q_starts || !ws)
     return MX_ERR_INVALID_ARG;
-  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4) ||
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_scales, 16) ||
       !aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(q_starts, 4) || !aligned(ws, 256))
     return MX_ERR_ALIGNMENT;
   return ws_bytes < 256 ? MX_ERR_WORKSPACE : MX_OK;
