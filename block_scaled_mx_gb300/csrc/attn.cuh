@@ -5,8 +5,10 @@
 // a KV head's keys are read once for all its query heads.  The units of the
 // whole batch lie on one line (sequence, then KV head, then row tile, then
 // keys) and every CTA takes an equal stretch of it, found from the lengths on
-// the device: ragged batches stay balanced and the host needs no lengths.  A
-// stretch ends inside at most two segments (a segment is one row tile's keys);
+// the device: ragged batches stay balanced and the host needs no lengths.  In
+// front of each segment's units the line has kCost places that hold no work:
+// what a segment costs beside its keys (its queries, its output), in units, so
+// that a CTA with many short segments gets fewer keys.  A stretch ends inside at most two segments (a segment is one row tile's keys);
 // those leave their accumulator and softmax statistics in the workspace, and
 // the last CTA to arrive at a segment joins its parts, always in key order, so
 // results do not depend on which one that is.
@@ -72,16 +74,17 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnArgs& a, const AttnSeq& 
   return t;
 }
 
-// Units of one KV head of a sequence; kWarp: the lanes of a warp (all with the
-// same sequence) take the tiles in turn.
-template <int kRows, int kUnit, bool kWarp>
-__device__ __forceinline__ int attn_seq_units(const AttnArgs& a, const AttnSeq& s) {
+// Places on the line of one KV head of a sequence; kWarp: the lanes of a warp
+// (all with the same sequence) take the tiles in turn.
+template <int kRows, int kUnit, int kCost, bool kWarp>
+__device__ __forceinline__ int attn_seq_places(const AttnArgs& a, const AttnSeq& s) {
   int u = 0;
-  for (int t = kWarp ? threadIdx.x & 31 : 0; t < s.tiles; t += kWarp ? 32 : 1) u += attn_tile<kRows, kUnit>(a, s, t).units;
+  for (int t = kWarp ? threadIdx.x & 31 : 0; t < s.tiles; t += kWarp ? 32 : 1)
+    u += attn_tile<kRows, kUnit>(a, s, t).units + kCost;
   return kWarp ? __reduce_add_sync(0xffffffffu, u) : u;
 }
 
-// The CTA whose stretch holds unit u: the largest c with total * c / ctas <= u.
+// The CTA whose stretch holds place u: the largest c with total * c / ctas <= u.
 __device__ __forceinline__ int attn_cta_of(int64_t u, int64_t total, int ctas) {
   return static_cast<int>(((u + 1) * ctas - 1) / total);
 }
@@ -99,7 +102,7 @@ constexpr int kAttnScan = 128;  // sequences looked at together
 
 // Block-wide (kThreads threads); `units` holds kAttnScan words.  kWarp: a warp
 // counts a sequence (long ones have hundreds of tiles), else a thread.
-template <int kRows, int kUnit, int kThreads, bool kWarp>
+template <int kRows, int kUnit, int kCost, int kThreads, bool kWarp>
 __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int64_t* units) {
   const int tid = threadIdx.x, lane = tid & 31;
   auto count = [&](int b0, bool report) {
@@ -107,7 +110,7 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int64_t* unit
       int64_t u = 0;
       if (b0 + i < a.n_seqs) {
         const AttnSeq s = attn_seq<kRows>(a, b0 + i, report && blockIdx.x == 0);
-        u = static_cast<int64_t>(attn_seq_units<kRows, kUnit, kWarp>(a, s)) * a.n_kv_heads;
+        u = static_cast<int64_t>(attn_seq_places<kRows, kUnit, kCost, kWarp>(a, s)) * a.n_kv_heads;
       }
       if (!kWarp || lane == 0) units[i] = u;
     }
@@ -174,9 +177,10 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int64_t* unit
 }
 
 // Where a CTA is on the line: a segment (one row tile of one KV head of one
-// sequence) and the unit `place` of it.
-template <int kRows, int kUnit>
+// sequence) and the unit `place` of it (below zero: the places without work).
+template <int kRows, int kUnit, int kCost>
 struct AttnCursor {
+  int64_t u, end;  // on the line
   int b, head, tile, place;
   AttnSeq s;
   AttnTile t;
@@ -184,17 +188,20 @@ struct AttnCursor {
   // At the share's first unit; whole warps call it.
   template <bool kWarp>
   __device__ __forceinline__ void start(const AttnArgs& a, const AttnShare& share) {
+    u = share.u;
+    end = share.end;
     b = share.seq;
+    head = tile = place = 0;
+    if (u >= end) return;
     s = attn_seq<kRows>(a, b, false);
-    const int per_head = attn_seq_units<kRows, kUnit, kWarp>(a, s);
+    const int per_head = attn_seq_places<kRows, kUnit, kCost, kWarp>(a, s);
     head = static_cast<int>(share.in_seq / max(per_head, 1));
     place = static_cast<int>(share.in_seq - static_cast<int64_t>(head) * per_head);
-    tile = 0;
     if (kWarp) {
       const int lane = threadIdx.x & 31;
       for (; tile < s.tiles; tile += 32) {
-        const int u = tile + lane < s.tiles ? attn_tile<kRows, kUnit>(a, s, tile + lane).units : 0;
-        int incl = u;
+        const int n = tile + lane < s.tiles ? attn_tile<kRows, kUnit>(a, s, tile + lane).units + kCost : 0;
+        int incl = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const int o = __shfl_up_sync(0xffffffffu, incl, d);
@@ -203,7 +210,7 @@ struct AttnCursor {
         const unsigned hit = __ballot_sync(0xffffffffu, place < incl);
         if (hit) {
           const int src = __ffs(hit) - 1;
-          place -= __shfl_sync(0xffffffffu, incl - u, src);
+          place -= __shfl_sync(0xffffffffu, incl - n, src);
           tile += src;
           break;
         }
@@ -212,32 +219,52 @@ struct AttnCursor {
       t = attn_tile<kRows, kUnit>(a, s, tile);
     } else {
       t = attn_tile<kRows, kUnit>(a, s, 0);
-      while (place >= t.units && tile + 1 < s.tiles) {
-        place -= t.units;
+      while (place >= t.units + kCost && tile + 1 < s.tiles) {
+        place -= t.units + kCost;
         t = attn_tile<kRows, kUnit>(a, s, ++tile);
       }
     }
+    place -= kCost;
   }
 
-  // To the next segment's first unit (there is one: the caller's stretch goes on).
-  __device__ __forceinline__ void next(const AttnArgs& a) {
-    place = 0;
-    if (++tile == s.tiles) {
-      tile = 0;
-      if (++head == a.n_kv_heads) {
-        head = 0;
-        do {
-          if (++b >= a.n_seqs) return;
-          s = attn_seq<kRows>(a, b, false);
-        } while (s.tiles == 0);
+  // Past what has no work: to a unit of the stretch, or false where it has no
+  // more.
+  __device__ __forceinline__ bool settle(const AttnArgs& a) {
+    while (u < end) {
+      if (place < 0) {
+        const int64_t d = min(static_cast<int64_t>(-place), end - u);
+        u += d;
+        place += static_cast<int>(d);
+        continue;
       }
+      if (place < t.units) return true;
+      place = -kCost;
+      if (++tile == s.tiles) {
+        tile = 0;
+        if (++head == a.n_kv_heads) {
+          head = 0;
+          do {
+            if (++b >= a.n_seqs) return false;
+            s = attn_seq<kRows>(a, b, false);
+          } while (s.tiles == 0);
+        }
+      }
+      t = attn_tile<kRows, kUnit>(a, s, tile);
     }
-    t = attn_tile<kRows, kUnit>(a, s, tile);
+    return false;
+  }
+  // Units of the segment from `place` on that lie in the stretch, and past them.
+  __device__ __forceinline__ int take() const {
+    return static_cast<int>(min(static_cast<int64_t>(t.units - place), end - u));
+  }
+  __device__ __forceinline__ void pass(int n) {
+    u += n;
+    place += n;
   }
 };
 
-// How a segment of `units` units from `seg` on is shared out: its parts lie
-// with CTAs first .. first + parts - 1.
+// How a segment of `units` units, its first at place `seg` of the line, is
+// shared out: its parts lie with CTAs first .. first + parts - 1.
 struct AttnParts {
   int first, parts;
 };

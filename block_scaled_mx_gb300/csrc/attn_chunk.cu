@@ -51,10 +51,27 @@ namespace {
 constexpr int kRows = 256;
 constexpr int kThreads = 512;
 constexpr int kMaxCtas = 152;
-constexpr int kMinUnits = 2;
+constexpr int kMinUnits = 12;
+constexpr int kCost = 8;      // a segment's queries and output take as long as that many units
 constexpr int kStages = 4;     // of K and of V
 constexpr int kRawStages = 4;  // of codes on their way to V
 constexpr int kMetaRing = 8;  // more units than can be between their scales' arrival and their softmax
+// AttnCursor::settle, out of line, and the units of a whole stretch.
+template <class Cursor>
+__device__ __noinline__ bool settle(Cursor& c, const AttnArgs& a) {
+  return c.settle(a);
+}
+template <class Cursor>
+__device__ __forceinline__ int units_of(Cursor& c, const AttnArgs& a) {
+  int n = 0;
+  while (settle(c, a)) {
+    const int k = c.take();
+    n += k;
+    c.pass(k);
+  }
+  return n;
+}
+
 // What the softmax and the MMA issuer need to know of a unit.
 struct UnitMeta {
   int v_exp;  // exponent of its largest V scale
@@ -302,7 +319,7 @@ __device__ __noinline__ void load_queries(const AttnArgs& a, Shared& sh, uint8_t
   const uint32_t lanes = static_cast<uint32_t>(threadIdx.x & 96) << 16;
   constexpr int kPieces = D / 8;
   uint8_t* hi_base = base + Sh::kQ + 2 * x * Sh::kQTile;
-#pragma unroll 2
+#pragma unroll 8
   for (int i = threadIdx.x & 127; i < 128 * kPieces; i += 128) {
     const int r = i / kPieces, p = i - r * kPieces;
     const int R = row0 + r;
@@ -467,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
                                                               const __grid_constant__ CUtensorMap v_map) {
   using Sh = Shape<D>;
   constexpr int kUnit = Sh::kUnit;
-  using Cursor = AttnCursor<kRows, kUnit>;
+  using Cursor = AttnCursor<kRows, kUnit, kCost>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -501,14 +518,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
     tmem_alloc(smem_u32(&sh.tmem), kTmemColumns);
     tmem_relinquish();
   }
-  const AttnShare share = attn_share<kRows, kUnit, kThreads, true>(a, sh.units);
+  const AttnShare share = attn_share<kRows, kUnit, kCost, kThreads, true>(a, sh.units);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   constexpr uint32_t tmem = 0;  // all of tensor memory is this CTA's
-  int64_t u = share.u;
   Cursor cur;
-  if (u < share.end) cur.template start<true>(a, share);
+  cur.template start<true>(a, share);
   if (warp < 8) {
     // ================================================================ softmax
     const int x = warp >> 2;                       // tile A or B
@@ -525,17 +541,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
       const int rows = c.s.n * a.group, row0 = c.tile * kRows + 128 * x;
       if (row0 < rows) load_queries<D>(a, sh, base, x, c.s.q0, c.head, row0, rows);
     };
-    if (u < share.end) queries_of(cur);
-    while (u < share.end && cur.b < a.n_seqs) {
-      const int take = static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), share.end - u));
+    bool more = settle(cur, a);
+    if (more) queries_of(cur);
+    while (more) {
+      const int take = cur.take();
       const int rows = cur.s.n * a.group;
       const int row0 = cur.tile * kRows + 128 * x;
       Cursor ahead;
       auto to_next = [&]() {  // and its queries
         ahead = cur;
-        if (u + take >= share.end) return;
-        ahead.next(a);
-        if (ahead.b < a.n_seqs) queries_of(ahead);
+        ahead.pass(take);
+        more = settle(ahead, a);
+        if (more) queries_of(ahead);
       };
       if (row0 < rows) {
         const int R = row0 + row;
@@ -636,13 +653,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
         const int64_t oh = static_cast<int64_t>(cur.s.q0 + tok) * (a.n_kv_heads * a.group) + cur.head * a.group + (R - tok * a.group);
         const bool whole = take == cur.t.units;
         AttnParts parts{};
-        if (!whole) parts = attn_parts(share, u - cur.place, cur.t.units);
+        if (!whole) parts = attn_parts(share, cur.u - cur.place, cur.t.units);
         write_rows<D>(a, sh, o_col, x, whole ? -1 : attn_slot(blockIdx.x, cur.place == 0), parts, oh, ok, warp_valid, valid, m, l);
       } else {
         to_next();  // this segment has no tile B
       }
       unit += take;
-      u += take;
       cur = ahead;
     }
   } else if (warp & 2) {
@@ -663,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
     const uint32_t v_at = (part / 4) * Sh::kVPanel + r0 * 128;
     const uint32_t v_at0 = v_at + (((part % 4 * 2) ^ (r0 & 7)) << 4), v_at1 = v_at + (((part % 4 * 2 + 1) ^ (r0 & 7)) << 4);
     const uint32_t k_at = D == 128 ? r0 * 128 + ((part ^ (r0 & 7)) << 4) : r0 * 64 + ((part ^ ((r0 >> 1) & 3)) << 4);
-    const int n = static_cast<int>(share.end - share.u);
+    const int n = units_of(cur, a);
     Ring<kStages> ring;
     Ring<kRawStages> raw;
 #pragma unroll 1
@@ -730,8 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
       uint32_t unit = 0;
       bool ok = true;
       Ring<kStages> kr, vr;  // the next stage to take
-      while (ok && u < share.end && cur.b < a.n_seqs) {
-        const int take = static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), share.end - u));
+      while (ok && settle(cur, a)) {
+        const int take = cur.take();
         const bool active = cur.s.n * a.group - cur.tile * kRows > 128 * static_cast<int>(x);
         if (active) {
           ok = wait(sh, &sh.q_full[x], q_phase, a);
@@ -787,8 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
             ++unit;
           }
         }
-        u += take;
-        if (ok && u < share.end) cur.next(a);
+        cur.pass(take);
       }
       // every MMA issued has completed before tensor memory is released
       mma_commit(smem_u32(&sh.drain[x]));
@@ -813,8 +828,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
       Ring<kRawStages> raw;
       int issued = 0;
       bool ok = true;
-      while (ok && u < share.end && cur.b < a.n_seqs) {
-        const int take = static_cast<int>(min(static_cast<int64_t>(cur.t.units - cur.place), share.end - u));
+      while (ok && settle(cur, a)) {
+        const int take = cur.take();
         const int32_t* table = a.block_table + static_cast<int64_t>(cur.b) * a.max_pages;
         const int first = cur.t.first + cur.place * kUnit;
         int entry = (first + 16 * group) / a.page_size, off = first + 16 * group - entry * a.page_size;
@@ -864,8 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
           lo -= kUnit, hi -= kUnit;
           for (off += kUnit; off >= a.page_size; off -= a.page_size) ++entry;
         }
-        u += take;
-        if (ok && u < share.end) cur.next(a);
+        cur.pass(take);
       }
       // the last fills have landed before the CTA exits, also where a wait of
       // the others ran out
@@ -877,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
     } else if (warp == 13) {
       // ================================================================ scales
       constexpr int kWords = kUnit / 32, kBlocks = D / 32;
-      const int n = static_cast<int>(share.end - share.u);
+      const int n = units_of(cur, a);
       Ring<kStages> ring;
       Ring<kRawStages> raw;
 #pragma unroll 1

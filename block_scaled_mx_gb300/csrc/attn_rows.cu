@@ -37,6 +37,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 3;
 constexpr int kMinUnits = 4;
+constexpr int kCost = 0;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -106,17 +107,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
   __shared__ int64_t s_units[kAttnScan];
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const AttnShare share = attn_share<kRows, kUnit, kThreads, false>(a, s_units);
+  const AttnShare share = attn_share<kRows, kUnit, kCost, kThreads, false>(a, s_units);
   const int n_heads = a.n_kv_heads * a.group;
-  int64_t u = share.u;
-  AttnCursor<kRows, kUnit> cur;
-  if (u < share.end) cur.template start<false>(a, share);
+  AttnCursor<kRows, kUnit, kCost> cur;
+  cur.template start<false>(a, share);
 
-  while (u < share.end && cur.b < a.n_seqs) {
+  while (cur.settle(a)) {
     const AttnSeq& s = cur.s;
     const AttnTile& t = cur.t;
     const int head = cur.head, tile = cur.tile, place = cur.place;
-    const int take = static_cast<int>(min(static_cast<int64_t>(t.units - place), share.end - u));
+    const int take = cur.take();
     const int rows = s.n * a.group;
     const int base = s.kv - s.n;
 
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
     __syncthreads();
 
     const bool whole = take == t.units;
-    const AttnParts p = attn_parts(share, u - place, t.units);
+    const AttnParts p = attn_parts(share, cur.u - place, t.units);
     const int slot = attn_slot(blockIdx.x, place == 0);
 
     // writes a finished row: four elements a lane
@@ -449,8 +449,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
       }
     }
     __syncthreads();  // the warps' parts are read before the next segment overwrites them
-    u += take;
-    if (u < share.end) cur.next(a);
+    cur.pass(take);
   }
 }
 
