@@ -51,8 +51,8 @@ namespace {
 constexpr int kRows = 256;
 constexpr int kThreads = 512;
 constexpr int kMaxCtas = 152;
-constexpr int kMinUnits = 12;
-constexpr int kCost = 8;      // a segment's queries and output take as long as that many units
+constexpr int kMinUnits = 20;
+constexpr int kCost = 16;      // a segment's queries and output take as long as that many units
 constexpr int kStages = 4;     // of K and of V
 constexpr int kRawStages = 4;  // of codes on their way to V
 constexpr int kMetaRing = 8;  // more units than can be between their scales' arrival and their softmax
@@ -317,44 +317,57 @@ __device__ __noinline__ void load_queries(const AttnArgs& a, Shared& sh, uint8_t
   constexpr uint32_t tmem = 0;
   const int lane = threadIdx.x & 31;
   const uint32_t lanes = static_cast<uint32_t>(threadIdx.x & 96) << 16;
-  constexpr int kPieces = D / 8;
+  constexpr int kPieces = D / 8;     // sixteen bytes of bf16
+  constexpr int kStep = 128 / kPieces;  // rows of the 128 threads
+  constexpr int kAhead = 4;          // loads in flight while as many are converted
+  const int p = threadIdx.x % kPieces, r0 = (threadIdx.x & 127) / kPieces;
   uint8_t* hi_base = base + Sh::kQ + 2 * x * Sh::kQTile;
-#pragma unroll 8
-  for (int i = threadIdx.x & 127; i < 128 * kPieces; i += 128) {
-    const int r = i / kPieces, p = i - r * kPieces;
+  auto load = [&](int r) {
     const int R = row0 + r;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (R < rows) {
-      const int tok = R / a.group;
-      v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                               static_cast<int64_t>(q0 + tok) * a.q_stride +
-                                               static_cast<int64_t>(head * a.group + (R - tok * a.group)) * D) + p);
-    }
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t amax = 0;
+    if (r >= 128 || R >= rows) return make_uint4(0u, 0u, 0u, 0u);
+    const int tok = R / a.group;
+    return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                static_cast<int64_t>(q0 + tok) * a.q_stride +
+                                                static_cast<int64_t>(head * a.group + (R - tok * a.group)) * D) + p);
+  };
+  uint4 now[kAhead], then[kAhead];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // the block's largest element lands in [2^7, 2^8): hi's rounding error
-    // is then at most 2^3 and 2^5 times it stays below E4M3's 448
-    const int s = max(static_cast<int>(amax >> 7) - 127 - 7, -122);
-    const float down = pow2_neg(s);
-    uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+  for (int n = 0; n < kAhead; ++n) then[n] = load(r0 + n * kStep);
+#pragma unroll 1
+  for (int rr = r0; rr < 128; rr += kAhead * kStep) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float x0 = __uint_as_float(w[k] << 16) * down, x1 = __uint_as_float(w[k] & 0xFFFF0000u) * down;
-      const uint32_t h = enc_e4m3x2(x0, x1);
-      const uint32_t back = f16x2_of_e4m3x2(h);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
-      hi[k >> 1] |= h << ((k & 1) * 16);
-      lo[k >> 1] |= enc_e4m3x2((x0 - f.x) * 32.0f, (x1 - f.y) * 32.0f) << ((k & 1) * 16);
+    for (int n = 0; n < kAhead; ++n) now[n] = then[n];
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) then[n] = load(rr + (kAhead + n) * kStep);
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      const int r = rr + n * kStep;
+      const uint32_t w[4] = {now[n].x, now[n].y, now[n].z, now[n].w};
+      uint32_t amax = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // the block's largest element lands in [2^7, 2^8): hi's rounding error
+      // is then at most 2^3 and 2^5 times it stays below E4M3's 448
+      const int s = max(static_cast<int>(amax >> 7) - 127 - 7, -122);
+      const float down = pow2_neg(s);
+      uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x0 = __uint_as_float(w[k] << 16) * down, x1 = __uint_as_float(w[k] & 0xFFFF0000u) * down;
+        const uint32_t h = enc_e4m3x2(x0, x1);
+        const uint32_t back = f16x2_of_e4m3x2(h);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+        hi[k >> 1] |= h << ((k & 1) * 16);
+        lo[k >> 1] |= enc_e4m3x2((x0 - f.x) * 32.0f, (x1 - f.y) * 32.0f) << ((k & 1) * 16);
+      }
+      const uint32_t at = D == 128 ? r * 128 + (((p >> 1) ^ (r & 7)) << 4) + (p & 1) * 8
+                                   : r * 64 + (((p >> 1) ^ ((r >> 1) & 3)) << 4) + (p & 1) * 8;
+      *reinterpret_cast<uint2*>(hi_base + at) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(hi_base + Sh::kQTile + at) = make_uint2(lo[0], lo[1]);
+      if ((p & 3) == 0) reinterpret_cast<uint8_t*>(&sh.q_scale[x][r])[p >> 2] = static_cast<uint8_t>(s + 127);
     }
-    const uint32_t at = D == 128 ? r * 128 + (((p >> 1) ^ (r & 7)) << 4) + (p & 1) * 8
-                                 : r * 64 + (((p >> 1) ^ ((r >> 1) & 3)) << 4) + (p & 1) * 8;
-    *reinterpret_cast<uint2*>(hi_base + at) = make_uint2(hi[0], hi[1]);
-    *reinterpret_cast<uint2*>(hi_base + Sh::kQTile + at) = make_uint2(lo[0], lo[1]);
-    if ((p & 3) == 0) reinterpret_cast<uint8_t*>(&sh.q_scale[x][r])[p >> 2] = static_cast<uint8_t>(s + 127);
   }
   fence_proxy_async_shared();
   tile_barrier(x);
