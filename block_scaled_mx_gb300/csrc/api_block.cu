@@ -207,6 +207,7 @@ int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride
   a.arrived = reinterpret_cast<unsigned*>(w + kArrivedOffset);
   a.part_ml = reinterpret_cast<float2*>(w + kArrivedOffset + al256(kArrivedBytes));
   a.wait_limit_ns = wait_limit_ns();
+  a.box_keys = a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   a.rows_above = 0;
   a.rows_upto = INT_MAX;

@@ -16,8 +16,12 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace mxk {
 
@@ -263,6 +267,50 @@ struct AttnCursor {
   }
 };
 
+// Where a unit's keys lie in the cache, for the warp that fetches them: 16-key
+// groups, group = lane % (kUnit / 16), in boxes of a.box_keys keys.
+template <int kUnit>
+struct AttnWalk {
+  static constexpr int kGroups = kUnit / 16;
+  const int32_t* table;
+  int entry, off;     // the group's first key: entry of the table, place in the page
+  int lo, hi;         // the keys to read, counted from the unit's first
+  int window, pages;  // 32 entries of the table from `window` on, one a lane
+
+  template <class Cursor>
+  __device__ __forceinline__ void start(const AttnArgs& a, const Cursor& c, int group) {
+    table = a.block_table + static_cast<int64_t>(c.b) * a.max_pages;
+    const int first = c.t.first + c.place * kUnit;
+    entry = (first + 16 * group) / a.page_size;
+    off = first + 16 * group - entry * a.page_size;
+    lo = c.t.lo - first;
+    hi = c.t.hi - first;
+    window = -64;
+    pages = 0;
+  }
+  // The group's box: its first cache row, or -1 where it has no page or no key
+  // to read; `here`: the groups (a bit each) that are there, `bad`: those whose
+  // page is not one, which is reported.
+  __device__ __forceinline__ int box(const AttnArgs& a, int head, int group, uint32_t& here, uint32_t& bad) {
+    if (__any_sync(0xffffffffu, entry - window >= 32)) {
+      window = __shfl_sync(0xffffffffu, entry, 0);
+      pages = __ldg(table + min(window + static_cast<int>(threadIdx.x & 31), a.max_pages - 1));
+    }
+    const int page = __shfl_sync(0xffffffffu, pages, entry - window);
+    const bool seen = 16 * group < hi && 16 * group + 16 > lo;
+    const bool there = seen && page >= 0 && page < a.num_pages;
+    if (seen && !there) set_status(a.status, MX_ERR_DEVICE_ARG);
+    here = __ballot_sync(0xffffffffu, there) & ((1u << kGroups) - 1);
+    bad = __ballot_sync(0xffffffffu, seen && !there) & ((1u << kGroups) - 1);
+    const bool some = (here >> group & ((1u << (a.box_keys / 16)) - 1)) != 0;
+    return some ? (page * a.n_kv_heads + head) * a.page_size + off : -1;
+  }
+  __device__ __forceinline__ void step(const AttnArgs& a) {
+    lo -= kUnit, hi -= kUnit;
+    for (off += kUnit; off >= a.page_size; off -= a.page_size) ++entry;
+  }
+};
+
 // How a segment of `units` units, its first at place `seg` of the line, is
 // shared out: its parts lie with CTAs first .. first + parts - 1.
 struct AttnParts {
@@ -278,10 +326,77 @@ __device__ __forceinline__ AttnParts attn_parts(const AttnShare& sh, int64_t seg
 // that continue one lie apart (a CTA has at most one of each that is not whole).
 __device__ __forceinline__ int attn_slot(int cta, bool begins) { return 2 * cta + (begins ? 1 : 0); }
 
+// A wait for an mbarrier's phase.  One that runs out sets the status word and
+// makes every later wait of the CTA (`failed` in its shared memory) give up at
+// once.
+__device__ __noinline__ inline bool attn_wait_long(volatile int* failed, uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                                   int* status) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if (n & 15u) continue;
+    if (*failed) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      *failed = 1;
+      set_status(status, MX_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool attn_wait(volatile int* failed, uint64_t* bar, uint32_t parity, const AttnArgs& a) {
+  const uint32_t b = smem_u32(bar);
+  if (__builtin_expect(mbar_try_wait(b, parity), 1)) return true;
+  return attn_wait_long(failed, b, parity, a.wait_limit_ns, a.status);
+}
+
+// A stage of a ring and the parity of its current round.
+template <int kN>
+struct Ring {
+  uint32_t stage = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == kN) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// One arrival for a warp's lanes, behind whatever each of them did before.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(bar));
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// Tensor map of a code table, a.box_keys rows a box, swizzled so that 16-byte
+// pieces of neighbouring rows lie in different banks (or not at all).
+inline cudaError_t attn_code_map(CUtensorMap* map, const AttnArgs& a, const uint8_t* codes, int row_bytes, bool swizzle) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  if (!encode) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return cudaErrorNotSupported;
+    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(a.num_pages) * a.n_kv_heads * a.page_size};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(row_bytes), static_cast<cuuint32_t>(a.box_keys)}, es[2] = {1, 1};
+  const CUtensorMapSwizzle sw = !swizzle           ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                : row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : row_bytes == 64  ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                   : CU_TENSOR_MAP_SWIZZLE_32B;
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
 }
 
 }  // namespace mxk

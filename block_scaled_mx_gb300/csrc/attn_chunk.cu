@@ -34,8 +34,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <atomic>
 #include <climits>
 #include <cstdint>
@@ -76,12 +74,14 @@ __device__ __forceinline__ int units_of(Cursor& c, const AttnArgs& a) {
 struct UnitMeta {
   int v_exp;  // exponent of its largest V scale
   int wide;   // V and P in bf16
+  uint32_t bad;  // UnitKeys::bad
 };
 // A unit's keys to read, counted from its first, and its 16-key groups that are
 // not there (a bit each).
 struct UnitKeys {
   int lo, hi;
   uint32_t gone;
+  uint32_t bad;  // of those, the ones that rows would see but for their page
 };
 
 template <int D>
@@ -125,48 +125,12 @@ struct Shared {
   int64_t units[kAttnScan];
 };
 
-// A stage of a ring and the parity of its current round.
-template <int kN>
-struct Ring {
-  uint32_t stage = 0, phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++stage == kN) {
-      stage = 0;
-      phase ^= 1u;
-    }
-  }
-};
-
-// A wait that runs out sets the status word and makes every later wait of the
-// CTA give up at once.
-//
 // Functions that are not inlined here and below: the roles' unit loops have to
 // fit the instruction caches together (measured: an SM's four schedulers run
 // code of up to 8 KB each at full speed, and at a quarter of it past 32 KB), so
 // what a unit seldom needs lies outside of them.
-__device__ __noinline__ bool wait_long(Shared& sh, uint32_t bar, uint32_t parity, uint64_t limit_ns, int* status) {
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
-    if (n & 15u) continue;
-    if (sh.failed) return false;
-    if (globaltimer_ns() - t0 > limit_ns) {
-      sh.failed = 1;
-      set_status(status, MX_ERR_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
 __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity, const AttnArgs& a) {
-  const uint32_t b = smem_u32(bar);
-  if (__builtin_expect(mbar_try_wait(b, parity), 1)) return true;
-  return wait_long(sh, b, parity, a.wait_limit_ns, a.status);
-}
-
-// One arrival for a warp's lanes, behind whatever each of them did before.
-__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(bar));
+  return attn_wait(&sh.failed, bar, parity, a);
 }
 
 // The 128 threads of a tile's softmax meet.
@@ -384,9 +348,10 @@ __device__ __noinline__ void load_queries(const AttnArgs& a, Shared& sh, uint8_t
   warp_arrive(&sh.q_full[x]);
 }
 
-// S columns outside [lo, hi) to -inf, of a unit at the edge of what rows see.
+// S columns outside [lo, hi), and those of the 16-column groups in `bad`, to
+// -inf, in a unit at the edge of what rows see.
 template <int kColumns>
-__device__ __noinline__ void mask_scores(uint32_t s_col, int lo, int hi) {
+__device__ __noinline__ void mask_scores(uint32_t s_col, int lo, int hi, uint32_t bad) {
 #pragma unroll 1
   for (int c = 0; c < kColumns; c += 16) {
     uint32_t v[16];
@@ -394,7 +359,7 @@ __device__ __noinline__ void mask_scores(uint32_t s_col, int lo, int hi) {
     tmem_ld_wait();
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (c + i >= hi || c + i < lo) v[i] = 0xFF800000u;
+      if (c + i >= hi || c + i < lo || (bad >> (c / 16) & 1u)) v[i] = 0xFF800000u;
     tmem_st_32x32b_x16(s_col + c, v);
   }
   tmem_st_wait();
@@ -590,7 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
           uint32_t v[kUnit];
           __syncwarp();
           if (work) {
-            if (__builtin_expect(key0 + kUnit > all_hi || key0 < all_lo, 0)) mask_scores<kUnit>(s_col, lo - key0, hi - key0);
+            if (__builtin_expect(key0 + kUnit > all_hi || key0 < all_lo || meta.bad != 0, 0))
+              mask_scores<kUnit>(s_col, lo - key0, hi - key0, meta.bad);
             tmem_load<kUnit>(s_col, v);
             tmem_ld_wait();
           }
@@ -834,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
       constexpr uint32_t kCodeBytes = kUnit * (E2M1 ? D / 2 : D);  // of K or V
       const int group = lane % kGroups, kind = lane / kGroups;  // of 16 keys
       const bool leads = 16 * group % a.box_keys == 0;          // a box
-      const uint32_t box_mask = (1u << (a.box_keys / 16)) - 1;
+      AttnWalk<kUnit> walk;
       const int none = a.num_pages * a.n_kv_heads * a.page_size;
       if (lane < 2) prefetch_tensormap(lane == 0 ? &k_map : &v_map);
       Ring<kStages> ring;
@@ -843,27 +809,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
       bool ok = true;
       while (ok && settle(cur, a)) {
         const int take = cur.take();
-        const int32_t* table = a.block_table + static_cast<int64_t>(cur.b) * a.max_pages;
-        const int first = cur.t.first + cur.place * kUnit;
-        int entry = (first + 16 * group) / a.page_size, off = first + 16 * group - entry * a.page_size;
-        int lo = cur.t.lo - first, hi = cur.t.hi - first;
-        // 32 entries of the table from `window` on, one a lane
-        int window = INT_MIN / 2, pages = 0;
+        walk.start(a, cur, group);
 #pragma unroll 1
         for (int j = 0; j < take; ++j) {
-          if (__any_sync(0xffffffffu, entry - window >= 32)) {
-            window = __shfl_sync(0xffffffffu, entry, 0);
-            pages = __ldg(table + min(window + lane, a.max_pages - 1));
-          }
-          const int page = __shfl_sync(0xffffffffu, pages, entry - window);
-          const bool seen = 16 * group < hi && 16 * group + 16 > lo;
-          const bool there = seen && page >= 0 && page < a.num_pages;
-          if (seen && !there) set_status(a.status, MX_ERR_DEVICE_ARG);
-          // 16-key groups that are there, and whether one of the lane's box is
-          const uint32_t here = __ballot_sync(0xffffffffu, there) & ((1u << kGroups) - 1);
-          const bool some = (here >> group & box_mask) != 0;
-          const int row = some ? (page * a.n_kv_heads + cur.head) * a.page_size + off : none;
-          const uint32_t boxes = __ballot_sync(0xffffffffu, leads && some) & ((1u << kGroups) - 1);
+          uint32_t here, bad;
+          const int row = walk.box(a, cur.head, group, here, bad);
+          const uint32_t boxes = __ballot_sync(0xffffffffu, leads && row >= 0) & ((1u << kGroups) - 1);
           if (!E2M1) ok = wait(sh, &sh.k_empty[ring.stage], ring.phase ^ 1u, a);
           if (ok) ok = wait(sh, &sh.raw_empty[raw.stage], raw.phase ^ 1u, a);
           ok = __all_sync(0xffffffffu, ok);
@@ -871,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
           const uint32_t raw_bar = smem_u32(&sh.raw_full[raw.stage]);
           const uint32_t k_bar = E2M1 ? raw_bar : smem_u32(&sh.k_full[ring.stage]);
           if (lane == 0) {
-            sh.keys[raw.stage] = UnitKeys{lo, hi, here ^ ((1u << kGroups) - 1)};
+            sh.keys[raw.stage] = UnitKeys{walk.lo, walk.hi, here ^ ((1u << kGroups) - 1), bad};
             mbar_arrive_expect_tx(raw_bar, (E2M1 ? 2 : 1) * kCodeBytes + 2 * __popc(boxes) * (a.box_keys * kBlocks));
             if (!E2M1) mbar_arrive_expect_tx(k_bar, kCodeBytes);
           }
@@ -879,9 +830,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
           const uint32_t to = smem_u32(base + Sh::kRaw + raw.stage * Sh::kRawStage);
           if (leads && kind < 2) {
             const uint32_t k_to = E2M1 ? to + kCodeBytes : smem_u32(base + Sh::kK + ring.stage * Sh::kKStage);
-            tma_load_2d((kind == 0 ? k_to : to) + group * (kCodeBytes / kGroups), kind == 0 ? &k_map : &v_map, 0, row,
+            tma_load_2d((kind == 0 ? k_to : to) + group * (kCodeBytes / kGroups), kind == 0 ? &k_map : &v_map, 0, row < 0 ? none : row,
                         kind == 0 ? k_bar : raw_bar);
-          } else if (leads && kind < 4 && some) {
+          } else if (leads && kind < 4 && row >= 0) {
             bulk_load(to + Sh::kRawScales + (kind - 2) * Sh::kScaleBytes + group * 16 * kBlocks,
                       (kind == 2 ? a.k_scales : a.v_scales) + static_cast<int64_t>(row) * kBlocks, a.box_keys * kBlocks, raw_bar);
           }
@@ -889,8 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
           ++issued;
           ring.next();
           raw.next();
-          lo -= kUnit, hi -= kUnit;
-          for (off += kUnit; off >= a.page_size; off -= a.page_size) ++entry;
+          walk.step(a);
         }
         cur.pass(take);
       }
@@ -942,6 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
         if (lane == 0) {
           UnitMeta meta;
           meta.v_exp = min(max(static_cast<int>(top) - 127, -100), 126);
+          meta.bad = keys.bad;
           meta.wide = meta.v_exp - (static_cast<int>(low) - 127) > 15;
           sh.meta[static_cast<uint32_t>(i) % kMetaRing] = meta;
         }
@@ -963,18 +914,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
   if (warp == 8) tmem_dealloc(sh.tmem, kTmemColumns);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
 template <int D, bool E2M1>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   constexpr int kSmem = Shape<D>::kBytes + 1024;
@@ -991,21 +930,11 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   }
   // K's E4M3 rows are an MMA operand as they are, swizzled on their way; the
   // codes that pass through V's warps keep their order
-  auto encode = encode_fn();
-  if (!encode) return cudaErrorNotSupported;
   CUtensorMap k_map, v_map;
-  const cuuint64_t row = E2M1 ? D / 2 : D;
-  cuuint64_t dims[2] = {row, static_cast<cuuint64_t>(a.num_pages) * a.n_kv_heads * a.page_size}, strides[1] = {row};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(row), static_cast<cuuint32_t>(a.box_keys)}, es[2] = {1, 1};
-  const CUtensorMapSwizzle k_swizzle =
-      E2M1 ? CU_TENSOR_MAP_SWIZZLE_NONE : D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  if (encode(&k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.k_codes), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, k_swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
-      encode(&v_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.v_codes), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
+  constexpr int kRowBytes = E2M1 ? D / 2 : D;
+  e = attn_code_map(&k_map, a, a.k_codes, kRowBytes, !E2M1);
+  if (e == cudaSuccess) e = attn_code_map(&v_map, a, a.v_codes, kRowBytes, false);
+  if (e != cudaSuccess) return e;
   k_attn_chunk<D, E2M1><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, kSmem, s>>>(a, k_map, v_map);
   return cudaGetLastError();
 }
@@ -1018,7 +947,6 @@ size_t attn_chunk_part_bytes(int head_dim) {
 
 cudaError_t launch_attn_chunk(AttnArgs a, cudaStream_t s) {
   a.min_units = kMinUnits;
-  a.box_keys = a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;
   a.part_o = reinterpret_cast<float*>(a.part_ml + static_cast<size_t>(2) * kMaxCtas * kRows);
   if (a.head_dim == 128) return a.e2m1 ? launch<128, true>(a, s) : launch<128, false>(a, s);
   return a.e2m1 ? launch<64, true>(a, s) : launch<64, false>(a, s);

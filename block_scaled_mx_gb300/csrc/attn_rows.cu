@@ -2,12 +2,11 @@
 // drafts): flash-decoding on register-level MMAs, bound by reading the cache.
 //
 // A tile is 16 rows (new tokens x the query heads of one KV head), so the
-// cache is read once for all heads that share it.  Four warps take 16 keys
-// each of a 64-key unit and keep their own running maximum, sum and
-// accumulator; they are joined when the CTA's stretch of a segment ends.  Keys
-// and values go from global memory to registers and MMA fragments with no
-// shared memory between: the contraction order of an MMA is free, so a lane
-// feeds it the 16-byte pieces that it loaded.
+// cache is read once for all heads that share it.  A fifth warp fetches units of
+// 64 keys ahead by TMA, over the segments' borders; four warps take 16 keys each
+// of a unit and keep their own running maximum, sum and accumulator, joined when
+// the CTA's stretch of a segment ends.  The contraction order of an MMA is free,
+// so a lane feeds it the 16-byte pieces that it reads from shared memory.
 //
 // Arithmetic.  Codes are exact in f16.  A key's blocks are scaled relative to
 // the key's largest block scale (a power of two: exact down to 2^-24 of the
@@ -22,6 +21,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "attn.cuh"
@@ -33,11 +33,11 @@ namespace {
 
 constexpr int kRows = 16;
 constexpr int kUnit = 64;
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 4;                  // that compute
+constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kCtasPerSm = 3;
 constexpr int kMinUnits = 4;
-constexpr int kCost = 0;
+constexpr int kCost = 1;                   // a segment's queries and output, in units
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -71,21 +71,21 @@ __device__ __forceinline__ int max_scale(uint32_t w) {
 template <int kWords>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[kWords]) {
   if constexpr (kWords == 1) {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else if constexpr (kWords == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
     w[0] = v.x, w[1] = v.y;
   } else {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
     w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
   }
 }
 
 // One row's scale bytes as a word.
 template <int kBlocks>
-__device__ __forceinline__ uint32_t load_scales(const uint8_t* p) {
-  if constexpr (kBlocks == 4) return __ldg(reinterpret_cast<const uint32_t*>(p));
-  else return __ldg(reinterpret_cast<const uint16_t*>(p));
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* p, int row) {
+  if constexpr (kBlocks == 4) return reinterpret_cast<const uint32_t*>(p)[row];
+  else return reinterpret_cast<const uint16_t*>(p)[row];
 }
 
 template <int D, bool E2M1>
@@ -94,70 +94,168 @@ struct RowsShape {
   static constexpr int kRowBytes = E2M1 ? D / 2 : D;
   static constexpr int kSteps = D / 16;                     // K = 16 steps of a score
   static constexpr int kTiles = D / 8;                      // n = 8 tiles of the output
-  static constexpr int kPieces = E2M1 || D == 64 ? 1 : 2;   // loads of a lane's share of a key
+  // a lane's D / 4 elements of a key of K, from c * D / 4 on, and its D / 8 of a
+  // key of V, from g * D / 8 on
+  static constexpr int kPieces = E2M1 || D == 64 ? 1 : 2;
   static constexpr int kPieceWords = E2M1 && D == 64 ? 2 : 4;
   static constexpr int kVWords = (E2M1 ? D / 16 : D / 8) / 4;
+  // a stage: K's codes, V's, K's scales, V's
+  static constexpr uint32_t kCodes = kUnit * kRowBytes, kScales = kUnit * kBlocks;
+  static constexpr uint32_t kStage = (2 * kCodes + 2 * kScales + 1023) / 1024 * 1024;
+  static constexpr int kStages = 53248 / kStage < 6 ? 53248 / kStage : 6;  // three CTAs share an SM
+  static constexpr uint32_t kJoin = 2 * kRows * D * sizeof(float);
+  static constexpr uint32_t kBytes = kStages * kStage + kJoin;
+  // where byte `b` of row r lies in a stage, as the TMA's swizzle puts it
+  static __device__ __forceinline__ uint32_t at(int r, int b) {
+    const int piece = b / 16;
+    const int moved = kRowBytes == 128 ? piece ^ (r & 7) : kRowBytes == 64 ? piece ^ ((r >> 1) & 3) : piece ^ ((r >> 2) & 1);
+    return static_cast<uint32_t>(r * kRowBytes + moved * 16 + b % 16);
+  }
 };
 
+// AttnCursor::settle, out of line: once a segment.
+template <class Cursor>
+__device__ __noinline__ bool settle(Cursor& c, const AttnArgs& a) {
+  return c.settle(a);
+}
+// The compute warps meet.
+__device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+
 template <int D, bool E2M1>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    k_attn_rows(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap k_map,
+                const __grid_constant__ CUtensorMap v_map) {
   using Sh = RowsShape<D, E2M1>;
-  __shared__ __align__(16) float s_o[kWarps][kRows][D];
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[Sh::kStages], empty[Sh::kStages];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  __shared__ __align__(16) uint32_t s_q[Sh::kSteps][32][4];
+  __shared__ int s_e[kRows];
+  __shared__ uint32_t s_here[Sh::kStages];  // 16-key groups that are there
   __shared__ int64_t s_units[kAttnScan];
+  __shared__ volatile int failed;
   __shared__ int s_last;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const AttnShare share = attn_share<kRows, kUnit, kCost, kThreads, false>(a, s_units);
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  float* s_o = reinterpret_cast<float*>(base + Sh::kStages * Sh::kStage);  // [2][kRows][D]
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (tid == 0) {
+    for (int i = 0; i < Sh::kStages; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), kWarps);
+    }
+    failed = 0;
+    fence_mbar_init();
+  }
+  const AttnShare share = attn_share<kRows, kUnit, kCost, kThreads, false>(a, s_units);  // its barriers cover the above
   const int n_heads = a.n_kv_heads * a.group;
   AttnCursor<kRows, kUnit, kCost> cur;
   cur.template start<false>(a, share);
+  Ring<Sh::kStages> ring;
 
-  while (cur.settle(a)) {
-    const AttnSeq& s = cur.s;
-    const AttnTile& t = cur.t;
+  if (warp == kWarps) {
+    // ---------------------------------------------------------------- fetching
+    constexpr int kGroups = kUnit / 16;
+    const int group = lane % kGroups, kind = lane / kGroups;  // K's codes, V's, K's scales, V's
+    const bool leads = 16 * group % a.box_keys == 0;
+    const int none = a.num_pages * a.n_kv_heads * a.page_size;
+    if (lane < 2) prefetch_tensormap(lane == 0 ? &k_map : &v_map);
+    AttnWalk<kUnit> walk;
+    int issued = 0;
+    bool ok = true;
+    while (ok && settle(cur, a)) {
+      const int take = cur.take();
+      walk.start(a, cur, group);
+#pragma unroll 1
+      for (int i = 0; i < take; ++i) {
+        uint32_t here, bad;
+        const int row = walk.box(a, cur.head, group, here, bad);
+        const uint32_t boxes = __ballot_sync(0xffffffffu, leads && row >= 0) & ((1u << kGroups) - 1);
+        ok = attn_wait(&failed, &empty[ring.stage], ring.phase ^ 1u, a);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t bar = smem_u32(&full[ring.stage]);
+        if (lane == 0) {
+          s_here[ring.stage] = here;
+          mbar_arrive_expect_tx(bar, 2 * Sh::kCodes + 2 * __popc(boxes) * (a.box_keys * Sh::kBlocks));
+        }
+        __syncwarp();
+        const uint32_t to = smem_u32(base + ring.stage * Sh::kStage);
+        if (leads && kind < 2) {
+          // a box that is not there is read past the table's end: zeros
+          tma_load_2d(to + kind * Sh::kCodes + group * (Sh::kCodes / kGroups), kind == 0 ? &k_map : &v_map, 0,
+                      row < 0 ? none : row, bar);
+        } else if (leads && kind < 4 && row >= 0) {
+          bulk_load(to + 2 * Sh::kCodes + (kind - 2) * Sh::kScales + group * (Sh::kScales / kGroups),
+                    (kind == 2 ? a.k_scales : a.v_scales) + static_cast<int64_t>(row) * Sh::kBlocks, a.box_keys * Sh::kBlocks, bar);
+        }
+        __syncwarp();
+        ++issued;
+        ring.next();
+        walk.step(a);
+      }
+      cur.pass(take);
+    }
+    // the last fills have landed before the CTA exits, also where a wait of the
+    // others ran out
+    for (int i = issued > Sh::kStages ? issued - Sh::kStages : 0; i < issued; ++i)
+      mbar_wait(smem_u32(&full[i % Sh::kStages]), (i / Sh::kStages) & 1u, 100000000ull);
+    return;
+  }
+
+  bool ok = true;
+  while (settle(cur, a)) {
+    const AttnSeq s = cur.s;
+    const AttnTile t = cur.t;
     const int head = cur.head, tile = cur.tile, place = cur.place;
     const int take = cur.take();
     const int rows = s.n * a.group;
-    const int base = s.kv - s.n;
+    const int old = s.kv - s.n;  // the position of the first new token
 
     // ---------------------------------------------------------------- queries
-    // rows g and g + 8; element e of a lane's share is d(e), sixteen at a time
-    uint32_t qa[Sh::kSteps][4];
-    float row_fac[2];
-    int row_lo[2], row_hi[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int R = tile * kRows + g + 8 * r;
+    // as the scores' A fragments, in shared memory: they would take 32 registers;
+    // warp r brings rows 8 r + g, their largest element scaled to [2^14, 2^15)
+    if (warp < 2) {
+      const int R = tile * kRows + g + 8 * warp;
       const bool valid = R < rows;
       const int tok = valid ? R / a.group : 0;
       const int hq = head * a.group + (valid ? R - tok * a.group : 0);
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + static_cast<int64_t>(s.q0 + tok) * a.q_stride +
-                               static_cast<int64_t>(hq) * D;
-      uint32_t w[D / 8];  // the lane's D / 4 elements
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                      static_cast<int64_t>(s.q0 + tok) * a.q_stride +
+                                                      static_cast<int64_t>(hq) * D + c * (D / 4));
+      uint4 w[D / 32];  // the lane's D / 4 elements
 #pragma unroll
-      for (int p = 0; p < D / 64; ++p) {
-        const int d = E2M1 ? c * (D / 4) + 16 * p : c * 16 + 64 * p;
-        const uint4* src = reinterpret_cast<const uint4*>(q + d);
-        const uint4 x = valid ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
-        const uint4 y = valid ? __ldg(src + 1) : make_uint4(0u, 0u, 0u, 0u);
-        w[8 * p] = x.x, w[8 * p + 1] = x.y, w[8 * p + 2] = x.z, w[8 * p + 3] = x.w;
-        w[8 * p + 4] = y.x, w[8 * p + 5] = y.y, w[8 * p + 6] = y.z, w[8 * p + 7] = y.w;
-      }
+      for (int i = 0; i < D / 32; ++i) w[i] = valid ? __ldg(q + i) : make_uint4(0u, 0u, 0u, 0u);
       uint32_t amax = 0;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) amax = max(amax, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) amax = max(amax, max(e[k] & 0x7FFFu, (e[k] >> 16) & 0x7FFFu));
+      }
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       const int e = max(static_cast<int>(amax >> 7) - 127, -100);
       const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);  // 14 - e <= 114
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint32_t h = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
-        qa[i / 2][(i & 1) * 2 + r] = h;
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          s_q[2 * i + k / 2][lane][(k & 1) * 2 + warp] =
+              pack_f16(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xFFFF0000u) * up);
       }
-      row_fac[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(max(127 + e - 14, 1)) << 23);
-      const int at = base + tok;
-      row_hi[r] = !valid ? 0 : a.causal ? min(s.kv, at + 1) : s.kv;
+      if (c == 0) s_e[g + 8 * warp] = e;
+    }
+    meet();
+    float row_fac[2];
+    int row_lo[2], row_hi[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int R = tile * kRows + g + 8 * r;
+      const int at = old + R / a.group;
+      row_fac[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(max(127 + s_e[g + 8 * r] - 14, 1)) << 23);
+      row_hi[r] = R >= rows ? 0 : a.causal ? min(s.kv, at + 1) : s.kv;
       row_lo[r] = a.window > 0 ? max(at - a.window + 1, 0) : 0;
     }
     // keys that every row of the tile sees need no mask
@@ -174,71 +272,48 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
     for (int i = 0; i < Sh::kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
-    const int32_t* table = a.block_table + static_cast<int64_t>(cur.b) * a.max_pages;
-    // Row index of 16 keys from `key` (a page holds a multiple of 16): or -1
-    // where there is nothing to read.
-    auto find_row = [&](int key) -> int64_t {
-      if (key >= t.hi || key + 16 <= t.lo) return -1;
-      const int entry = key / a.page_size;
-      const int page = __ldg(table + entry);
-      if (page < 0 || page >= a.num_pages) {
-        if (lane == 0) set_status(a.status, MX_ERR_DEVICE_ARG);
-        return -1;
-      }
-      return (static_cast<int64_t>(page) * a.n_kv_heads + head) * a.page_size + (key - entry * a.page_size);
-    };
-    uint32_t kw[2][Sh::kPieces][Sh::kPieceWords], ks[2], vw[4][Sh::kVWords], vs[4];
-    auto load_k = [&](int64_t row) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t r = row + 8 * j + g;
-#pragma unroll
-        for (int p = 0; p < Sh::kPieces; ++p)
-          load_words(a.k_codes + r * Sh::kRowBytes + c * (4 * Sh::kPieceWords) + 64 * p, kw[j][p]);
-        ks[j] = load_scales<Sh::kBlocks>(a.k_scales + r * Sh::kBlocks);
-      }
-    };
-    // the keys of the lane's score columns: 2c, 2c + 1, 8 + 2c, 9 + 2c
-    auto load_v = [&](int64_t row) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t r = row + 8 * (j >> 1) + 2 * c + (j & 1);
-        load_words(a.v_codes + r * Sh::kRowBytes + g * (4 * Sh::kVWords), vw[j]);
-        vs[j] = load_scales<Sh::kBlocks>(a.v_scales + r * Sh::kBlocks);
-      }
-    };
-
-    int key = t.first + place * kUnit + warp * 16;
-    const int key_end = t.first + (place + take) * kUnit;
-    int64_t row = key < key_end ? find_row(key) : -1;
-    if (row >= 0) {
-      load_k(row);
-      load_v(row);
-    }
-    for (; key < key_end; key += kUnit) {
-      const int64_t next = key + kUnit < key_end ? find_row(key + kUnit) : -1;
-      if (row < 0) {
-        row = next;
-        if (row >= 0) {
-          load_k(row);
-          load_v(row);
-        }
+#pragma unroll 1
+    for (int i = 0; i < take; ++i, ring.next()) {
+      const int key = t.first + (place + i) * kUnit + warp * 16;
+      if (ok) ok = attn_wait(&failed, &full[ring.stage], ring.phase, a);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok || !(s_here[ring.stage] >> warp & 1u)) {
+        warp_arrive(&empty[ring.stage]);
         continue;
       }
-      // scores of 2 x 8 keys
-      float x[2][4];
+      const uint8_t* k_codes = base + ring.stage * Sh::kStage;
+      const uint8_t* v_codes = k_codes + Sh::kCodes;
+      const uint8_t* k_scales = v_codes + Sh::kCodes;
+      const uint8_t* v_scales = k_scales + Sh::kScales;
+      uint32_t kw[2][Sh::kPieces][Sh::kPieceWords], ks[2], vw[4][Sh::kVWords], vs[4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int top = max_scale<Sh::kBlocks>(ks[j]);
-        uint32_t mult[D / 64];  // of the lane's 16-element groups
+        const int r = warp * 16 + 8 * j + g;
 #pragma unroll
-        for (int p = 0; p < D / 64; ++p) {
-          const int blk = E2M1 ? (D == 128 ? c : c >> 1) : (c >> 1) + 2 * p;
-          mult[p] = f16_pow2(static_cast<int>((ks[j] >> (8 * blk)) & 0xFFu) - top) * 0x10001u;
-        }
-        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int p = 0; p < Sh::kPieces; ++p) load_words(k_codes + Sh::at(r, c * (Sh::kRowBytes / 4) + 16 * p), kw[j][p]);
+        ks[j] = load_scales<Sh::kBlocks>(k_scales, r);
+      }
+      // the keys of the lane's score columns: 2c, 2c + 1, 8 + 2c, 9 + 2c
 #pragma unroll
-        for (int st = 0; st < Sh::kSteps; ++st) {
+      for (int j = 0; j < 4; ++j) {
+        const int r = warp * 16 + 8 * (j >> 1) + 2 * c + (j & 1);
+        load_words(v_codes + Sh::at(r, g * (Sh::kRowBytes / 8)), vw[j]);
+        vs[j] = load_scales<Sh::kBlocks>(v_scales, r);
+      }
+      // scores of 2 x 8 keys
+      float acc[2][4] = {};
+      uint32_t k_mult[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int blk = D == 128 ? c : c >> 1;  // of the lane's elements
+        k_mult[j] = f16_pow2(static_cast<int>((ks[j] >> (8 * blk)) & 0xFFu) - max_scale<Sh::kBlocks>(ks[j])) * 0x10001u;
+      }
+#pragma unroll
+      for (int st = 0; st < Sh::kSteps; ++st) {
+        const uint4 q4 = *reinterpret_cast<const uint4*>(s_q[st][lane]);
+        const uint32_t qa[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
           uint32_t b0, b1;
           if (E2M1) {
             const uint32_t w = kw[j][0][st / 2] >> ((st & 1) * 16);
@@ -249,16 +324,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
             b0 = f16x2_of_e4m3x2(w & 0xFFFFu);
             b1 = f16x2_of_e4m3x2(w >> 16);
           }
-          mma_f16(acc, qa[st], mul2(b0, mult[st / 4]), mul2(b1, mult[st / 4]));
+          mma_f16(acc[j], qa, mul2(b0, k_mult[j]), mul2(b1, k_mult[j]));
         }
-        const float key_fac = e8m0_value(top);
-        const float f0 = __shfl_sync(0xffffffffu, key_fac, 8 * c), f1 = __shfl_sync(0xffffffffu, key_fac, 8 * c + 4);
-        x[j][0] = acc[0] * (row_fac[0] * f0);
-        x[j][1] = acc[1] * (row_fac[0] * f1);
-        x[j][2] = acc[2] * (row_fac[1] * f0);
-        x[j][3] = acc[3] * (row_fac[1] * f1);
       }
-      if (next >= 0) load_k(next);
+      float x[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float key_fac = e8m0_value(max_scale<Sh::kBlocks>(ks[j]));
+        const float f0 = __shfl_sync(0xffffffffu, key_fac, 8 * c), f1 = __shfl_sync(0xffffffffu, key_fac, 8 * c + 4);
+        x[j][0] = acc[j][0] * (row_fac[0] * f0);
+        x[j][1] = acc[j][1] * (row_fac[0] * f1);
+        x[j][2] = acc[j][2] * (row_fac[1] * f0);
+        x[j][3] = acc[j][3] * (row_fac[1] * f1);
+      }
       // exponents of the values' keys; masks
       float e_inv[4];
       uint32_t v_mult[4];
@@ -349,11 +427,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
           }
         }
       }
-      if (next >= 0) load_v(next);
-      row = next;
+      warp_arrive(&empty[ring.stage]);
     }
 
     // ---------------------------------------------------------------- join the warps
+    // in two steps: warps 2 and 3 hand theirs to 0 and 1
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -362,16 +440,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
         s_m[warp][g + 8 * r] = m[r];
         s_l[warp][g + 8 * r] = l[r];
       }
-      // column n of output tile i is element n * D / 8 + i
+    }
+    // column n of output tile i is element n * D / 8 + i
+    auto mine = [&](int r, int k, int i) {
+      return reinterpret_cast<float4*>(s_o + ((warp & 1) * kRows + g + 8 * r) * D + (2 * c + k) * (D / 8) + i);
+    };
+    if (warp >= 2) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int i = 0; i < Sh::kTiles; i += 4)
-          *reinterpret_cast<float4*>(&s_o[warp][g + 8 * r][(2 * c + k) * (D / 8) + i]) =
-              make_float4(o[i][2 * r + k], o[i + 1][2 * r + k], o[i + 2][2 * r + k], o[i + 3][2 * r + k]);
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < Sh::kTiles; i += 4)
+            *mine(r, k, i) = make_float4(o[i][2 * r + k], o[i + 1][2 * r + k], o[i + 2][2 * r + k], o[i + 3][2 * r + k]);
+    }
+    meet();
+    if (warp < 2) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float other = s_m[warp + 2][g + 8 * r], M = fmaxf(m[r], other), from = M == -INFINITY ? 0.0f : M;
+        const float f = exp2_approx(m[r] - from), h = exp2_approx(other - from);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < Sh::kTiles; i += 4) {
+            const float4 v = *mine(r, k, i);
+            *mine(r, k, i) = make_float4(fmaf(o[i][2 * r + k], f, v.x * h), fmaf(o[i + 1][2 * r + k], f, v.y * h),
+                                         fmaf(o[i + 2][2 * r + k], f, v.z * h), fmaf(o[i + 3][2 * r + k], f, v.w * h));
+          }
       }
     }
-    __syncthreads();
+    meet();
 
     const bool whole = take == t.units;
     const AttnParts p = attn_parts(share, cur.u - place, t.units);
@@ -392,22 +491,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
       if (a.lse && d4 == 0) a.lse[oh] = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
     };
     constexpr int kLanes = D / 4;  // lanes of a row
-    for (int i = tid; i < kRows * kLanes; i += kThreads) {
+    for (int i = tid; i < kRows * kLanes; i += 32 * kWarps) {
       const int r = i / kLanes, d4 = i - r * kLanes;
       if (tile * kRows + r >= rows) continue;
-      float M = s_m[0][r];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
+      const float m0 = fmaxf(s_m[0][r], s_m[2][r]), m1 = fmaxf(s_m[1][r], s_m[3][r]);
+      const float M = fmaxf(m0, m1), from = M == -INFINITY ? 0.0f : M;
       float L = 0.0f;
-      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = M == -INFINITY ? 0.0f : exp2_approx(s_m[w][r] - M);
-        const float4 v = *reinterpret_cast<const float4*>(&s_o[w][r][4 * d4]);
-        L = fmaf(s_l[w][r], f, L);
-        acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
-      }
+      for (int w = 0; w < kWarps; ++w) L = fmaf(s_l[w][r], exp2_approx(s_m[w][r] - from), L);
+      const float f0 = exp2_approx(m0 - from), f1 = exp2_approx(m1 - from);
+      const float4 v0 = *reinterpret_cast<const float4*>(s_o + r * D + 4 * d4);
+      const float4 v1 = *reinterpret_cast<const float4*>(s_o + (kRows + r) * D + 4 * d4);
+      const float4 acc = make_float4(fmaf(v0.x, f0, v1.x * f1), fmaf(v0.y, f0, v1.y * f1), fmaf(v0.z, f0, v1.z * f1),
+                                     fmaf(v0.w, f0, v1.w * f1));
       if (whole) {
         finish(r, d4, acc, M, L);
       } else {
@@ -417,10 +513,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
     }
     if (!whole) {
       // ---------------------------------------------------------------- join the CTAs
+      // also after a wait that ran out: the counters are zero for the next call
       __threadfence();
-      __syncthreads();
+      meet();
       if (tid == 0) s_last = atomicAdd(&a.arrived[p.first], 1u) == static_cast<unsigned>(p.parts - 1);
-      __syncthreads();
+      meet();
       if (s_last) {
         __threadfence();
         auto slot_of = [&](int i) { return attn_slot(p.first + i, i == 0); };
@@ -448,17 +545,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_rows(const AttnAr
         if (tid == 0) a.arrived[p.first] = 0u;  // ready for the next launch
       }
     }
-    __syncthreads();  // the warps' parts are read before the next segment overwrites them
+    meet();  // the warps' parts are read before the next segment overwrites them
     cur.pass(take);
   }
 }
 
 template <int D, bool E2M1>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
-  int sms = 0;
-  const cudaError_t e = attn_sm_count(&sms);
+  using Sh = RowsShape<D, E2M1>;
+  constexpr int kSmem = Sh::kBytes + 1024;
+  constexpr int kMaxDevices = 64;
+  static std::atomic<bool> ready[kMaxDevices];
+  int sms = 0, dev = 0;
+  cudaError_t e = attn_sm_count(&sms);
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  k_attn_rows<D, E2M1><<<sms * kCtasPerSm < kAttnMaxCtas ? sms * kCtasPerSm : kAttnMaxCtas, kThreads, 0, s>>>(a);
+  if (dev < 0 || dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(k_attn_rows<D, E2M1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
+  }
+  CUtensorMap k_map, v_map;
+  e = attn_code_map(&k_map, a, a.k_codes, Sh::kRowBytes, true);
+  if (e == cudaSuccess) e = attn_code_map(&v_map, a, a.v_codes, Sh::kRowBytes, true);
+  if (e != cudaSuccess) return e;
+  k_attn_rows<D, E2M1><<<sms * kCtasPerSm < kAttnMaxCtas ? sms * kCtasPerSm : kAttnMaxCtas, kThreads, kSmem, s>>>(a, k_map, v_map);
   return cudaGetLastError();
 }
 

@@ -151,7 +151,7 @@ struct AttnArgs {
   float2* part_ml;                                   // [2 * CTAs][tile rows] maximum and sum
   float* part_o;                                     // [2 * CTAs][tile rows][head_dim]
   uint64_t wait_limit_ns;
-  int box_keys;                                      // keys that the chunk kernel fetches at once
+  int box_keys;                                      // keys fetched at once: 16, 32 or 64, what divides a page
 };
 cudaError_t attn_sm_count(int* sms);                 // of the current device
 size_t attn_rows_part_bytes(int head_dim);           // part_ml and part_o of the few-rows kernel

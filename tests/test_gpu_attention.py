@@ -229,3 +229,42 @@ def test_wait_that_runs_out_is_reported_and_the_next_call_is_right():
     mx.mx_paged_attention(q, cache, *batch.device(), out, ws, max_q_len=max(n), lse=lse)
     assert mx.moe_get_status(ws) == 0
     assert torch.equal(out, want) and torch.equal(lse, want_l)
+
+
+def test_few_rows_wait_that_runs_out():
+    n, kv = [1] * 9, [900] * 9
+    batch, q, cache = _setup(n, kv, 8, 2, 128, 16, "e4m3", seed=72)
+    want, want_l, status, ws = _call(batch, q, cache)
+    assert status == 0
+    out, lse = torch.empty_like(want), torch.empty_like(want_l)
+    try:
+        mx.mx_debug_set_wait_limit_ns(0)
+        mx.mx_paged_attention(q, cache, *batch.device(), out, ws, max_q_len=1, lse=lse)
+        assert mx.moe_get_status(ws) in (0, mx.MX_ERR_TIMEOUT)   # a wait may be over before it is asked for
+    finally:
+        mx.mx_debug_set_wait_limit_ns(2_000_000_000)
+    mx.mx_paged_attention(q, cache, *batch.device(), out, ws, max_q_len=1, lse=lse)
+    assert mx.moe_get_status(ws) == 0
+    assert torch.equal(out, want) and torch.equal(lse, want_l)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("page", [16, 48, 64])
+def test_bad_page_of_a_chunk_is_left_out(fmt, page):
+    """Rows of a chunk see the other pages' keys only."""
+    kv = 4 * page
+    batch, q, cache = _setup([40], [kv], 8, 2, 128, page, fmt, seed=81)
+    table, lens, starts = (t.clone() for t in batch.device())
+    table[0, 1] = batch.pages + 5
+    out, lse, status, _ = _call(batch, q, cache, dev=(table, lens, starts), causal=False)
+    assert status == mx.MX_ERR_DEVICE_ARG
+    less = ref.Batch([40], [kv - page], page, batch.pages, torch.cat([batch.table[:, :1], batch.table[:, 2:4]], 1))
+    tables = [t.cpu() for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)]
+    o, l, tol, tol_l = ref.attention(q.cpu(), *tables, fmt, less, 128 ** -0.5, False, 0)
+    assert torch.all((out.cpu().double() - o).abs() <= tol) and torch.all((lse.cpu().double() - l).abs() <= tol_l)
+
+
+@pytest.mark.parametrize("rows", [15, 16, 17, 33, 48, 64, 65, 127, 129, 255, 257])
+def test_row_counts_at_the_tiles_edges(rows):
+    """One query head of its own KV head: new tokens are rows."""
+    _check([rows, 1], [rows + 70, 100], 2, 2, 64, 16, seed=90 + rows)
