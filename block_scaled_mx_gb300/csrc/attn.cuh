@@ -38,8 +38,12 @@ struct AttnTile {
 // Sequence b as this launch handles it: only sequences of more than
 // a.rows_above and at most a.rows_upto rows; bad metadata sets the status word
 // (where `report`) and leaves nothing to do.
+//
+// This and what else runs once a segment or less is not inlined: its copies
+// would push the unit loops out of the instruction caches, and make a kernel's
+// first pass wait for its code.
 template <int kRows>
-__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b, bool report) {
+__device__ __noinline__ AttnSeq attn_seq(const AttnArgs& a, int b, bool report) {
   AttnSeq s;
   s.q0 = a.q_starts[b];
   const int end = a.q_starts[b + 1];
@@ -58,7 +62,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b, bool repor
 }
 
 template <int kRows, int kUnit>
-__device__ __forceinline__ AttnTile attn_tile(const AttnArgs& a, const AttnSeq& s, int tile) {
+__device__ __noinline__ AttnTile attn_tile(const AttnArgs& a, const AttnSeq& s, int tile) {
   AttnTile t;
   t.lo = 0;
   t.hi = s.kv;
@@ -88,18 +92,23 @@ __device__ __forceinline__ int attn_seq_places(const AttnArgs& a, const AttnSeq&
   return kWarp ? __reduce_add_sync(0xffffffffu, u) : u;
 }
 
-// The CTA whose stretch holds place u: the largest c with total * c / ctas <= u.
-__device__ __forceinline__ int attn_cta_of(int64_t u, int64_t total, int ctas) {
-  return static_cast<int>(((u + 1) * ctas - 1) / total);
-}
-
-// A CTA's stretch [u, end) of the line.
+// A CTA's stretch [u, end) of the line; the line's first `longer` stretches have
+// `each` + 1 places, the others `each`.  Places are 32-bit: the host refuses
+// what could have more.
 struct AttnShare {
-  int64_t total;
-  int ctas;        // CTAs that have a stretch
-  int64_t u, end;
-  int seq;         // the sequence that holds u,
-  int64_t in_seq;  // and u's place in it
+  uint32_t total;
+  int ctas;             // CTAs that have a stretch
+  uint32_t each, longer;
+  uint32_t u, end;
+  int seq;              // the sequence that holds u,
+  uint32_t in_seq;      // and u's place in it
+
+  __device__ __forceinline__ uint32_t start_of(uint32_t c) const { return c * each + min(c, longer); }
+  // the CTA whose stretch holds place v
+  __device__ __forceinline__ int cta_of(uint32_t v) const {
+    const uint32_t head = longer * (each + 1);
+    return static_cast<int>(v < head ? v / (each + 1) : longer + (v - head) / each);
+  }
 };
 
 constexpr int kAttnScan = 128;  // sequences looked at together
@@ -107,74 +116,74 @@ constexpr int kAttnScan = 128;  // sequences looked at together
 // Block-wide (kThreads threads); `units` holds kAttnScan words.  kWarp: a warp
 // counts a sequence (long ones have hundreds of tiles), else a thread.
 template <int kRows, int kUnit, int kCost, int kThreads, bool kWarp>
-__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int64_t* units) {
+__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, uint32_t* units) {
   const int tid = threadIdx.x, lane = tid & 31;
-  auto count = [&](int b0, bool report) {
-    for (int i = kWarp ? tid / 32 : tid; i < kAttnScan; i += kWarp ? kThreads / 32 : kThreads) {
-      int64_t u = 0;
-      if (b0 + i < a.n_seqs) {
-        const AttnSeq s = attn_seq<kRows>(a, b0 + i, report && blockIdx.x == 0);
-        u = static_cast<int64_t>(attn_seq_places<kRows, kUnit, kCost, kWarp>(a, s)) * a.n_kv_heads;
-      }
-      if (!kWarp || lane == 0) units[i] = u;
-    }
-    __syncthreads();
-  };
   constexpr int kPer = kAttnScan / 32;
   AttnShare r;
   r.total = 0;
-  int64_t v[kPer], mine = 0;
-  for (int b0 = 0; b0 < a.n_seqs; b0 += kAttnScan) {
-    count(b0, true);
-    mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) mine += v[i] = units[lane * kPer + i];
-    int64_t all = mine;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
-    r.total += all;
-    __syncthreads();
-  }
-  const int64_t n = (r.total + a.min_units - 1) / a.min_units;
-  r.ctas = static_cast<int>(n < gridDim.x ? n : gridDim.x);
   r.seq = 0;
   r.in_seq = r.u = r.end = 0;
-  if (static_cast<int>(blockIdx.x) >= r.ctas) return r;
-  r.u = r.total * blockIdx.x / r.ctas;
-  r.end = r.total * (blockIdx.x + 1) / r.ctas;
-  int64_t before = 0;
-  for (int b0 = 0; b0 < a.n_seqs; b0 += kAttnScan) {
-    if (a.n_seqs > kAttnScan) {
-      count(b0, false);
-      mine = 0;
+  uint32_t v[kPer], mine = 0, before = 0;
+  // Once over all sequences for the line's length, then again for the one that
+  // holds u; with one scan's worth of sequences the second pass has them.
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.n_seqs; b0 += kAttnScan) {
+      if (pass == 0 || a.n_seqs > kAttnScan) {
+        for (int i = kWarp ? tid / 32 : tid; i < kAttnScan; i += kWarp ? kThreads / 32 : kThreads) {
+          uint32_t u = 0;
+          if (b0 + i < a.n_seqs) {
+            const AttnSeq s = attn_seq<kRows>(a, b0 + i, pass == 0 && blockIdx.x == 0);
+            u = static_cast<uint32_t>(attn_seq_places<kRows, kUnit, kCost, kWarp>(a, s)) * a.n_kv_heads;
+          }
+          if (!kWarp || lane == 0) units[i] = u;
+        }
+        __syncthreads();
+        mine = 0;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) mine += v[i] = units[lane * kPer + i];
-      __syncthreads();
-    }
-    int64_t incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += o;
-    }
-    int64_t from = before + incl - mine;
-    int at = -1;
-    int64_t in = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (r.u >= from && r.u < from + v[i]) {
-        at = b0 + lane * kPer + i;
-        in = r.u - from;
+        for (int i = 0; i < kPer; ++i) mine += v[i] = units[lane * kPer + i];
+        __syncthreads();
       }
-      from += v[i];
+      uint32_t incl = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+      if (pass == 0) {
+        r.total += all;
+        continue;
+      }
+      uint32_t from = before + incl - mine;
+      int at = -1;
+      uint32_t in = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (r.u >= from && r.u - from < v[i]) {
+          at = b0 + lane * kPer + i;
+          in = r.u - from;
+        }
+        from += v[i];
+      }
+      before += all;
+      const unsigned hit = __ballot_sync(0xffffffffu, at >= 0);
+      if (hit && r.end > r.u) {
+        const int src = __ffs(hit) - 1;
+        r.seq = __shfl_sync(0xffffffffu, at, src);
+        r.in_seq = __shfl_sync(0xffffffffu, in, src);
+      }
     }
-    before += __shfl_sync(0xffffffffu, incl, 31);
-    const unsigned hit = __ballot_sync(0xffffffffu, at >= 0);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      r.seq = __shfl_sync(0xffffffffu, at, src);
-      r.in_seq = __shfl_sync(0xffffffffu, in, src);
-      break;
+    if (pass == 0) {
+      const uint32_t n = (r.total + a.min_units - 1) / a.min_units;
+      r.ctas = static_cast<int>(min(n, gridDim.x));
+      r.each = r.ctas > 0 ? r.total / r.ctas : 1;
+      r.longer = r.total - r.each * r.ctas;
+      if (blockIdx.x < static_cast<unsigned>(r.ctas)) {
+        r.u = r.start_of(blockIdx.x);
+        r.end = r.start_of(blockIdx.x + 1);
+      }
     }
   }
   return r;
@@ -184,7 +193,7 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int64_t* unit
 // sequence) and the unit `place` of it (below zero: the places without work).
 template <int kRows, int kUnit, int kCost>
 struct AttnCursor {
-  int64_t u, end;  // on the line
+  uint32_t u, end;  // on the line
   int b, head, tile, place;
   AttnSeq s;
   AttnTile t;
@@ -200,7 +209,7 @@ struct AttnCursor {
     s = attn_seq<kRows>(a, b, false);
     const int per_head = attn_seq_places<kRows, kUnit, kCost, kWarp>(a, s);
     head = static_cast<int>(share.in_seq / max(per_head, 1));
-    place = static_cast<int>(share.in_seq - static_cast<int64_t>(head) * per_head);
+    place = static_cast<int>(share.in_seq - static_cast<uint32_t>(head) * per_head);
     if (kWarp) {
       const int lane = threadIdx.x & 31;
       for (; tile < s.tiles; tile += 32) {
@@ -236,9 +245,9 @@ struct AttnCursor {
   __device__ __forceinline__ bool settle(const AttnArgs& a) {
     while (u < end) {
       if (place < 0) {
-        const int64_t d = min(static_cast<int64_t>(-place), end - u);
+        const int d = static_cast<int>(min(static_cast<uint32_t>(-place), end - u));
         u += d;
-        place += static_cast<int>(d);
+        place += d;
         continue;
       }
       if (place < t.units) return true;
@@ -259,7 +268,7 @@ struct AttnCursor {
   }
   // Units of the segment from `place` on that lie in the stretch, and past them.
   __device__ __forceinline__ int take() const {
-    return static_cast<int>(min(static_cast<int64_t>(t.units - place), end - u));
+    return static_cast<int>(min(static_cast<uint32_t>(t.units - place), end - u));
   }
   __device__ __forceinline__ void pass(int n) {
     u += n;
@@ -316,10 +325,10 @@ struct AttnWalk {
 struct AttnParts {
   int first, parts;
 };
-__device__ __forceinline__ AttnParts attn_parts(const AttnShare& sh, int64_t seg, int units) {
+__device__ __forceinline__ AttnParts attn_parts(const AttnShare& sh, uint32_t seg, int units) {
   AttnParts p;
-  p.first = attn_cta_of(seg, sh.total, sh.ctas);
-  p.parts = attn_cta_of(seg + units - 1, sh.total, sh.ctas) - p.first + 1;
+  p.first = sh.cta_of(seg);
+  p.parts = sh.cta_of(seg + units - 1) - p.first + 1;
   return p;
 }
 // The workspace slot of a CTA's part: the part that begins a segment and those

@@ -122,7 +122,7 @@ struct Shared {
   uint32_t q_scale[2][128];  // a row's scale bytes
   alignas(128) uint32_t k_scale[kStages][32][4];  // keys 32 j + lane, by lane
   UnitKeys keys[kRawStages];
-  int64_t units[kAttnScan];
+  uint32_t units[kAttnScan];
 };
 
 // Functions that are not inlined here and below: the roles' unit loops have to
@@ -442,16 +442,16 @@ __device__ __noinline__ void write_rows(const AttnArgs& a, Shared& sh, uint32_t 
   }
   if (slot < 0) return;
   // also after a wait that ran out: the counters are zero for the next call
-  __threadfence();
   tile_barrier(x);
   unsigned* counter = &a.arrived[2 * parts.first + x];
   if (row == 0) {
+    __threadfence();  // for all: the barrier orders their writes before it
     sh.last[x] = atomicAdd(counter, 1u) == static_cast<unsigned>(parts.parts - 1);
+    __threadfence();
     if (sh.last[x]) *counter = 0u;
   }
   tile_barrier(x);
   if (sh.last[x] && ok && valid) {
-    __threadfence();
     join_parts<D>(a, parts, 128 * x + row, oh);
   }
   __syncwarp();

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   __shared__ __align__(16) uint32_t s_q[Sh::kSteps][32][4];
   __shared__ int s_e[kRows];
   __shared__ uint32_t s_here[Sh::kStages];  // 16-key groups that are there
-  __shared__ int64_t s_units[kAttnScan];
+  __shared__ uint32_t s_units[kAttnScan];
   __shared__ volatile int failed;
   __shared__ int s_last;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -514,12 +514,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (!whole) {
       // ---------------------------------------------------------------- join the CTAs
       // also after a wait that ran out: the counters are zero for the next call
-      __threadfence();
       meet();
-      if (tid == 0) s_last = atomicAdd(&a.arrived[p.first], 1u) == static_cast<unsigned>(p.parts - 1);
+      if (tid == 0) {
+        __threadfence();  // for all: the barrier orders their writes before it
+        s_last = atomicAdd(&a.arrived[p.first], 1u) == static_cast<unsigned>(p.parts - 1);
+        __threadfence();
+      }
       meet();
       if (s_last) {
-        __threadfence();
         auto slot_of = [&](int i) { return attn_slot(p.first + i, i == 0); };
         for (int r = warp; r < kRows && tile * kRows + r < rows; r += kWarps) {
           float M = -INFINITY;
