@@ -66,10 +66,15 @@ KvArgs kv_args(const mx_kv_cache* c, const int32_t* block_table, const int32_t* 
 constexpr size_t kArrivedOffset = 256;
 constexpr size_t kArrivedBytes = sizeof(unsigned) * kAttnMaxCtas;
 
-// Sequences of up to kFewRows rows (new tokens x query heads of a KV head) are
-// the few-rows kernel's, others the chunk kernel's.
-constexpr int kFewRows = 16;
-bool has_chunks(int group, int max_q_len) { return static_cast<int64_t>(max_q_len) * group > kFewRows; }
+// Sequences of up to this many rows (new tokens x query heads of a KV head) are
+// the few-rows kernel's, others the chunk kernel's.  The few-rows kernel works
+// through the keys again for every 16 rows, the chunk kernel takes as long for
+// 256 as for one but starts and ends slower: over 8 sequences of 8192 tokens and
+// 4 KV heads, 16 rows took 43 us against 54, and 32 rows are even.  With few
+// (sequence, KV head) pairs the start weighs more: 48 rows over 2 pairs of 2051
+// keys took 27 us against 38.
+constexpr int kMostFewRows = 64;
+int few_rows(int n_seqs, int n_kv_heads) { return static_cast<int64_t>(n_seqs) * n_kv_heads <= 16 ? kMostFewRows : 32; }
 
 int check_attention(int T, int n_seqs, int n_heads, int n_kv_heads, int head_dim, int max_q_len) {
   if (T < 0 || n_seqs < 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || max_q_len < 0) return MX_ERR_INVALID_ARG;
@@ -153,7 +158,7 @@ int mx_kv_read(const mx_kv_cache* cache, const int32_t* block_table, const int32
 size_t mx_paged_attention_workspace_size(int T, int n_seqs, int n_heads, int n_kv_heads, int head_dim, int max_q_len) {
   if (check_attention(T, n_seqs, n_heads, n_kv_heads, head_dim, max_q_len) != MX_OK) return 0;
   size_t part = attn_rows_part_bytes(head_dim);
-  if (has_chunks(n_heads / n_kv_heads, max_q_len) && attn_chunk_part_bytes(head_dim) > part) part = attn_chunk_part_bytes(head_dim);
+  if (static_cast<int64_t>(max_q_len) * (n_heads / n_kv_heads) > few_rows(n_seqs, n_kv_heads) && attn_chunk_part_bytes(head_dim) > part) part = attn_chunk_part_bytes(head_dim);
   return kArrivedOffset + al256(kArrivedBytes) + part;
 }
 
@@ -172,7 +177,7 @@ int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride
   if (static_cast<int64_t>(cache->num_pages) * cache->page_size > INT_MAX / cache->n_kv_heads) return MX_ERR_UNSUPPORTED;
   // Places of work are counted in 32 bits.  At most: 256-row tiles, and 16-row
   // ones of the sequences with few rows, times 64-key units and a tile's cost.
-  const double tiles = static_cast<double>(T) * (n_heads / cache->n_kv_heads) / 256 + n_seqs * (1.0 + kFewRows / 16);
+  const double tiles = static_cast<double>(T) * (n_heads / cache->n_kv_heads) / 256 + n_seqs * (1.0 + kMostFewRows / 16);
   if (tiles * cache->n_kv_heads * (static_cast<double>(max_pages) * cache->page_size / 64 + 32) > 4.0e9)
     return MX_ERR_UNSUPPORTED;
   if (T == 0 || n_seqs == 0 || max_q_len == 0) return MX_OK;
@@ -216,14 +221,15 @@ int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   a.rows_above = 0;
   a.rows_upto = INT_MAX;
-  if (!has_chunks(a.group, max_q_len)) return cuda_status(launch_attn_rows(a, cs));
+  const int few = few_rows(n_seqs, a.n_kv_heads);
+  if (static_cast<int64_t>(max_q_len) * a.group <= few) return cuda_status(launch_attn_rows(a, cs));
   // Where all sequences are as long as the longest (T has room for it), one
   // launch takes them all; a shorter one among them is right there too.
   if (T >= static_cast<int64_t>(n_seqs) * max_q_len) return cuda_status(launch_attn_chunk(a, cs));
-  a.rows_upto = kFewRows;
+  a.rows_upto = few;
   st = cuda_status(launch_attn_rows(a, cs));
   if (st != MX_OK) return st;
-  a.rows_above = kFewRows;
+  a.rows_above = few;
   a.rows_upto = INT_MAX;
   return cuda_status(launch_attn_chunk(a, cs));
 }
