@@ -307,7 +307,7 @@ def _dense(t, dtype, shape, what) -> Optional[int]:
         return None
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
-    return _ptr(t)
+    return t.data_ptr() if t.is_cuda and t.is_contiguous() else _ptr(t)
 
 
 def mx_add_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, codes=None, scales=None, fmt="e4m3",
