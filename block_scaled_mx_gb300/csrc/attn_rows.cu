@@ -1,12 +1,20 @@
 // Attention of few new tokens over the paged MX cache (decoding, verifying
 // drafts): flash-decoding on register-level MMAs, bound by reading the cache.
 //
-// A tile is 16 rows (new tokens x the query heads of one KV head), so the
+// A tile is 8 or 16 rows (new tokens x the query heads of one KV head), so the
 // cache is read once for all heads that share it.  A fifth warp fetches units of
 // 64 keys ahead by TMA, over the segments' borders; four warps take 16 keys each
 // of a unit and keep their own running maximum, sum and accumulator, joined when
-// the CTA's stretch of a segment ends.  The contraction order of an MMA is free,
-// so a lane feeds it the 16-byte pieces that it reads from shared memory.
+// the CTA's stretch of a segment ends.
+//
+// Both products are transposed, S^T = K Q^T and O^T += V^T P^T, so that the query
+// rows are the MMAs' columns, of which there are 8 where there are 16 rows of
+// keys or elements: with up to 8 query rows nothing of an MMA is wasted, and the
+// widened codes are used again for the next 8.  P^T goes from the layout of S^T's
+// results to that of an operand by a transposing move.  The contraction order of
+// an MMA is free, so a lane feeds it the 16-byte pieces that it reads from shared
+// memory.  (The MMAs on 8-bit codes are no way around the widening: the compiler
+// makes them of conversions and MMAs on f16.)
 //
 // Arithmetic.  Codes are exact in f16.  A key's blocks are scaled relative to
 // the key's largest block scale (a power of two: exact down to 2^-24 of the
@@ -22,6 +30,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <atomic>
+#include <climits>
 #include <cstdint>
 
 #include "attn.cuh"
@@ -31,7 +40,7 @@ namespace mxk {
 
 namespace {
 
-constexpr int kRows = 16;
+constexpr int kMostRows = 16;              // of a tile
 constexpr int kUnit = 64;
 constexpr int kWarps = 4;                  // that compute
 constexpr int kThreads = 32 * (kWarps + 1);
@@ -55,10 +64,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// 2^d as the bits of an f16, d <= 15: subnormal below -14, 0 below -24.
-__device__ __forceinline__ uint32_t f16_pow2(int d) {
-  return d >= -14 ? static_cast<uint32_t>(15 + d) << 10 : 0x400u >> min(-14 - d, 31);
+// The warp's 8 x 8 matrix of 16-bit elements, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
+
+// The float 2^d, 0 below -126.
+__device__ __forceinline__ float pow2_or_zero(int d) { return __uint_as_float(static_cast<uint32_t>(max(127 + d, 0)) << 23); }
 
 // The largest byte of a row's scale word (kBlocks bytes).
 template <int kBlocks>
@@ -88,17 +102,18 @@ __device__ __forceinline__ uint32_t load_scales(const uint8_t* p, int row) {
   else return reinterpret_cast<const uint16_t*>(p)[row];
 }
 
-template <int D, bool E2M1>
+template <int D, bool E2M1, int NT>
 struct RowsShape {
+  static constexpr int kRows = 8 * NT;
   static constexpr int kBlocks = D / 32;                    // scales of a row
   static constexpr int kRowBytes = E2M1 ? D / 2 : D;
+  static constexpr int kTiles = D / 16;                     // m = 16 tiles of the output
   static constexpr int kSteps = D / 16;                     // K = 16 steps of a score
-  static constexpr int kTiles = D / 8;                      // n = 8 tiles of the output
   // a lane's D / 4 elements of a key of K, from c * D / 4 on, and its D / 8 of a
   // key of V, from g * D / 8 on
   static constexpr int kPieces = E2M1 || D == 64 ? 1 : 2;
   static constexpr int kPieceWords = E2M1 && D == 64 ? 2 : 4;
-  static constexpr int kVWords = (E2M1 ? D / 16 : D / 8) / 4;
+  static constexpr int kVWords = kRowBytes / 32;
   // a stage: K's codes, V's, K's scales, V's
   static constexpr uint32_t kCodes = kUnit * kRowBytes, kScales = kUnit * kBlocks;
   static constexpr uint32_t kStage = (2 * kCodes + 2 * kScales + 1023) / 1024 * 1024;
@@ -121,15 +136,24 @@ __device__ __noinline__ bool settle(Cursor& c, const AttnArgs& a) {
 // The compute warps meet.
 __device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
-template <int D, bool E2M1>
+// What the scales of a warp's 16 keys say, worked out half a key a lane.
+struct KeyTable {
+  float4 key[16];          // K's largest scale; V's largest scale's exponent e, 2^-e
+  uint32_t k_rel[4][16];   // a block's K scale relative to the key's largest, in f16, twice
+  __half v_rel[4][16];     // a block's V scale relative to the key's largest
+};
+
+template <int D, bool E2M1, int NT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     k_attn_rows(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap k_map,
                 const __grid_constant__ CUtensorMap v_map) {
-  using Sh = RowsShape<D, E2M1>;
+  using Sh = RowsShape<D, E2M1, NT>;
+  constexpr int kRows = Sh::kRows;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[Sh::kStages], empty[Sh::kStages];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
-  __shared__ __align__(16) uint32_t s_q[Sh::kSteps][32][4];
+  __shared__ uint2 s_q[NT][Sh::kSteps][32];
+  __shared__ __align__(16) KeyTable s_table[kWarps];
   __shared__ int s_e[kRows];
   __shared__ uint32_t s_here[Sh::kStages];  // 16-key groups that are there
   __shared__ uint32_t s_units[kAttnScan];
@@ -203,6 +227,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     return;
   }
 
+  KeyTable& table = s_table[warp];
+  const int half = lane >> 4;  // of the blocks of key lane % 16, whose scales the lane works out
+  // where the lane's codes lie in a stage
+  int k_off[Sh::kPieces], v_off[2];
+#pragma unroll
+  for (int p = 0; p < Sh::kPieces; ++p) k_off[p] = Sh::at(warp * 16 + g, c * (Sh::kRowBytes / 4) + 16 * p);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) v_off[p] = Sh::at(warp * 16 + 2 * c + p, g * (Sh::kRowBytes / 8));
+
   bool ok = true;
   while (settle(cur, a)) {
     const AttnSeq s = cur.s;
@@ -213,9 +246,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int old = s.kv - s.n;  // the position of the first new token
 
     // ---------------------------------------------------------------- queries
-    // as the scores' A fragments, in shared memory: they would take 32 registers;
-    // warp r brings rows 8 r + g, their largest element scaled to [2^14, 2^15)
-    if (warp < 2) {
+    // as the scores' B fragments; warp r brings rows 8 r + g, their largest element
+    // scaled to [2^14, 2^15)
+    if (warp < NT) {
       const int R = tile * kRows + g + 8 * warp;
       const bool valid = R < rows;
       const int tok = valid ? R / a.group : 0;
@@ -240,37 +273,48 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        uint32_t y[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          s_q[2 * i + k / 2][lane][(k & 1) * 2 + warp] =
-              pack_f16(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xFFFF0000u) * up);
+        for (int k = 0; k < 4; ++k) y[k] = pack_f16(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xFFFF0000u) * up);
+        s_q[warp][2 * i][lane] = make_uint2(y[0], y[1]);
+        s_q[warp][2 * i + 1][lane] = make_uint2(y[2], y[3]);
       }
       if (c == 0) s_e[g + 8 * warp] = e;
     }
     meet();
-    float row_fac[2];
-    int row_lo[2], row_hi[2];
+    // of the lane's rows 8 r + 2 c + k
+    float row_fac[NT][2];
+    int row_lo[NT][2], row_hi[NT][2], all_hi = INT_MAX, all_lo = 0;  // keys in [all_lo, all_hi) need no mask
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int R = tile * kRows + g + 8 * r;
-      const int at = old + R / a.group;
-      row_fac[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(max(127 + s_e[g + 8 * r] - 14, 1)) << 23);
-      row_hi[r] = R >= rows ? 0 : a.causal ? min(s.kv, at + 1) : s.kv;
-      row_lo[r] = a.window > 0 ? max(at - a.window + 1, 0) : 0;
-    }
-    // keys that every row of the tile sees need no mask
-    int all_hi = min(row_hi[0], row_hi[1]), all_lo = max(row_lo[0], row_lo[1]);
+    for (int r = 0; r < NT; ++r)
 #pragma unroll
-    for (int d = 4; d < 32; d <<= 1) {
-      all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, d));
-      all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, d));
+      for (int k = 0; k < 2; ++k) {
+        const int in = 8 * r + 2 * c + k, R = tile * kRows + in;
+        const int at = old + R / a.group;
+        row_fac[r][k] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(max(127 + s_e[in] - 14, 1)) << 23);
+        // rows past the tile's are zeros that nobody reads
+        row_hi[r][k] = R >= rows ? INT_MAX : a.causal ? min(s.kv, at + 1) : s.kv;
+        row_lo[r][k] = R < rows && a.window > 0 ? max(at - a.window + 1, 0) : 0;
+        all_hi = min(all_hi, row_hi[r][k]);
+        all_lo = max(all_lo, row_lo[r][k]);
+      }
+    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+    uint2 qb[Sh::kSteps];  // of one row group: it stays in registers
+    if (NT == 1) {
+#pragma unroll
+      for (int st = 0; st < Sh::kSteps; ++st) qb[st] = s_q[0][st][lane];
     }
 
     // ---------------------------------------------------------------- keys and values
-    float o[Sh::kTiles][4];
+    // o[r][i][k + 2 d]: row 8 r + 2 c + k, element g * D / 8 + 2 i + d
+    float o[NT][Sh::kTiles][4], m[NT][2], l[NT][2];
 #pragma unroll
-    for (int i = 0; i < Sh::kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    for (int r = 0; r < NT; ++r) {
+      m[r][0] = m[r][1] = -INFINITY, l[r][0] = l[r][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < Sh::kTiles; ++i) o[r][i][0] = o[r][i][1] = o[r][i][2] = o[r][i][3] = 0.0f;
+    }
 
 #pragma unroll 1
     for (int i = 0; i < take; ++i, ring.next()) {
@@ -285,33 +329,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const uint8_t* v_codes = k_codes + Sh::kCodes;
       const uint8_t* k_scales = v_codes + Sh::kCodes;
       const uint8_t* v_scales = k_scales + Sh::kScales;
-      uint32_t kw[2][Sh::kPieces][Sh::kPieceWords], ks[2], vw[4][Sh::kVWords], vs[4];
+      uint32_t kw[2][Sh::kPieces][Sh::kPieceWords], vw[4][Sh::kVWords];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = warp * 16 + 8 * j + g;
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int p = 0; p < Sh::kPieces; ++p) load_words(k_codes + Sh::at(r, c * (Sh::kRowBytes / 4) + 16 * p), kw[j][p]);
-        ks[j] = load_scales<Sh::kBlocks>(k_scales, r);
+        for (int p = 0; p < Sh::kPieces; ++p) load_words(k_codes + k_off[p] + j * 8 * Sh::kRowBytes, kw[j][p]);
+      // the keys 2c, 2c + 1, 8 + 2c, 9 + 2c of the lane's operands
+      auto load_values = [&] {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_words(v_codes + v_off[j & 1] + (j >> 1) * 8 * Sh::kRowBytes, vw[j]);
+      };
+      if (NT == 1) load_values();  // else there are no registers for them yet
+      {
+        const uint32_t ks = load_scales<Sh::kBlocks>(k_scales, warp * 16 + (lane & 15));
+        const uint32_t vs = load_scales<Sh::kBlocks>(v_scales, warp * 16 + (lane & 15));
+        const int k_top = max_scale<Sh::kBlocks>(ks), e = min(max(max_scale<Sh::kBlocks>(vs) - 127, -100), 126);
+        constexpr int kHalf = Sh::kBlocks / 2;
+        const uint32_t kh = ks >> (8 * kHalf * half), vh = vs >> (8 * kHalf * half);
+#pragma unroll
+        for (int b = 0; b < kHalf; ++b) {
+          const float kr = pow2_or_zero(static_cast<int>((kh >> (8 * b)) & 0xFFu) - k_top);
+          table.k_rel[kHalf * half + b][lane & 15] = pack_f16(kr, kr);
+          table.v_rel[kHalf * half + b][lane & 15] =
+              __float2half_rn(pow2_or_zero(min(static_cast<int>((vh >> (8 * b)) & 0xFFu) - 127 - e, 2)));
+        }
+        table.key[lane & 15] = make_float4(e8m0_value(k_top), static_cast<float>(e),
+                                           __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 0.0f);
+        __syncwarp();
       }
-      // the keys of the lane's score columns: 2c, 2c + 1, 8 + 2c, 9 + 2c
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = warp * 16 + 8 * (j >> 1) + 2 * c + (j & 1);
-        load_words(v_codes + Sh::at(r, g * (Sh::kRowBytes / 8)), vw[j]);
-        vs[j] = load_scales<Sh::kBlocks>(v_scales, r);
-      }
-      // scores of 2 x 8 keys
-      float acc[2][4] = {};
-      uint32_t k_mult[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int blk = D == 128 ? c : c >> 1;  // of the lane's elements
-        k_mult[j] = f16_pow2(static_cast<int>((ks[j] >> (8 * blk)) & 0xFFu) - max_scale<Sh::kBlocks>(ks[j])) * 0x10001u;
-      }
+      // scores of keys g and g + 8 for the lane's rows
+      const int k_blk = D == 128 ? c : c >> 1;  // of the lane's elements
+      const uint32_t k_mult[2] = {table.k_rel[k_blk][g], table.k_rel[k_blk][g + 8]};
+      float x[NT][4] = {};
 #pragma unroll
       for (int st = 0; st < Sh::kSteps; ++st) {
-        const uint4 q4 = *reinterpret_cast<const uint4*>(s_q[st][lane]);
-        const uint32_t qa[4] = {q4.x, q4.y, q4.z, q4.w};
+        uint32_t ka[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           uint32_t b0, b1;
@@ -324,40 +376,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             b0 = f16x2_of_e4m3x2(w & 0xFFFFu);
             b1 = f16x2_of_e4m3x2(w >> 16);
           }
-          mma_f16(acc[j], qa, mul2(b0, k_mult[j]), mul2(b1, k_mult[j]));
+          ka[j] = mul2(b0, k_mult[j]);
+          ka[2 + j] = mul2(b1, k_mult[j]);
+        }
+#pragma unroll
+        for (int r = 0; r < NT; ++r) {
+          const uint2 q2 = NT == 1 ? qb[st] : s_q[r][st][lane];
+          mma_f16(x[r], ka, q2.x, q2.y);
         }
       }
-      float x[2][4];
+      if (NT > 1) load_values();
+      const float4 key4[2] = {table.key[g], table.key[g + 8]};
+      // x[r][2 j + k]: key g + 8 j, row 8 r + 2 c + k
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float key_fac = e8m0_value(max_scale<Sh::kBlocks>(ks[j]));
-        const float f0 = __shfl_sync(0xffffffffu, key_fac, 8 * c), f1 = __shfl_sync(0xffffffffu, key_fac, 8 * c + 4);
-        x[j][0] = acc[j][0] * (row_fac[0] * f0);
-        x[j][1] = acc[j][1] * (row_fac[0] * f1);
-        x[j][2] = acc[j][2] * (row_fac[1] * f0);
-        x[j][3] = acc[j][3] * (row_fac[1] * f1);
-      }
-      // exponents of the values' keys; masks
-      float e_inv[4];
-      uint32_t v_mult[4];
+      for (int r = 0; r < NT; ++r)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = min(max(max_scale<Sh::kBlocks>(vs[j]) - 127, -100), 126);
-        const int blk = D == 128 ? g >> 1 : g >> 2;
-        v_mult[j] = f16_pow2(min(static_cast<int>((vs[j] >> (8 * blk)) & 0xFFu) - 127 - e, 2));
-        e_inv[j] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        const float ef = static_cast<float>(e);
-        x[j >> 1][j & 1] += ef;
-        x[j >> 1][2 + (j & 1)] += ef;
-      }
+        for (int i = 0; i < 4; ++i) x[r][i] = fmaf(x[r][i], row_fac[r][i & 1] * key4[i >> 1].x, key4[i >> 1].y);
       if (key + 16 > all_hi || key < all_lo) {
+#pragma unroll
+        for (int r = 0; r < NT; ++r)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = key + g + 8 * (i >> 1);
+            if (at >= row_hi[r][i & 1] || at < row_lo[r][i & 1]) x[r][i] = -INFINITY;
+          }
+        // a place that no row sees may hold anything, NaN included
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int at = key + 8 * (j >> 1) + 2 * c + (j & 1);
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-            if (at >= row_hi[r] || at < row_lo[r]) x[j >> 1][2 * r + (j & 1)] = -INFINITY;
-          // a place that no row sees may hold anything, NaN included
           if (at >= t.hi || at < t.lo) {
 #pragma unroll
             for (int i = 0; i < Sh::kVWords; ++i) vw[j][i] = 0u;
@@ -365,41 +411,54 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
       }
       // running maximum
-      float top[2];
+      bool above = false;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        top[r] = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-      }
-      if (__any_sync(0xffffffffu, top[0] > m[0] + 8.0f || top[1] > m[1] + 8.0f)) {
+      for (int r = 0; r < NT; ++r)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float to = fmaxf(m[r], top[r]);
-          const float f = to == -INFINITY ? 1.0f : exp2_approx(m[r] - to);
-          m[r] = to;
-          l[r] *= f;
+        for (int k = 0; k < 2; ++k) above = above || fmaxf(x[r][k], x[r][2 + k]) > m[r][k] + 8.0f;
+      if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-          for (int i = 0; i < Sh::kTiles; ++i) {
-            o[i][2 * r] *= f;
-            o[i][2 * r + 1] *= f;
+        for (int r = 0; r < NT; ++r)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float to = fmaxf(x[r][k], x[r][2 + k]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
+            to = fmaxf(to, m[r][k]);
+            const float f = to == -INFINITY ? 1.0f : exp2_approx(m[r][k] - to);
+            m[r][k] = to;
+            l[r][k] *= f;
+#pragma unroll
+            for (int i = 0; i < Sh::kTiles; ++i) {
+              o[r][i][k] *= f;
+              o[r][i][2 + k] *= f;
+            }
           }
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int r = 0; r < NT; ++r) {
+        const float from[2] = {m[r][0] == -INFINITY ? 0.0f : m[r][0], m[r][1] == -INFINITY ? 0.0f : m[r][1]};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float w[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            w[k] = exp2_approx(x[r][2 * j + k] - from[k]);
+            l[r][k] = fmaf(w[k], key4[j].z, l[r][k]);
+          }
+          pb[r][j] = transposed(pack_f16(w[0], w[1]));
         }
       }
-      uint32_t pa[4];
+      const int v_blk = D == 128 ? g >> 1 : g >> 2;
+      const uint32_t rel[2] = {*reinterpret_cast<const uint32_t*>(&table.v_rel[v_blk][2 * c]),
+                               *reinterpret_cast<const uint32_t*>(&table.v_rel[v_blk][8 + 2 * c])};
+      // two elements (rows g and g + 8 of the MMA) of keys 0, 1 and 2, 3
+      auto values = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+        const uint32_t va[4] = {mul2(a0, rel[0]), mul2(a1, rel[0]), mul2(a2, rel[1]), mul2(a3, rel[1])};
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float from = m[r] == -INFINITY ? 0.0f : m[r];
-        float w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          w[j] = exp2_approx(x[j >> 1][2 * r + (j & 1)] - from);
-          l[r] = fmaf(w[j], e_inv[j], l[r]);
-        }
-        pa[r] = pack_f16(w[0], w[1]);
-        pa[2 + r] = pack_f16(w[2], w[3]);
-      }
-      const uint32_t m01 = v_mult[0] | (v_mult[1] << 16), m23 = v_mult[2] | (v_mult[3] << 16);
+        for (int r = 0; r < NT; ++r) mma_f16(o[r][i], va, pb[r][0], pb[r][1]);
+      };
 #pragma unroll
       for (int i = 0; i < Sh::kVWords; ++i) {
         if (E2M1) {
@@ -409,21 +468,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           const uint32_t even23 = (vw[2][i] & 0x0F0F0F0Fu) | ((vw[3][i] & 0x0F0F0F0Fu) << 4);
           const uint32_t odd23 = ((vw[2][i] >> 4) & 0x0F0F0F0Fu) | (vw[3][i] & 0xF0F0F0F0u);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            mma_f16(o[8 * i + 2 * k], pa, mul2(f16x2_of_e2m1x2((even01 >> (8 * k)) & 0xFFu), m01),
-                    mul2(f16x2_of_e2m1x2((even23 >> (8 * k)) & 0xFFu), m23));
-            mma_f16(o[8 * i + 2 * k + 1], pa, mul2(f16x2_of_e2m1x2((odd01 >> (8 * k)) & 0xFFu), m01),
-                    mul2(f16x2_of_e2m1x2((odd23 >> (8 * k)) & 0xFFu), m23));
-          }
+          for (int k = 0; k < 4; ++k)
+            values(4 * i + k, f16x2_of_e2m1x2((even01 >> (8 * k)) & 0xFFu), f16x2_of_e2m1x2((odd01 >> (8 * k)) & 0xFFu),
+                   f16x2_of_e2m1x2((even23 >> (8 * k)) & 0xFFu), f16x2_of_e2m1x2((odd23 >> (8 * k)) & 0xFFu));
         } else {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint32_t sel = k == 0 ? 0x5140u : 0x7362u;
             const uint32_t y01 = __byte_perm(vw[0][i], vw[1][i], sel), y23 = __byte_perm(vw[2][i], vw[3][i], sel);
-            mma_f16(o[4 * i + 2 * k], pa, mul2(f16x2_of_e4m3x2(y01 & 0xFFFFu), m01),
-                    mul2(f16x2_of_e4m3x2(y23 & 0xFFFFu), m23));
-            mma_f16(o[4 * i + 2 * k + 1], pa, mul2(f16x2_of_e4m3x2(y01 >> 16), m01),
-                    mul2(f16x2_of_e4m3x2(y23 >> 16), m23));
+            values(2 * i + k, f16x2_of_e4m3x2(y01 & 0xFFFFu), f16x2_of_e4m3x2(y01 >> 16), f16x2_of_e4m3x2(y23 & 0xFFFFu),
+                   f16x2_of_e4m3x2(y23 >> 16));
           }
         }
       }
@@ -433,42 +487,44 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // ---------------------------------------------------------------- join the warps
     // in two steps: warps 2 and 3 hand theirs to 0 and 1
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (c == 0) {
-        s_m[warp][g + 8 * r] = m[r];
-        s_l[warp][g + 8 * r] = l[r];
+    for (int r = 0; r < NT; ++r)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[r][k] += __shfl_xor_sync(0xffffffffu, l[r][k], d);
+        if (g == 0) {
+          s_m[warp][8 * r + 2 * c + k] = m[r][k];
+          s_l[warp][8 * r + 2 * c + k] = l[r][k];
+        }
       }
-    }
-    // column n of output tile i is element n * D / 8 + i
-    auto mine = [&](int r, int k, int i) {
-      return reinterpret_cast<float4*>(s_o + ((warp & 1) * kRows + g + 8 * r) * D + (2 * c + k) * (D / 8) + i);
+    auto mine = [&](int row, int i) {
+      return reinterpret_cast<float4*>(s_o + ((warp & 1) * kRows + row) * D + g * (D / 8) + 2 * i);
     };
     if (warp >= 2) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < NT; ++r)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int i = 0; i < Sh::kTiles; i += 4)
-            *mine(r, k, i) = make_float4(o[i][2 * r + k], o[i + 1][2 * r + k], o[i + 2][2 * r + k], o[i + 3][2 * r + k]);
+          for (int i = 0; i < Sh::kTiles; i += 2)
+            *mine(8 * r + 2 * c + k, i) = make_float4(o[r][i][k], o[r][i][2 + k], o[r][i + 1][k], o[r][i + 1][2 + k]);
     }
     meet();
     if (warp < 2) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float other = s_m[warp + 2][g + 8 * r], M = fmaxf(m[r], other), from = M == -INFINITY ? 0.0f : M;
-        const float f = exp2_approx(m[r] - from), h = exp2_approx(other - from);
+      for (int r = 0; r < NT; ++r)
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 2; ++k) {
+          const int row = 8 * r + 2 * c + k;
+          const float own = m[r][k], other = s_m[warp + 2][row], M = fmaxf(own, other), from = M == -INFINITY ? 0.0f : M;
+          const float f = exp2_approx(own - from), h = exp2_approx(other - from);
 #pragma unroll
-          for (int i = 0; i < Sh::kTiles; i += 4) {
-            const float4 v = *mine(r, k, i);
-            *mine(r, k, i) = make_float4(fmaf(o[i][2 * r + k], f, v.x * h), fmaf(o[i + 1][2 * r + k], f, v.y * h),
-                                         fmaf(o[i + 2][2 * r + k], f, v.z * h), fmaf(o[i + 3][2 * r + k], f, v.w * h));
+          for (int i = 0; i < Sh::kTiles; i += 2) {
+            const float4 v = *mine(row, i);
+            *mine(row, i) = make_float4(fmaf(o[r][i][k], f, v.x * h), fmaf(o[r][i][2 + k], f, v.y * h),
+                                        fmaf(o[r][i + 1][k], f, v.z * h), fmaf(o[r][i + 1][2 + k], f, v.w * h));
           }
-      }
+        }
     }
     meet();
 
@@ -481,14 +537,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const int R = tile * kRows + r;
       const int tok = R / a.group;
       const int64_t oh = static_cast<int64_t>(s.q0 + tok) * n_heads + head * a.group + (R - tok * a.group);
-      const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
       const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
       const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
       uint2 w;
       w.x = *reinterpret_cast<const uint32_t*>(&lo);
       w.y = *reinterpret_cast<const uint32_t*>(&hi);
       reinterpret_cast<uint2*>(a.out)[oh * (D / 4) + d4] = w;
-      if (a.lse && d4 == 0) a.lse[oh] = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+      if (a.lse && d4 == 0) a.lse[oh] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
     };
     constexpr int kLanes = D / 4;  // lanes of a row
     for (int i = tid; i < kRows * kLanes; i += 32 * kWarps) {
@@ -552,9 +608,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
 }
 
-template <int D, bool E2M1>
+template <int D, bool E2M1, int NT>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
-  using Sh = RowsShape<D, E2M1>;
+  using Sh = RowsShape<D, E2M1, NT>;
   constexpr int kSmem = Sh::kBytes + 1024;
   constexpr int kMaxDevices = 64;
   static std::atomic<bool> ready[kMaxDevices];
@@ -563,7 +619,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(k_attn_rows<D, E2M1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(k_attn_rows<D, E2M1, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
   }
@@ -571,7 +627,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   e = attn_code_map(&k_map, a, a.k_codes, Sh::kRowBytes, true);
   if (e == cudaSuccess) e = attn_code_map(&v_map, a, a.v_codes, Sh::kRowBytes, true);
   if (e != cudaSuccess) return e;
-  k_attn_rows<D, E2M1><<<sms * kCtasPerSm < kAttnMaxCtas ? sms * kCtasPerSm : kAttnMaxCtas, kThreads, kSmem, s>>>(a, k_map, v_map);
+  k_attn_rows<D, E2M1, NT><<<sms * kCtasPerSm < kAttnMaxCtas ? sms * kCtasPerSm : kAttnMaxCtas, kThreads, kSmem, s>>>(a, k_map, v_map);
   return cudaGetLastError();
 }
 
@@ -584,14 +640,18 @@ cudaError_t attn_sm_count(int* sms) {
 }
 
 size_t attn_rows_part_bytes(int head_dim) {
-  return static_cast<size_t>(2) * kAttnMaxCtas * kRows * (sizeof(float2) + sizeof(float) * head_dim);
+  return static_cast<size_t>(2) * kAttnMaxCtas * kMostRows * (sizeof(float2) + sizeof(float) * head_dim);
 }
 
 cudaError_t launch_attn_rows(AttnArgs a, cudaStream_t s) {
   a.min_units = kMinUnits;
-  a.part_o = reinterpret_cast<float*>(a.part_ml + static_cast<size_t>(2) * kAttnMaxCtas * kRows);
-  if (a.head_dim == 128) return a.e2m1 ? launch<128, true>(a, s) : launch<128, false>(a, s);
-  return a.e2m1 ? launch<64, true>(a, s) : launch<64, false>(a, s);
+  a.part_o = reinterpret_cast<float*>(a.part_ml + static_cast<size_t>(2) * kAttnMaxCtas * kMostRows);
+  if (a.max_q_len * a.group <= 8) {
+    if (a.head_dim == 128) return a.e2m1 ? launch<128, true, 1>(a, s) : launch<128, false, 1>(a, s);
+    return a.e2m1 ? launch<64, true, 1>(a, s) : launch<64, false, 1>(a, s);
+  }
+  if (a.head_dim == 128) return a.e2m1 ? launch<128, true, 2>(a, s) : launch<128, false, 2>(a, s);
+  return a.e2m1 ? launch<64, true, 2>(a, s) : launch<64, false, 2>(a, s);
 }
 
 }  // namespace mxk
