@@ -68,13 +68,13 @@ constexpr size_t kArrivedBytes = sizeof(unsigned) * kAttnMaxCtas;
 
 // Sequences of up to this many rows (new tokens x query heads of a KV head) are
 // the few-rows kernel's, others the chunk kernel's.  The few-rows kernel works
-// through the keys again for every 16 rows, the chunk kernel takes as long for
+// through the keys again for every 8 rows, the chunk kernel takes as long for
 // 256 as for one but starts and ends slower: over 8 sequences of 8192 tokens and
-// 4 KV heads, 16 rows took 43 us against 54, and 32 rows are even.  With few
-// (sequence, KV head) pairs the start weighs more: 48 rows over 2 pairs of 2051
-// keys took 27 us against 38.
-constexpr int kMostFewRows = 64;
-int few_rows(int n_seqs, int n_kv_heads) { return static_cast<int64_t>(n_seqs) * n_kv_heads <= 16 ? kMostFewRows : 32; }
+// 4 KV heads, 16 rows took 35 us against 52, 24 46 against 52, 32 58 against 52.
+// With few (sequence, KV head) pairs the start weighs more: over 2 pairs of 2051
+// keys, 128 rows took 24 us against 41, 192 37 against 45.
+constexpr int kMostFewRows = 128;
+int few_rows(int n_seqs, int n_kv_heads) { return static_cast<int64_t>(n_seqs) * n_kv_heads <= 16 ? kMostFewRows : 24; }
 
 int check_attention(int T, int n_seqs, int n_heads, int n_kv_heads, int head_dim, int max_q_len) {
   if (T < 0 || n_seqs < 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || max_q_len < 0) return MX_ERR_INVALID_ARG;
@@ -175,9 +175,9 @@ int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride
   if (cache->page_size % 16) return MX_ERR_UNSUPPORTED;
   // cache rows are counted in ints
   if (static_cast<int64_t>(cache->num_pages) * cache->page_size > INT_MAX / cache->n_kv_heads) return MX_ERR_UNSUPPORTED;
-  // Places of work are counted in 32 bits.  At most: 256-row tiles, and 16-row
+  // Places of work are counted in 32 bits.  At most: 256-row tiles, and 8-row
   // ones of the sequences with few rows, times 64-key units and a tile's cost.
-  const double tiles = static_cast<double>(T) * (n_heads / cache->n_kv_heads) / 256 + n_seqs * (1.0 + kMostFewRows / 16);
+  const double tiles = static_cast<double>(T) * (n_heads / cache->n_kv_heads) / 256 + n_seqs * (1.0 + kMostFewRows / 8);
   if (tiles * cache->n_kv_heads * (static_cast<double>(max_pages) * cache->page_size / 64 + 32) > 4.0e9)
     return MX_ERR_UNSUPPORTED;
   if (T == 0 || n_seqs == 0 || max_q_len == 0) return MX_OK;
@@ -207,6 +207,8 @@ int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride
   a.max_pages = max_pages;
   a.T = T;
   a.group = n_heads / cache->n_kv_heads;
+  a.group_div = FastDiv::by(a.group);
+  a.page_div = FastDiv::by(a.page_size);
   a.max_q_len = max_q_len;
   a.causal = causal != 0;
   a.window = window;

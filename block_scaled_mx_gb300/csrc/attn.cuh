@@ -68,12 +68,12 @@ __device__ __noinline__ AttnTile attn_tile(const AttnArgs& a, const AttnSeq& s, 
   t.hi = s.kv;
   const int base = s.kv - s.n;  // the position of the first new token
   if (a.causal) {
-    const int last = min(((tile + 1) * kRows - 1) / a.group, s.n - 1);
+    const int last = min(a.group_div.of((tile + 1) * kRows - 1), s.n - 1);
     t.hi = min(s.kv, max(base + last + 1, 0));
   }
   if (a.window > 0) {
     // in 64 bits: base may be negative and the window as large as an int
-    const int64_t lo = static_cast<int64_t>(base) + tile * kRows / a.group + 1 - a.window;
+    const int64_t lo = static_cast<int64_t>(base) + a.group_div.of(tile * kRows) + 1 - a.window;
     t.lo = static_cast<int>(lo < 0 ? 0 : lo);
   }
   t.lo = min(t.lo, t.hi);
@@ -290,7 +290,7 @@ struct AttnWalk {
   __device__ __forceinline__ void start(const AttnArgs& a, const Cursor& c, int group) {
     table = a.block_table + static_cast<int64_t>(c.b) * a.max_pages;
     const int first = c.t.first + c.place * kUnit;
-    entry = (first + 16 * group) / a.page_size;
+    entry = a.page_div.of(first + 16 * group);
     off = first + 16 * group - entry * a.page_size;
     lo = c.t.lo - first;
     hi = c.t.hi - first;

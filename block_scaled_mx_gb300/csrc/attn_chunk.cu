@@ -289,7 +289,7 @@ __device__ __noinline__ void load_queries(const AttnArgs& a, Shared& sh, uint8_t
   auto load = [&](int r) {
     const int R = row0 + r;
     if (r >= 128 || R >= rows) return make_uint4(0u, 0u, 0u, 0u);
-    const int tok = R / a.group;
+    const int tok = a.group_div.of(R);
     return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
                                                 static_cast<int64_t>(q0 + tok) * a.q_stride +
                                                 static_cast<int64_t>(head * a.group + (R - tok * a.group)) * D) + p);
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
       if (row0 < rows) {
         const int R = row0 + row;
         const bool valid = R < rows;
-        const int tok = valid ? R / a.group : 0;
+        const int tok = valid ? a.group_div.of(R) : 0;
         const int at = cur.s.kv - cur.s.n + tok;
         // rows past the last see everything: their queries are zero
         const int hi = !valid ? INT_MAX : a.causal ? min(cur.s.kv, max(at + 1, 0)) : cur.s.kv;

@@ -1,7 +1,7 @@
 // Attention of few new tokens over the paged MX cache (decoding, verifying
 // drafts): flash-decoding on register-level MMAs, bound by reading the cache.
 //
-// A tile is 8 or 16 rows (new tokens x the query heads of one KV head), so the
+// A tile is 8 rows (new tokens x the query heads of one KV head), so the
 // cache is read once for all heads that share it.  A fifth warp fetches units of
 // 64 keys ahead by TMA, over the segments' borders; four warps take 16 keys each
 // of a unit and keep their own running maximum, sum and accumulator, joined when
@@ -9,8 +9,9 @@
 //
 // Both products are transposed, S^T = K Q^T and O^T += V^T P^T, so that the query
 // rows are the MMAs' columns, of which there are 8 where there are 16 rows of
-// keys or elements: with up to 8 query rows nothing of an MMA is wasted, and the
-// widened codes are used again for the next 8.  P^T goes from the layout of S^T's
+// keys or elements.  More rows are more tiles, which read the keys again, mostly
+// from L2: tiles of 16 rows share the widened codes, but their registers spill
+// (8 sequences of 8192 and 4 KV heads, 16 rows: 53 us, as two tiles 39).  P^T goes from the layout of S^T's
 // results to that of an operand by a transposing move.  The contraction order of
 // an MMA is free, so a lane feeds it the 16-byte pieces that it reads from shared
 // memory.  (The MMAs on 8-bit codes are no way around the widening: the compiler
@@ -40,13 +41,15 @@ namespace mxk {
 
 namespace {
 
-constexpr int kMostRows = 16;              // of a tile
+constexpr int kRows = 8;                   // of a tile
 constexpr int kUnit = 64;
 constexpr int kWarps = 4;                  // that compute
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kCtasPerSm = 3;
 constexpr int kMinUnits = 4;
-constexpr int kCost = 1;                   // a segment's queries and output, in units
+// A segment's queries and output, in units (32 sequences of up to 8192: 76 us with
+// 1, 68 with 4, 65 with 8).
+constexpr int kCost = 8;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -62,6 +65,15 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 r = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The E2M1 codes at nibbles i and 4 + i of a word as two f16 of 2^-14 their size,
+// by moving their bits: the codes' conversion takes two instructions and, for
+// half of the bytes, a third.
+constexpr int kE2m1Shift = 14;
+__device__ __forceinline__ uint32_t f16x2_of_nibbles(uint32_t w, int i) {
+  const uint32_t size = i < 3 ? w << (9 - 4 * i) : w >> 3, sign = w << (12 - 4 * i);
+  return (size & 0x0E000E00u) | (sign & 0x80008000u);
 }
 
 // The warp's 8 x 8 matrix of 16-bit elements, transposed.
@@ -102,9 +114,8 @@ __device__ __forceinline__ uint32_t load_scales(const uint8_t* p, int row) {
   else return reinterpret_cast<const uint16_t*>(p)[row];
 }
 
-template <int D, bool E2M1, int NT>
+template <int D, bool E2M1>
 struct RowsShape {
-  static constexpr int kRows = 8 * NT;
   static constexpr int kBlocks = D / 32;                    // scales of a row
   static constexpr int kRowBytes = E2M1 ? D / 2 : D;
   static constexpr int kTiles = D / 16;                     // m = 16 tiles of the output
@@ -143,16 +154,15 @@ struct KeyTable {
   __half v_rel[4][16];     // a block's V scale relative to the key's largest
 };
 
-template <int D, bool E2M1, int NT>
+template <int D, bool E2M1>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     k_attn_rows(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap k_map,
                 const __grid_constant__ CUtensorMap v_map) {
-  using Sh = RowsShape<D, E2M1, NT>;
-  constexpr int kRows = Sh::kRows;
+  using Sh = RowsShape<D, E2M1>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[Sh::kStages], empty[Sh::kStages];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
-  __shared__ uint2 s_q[NT][Sh::kSteps][32];
+  __shared__ uint2 s_q[Sh::kSteps][32];
   __shared__ __align__(16) KeyTable s_table[kWarps];
   __shared__ int s_e[kRows];
   __shared__ uint32_t s_here[Sh::kStages];  // 16-key groups that are there
@@ -246,12 +256,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int old = s.kv - s.n;  // the position of the first new token
 
     // ---------------------------------------------------------------- queries
-    // as the scores' B fragments; warp r brings rows 8 r + g, their largest element
-    // scaled to [2^14, 2^15)
-    if (warp < NT) {
-      const int R = tile * kRows + g + 8 * warp;
+    // as the scores' B fragments, a row's largest element scaled to [2^14, 2^15)
+    if (warp == 0) {
+      const int R = tile * kRows + g;
       const bool valid = R < rows;
-      const int tok = valid ? R / a.group : 0;
+      const int tok = valid ? a.group_div.of(R) : 0;
       const int hq = head * a.group + (valid ? R - tok * a.group : 0);
       const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
                                                       static_cast<int64_t>(s.q0 + tok) * a.q_stride +
@@ -273,48 +282,45 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        uint32_t y[4];
+        float f[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = pack_f16(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xFFFF0000u) * up);
-        s_q[warp][2 * i][lane] = make_uint2(y[0], y[1]);
-        s_q[warp][2 * i + 1][lane] = make_uint2(y[2], y[3]);
+        for (int k = 0; k < 4; ++k) {
+          f[2 * k] = __uint_as_float(x[k] << 16) * up;
+          f[2 * k + 1] = __uint_as_float(x[k] & 0xFFFF0000u) * up;
+        }
+        uint32_t y[4];  // E2M1: elements k and 4 + k, as they come from a word of K
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = E2M1 ? pack_f16(f[k], f[4 + k]) : pack_f16(f[2 * k], f[2 * k + 1]);
+        s_q[2 * i][lane] = make_uint2(y[0], y[1]);
+        s_q[2 * i + 1][lane] = make_uint2(y[2], y[3]);
       }
-      if (c == 0) s_e[g + 8 * warp] = e;
+      if (c == 0) s_e[g] = e;
     }
     meet();
-    // of the lane's rows 8 r + 2 c + k
-    float row_fac[NT][2];
-    int row_lo[NT][2], row_hi[NT][2], all_hi = INT_MAX, all_lo = 0;  // keys in [all_lo, all_hi) need no mask
+    // of the lane's rows 2 c + k
+    float row_fac[2];
+    int row_lo[2], row_hi[2];
 #pragma unroll
-    for (int r = 0; r < NT; ++r)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int in = 8 * r + 2 * c + k, R = tile * kRows + in;
-        const int at = old + R / a.group;
-        row_fac[r][k] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(max(127 + s_e[in] - 14, 1)) << 23);
-        // rows past the tile's are zeros that nobody reads
-        row_hi[r][k] = R >= rows ? INT_MAX : a.causal ? min(s.kv, at + 1) : s.kv;
-        row_lo[r][k] = R < rows && a.window > 0 ? max(at - a.window + 1, 0) : 0;
-        all_hi = min(all_hi, row_hi[r][k]);
-        all_lo = max(all_lo, row_lo[r][k]);
-      }
-    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
-    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
-    uint2 qb[Sh::kSteps];  // of one row group: it stays in registers
-    if (NT == 1) {
-#pragma unroll
-      for (int st = 0; st < Sh::kSteps; ++st) qb[st] = s_q[0][st][lane];
+    for (int k = 0; k < 2; ++k) {
+      const int R = tile * kRows + 2 * c + k;
+      const int at = old + a.group_div.of(R);
+      row_fac[k] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(max(127 + s_e[2 * c + k] - 14, 1)) << 23);
+      // rows past the tile's are zeros that nobody reads
+      row_hi[k] = R >= rows ? INT_MAX : a.causal ? min(s.kv, at + 1) : s.kv;
+      row_lo[k] = R < rows && a.window > 0 ? max(at - a.window + 1, 0) : 0;
     }
+    // keys in [all_lo, all_hi) need no mask
+    const int all_hi = __reduce_min_sync(0xffffffffu, min(row_hi[0], row_hi[1]));
+    const int all_lo = __reduce_max_sync(0xffffffffu, max(row_lo[0], row_lo[1]));
+    uint2 qb[Sh::kSteps];
+#pragma unroll
+    for (int st = 0; st < Sh::kSteps; ++st) qb[st] = s_q[st][lane];
 
     // ---------------------------------------------------------------- keys and values
-    // o[r][i][k + 2 d]: row 8 r + 2 c + k, element g * D / 8 + 2 i + d
-    float o[NT][Sh::kTiles][4], m[NT][2], l[NT][2];
+    // o[i][k + 2 d]: row 2 c + k, element g * D / 8 + 2 i + d
+    float o[Sh::kTiles][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int r = 0; r < NT; ++r) {
-      m[r][0] = m[r][1] = -INFINITY, l[r][0] = l[r][1] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < Sh::kTiles; ++i) o[r][i][0] = o[r][i][1] = o[r][i][2] = o[r][i][3] = 0.0f;
-    }
+    for (int i = 0; i < Sh::kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
 #pragma unroll 1
     for (int i = 0; i < take; ++i, ring.next()) {
@@ -335,23 +341,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
         for (int p = 0; p < Sh::kPieces; ++p) load_words(k_codes + k_off[p] + j * 8 * Sh::kRowBytes, kw[j][p]);
       // the keys 2c, 2c + 1, 8 + 2c, 9 + 2c of the lane's operands
-      auto load_values = [&] {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) load_words(v_codes + v_off[j & 1] + (j >> 1) * 8 * Sh::kRowBytes, vw[j]);
-      };
-      if (NT == 1) load_values();  // else there are no registers for them yet
+      for (int j = 0; j < 4; ++j) load_words(v_codes + v_off[j & 1] + (j >> 1) * 8 * Sh::kRowBytes, vw[j]);
       {
         const uint32_t ks = load_scales<Sh::kBlocks>(k_scales, warp * 16 + (lane & 15));
         const uint32_t vs = load_scales<Sh::kBlocks>(v_scales, warp * 16 + (lane & 15));
         const int k_top = max_scale<Sh::kBlocks>(ks), e = min(max(max_scale<Sh::kBlocks>(vs) - 127, -100), 126);
-        constexpr int kHalf = Sh::kBlocks / 2;
+        constexpr int kHalf = Sh::kBlocks / 2, kShift = E2M1 ? kE2m1Shift : 0;
         const uint32_t kh = ks >> (8 * kHalf * half), vh = vs >> (8 * kHalf * half);
 #pragma unroll
         for (int b = 0; b < kHalf; ++b) {
-          const float kr = pow2_or_zero(static_cast<int>((kh >> (8 * b)) & 0xFFu) - k_top);
+          const float kr = pow2_or_zero(static_cast<int>((kh >> (8 * b)) & 0xFFu) - k_top + kShift);
           table.k_rel[kHalf * half + b][lane & 15] = pack_f16(kr, kr);
           table.v_rel[kHalf * half + b][lane & 15] =
-              __float2half_rn(pow2_or_zero(min(static_cast<int>((vh >> (8 * b)) & 0xFFu) - 127 - e, 2)));
+              __float2half_rn(pow2_or_zero(min(static_cast<int>((vh >> (8 * b)) & 0xFFu) - 127 - e, 1) + kShift));
         }
         table.key[lane & 15] = make_float4(e8m0_value(k_top), static_cast<float>(e),
                                            __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 0.0f);
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       // scores of keys g and g + 8 for the lane's rows
       const int k_blk = D == 128 ? c : c >> 1;  // of the lane's elements
       const uint32_t k_mult[2] = {table.k_rel[k_blk][g], table.k_rel[k_blk][g + 8]};
-      float x[NT][4] = {};
+      float x[4] = {};
 #pragma unroll
       for (int st = 0; st < Sh::kSteps; ++st) {
         uint32_t ka[4];
@@ -368,9 +371,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int j = 0; j < 2; ++j) {
           uint32_t b0, b1;
           if (E2M1) {
-            const uint32_t w = kw[j][0][st / 2] >> ((st & 1) * 16);
-            b0 = f16x2_of_e2m1x2(w & 0xFFu);
-            b1 = f16x2_of_e2m1x2((w >> 8) & 0xFFu);
+            // a word of eight elements for two steps; the queries lie in the same order
+            b0 = f16x2_of_nibbles(kw[j][0][st / 2], 2 * (st & 1));
+            b1 = f16x2_of_nibbles(kw[j][0][st / 2], 2 * (st & 1) + 1);
           } else {
             const uint32_t w = kw[j][st / 4][st % 4];
             b0 = f16x2_of_e4m3x2(w & 0xFFFFu);
@@ -379,27 +382,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           ka[j] = mul2(b0, k_mult[j]);
           ka[2 + j] = mul2(b1, k_mult[j]);
         }
-#pragma unroll
-        for (int r = 0; r < NT; ++r) {
-          const uint2 q2 = NT == 1 ? qb[st] : s_q[r][st][lane];
-          mma_f16(x[r], ka, q2.x, q2.y);
-        }
+        mma_f16(x, ka, qb[st].x, qb[st].y);
       }
-      if (NT > 1) load_values();
       const float4 key4[2] = {table.key[g], table.key[g + 8]};
-      // x[r][2 j + k]: key g + 8 j, row 8 r + 2 c + k
+      // x[2 j + k]: key g + 8 j, row 2 c + k
 #pragma unroll
-      for (int r = 0; r < NT; ++r)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[r][i] = fmaf(x[r][i], row_fac[r][i & 1] * key4[i >> 1].x, key4[i >> 1].y);
+      for (int i = 0; i < 4; ++i) x[i] = fmaf(x[i], row_fac[i & 1] * key4[i >> 1].x, key4[i >> 1].y);
       if (key + 16 > all_hi || key < all_lo) {
 #pragma unroll
-        for (int r = 0; r < NT; ++r)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int at = key + g + 8 * (i >> 1);
-            if (at >= row_hi[r][i & 1] || at < row_lo[r][i & 1]) x[r][i] = -INFINITY;
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int at = key + g + 8 * (i >> 1);
+          if (at >= row_hi[i & 1] || at < row_lo[i & 1]) x[i] = -INFINITY;
+        }
         // a place that no row sees may hold anything, NaN included
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -411,44 +405,35 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
       }
       // running maximum
-      bool above = false;
-#pragma unroll
-      for (int r = 0; r < NT; ++r)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) above = above || fmaxf(x[r][k], x[r][2 + k]) > m[r][k] + 8.0f;
+      const bool above = fmaxf(x[0], x[2]) > m[0] + 8.0f || fmaxf(x[1], x[3]) > m[1] + 8.0f;
       if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-        for (int r = 0; r < NT; ++r)
+        for (int k = 0; k < 2; ++k) {
+          float to = fmaxf(x[k], x[2 + k]);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float to = fmaxf(x[r][k], x[r][2 + k]);
+          for (int d = 4; d < 32; d <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
+          to = fmaxf(to, m[k]);
+          const float f = to == -INFINITY ? 1.0f : exp2_approx(m[k] - to);
+          m[k] = to;
+          l[k] *= f;
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
-            to = fmaxf(to, m[r][k]);
-            const float f = to == -INFINITY ? 1.0f : exp2_approx(m[r][k] - to);
-            m[r][k] = to;
-            l[r][k] *= f;
-#pragma unroll
-            for (int i = 0; i < Sh::kTiles; ++i) {
-              o[r][i][k] *= f;
-              o[r][i][2 + k] *= f;
-            }
+          for (int i = 0; i < Sh::kTiles; ++i) {
+            o[i][k] *= f;
+            o[i][2 + k] *= f;
           }
-      }
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int r = 0; r < NT; ++r) {
-        const float from[2] = {m[r][0] == -INFINITY ? 0.0f : m[r][0], m[r][1] == -INFINITY ? 0.0f : m[r][1]};
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float w[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            w[k] = exp2_approx(x[r][2 * j + k] - from[k]);
-            l[r][k] = fmaf(w[k], key4[j].z, l[r][k]);
-          }
-          pb[r][j] = transposed(pack_f16(w[0], w[1]));
         }
+      }
+      const float from[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+      uint32_t pb[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float w[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          w[k] = exp2_approx(x[2 * j + k] - from[k]);
+          l[k] = fmaf(w[k], key4[j].z, l[k]);
+        }
+        pb[j] = transposed(pack_f16(w[0], w[1]));
       }
       const int v_blk = D == 128 ? g >> 1 : g >> 2;
       const uint32_t rel[2] = {*reinterpret_cast<const uint32_t*>(&table.v_rel[v_blk][2 * c]),
@@ -456,21 +441,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       // two elements (rows g and g + 8 of the MMA) of keys 0, 1 and 2, 3
       auto values = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
         const uint32_t va[4] = {mul2(a0, rel[0]), mul2(a1, rel[0]), mul2(a2, rel[1]), mul2(a3, rel[1])};
-#pragma unroll
-        for (int r = 0; r < NT; ++r) mma_f16(o[r][i], va, pb[r][0], pb[r][1]);
+        mma_f16(o[i], va, pb[0], pb[1]);
       };
 #pragma unroll
       for (int i = 0; i < Sh::kVWords; ++i) {
         if (E2M1) {
-          // low nibbles are the even elements; a byte pairs one element of two keys
-          const uint32_t even01 = (vw[0][i] & 0x0F0F0F0Fu) | ((vw[1][i] & 0x0F0F0F0Fu) << 4);
-          const uint32_t odd01 = ((vw[0][i] >> 4) & 0x0F0F0F0Fu) | (vw[1][i] & 0xF0F0F0F0u);
-          const uint32_t even23 = (vw[2][i] & 0x0F0F0F0Fu) | ((vw[3][i] & 0x0F0F0F0Fu) << 4);
-          const uint32_t odd23 = ((vw[2][i] >> 4) & 0x0F0F0F0Fu) | (vw[3][i] & 0xF0F0F0F0u);
+          // four elements of two keys in a word
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            values(4 * i + k, f16x2_of_e2m1x2((even01 >> (8 * k)) & 0xFFu), f16x2_of_e2m1x2((odd01 >> (8 * k)) & 0xFFu),
-                   f16x2_of_e2m1x2((even23 >> (8 * k)) & 0xFFu), f16x2_of_e2m1x2((odd23 >> (8 * k)) & 0xFFu));
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t sel = h == 0 ? 0x5410u : 0x7632u;
+            const uint32_t w01 = __byte_perm(vw[0][i], vw[1][i], sel), w23 = __byte_perm(vw[2][i], vw[3][i], sel);
+#pragma unroll
+            for (int k = 0; k < 4; k += 2)
+              values(4 * i + 2 * h + k / 2, f16x2_of_nibbles(w01, k), f16x2_of_nibbles(w01, k + 1), f16x2_of_nibbles(w23, k),
+                     f16x2_of_nibbles(w23, k + 1));
+          }
         } else {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -487,44 +472,36 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // ---------------------------------------------------------------- join the warps
     // in two steps: warps 2 and 3 hand theirs to 0 and 1
 #pragma unroll
-    for (int r = 0; r < NT; ++r)
+    for (int k = 0; k < 2; ++k) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[r][k] += __shfl_xor_sync(0xffffffffu, l[r][k], d);
-        if (g == 0) {
-          s_m[warp][8 * r + 2 * c + k] = m[r][k];
-          s_l[warp][8 * r + 2 * c + k] = l[r][k];
-        }
+      for (int d = 4; d < 32; d <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], d);
+      if (g == 0) {
+        s_m[warp][2 * c + k] = m[k];
+        s_l[warp][2 * c + k] = l[k];
       }
-    auto mine = [&](int row, int i) {
-      return reinterpret_cast<float4*>(s_o + ((warp & 1) * kRows + row) * D + g * (D / 8) + 2 * i);
+    }
+    auto mine = [&](int k, int i) {
+      return reinterpret_cast<float4*>(s_o + ((warp & 1) * kRows + 2 * c + k) * D + g * (D / 8) + 2 * i);
     };
     if (warp >= 2) {
 #pragma unroll
-      for (int r = 0; r < NT; ++r)
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int i = 0; i < Sh::kTiles; i += 2)
-            *mine(8 * r + 2 * c + k, i) = make_float4(o[r][i][k], o[r][i][2 + k], o[r][i + 1][k], o[r][i + 1][2 + k]);
+        for (int i = 0; i < Sh::kTiles; i += 2) *mine(k, i) = make_float4(o[i][k], o[i][2 + k], o[i + 1][k], o[i + 1][2 + k]);
     }
     meet();
     if (warp < 2) {
 #pragma unroll
-      for (int r = 0; r < NT; ++r)
+      for (int k = 0; k < 2; ++k) {
+        const float other = s_m[warp + 2][2 * c + k], M = fmaxf(m[k], other), from = M == -INFINITY ? 0.0f : M;
+        const float f = exp2_approx(m[k] - from), h = exp2_approx(other - from);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int row = 8 * r + 2 * c + k;
-          const float own = m[r][k], other = s_m[warp + 2][row], M = fmaxf(own, other), from = M == -INFINITY ? 0.0f : M;
-          const float f = exp2_approx(own - from), h = exp2_approx(other - from);
-#pragma unroll
-          for (int i = 0; i < Sh::kTiles; i += 2) {
-            const float4 v = *mine(row, i);
-            *mine(row, i) = make_float4(fmaf(o[r][i][k], f, v.x * h), fmaf(o[r][i][2 + k], f, v.y * h),
-                                        fmaf(o[r][i + 1][k], f, v.z * h), fmaf(o[r][i + 1][2 + k], f, v.w * h));
-          }
+        for (int i = 0; i < Sh::kTiles; i += 2) {
+          const float4 v = *mine(k, i);
+          *mine(k, i) = make_float4(fmaf(o[i][k], f, v.x * h), fmaf(o[i][2 + k], f, v.y * h), fmaf(o[i + 1][k], f, v.z * h),
+                                    fmaf(o[i + 1][2 + k], f, v.w * h));
         }
+      }
     }
     meet();
 
@@ -535,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // writes a finished row: four elements a lane
     auto finish = [&](int r, int d4, float4 acc, float M, float L) {
       const int R = tile * kRows + r;
-      const int tok = R / a.group;
+      const int tok = a.group_div.of(R);
       const int64_t oh = static_cast<int64_t>(s.q0 + tok) * n_heads + head * a.group + (R - tok * a.group);
       const float inv = L == 0.0f ? 0.0f : 1.0f / L;
       const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
@@ -608,9 +585,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
 }
 
-template <int D, bool E2M1, int NT>
+template <int D, bool E2M1>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
-  using Sh = RowsShape<D, E2M1, NT>;
+  using Sh = RowsShape<D, E2M1>;
   constexpr int kSmem = Sh::kBytes + 1024;
   constexpr int kMaxDevices = 64;
   static std::atomic<bool> ready[kMaxDevices];
@@ -619,7 +596,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(k_attn_rows<D, E2M1, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(k_attn_rows<D, E2M1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
   }
@@ -627,7 +604,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   e = attn_code_map(&k_map, a, a.k_codes, Sh::kRowBytes, true);
   if (e == cudaSuccess) e = attn_code_map(&v_map, a, a.v_codes, Sh::kRowBytes, true);
   if (e != cudaSuccess) return e;
-  k_attn_rows<D, E2M1, NT><<<sms * kCtasPerSm < kAttnMaxCtas ? sms * kCtasPerSm : kAttnMaxCtas, kThreads, kSmem, s>>>(a, k_map, v_map);
+  k_attn_rows<D, E2M1><<<sms * kCtasPerSm < kAttnMaxCtas ? sms * kCtasPerSm : kAttnMaxCtas, kThreads, kSmem, s>>>(a, k_map, v_map);
   return cudaGetLastError();
 }
 
@@ -640,18 +617,14 @@ cudaError_t attn_sm_count(int* sms) {
 }
 
 size_t attn_rows_part_bytes(int head_dim) {
-  return static_cast<size_t>(2) * kAttnMaxCtas * kMostRows * (sizeof(float2) + sizeof(float) * head_dim);
+  return static_cast<size_t>(2) * kAttnMaxCtas * kRows * (sizeof(float2) + sizeof(float) * head_dim);
 }
 
 cudaError_t launch_attn_rows(AttnArgs a, cudaStream_t s) {
   a.min_units = kMinUnits;
-  a.part_o = reinterpret_cast<float*>(a.part_ml + static_cast<size_t>(2) * kAttnMaxCtas * kMostRows);
-  if (a.max_q_len * a.group <= 8) {
-    if (a.head_dim == 128) return a.e2m1 ? launch<128, true, 1>(a, s) : launch<128, false, 1>(a, s);
-    return a.e2m1 ? launch<64, true, 1>(a, s) : launch<64, false, 1>(a, s);
-  }
-  if (a.head_dim == 128) return a.e2m1 ? launch<128, true, 2>(a, s) : launch<128, false, 2>(a, s);
-  return a.e2m1 ? launch<64, true, 2>(a, s) : launch<64, false, 2>(a, s);
+  a.part_o = reinterpret_cast<float*>(a.part_ml + static_cast<size_t>(2) * kAttnMaxCtas * kRows);
+  if (a.head_dim == 128) return a.e2m1 ? launch<128, true>(a, s) : launch<128, false>(a, s);
+  return a.e2m1 ? launch<64, true>(a, s) : launch<64, false>(a, s);
 }
 
 }  // namespace mxk

@@ -131,6 +131,19 @@ cudaError_t launch_kv_read(const KvArgs& a, cudaStream_t s);
 
 // ---- attn_rows.cu, attn_chunk.cu
 constexpr int kAttnMaxCtas = 608;                    // 152 SMs x 4: partial slots and counters of the workspace
+// Division by a number that the host knows, of 0 <= n < 2^31, in three
+// instructions: with 2^l >= d the error of m = 2^(31 + l) / d + 1 is below 1 / n.
+struct FastDiv {
+  uint32_t m;
+  int shift;
+  static FastDiv by(int d) {
+    int l = 0;
+    while ((1ll << l) < d) ++l;
+    return {static_cast<uint32_t>((1ull << (31 + l)) / d + 1), 31 + l};
+  }
+  __host__ __device__ int of(int n) const { return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * m) >> shift); }
+};
+
 struct AttnArgs {
   const void* q;                                     // bf16 [T, n_heads, head_dim]
   int64_t q_stride;                                  // elements between tokens
@@ -140,6 +153,7 @@ struct AttnArgs {
   const int32_t* kv_lens;
   const int32_t* q_starts;
   int n_seqs, max_pages, T, group;                   // group: query heads of one KV head
+  FastDiv group_div, page_div;
   int max_q_len, causal, window;
   float scale_log2;                                  // softmax scale * log2(e)
   int rows_above, rows_upto;                         // the sequences (by rows) this launch handles
