@@ -114,7 +114,7 @@ struct AttnShare {
 constexpr int kAttnScan = 128;  // sequences looked at together
 
 // Block-wide (kThreads threads); `units` holds kAttnScan words.  kWarp: a warp
-// counts a sequence (long ones have hundreds of tiles), else a thread.
+// counts a sequence of several tiles (long ones have hundreds), else a thread.
 template <int kRows, int kUnit, int kCost, int kThreads, bool kWarp>
 __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, uint32_t* units) {
   const int tid = threadIdx.x, lane = tid & 31;
@@ -131,15 +131,28 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, uint32_t* uni
 #pragma unroll 1
     for (int b0 = 0; b0 < a.n_seqs; b0 += kAttnScan) {
       if (pass == 0 || a.n_seqs > kAttnScan) {
-        for (int i = kWarp ? tid / 32 : tid; i < kAttnScan; i += kWarp ? kThreads / 32 : kThreads) {
+        // a thread a sequence, and then a warp each of those with several tiles
+        // (kWarp), which are marked
+        constexpr uint32_t kLong = ~0u;
+        for (int i = tid; i < kAttnScan; i += kThreads) {
           uint32_t u = 0;
           if (b0 + i < a.n_seqs) {
             const AttnSeq s = attn_seq<kRows>(a, b0 + i, pass == 0 && blockIdx.x == 0);
-            u = static_cast<uint32_t>(attn_seq_places<kRows, kUnit, kCost, kWarp>(a, s)) * a.n_kv_heads;
+            if (kWarp && s.tiles > 1) u = kLong;
+            else u = static_cast<uint32_t>(attn_seq_places<kRows, kUnit, kCost, false>(a, s)) * a.n_kv_heads;
           }
-          if (!kWarp || lane == 0) units[i] = u;
+          units[i] = u;
         }
         __syncthreads();
+        if (kWarp) {
+          for (int i = tid / 32; i < kAttnScan && b0 + i < a.n_seqs; i += kThreads / 32) {
+            if (units[i] != kLong) continue;
+            const AttnSeq s = attn_seq<kRows>(a, b0 + i, false);
+            const uint32_t u = static_cast<uint32_t>(attn_seq_places<kRows, kUnit, kCost, true>(a, s)) * a.n_kv_heads;
+            if (lane == 0) units[i] = u;
+          }
+          __syncthreads();
+        }
         mine = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) mine += v[i] = units[lane * kPer + i];

@@ -120,6 +120,7 @@ struct Shared {
   int last[2];
   UnitMeta meta[kMetaRing];
   uint32_t q_scale[2][128];  // a row's scale bytes
+  alignas(16) uint4 rows[8][32][4];  // a warp's finished rows on their way to the output, 32 elements of each
   alignas(128) uint32_t k_scale[kStages][32][4];  // keys 32 j + lane, by lane
   UnitKeys keys[kRawStages];
   uint32_t units[kAttnScan];
@@ -264,7 +265,7 @@ __device__ __forceinline__ void put(const AttnArgs& a, int64_t oh, int c, const 
                         pack_bf16(v[8 * i + 4] * inv, v[8 * i + 5] * inv), pack_bf16(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
 }
 __device__ __forceinline__ void put_lse(const AttnArgs& a, int64_t oh, float M, float L) {
-  if (a.lse) a.lse[oh] = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+  if (a.lse) a.lse[oh] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 // Four elements of a row of a part: the same elements of all rows side by side.
 template <int D>
@@ -315,7 +316,8 @@ __device__ __noinline__ void load_queries(const AttnArgs& a, Shared& sh, uint8_t
       // the block's largest element lands in [2^7, 2^8): hi's rounding error
       // is then at most 2^3 and 2^5 times it stays below E4M3's 448
       const int s = max(static_cast<int>(amax >> 7) - 127 - 7, -122);
-      const float down = pow2_neg(s);
+      // a block with an infinity or NaN has no scores
+      const float down = amax >= 0x7F80u ? __uint_as_float(0x7FC00000u) : pow2_neg(s);
       uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -405,7 +407,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, AttnParts p, int r
         f[4 * k + 2] = fmaf(v.z, w, f[4 * k + 2]), f[4 * k + 3] = fmaf(v.w, w, f[4 * k + 3]);
       }
     }
-    put<D>(a, oh, c, f, L > 0.0f ? 1.0f / L : 0.0f);
+    put<D>(a, oh, c, f, L == 0.0f ? 0.0f : 1.0f / L);
   }
   put_lse(a, oh, M, L);
 }
@@ -416,29 +418,59 @@ template <int D>
 __device__ __noinline__ void write_rows(const AttnArgs& a, Shared& sh, uint32_t o_col, int x, int slot, AttnParts parts,
                                         int64_t oh, bool ok, bool warp_valid, bool valid, float m, float l) {
   const int row = threadIdx.x & 127;
-  if (ok && warp_valid) {
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const int lane = threadIdx.x & 31;
+  if (ok && warp_valid && slot < 0) {
+    // 32 elements of every row at a time by way of shared memory: a warp's store
+    // is then eight rows of 64 bytes, not 32 of 16 (64 new tokens over 256 keys
+    // of 114 sequences and 8 KV heads: 128 -> 115 us)
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint4(&stage)[32][4] = sh.rows[threadIdx.x >> 5];
+    // of the rows that the lane stores
+    int64_t at[4];
+    bool there[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      at[i] = __shfl_sync(0xffffffffu, oh, 8 * i + lane / 4) * D + lane % 4 * 8;
+      there[i] = __shfl_sync(0xffffffffu, static_cast<int>(valid), 8 * i + lane / 4);
+    }
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(o_col + c, v);
+      tmem_ld_wait();
+      // a row without a visible key never had its accumulator's weights defined
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        w[i] = l == 0.0f ? 0u : pack_bf16(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        stage[lane][i ^ (lane >> 1 & 3)] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + lane / 4;
+        if (there[i]) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at[i] + c) = stage[r][lane % 4 ^ (r >> 1 & 3)];
+      }
+      __syncwarp();
+    }
+    if (valid) put_lse(a, oh, m, l);
+  } else if (ok && warp_valid) {
 #pragma unroll 1
     for (int c = 0; c < D; c += 16) {
       uint32_t v[16];
       tmem_ld_32x32b_x16(o_col + c, v);
       tmem_ld_wait();
       float f[16];
-      // a row without a visible key never had its accumulator's weights defined
 #pragma unroll
-      for (int i = 0; i < 16; ++i) f[i] = l > 0.0f ? __uint_as_float(v[i]) : 0.0f;
-      if (valid && slot < 0) {
-        put<D>(a, oh, c, f, inv);
-      } else if (valid) {
+      for (int i = 0; i < 16; ++i) f[i] = l == 0.0f ? 0.0f : __uint_as_float(v[i]);
+      if (valid) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) *part_at<D>(a, slot, c / 4 + i, 128 * x + row) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
       }
       __syncwarp();
     }
-    if (valid) {
-      if (slot < 0) put_lse(a, oh, m, l);
-      else a.part_ml[slot * kRows + 128 * x + row] = make_float2(m, l);
-    }
+    if (valid) a.part_ml[slot * kRows + 128 * x + row] = make_float2(m, l);
   }
   if (slot < 0) return;
   // also after a wait that ran out: the counters are zero for the next call
