@@ -8,10 +8,11 @@
 // the device: ragged batches stay balanced and the host needs no lengths.  In
 // front of each segment's units the line has kCost places that hold no work:
 // what a segment costs beside its keys (its queries, its output), in units, so
-// that a CTA with many short segments gets fewer keys.  A stretch ends inside at most two segments (a segment is one row tile's keys);
-// those leave their accumulator and softmax statistics in the workspace, and
-// the last CTA to arrive at a segment joins its parts, always in key order, so
-// results do not depend on which one that is.
+// that a CTA with many short segments gets fewer keys.  A stretch ends inside at
+// most two segments (a segment is one row tile's keys); those leave their
+// accumulator and softmax statistics in the workspace, and the last CTA to arrive
+// at a segment joins its parts, always in key order, so results do not depend on
+// which one that is.
 #pragma once
 #include <cstdint>
 #include <cuda_runtime.h>

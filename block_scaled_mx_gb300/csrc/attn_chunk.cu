@@ -1,6 +1,16 @@
 // Attention of chunks of new tokens over the paged MX cache on the tensor
-// cores: tcgen05 MMAs with the accumulators in tensor memory, bound by the
-// MMAs (4 * head_dim flops for each visible (row, key) pair).
+// cores: tcgen05 MMAs with the accumulators in tensor memory.
+//
+// What bounds it.  With heads of 128 a unit of 64 keys and 256 rows is 1024
+// cycles of MMAs at their rate; it takes 1770: the 8-bit MMAs read Q again for
+// every unit (64 KB of the 128 KB that a unit's operands are, at 128 bytes a
+// cycle), which tensor memory, full, cannot hold, and the softmax's two warps a
+// scheduler need about as long.  With heads of 64 the softmax alone bounds a
+// unit (1560).  A segment costs 17 (10) units more: queries split into their
+// two parts, the accumulator written out, the first keys of the next on their
+// way through empty stages.  2048 new tokens behind 14336 take 419 us (1230
+// TFLOP/s of 4 head_dim flops for each visible (row, key) pair, 64% of a plain
+// bf16 product's), a prompt of 8192 518 us (1060).
 //
 // A tile is 256 rows (new tokens x the query heads of one KV head) as two MMA
 // tiles of 128, A and B, that take turns: while the tensor cores work for one,
@@ -49,8 +59,10 @@ namespace {
 constexpr int kRows = 256;
 constexpr int kThreads = 512;
 constexpr int kMaxCtas = 152;
-constexpr int kMinUnits = 20;
-constexpr int kCost = 16;      // a segment's queries and output take as long as that many units
+constexpr int kMinUnits = 20;  // places of a CTA's stretch at least
+// A segment's queries and output, in units (a prompt of 8192: 518 us with 16, 539
+// with 12, 527 with 20).
+constexpr int kCost = 16;
 constexpr int kStages = 4;     // of K and of V
 constexpr int kRawStages = 4;  // of codes on their way to V
 constexpr int kMetaRing = 8;  // more units than can be between their scales' arrival and their softmax
@@ -824,10 +836,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
     } else if (warp == 9) {
       // ================================================================ fetching
       // K's codes, V's, K's scales and V's, in boxes of a.box_keys keys (16, 32
-      // or 64: what divides a page; a copy costs the same whatever its size, so
-      // 64 keys in one instead of four took the 2048-token case below from 550
-      // to 360 us), a lane a box.  A box that is not there is read past the
-      // codes' end, which fills zeros, and its scales are not read.
+      // or 64: what divides a page; a copy costs the same whatever its size: with
+      // pages of 64 and the arithmetic taken out, 2048 tokens behind 14336 took
+      // 313 us in boxes of 64 and 414 in boxes of 16), a lane a box.  A box that
+      // is not there is read past the codes' end, which fills zeros, and its
+      // scales are not read.
       constexpr int kGroups = kUnit / 16, kBlocks = D / 32;
       constexpr uint32_t kCodeBytes = kUnit * (E2M1 ? D / 2 : D);  // of K or V
       const int group = lane % kGroups, kind = lane / kGroups;  // of 16 keys

@@ -1,5 +1,6 @@
 // Attention of few new tokens over the paged MX cache (decoding, verifying
-// drafts): flash-decoding on register-level MMAs, bound by reading the cache.
+// drafts): the keys split over all SMs, one pass with a running softmax, on
+// register-level MMAs (with 8 rows a tensor-memory tile of 128 would be 94% empty).
 //
 // A tile is 8 rows (new tokens x the query heads of one KV head), so the
 // cache is read once for all heads that share it.  A fifth warp fetches units of
@@ -7,15 +8,25 @@
 // of a unit and keep their own running maximum, sum and accumulator, joined when
 // the CTA's stretch of a segment ends.
 //
+// What bounds it.  With MXFP8 the cache's bytes: of what 64 instead of 32
+// sequences of 8192 add, 6.5 TB/s (96% of a copy's).  A call has 18 us beside
+// that: 4 until every CTA knows its stretch, 2 until the first keys are there, 4
+// to join, launch and uneven ends; so 32 ragged sequences of up to 8192 (300 MB)
+// take 64 us where a copy of the bytes takes 44, and 6 drafts over 2051 keys 18.
+// With MXFP4 the instructions: half the bytes a key and 560 instructions for 16
+// keys of a warp, issued on 64% of the cycles: 3.1 TB/s; 3 sequences of 65536
+// take 82 us (copy: 32).
+//
 // Both products are transposed, S^T = K Q^T and O^T += V^T P^T, so that the query
 // rows are the MMAs' columns, of which there are 8 where there are 16 rows of
 // keys or elements.  More rows are more tiles, which read the keys again, mostly
 // from L2: tiles of 16 rows share the widened codes, but their registers spill
-// (8 sequences of 8192 and 4 KV heads, 16 rows: 53 us, as two tiles 39).  P^T goes from the layout of S^T's
-// results to that of an operand by a transposing move.  The contraction order of
-// an MMA is free, so a lane feeds it the 16-byte pieces that it reads from shared
-// memory.  (The MMAs on 8-bit codes are no way around the widening: the compiler
-// makes them of conversions and MMAs on f16.)
+// (8 sequences of 8192 and 4 KV heads, 16 rows: 53 us, as two tiles 35).  P^T goes
+// from the layout of S^T's results to that of an operand by a transposing move.
+// The contraction order of an MMA is free, so a lane feeds it the 16-byte pieces
+// that it reads from shared memory.  (The register-level MMAs on 8-bit codes are
+// no way around the widening: they compile to conversions and MMAs on f16; with
+// them 32 sequences took 84 us.)
 //
 // Arithmetic.  Codes are exact in f16.  A key's blocks are scaled relative to
 // the key's largest block scale (a power of two: exact down to 2^-24 of the
@@ -45,7 +56,9 @@ constexpr int kRows = 8;                   // of a tile
 constexpr int kUnit = 64;
 constexpr int kWarps = 4;                  // that compute
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kCtasPerSm = 3;
+constexpr int kCtasPerSm = 3;              // what the registers allow: 160 threads of 128
+// Places of a CTA's stretch at least (6 drafts over 2051 keys: 18.4 us with 4, 20.1
+// with 2, 19.6 with 6).
 constexpr int kMinUnits = 4;
 // A segment's queries and output, in units (32 sequences of up to 8192: 76 us with
 // 1, 68 with 4, 65 with 8).
