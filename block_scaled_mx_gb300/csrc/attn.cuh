@@ -349,6 +349,15 @@ __device__ __forceinline__ AttnParts attn_parts(const AttnShare& sh, uint32_t se
 // that continue one lie apart (a CTA has at most one of each that is not whole).
 __device__ __forceinline__ int attn_slot(int cta, bool begins) { return 2 * cta + (begins ? 1 : 0); }
 
+// One more part of a segment is there; returns how many were before it.  What the
+// block wrote ahead of a barrier is seen by whoever finds it the last, and what
+// the others wrote by the block behind the next barrier.
+__device__ __forceinline__ unsigned attn_arrive(unsigned* counter) {
+  unsigned before;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+  return before;
+}
+
 // A wait for an mbarrier's phase.  One that runs out sets the status word and
 // makes every later wait of the CTA (`failed` in its shared memory) give up at
 // once.

@@ -489,9 +489,7 @@ __device__ __noinline__ void write_rows(const AttnArgs& a, Shared& sh, uint32_t 
   tile_barrier(x);
   unsigned* counter = &a.arrived[2 * parts.first + x];
   if (row == 0) {
-    __threadfence();  // for all: the barrier orders their writes before it
-    sh.last[x] = atomicAdd(counter, 1u) == static_cast<unsigned>(parts.parts - 1);
-    __threadfence();
+    sh.last[x] = attn_arrive(counter) == static_cast<unsigned>(parts.parts - 1);
     if (sh.last[x]) *counter = 0u;
   }
   tile_barrier(x);

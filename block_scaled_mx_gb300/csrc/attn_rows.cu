@@ -561,11 +561,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       // ---------------------------------------------------------------- join the CTAs
       // also after a wait that ran out: the counters are zero for the next call
       meet();
-      if (tid == 0) {
-        __threadfence();  // for all: the barrier orders their writes before it
-        s_last = atomicAdd(&a.arrived[p.first], 1u) == static_cast<unsigned>(p.parts - 1);
-        __threadfence();
-      }
+      if (tid == 0) s_last = attn_arrive(&a.arrived[p.first]) == static_cast<unsigned>(p.parts - 1);
       meet();
       if (s_last) {
         auto slot_of = [&](int i) { return attn_slot(p.first + i, i == 0); };
