@@ -291,7 +291,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       const int e = max(static_cast<int>(amax >> 7) - 127, -100);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);  // 14 - e <= 114
+      // 14 - e <= 114; a row with an infinity or NaN has no scores
+      const float up = e == 128 ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};

@@ -432,6 +432,8 @@ MX_API size_t mx_paged_attention_workspace_size(int T, int n_seqs, int n_heads, 
  * Scores, softmax statistics and sums are fp32.  Rows of padding and of bad
  * metadata are not written; a bad page's keys are left out.  Cache places that
  * no row sees may hold anything, also pages behind the window may be gone.
+ * A NaN or infinity in a query makes its row NaN; a NaN among the values that
+ * some new token sees may reach the sequence's other new tokens of the call.
  * Deterministic: the same call gives the same bits.  Two launches at most: one
  * for sequences with few rows, one for chunks.
  * Errors: MX_ERR_INVALID_ARG (null, sizes, n_heads % n_kv_heads, scale not

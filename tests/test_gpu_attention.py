@@ -268,3 +268,39 @@ def test_bad_page_of_a_chunk_is_left_out(fmt, page):
 def test_row_counts_at_the_tiles_edges(rows):
     """One query head of its own KV head: new tokens are rows."""
     _check([rows, 1], [rows + 70, 100], 2, 2, 64, 16, seed=90 + rows)
+
+
+@pytest.mark.parametrize("n,kv", [([1, 2], [90, 300]), ([70], [260]), ([40, 1, 3], [40, 200, 64])])
+def test_queries_that_are_not_finite(n, kv):
+    """An infinity or NaN in a query makes its own row NaN and leaves the others alone."""
+    batch, q, cache = _setup(n, kv, 8, 2, 128, 16, "e4m3", seed=61)
+    clean, bad = q.clone(), q.clone()
+    last = batch.T - 1
+    bad[0, 0, 3], bad[last, 5, 127], bad[last // 2, 6, 64] = float("inf"), float("nan"), float("-inf")
+    for t, h in ((0, 0), (last, 5), (last // 2, 6)):
+        clean[t, h] = 0.0
+    want, want_l, status, _ = _call(batch, clean, cache)
+    assert status == 0
+    out, lse, status, _ = _call(batch, bad, cache)
+    assert status == 0
+    hit = torch.zeros(batch.T, 8, dtype=torch.bool, device="cuda")
+    for t, h in ((0, 0), (last, 5), (last // 2, 6)):
+        hit[t, h] = True
+    assert torch.all(torch.isnan(out[hit])) and torch.all(torch.isnan(lse[hit]))
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], want_l[~hit])
+
+
+def test_many_sequences_of_all_kinds():
+    """More sequences than are looked at together, of all kinds: none, single
+    tokens, drafts, chunks of one and of several tiles."""
+    g = torch.Generator().manual_seed(71)
+    n = [[0, 1, 1, 1, 4, 1, 9, 40][int(i)] for i in torch.randint(0, 8, (300,), generator=g)]
+    n[7], n[131], n[299] = 90, 200, 70
+    kv = [a + int(b) for a, b in zip(n, torch.randint(0, 60, (300,), generator=g))]
+    _check(n, kv, 8, 2, 64, 16, seed=72)
+
+
+@pytest.mark.parametrize("rows", [24, 32, 120, 128, 136, 256])
+def test_row_counts_at_the_rule_between_the_kernels(rows):
+    _check([rows // 8], [rows // 8 + 130], 8, 1, 64, 16, seed=81)              # few pairs
+    _check([rows // 8, 1] * 9, [rows // 8 + 30, 70] * 9, 8, 1, 64, 16, seed=82)  # many
