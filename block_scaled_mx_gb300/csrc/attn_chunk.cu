@@ -157,6 +157,16 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// E4M3 codes of two f16, to nearest even, saturating.
+__device__ __forceinline__ uint32_t enc_e4m3x2_f16(uint32_t x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 r = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -296,7 +306,8 @@ __device__ __noinline__ void load_queries(const AttnArgs& a, Shared& sh, uint8_t
   const uint32_t lanes = static_cast<uint32_t>(threadIdx.x & 96) << 16;
   constexpr int kPieces = D / 8;     // sixteen bytes of bf16
   constexpr int kStep = 128 / kPieces;  // rows of the 128 threads
-  constexpr int kAhead = 4;          // loads in flight while as many are converted
+  constexpr int kTogether = 2;       // pieces converted side by side,
+  constexpr int kAhead = 4;          // and on their way behind them
   const int p = threadIdx.x % kPieces, r0 = (threadIdx.x & 127) / kPieces;
   uint8_t* hi_base = base + Sh::kQ + 2 * x * Sh::kQTile;
   auto load = [&](int r) {
@@ -307,22 +318,21 @@ __device__ __noinline__ void load_queries(const AttnArgs& a, Shared& sh, uint8_t
                                                 static_cast<int64_t>(q0 + tok) * a.q_stride +
                                                 static_cast<int64_t>(head * a.group + (R - tok * a.group)) * D) + p);
   };
-  uint4 now[kAhead], then[kAhead];
+  uint4 queue[kAhead + kTogether];
 #pragma unroll
-  for (int n = 0; n < kAhead; ++n) then[n] = load(r0 + n * kStep);
+  for (int n = 0; n < kAhead; ++n) queue[n] = load(r0 + n * kStep);
 #pragma unroll 1
-  for (int rr = r0; rr < 128; rr += kAhead * kStep) {
+  for (int rr = r0; rr < 128; rr += kTogether * kStep) {
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n) now[n] = then[n];
+    for (int n = 0; n < kTogether; ++n) queue[kAhead + n] = load(rr + (kAhead + n) * kStep);
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n) then[n] = load(rr + (kAhead + n) * kStep);
-#pragma unroll
-    for (int n = 0; n < kAhead; ++n) {
+    for (int n = 0; n < kTogether; ++n) {
       const int r = rr + n * kStep;
-      const uint32_t w[4] = {now[n].x, now[n].y, now[n].z, now[n].w};
+      const uint32_t w[4] = {queue[n].x, queue[n].y, queue[n].z, queue[n].w};
       uint32_t amax = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+      for (int k = 0; k < 4; ++k) amax = __vmaxu2(amax, w[k] & 0x7FFF7FFFu);
+      amax = max(amax & 0xFFFFu, amax >> 16);
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       // the block's largest element lands in [2^7, 2^8): hi's rounding error
@@ -330,15 +340,19 @@ __device__ __noinline__ void load_queries(const AttnArgs& a, Shared& sh, uint8_t
       const int s = max(static_cast<int>(amax >> 7) - 127 - 7, -122);
       // a block with an infinity or NaN has no scores
       const float down = amax >= 0x7F80u ? __uint_as_float(0x7FC00000u) : pow2_neg(s);
-      uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+      uint32_t hi[2], lo[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float x0 = __uint_as_float(w[k] << 16) * down, x1 = __uint_as_float(w[k] & 0xFFFF0000u) * down;
-        const uint32_t h = enc_e4m3x2(x0, x1);
-        const uint32_t back = f16x2_of_e4m3x2(h);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
-        hi[k >> 1] |= h << ((k & 1) * 16);
-        lo[k >> 1] |= enc_e4m3x2((x0 - f.x) * 32.0f, (x1 - f.y) * 32.0f) << ((k & 1) * 16);
+      for (int k = 0; k < 4; k += 2) {
+        uint32_t h[2], l[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          // in f16 (exact down to 2^-25 of the block's largest, which lo does not hold)
+          const uint32_t x = pack_f16(__uint_as_float(w[k + m] << 16) * down, __uint_as_float(w[k + m] & 0xFFFF0000u) * down);
+          h[m] = enc_e4m3x2_f16(x);
+          l[m] = enc_e4m3x2_f16(mul_f16x2(sub_f16x2(x, f16x2_of_e4m3x2(h[m])), 0x50005000u));  // 32
+        }
+        hi[k / 2] = __byte_perm(h[0], h[1], 0x5410);
+        lo[k / 2] = __byte_perm(l[0], l[1], 0x5410);
       }
       const uint32_t at = D == 128 ? r * 128 + (((p >> 1) ^ (r & 7)) << 4) + (p & 1) * 8
                                    : r * 64 + (((p >> 1) ^ ((r >> 1) & 3)) << 4) + (p & 1) * 8;
@@ -346,6 +360,8 @@ __device__ __noinline__ void load_queries(const AttnArgs& a, Shared& sh, uint8_t
       *reinterpret_cast<uint2*>(hi_base + Sh::kQTile + at) = make_uint2(lo[0], lo[1]);
       if ((p & 3) == 0) reinterpret_cast<uint8_t*>(&sh.q_scale[x][r])[p >> 2] = static_cast<uint8_t>(s + 127);
     }
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) queue[n] = queue[n + kTogether];
   }
   fence_proxy_async_shared();
   tile_barrier(x);
