@@ -2,15 +2,15 @@
 // cores: tcgen05 MMAs with the accumulators in tensor memory.
 //
 // What bounds it.  With heads of 128 a unit of 64 keys and 256 rows is 1024
-// cycles of MMAs at their rate; it takes 1770: the 8-bit MMAs read Q again for
+// cycles of MMAs at their rate; it takes 1750: the 8-bit MMAs read Q again for
 // every unit (64 KB of the 128 KB that a unit's operands are, at 128 bytes a
 // cycle), which tensor memory, full, cannot hold, and the softmax's two warps a
 // scheduler need about as long.  With heads of 64 the softmax alone bounds a
-// unit (1560).  A segment costs 17 (10) units more: queries split into their
+// unit (1560).  A segment costs 16 (10) units more: queries split into their
 // two parts, the accumulator written out, the first keys of the next on their
-// way through empty stages.  2048 new tokens behind 14336 take 419 us (1230
-// TFLOP/s of 4 head_dim flops for each visible (row, key) pair, 64% of a plain
-// bf16 product's), a prompt of 8192 518 us (1060).
+// way through empty stages.  2048 new tokens behind 14336 take 411 us (1255
+// TFLOP/s of 4 head_dim flops for each visible (row, key) pair, 65% of a plain
+// bf16 product's), a prompt of 8192 506 us (1086).
 //
 // A tile is 256 rows (new tokens x the query heads of one KV head) as two MMA
 // tiles of 128, A and B, that take turns: while the tensor cores work for one,
@@ -306,8 +306,10 @@ __device__ __noinline__ void load_queries(const AttnArgs& a, Shared& sh, uint8_t
   const uint32_t lanes = static_cast<uint32_t>(threadIdx.x & 96) << 16;
   constexpr int kPieces = D / 8;     // sixteen bytes of bf16
   constexpr int kStep = 128 / kPieces;  // rows of the 128 threads
-  constexpr int kTogether = 2;       // pieces converted side by side,
-  constexpr int kAhead = 4;          // and on their way behind them
+  // Pieces converted side by side, and on their way behind them (a prompt of 8192:
+  // 506 us; 1 and 4: 517; 4 and 4: 512; with more on their way the unit loop's
+  // registers spill: 530 and worse).
+  constexpr int kTogether = 2, kAhead = 4;
   const int p = threadIdx.x % kPieces, r0 = (threadIdx.x & 127) / kPieces;
   uint8_t* hi_base = base + Sh::kQ + 2 * x * Sh::kQTile;
   auto load = [&](int r) {
