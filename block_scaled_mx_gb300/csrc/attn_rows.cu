@@ -13,9 +13,9 @@
 // that: 4 until every CTA knows its stretch, 2 until the first keys are there, 4
 // to join, launch and uneven ends; so 32 ragged sequences of up to 8192 (300 MB)
 // take 64 us where a copy of the bytes takes 44, and 6 drafts over 2051 keys 18.
-// With MXFP4 the instructions: half the bytes a key and 560 instructions for 16
-// keys of a warp, issued on 64% of the cycles: 3.1 TB/s; 3 sequences of 65536
-// take 82 us (copy: 32).
+// With MXFP4 the instructions: half the bytes a key and 504 instructions for 16
+// keys of a warp, with the pipe of conversions and bit operations busy for 63% of
+// the cycles: 3.2 TB/s; 3 sequences of up to 65536 take 79 us (copy: 32).
 //
 // Both products are transposed, S^T = K Q^T and O^T += V^T P^T, so that the query
 // rows are the MMAs' columns, of which there are 8 where there are 16 rows of
@@ -80,14 +80,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// The E2M1 codes at nibbles i and 4 + i of a word as two f16 of 2^-14 their size,
-// by moving their bits: the codes' conversion takes two instructions and, for
-// half of the bytes, a third.
-constexpr int kE2m1Shift = 14;
-__device__ __forceinline__ uint32_t f16x2_of_nibbles(uint32_t w, int i) {
-  const uint32_t size = i < 3 ? w << (9 - 4 * i) : w >> 3, sign = w << (12 - 4 * i);
-  return (size & 0x0E000E00u) | (sign & 0x80008000u);
-}
+// A word's four even or odd E2M1 codes as E4M3 codes of 2^-6 their size, by moving
+// their bits; from those the conversion takes an instruction for two, which from
+// E2M1 itself takes two, and for half of the bytes three (3 sequences of up to
+// 65536: 83 us from E2M1, 82 moving its bits into f16, 79 this way).
+constexpr int kE2m1Shift = 6;
+__device__ __forceinline__ uint32_t e4m3_of_even(uint32_t w) { return (w << 4 & 0x80808080u) | (w << 2 & 0x1C1C1C1Cu); }
+__device__ __forceinline__ uint32_t e4m3_of_odd(uint32_t w) { return (w & 0x80808080u) | (w >> 2 & 0x1C1C1C1Cu); }
 
 // The warp's 8 x 8 matrix of 16-bit elements, transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -302,9 +301,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           f[2 * k] = __uint_as_float(x[k] << 16) * up;
           f[2 * k + 1] = __uint_as_float(x[k] & 0xFFFF0000u) * up;
         }
-        uint32_t y[4];  // E2M1: elements k and 4 + k, as they come from a word of K
+        uint32_t y[4];  // E2M1: the even elements, then the odd ones, as they come from a word of K
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = E2M1 ? pack_f16(f[k], f[4 + k]) : pack_f16(f[2 * k], f[2 * k + 1]);
+        for (int k = 0; k < 4; ++k)
+          y[k] = E2M1 ? pack_f16(f[4 * (k & 1) + k / 2], f[4 * (k & 1) + 2 + k / 2]) : pack_f16(f[2 * k], f[2 * k + 1]);
         s_q[2 * i][lane] = make_uint2(y[0], y[1]);
         s_q[2 * i + 1][lane] = make_uint2(y[2], y[3]);
       }
@@ -384,15 +384,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           uint32_t b0, b1;
-          if (E2M1) {
-            // a word of eight elements for two steps; the queries lie in the same order
-            b0 = f16x2_of_nibbles(kw[j][0][st / 2], 2 * (st & 1));
-            b1 = f16x2_of_nibbles(kw[j][0][st / 2], 2 * (st & 1) + 1);
-          } else {
-            const uint32_t w = kw[j][st / 4][st % 4];
-            b0 = f16x2_of_e4m3x2(w & 0xFFFFu);
-            b1 = f16x2_of_e4m3x2(w >> 16);
-          }
+          // E2M1: a word of eight elements for two steps, the even ones first; the
+          // queries lie in the same order
+          uint32_t w;
+          if (E2M1) w = st & 1 ? e4m3_of_odd(kw[j][0][st / 2]) : e4m3_of_even(kw[j][0][st / 2]);
+          else w = kw[j][st / 4][st % 4];
+          b0 = f16x2_of_e4m3x2(w & 0xFFFFu);
+          b1 = f16x2_of_e4m3x2(w >> 16);
           ka[j] = mul2(b0, k_mult[j]);
           ka[2 + j] = mul2(b1, k_mult[j]);
         }
@@ -459,21 +457,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       };
 #pragma unroll
       for (int i = 0; i < Sh::kVWords; ++i) {
-        if (E2M1) {
-          // four elements of two keys in a word
+        // an element of two keys side by side, two such in a word
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t sel = h == 0 ? 0x5410u : 0x7632u;
-            const uint32_t w01 = __byte_perm(vw[0][i], vw[1][i], sel), w23 = __byte_perm(vw[2][i], vw[3][i], sel);
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t sel = k == 0 ? 0x5140u : 0x7362u;
+          if (E2M1) {
+            const uint32_t even01 = __byte_perm(e4m3_of_even(vw[0][i]), e4m3_of_even(vw[1][i]), sel);
+            const uint32_t even23 = __byte_perm(e4m3_of_even(vw[2][i]), e4m3_of_even(vw[3][i]), sel);
+            const uint32_t odd01 = __byte_perm(e4m3_of_odd(vw[0][i]), e4m3_of_odd(vw[1][i]), sel);
+            const uint32_t odd23 = __byte_perm(e4m3_of_odd(vw[2][i]), e4m3_of_odd(vw[3][i]), sel);
 #pragma unroll
-            for (int k = 0; k < 4; k += 2)
-              values(4 * i + 2 * h + k / 2, f16x2_of_nibbles(w01, k), f16x2_of_nibbles(w01, k + 1), f16x2_of_nibbles(w23, k),
-                     f16x2_of_nibbles(w23, k + 1));
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t sel = k == 0 ? 0x5140u : 0x7362u;
+            for (int h = 0; h < 2; ++h)
+              values(4 * i + 2 * k + h, f16x2_of_e4m3x2(even01 >> (16 * h) & 0xFFFFu), f16x2_of_e4m3x2(odd01 >> (16 * h) & 0xFFFFu),
+                     f16x2_of_e4m3x2(even23 >> (16 * h) & 0xFFFFu), f16x2_of_e4m3x2(odd23 >> (16 * h) & 0xFFFFu));
+          } else {
             const uint32_t y01 = __byte_perm(vw[0][i], vw[1][i], sel), y23 = __byte_perm(vw[2][i], vw[3][i], sel);
             values(2 * i + k, f16x2_of_e4m3x2(y01 & 0xFFFFu), f16x2_of_e4m3x2(y01 >> 16), f16x2_of_e4m3x2(y23 & 0xFFFFu),
                    f16x2_of_e4m3x2(y23 >> 16));
