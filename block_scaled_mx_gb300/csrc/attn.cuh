@@ -203,9 +203,21 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, uint32_t* uni
   return r;
 }
 
+// Between CTAs' stretches a segment of `units` units is split before unit k only
+// for before <= k <= units - behind: a part of fewer than kSnap units costs more
+// than it saves, and goes to the neighbour.
+template <int kSnap>
+struct AttnSplit {
+  int before, behind;
+  __device__ __forceinline__ explicit AttnSplit(int units) {
+    before = min(kSnap, (units + 1) / 2);
+    behind = min(kSnap, units + 1 - before);
+  }
+};
+
 // Where a CTA is on the line: a segment (one row tile of one KV head of one
 // sequence) and the unit `place` of it (below zero: the places without work).
-template <int kRows, int kUnit, int kCost>
+template <int kRows, int kUnit, int kCost, int kSnap>
 struct AttnCursor {
   uint32_t u, end;  // on the line
   int b, head, tile, place;
@@ -252,6 +264,12 @@ struct AttnCursor {
       }
     }
     place -= kCost;
+    if (place > 0 && place < t.units) {
+      const AttnSplit<kSnap> split(t.units);
+      const int to = place < split.before ? 0 : place > t.units - split.behind ? t.units : place;
+      u += to - place;
+      place = to;
+    }
   }
 
   // Past what has no work: to a unit of the stretch, or false where it has no
@@ -264,7 +282,12 @@ struct AttnCursor {
         place += d;
         continue;
       }
-      if (place < t.units) return true;
+      if (place < t.units) {
+        const int k = place + static_cast<int>(end - u);  // the next stretch's first unit, where that lies in the segment
+        if (k >= t.units || k >= AttnSplit<kSnap>(t.units).before) return true;
+        u = end;
+        return false;
+      }
       place = -kCost;
       if (++tile == s.tiles) {
         tile = 0;
@@ -282,7 +305,8 @@ struct AttnCursor {
   }
   // Units of the segment from `place` on that lie in the stretch, and past them.
   __device__ __forceinline__ int take() const {
-    return static_cast<int>(min(static_cast<uint32_t>(t.units - place), end - u));
+    const int k = place + static_cast<int>(min(end - u, static_cast<uint32_t>(t.units)));
+    return (k > t.units - AttnSplit<kSnap>(t.units).behind ? t.units : k) - place;
   }
   __device__ __forceinline__ void pass(int n) {
     u += n;
@@ -339,10 +363,12 @@ struct AttnWalk {
 struct AttnParts {
   int first, parts;
 };
+template <int kSnap>
 __device__ __forceinline__ AttnParts attn_parts(const AttnShare& sh, uint32_t seg, int units) {
+  const AttnSplit<kSnap> split(units);
   AttnParts p;
-  p.first = sh.cta_of(seg);
-  p.parts = sh.cta_of(seg + units - 1) - p.first + 1;
+  p.first = sh.cta_of(seg + split.before - 1);
+  p.parts = sh.cta_of(seg + units - split.behind) - p.first + 1;
   return p;
 }
 // The workspace slot of a CTA's part: the part that begins a segment and those

@@ -8,9 +8,9 @@
 // scheduler need about as long.  With heads of 64 the softmax alone bounds a
 // unit (1560).  A segment costs 16 (10) units more: queries split into their
 // two parts, the accumulator written out, the first keys of the next on their
-// way through empty stages.  2048 new tokens behind 14336 take 411 us (1255
+// way through empty stages.  2048 new tokens behind 14336 take 412 us (1250
 // TFLOP/s of 4 head_dim flops for each visible (row, key) pair, 65% of a plain
-// bf16 product's), a prompt of 8192 506 us (1086).
+// bf16 product's), a prompt of 8192 508 us (1080).
 //
 // A tile is 256 rows (new tokens x the query heads of one KV head) as two MMA
 // tiles of 128, A and B, that take turns: while the tensor cores work for one,
@@ -63,6 +63,10 @@ constexpr int kMinUnits = 20;  // places of a CTA's stretch at least
 // A segment's queries and output, in units (a prompt of 8192: 518 us with 16, 539
 // with 12, 527 with 20).
 constexpr int kCost = 16;
+// Least units of a split segment's part: a part costs queries and an output again
+// (6 prompts of up to 662: 70 us with 1, 46 with 4, 44 with 8 and 12; 256 new
+// tokens over 4096, whose 8 segments are all there is to share out: 52, 51, 54, 59).
+constexpr int kSnap = 8;
 constexpr int kStages = 4;     // of K and of V
 constexpr int kRawStages = 4;  // of codes on their way to V
 constexpr int kMetaRing = 8;  // more units than can be between their scales' arrival and their softmax
@@ -522,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
                                                               const __grid_constant__ CUtensorMap v_map) {
   using Sh = Shape<D>;
   constexpr int kUnit = Sh::kUnit;
-  using Cursor = AttnCursor<kRows, kUnit, kCost>;
+  using Cursor = AttnCursor<kRows, kUnit, kCost, kSnap>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -692,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
         const int64_t oh = static_cast<int64_t>(cur.s.q0 + tok) * (a.n_kv_heads * a.group) + cur.head * a.group + (R - tok * a.group);
         const bool whole = take == cur.t.units;
         AttnParts parts{};
-        if (!whole) parts = attn_parts(share, cur.u - cur.place, cur.t.units);
+        if (!whole) parts = attn_parts<kSnap>(share, cur.u - cur.place, cur.t.units);
         write_rows<D>(a, sh, o_col, x, whole ? -1 : attn_slot(blockIdx.x, cur.place == 0), parts, oh, ok, warp_valid, valid, m, l);
       } else {
         to_next();  // this segment has no tile B

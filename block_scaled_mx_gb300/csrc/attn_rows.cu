@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
   const AttnShare share = attn_share<kRows, kUnit, kCost, kThreads, false>(a, s_units);  // its barriers cover the above
   const int n_heads = a.n_kv_heads * a.group;
-  AttnCursor<kRows, kUnit, kCost> cur;
+  AttnCursor<kRows, kUnit, kCost, 1> cur;
   cur.template start<false>(a, share);
   Ring<Sh::kStages> ring;
 
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     meet();
 
     const bool whole = take == t.units;
-    const AttnParts p = attn_parts(share, cur.u - place, t.units);
+    const AttnParts p = attn_parts<1>(share, cur.u - place, t.units);
     const int slot = attn_slot(blockIdx.x, place == 0);
 
     // writes a finished row: four elements a lane

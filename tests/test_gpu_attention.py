@@ -304,3 +304,9 @@ def test_many_sequences_of_all_kinds():
 def test_row_counts_at_the_rule_between_the_kernels(rows):
     _check([rows // 8], [rows // 8 + 130], 8, 1, 64, 16, seed=81)              # few pairs
     _check([rows // 8, 1] * 9, [rows // 8 + 30, 70] * 9, 8, 1, 64, 16, seed=82)  # many
+
+
+@pytest.mark.parametrize("n,kv", [([400] * 6, [400] * 6), ([330, 90, 200], [900, 90, 1400]), ([40], [3000])])
+def test_segments_that_are_split_or_not(n, kv):
+    """Prompts whose tiles are about as long as a CTA's stretch."""
+    _check(n, kv, 4, 2, 64, 16, seed=91)
