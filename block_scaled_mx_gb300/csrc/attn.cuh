@@ -210,8 +210,8 @@ template <int kSnap>
 struct AttnSplit {
   int before, behind;
   __device__ __forceinline__ explicit AttnSplit(int units) {
-    before = min(kSnap, (units + 1) / 2);
-    behind = min(kSnap, units + 1 - before);
+    before = kSnap == 1 ? 1 : min(kSnap, (units + 1) / 2);
+    behind = kSnap == 1 ? 1 : min(kSnap, units + 1 - before);
   }
 };
 
@@ -264,7 +264,7 @@ struct AttnCursor {
       }
     }
     place -= kCost;
-    if (place > 0 && place < t.units) {
+    if (kSnap > 1 && place > 0 && place < t.units) {
       const AttnSplit<kSnap> split(t.units);
       const int to = place < split.before ? 0 : place > t.units - split.behind ? t.units : place;
       u += to - place;
@@ -284,7 +284,7 @@ struct AttnCursor {
       }
       if (place < t.units) {
         const int k = place + static_cast<int>(end - u);  // the next stretch's first unit, where that lies in the segment
-        if (k >= t.units || k >= AttnSplit<kSnap>(t.units).before) return true;
+        if (kSnap == 1 || k >= t.units || k >= AttnSplit<kSnap>(t.units).before) return true;
         u = end;
         return false;
       }
@@ -305,6 +305,7 @@ struct AttnCursor {
   }
   // Units of the segment from `place` on that lie in the stretch, and past them.
   __device__ __forceinline__ int take() const {
+    if (kSnap == 1) return static_cast<int>(min(static_cast<uint32_t>(t.units - place), end - u));
     const int k = place + static_cast<int>(min(end - u, static_cast<uint32_t>(t.units)));
     return (k > t.units - AttnSplit<kSnap>(t.units).behind ? t.units : k) - place;
   }

@@ -8,9 +8,9 @@
 // scheduler need about as long.  With heads of 64 the softmax alone bounds a
 // unit (1560).  A segment costs 16 (10) units more: queries split into their
 // two parts, the accumulator written out, the first keys of the next on their
-// way through empty stages.  2048 new tokens behind 14336 take 412 us (1250
-// TFLOP/s of 4 head_dim flops for each visible (row, key) pair, 65% of a plain
-// bf16 product's), a prompt of 8192 508 us (1080).
+// way through empty stages.  2048 new tokens behind 14336 take 414 us (1245
+// TFLOP/s of 4 head_dim flops for each visible (row, key) pair, 64% of a plain
+// bf16 product's), a prompt of 8192 509 us (1078).
 //
 // A tile is 256 rows (new tokens x the query heads of one KV head) as two MMA
 // tiles of 128, A and B, that take turns: while the tensor cores work for one,
