@@ -175,11 +175,12 @@ int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride
   if (cache->page_size % 16) return MX_ERR_UNSUPPORTED;
   // cache rows are counted in ints
   if (static_cast<int64_t>(cache->num_pages) * cache->page_size > INT_MAX / cache->n_kv_heads) return MX_ERR_UNSUPPORTED;
-  // Places of work are counted in 32 bits.  At most: 256-row tiles, and 8-row
-  // ones of the sequences with few rows, times 64-key units and a tile's cost.
+  // Places of work are counted in 32 bits, those of one KV head in a signed int.  At
+  // most: 256-row tiles, and 8-row ones of the sequences with few rows, times 64-key
+  // units and a tile's cost.
   const double tiles = static_cast<double>(T) * (n_heads / cache->n_kv_heads) / 256 + n_seqs * (1.0 + kMostFewRows / 8);
-  if (tiles * cache->n_kv_heads * (static_cast<double>(max_pages) * cache->page_size / 64 + 32) > 4.0e9)
-    return MX_ERR_UNSUPPORTED;
+  const double places = tiles * (static_cast<double>(max_pages) * cache->page_size / 64 + 32);
+  if (places > 2147483647.0 || places * cache->n_kv_heads > 4.0e9) return MX_ERR_UNSUPPORTED;
   if (T == 0 || n_seqs == 0 || max_q_len == 0) return MX_OK;
   if (!q || !out) return MX_ERR_INVALID_ARG;
   st = check_cache_pointers(cache, block_table, kv_lens, q_starts, ws, ws_bytes);

@@ -94,8 +94,8 @@ __device__ __forceinline__ int attn_seq_places(const AttnArgs& a, const AttnSeq&
 }
 
 // A CTA's stretch [u, end) of the line; the line's first `longer` stretches have
-// `each` + 1 places, the others `each`.  Places are 32-bit: the host refuses
-// what could have more.
+// `each` + 1 places, the others `each`.  Places are 32-bit, and those of one KV head
+// a signed int: the host refuses what could have more.
 struct AttnShare {
   uint32_t total;
   int ctas;             // CTAs that have a stretch

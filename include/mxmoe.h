@@ -439,8 +439,9 @@ MX_API size_t mx_paged_attention_workspace_size(int T, int n_seqs, int n_heads, 
  * Errors: MX_ERR_INVALID_ARG (null, sizes, n_heads % n_kv_heads, scale not
  * positive and finite, window < 0 or without causal, stride),
  * MX_ERR_UNSUPPORTED (head_dim other than 64 and 128, page_size % 16, more
- * than 2^30 rows of q or 2^31 of a cache table, or 4e9 (256 query rows x 64
- * keys) of work by the sizes given), MX_ERR_ALIGNMENT, MX_ERR_WORKSPACE, MX_ERR_CUDA. */
+ * than 2^30 rows of q or 2^31 of a cache table, or 2^31 (256 query rows x 64
+ * keys) of work for one KV head, 4e9 in all, by the sizes given),
+ * MX_ERR_ALIGNMENT, MX_ERR_WORKSPACE, MX_ERR_CUDA. */
 MX_API int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride, int n_heads,
                               const int32_t* block_table, const int32_t* kv_lens, const int32_t* q_starts, int n_seqs,
                               int max_pages, int T, int max_q_len, float scale, int causal, int window, void* out,

@@ -131,3 +131,23 @@ def test_binding_checks_tensors(L):
         mx._rows(torch.empty(4, 64, 8, dtype=torch.bfloat16, **meta).transpose(1, 2), 8, 64, "q")
     with pytest.raises(ValueError, match="bf16"):
         mx._rows(torch.empty(4, 8, 64, **meta), 8, 64, "q")
+
+
+def test_attention_refuses_work_that_its_counters_cannot_hold(L):
+    """The kernels count places of work in 32 bits, and those of one KV head in a
+    signed int: one head of 2^20 new tokens and 32 query heads over 2^20 keys has
+    131072 tiles of 16400 places, more than 2^31 - 1.  The workspace is too small
+    in every call, so that none is launched."""
+    size = L.mx_paged_attention_workspace_size
+    assert size(2 ** 20, 1, 32, 1, 128, 2 ** 20) > 256
+
+    def attend(T, heads, kv_heads, keys, n=1):
+        c = _cache(num_pages=keys // 64, page_size=64, n_kv_heads=kv_heads, head_dim=128)
+        return L.mx_paged_attention(ctypes.addressof(c), fake, heads * 128, heads, fake, fake, fake, n, keys // 64, T, T, 0.1, 0, 0,
+                                    fake, fake, fake, 256, None)
+
+    assert attend(2 ** 20, 32, 1, 2 ** 20) == 2        # 2.15e9 places of the one head
+    assert attend(2 ** 19, 64, 1, 2 ** 20) == 2
+    assert attend(2 ** 20, 32, 2, 2 ** 20) == 4        # 1.07e9 of each of two
+    assert attend(2 ** 19, 32, 1, 2 ** 20) == 4
+    assert attend(2 ** 20, 32, 8, 2 ** 22) == 2        # 8.6e9 in all
