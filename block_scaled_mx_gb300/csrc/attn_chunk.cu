@@ -613,13 +613,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
           if (ok && !wait(sh, &sh.s_full[x], s_phase, a)) ok = false;
           s_phase ^= 1u;
           tc_fence_after();
-          const bool work = ok && warp_valid;  // the same for the warp: a barrier's wait is
           const UnitMeta meta = sh.meta[(unit + j) % kMetaRing];
           const int key0 = cur.t.first + (cur.place + j) * kUnit;
           uint32_t v[kUnit];
           __syncwarp();
-          if (work) {
-            if (__builtin_expect(key0 + kUnit > all_hi || key0 < all_lo || meta.bad != 0, 0))
+          // Lanes may differ in whether their wait ran out, and what follows is for
+          // the whole warp (tensor memory, votes): so what leads there is either the
+          // same for all lanes or voted on (the vote: 412 -> 414 us in the header's
+          // chunk), and a warp goes on with whatever it finds; its rows are not
+          // written at the end.
+          if (warp_valid) {
+            if (__any_sync(0xffffffffu, key0 + kUnit > all_hi || key0 < all_lo || meta.bad != 0))
               mask_scores<kUnit>(s_col, lo - key0, hi - key0, meta.bad);
             tmem_load<kUnit>(s_col, v);
             tmem_ld_wait();
@@ -635,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
             __syncwarp();
             tc_fence_after();
           };
-          if (work) {
+          if (warp_valid) {
             float t4[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) t4[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[4 + k]));

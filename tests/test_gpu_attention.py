@@ -310,3 +310,26 @@ def test_row_counts_at_the_rule_between_the_kernels(rows):
 def test_segments_that_are_split_or_not(n, kv):
     """Prompts whose tiles are about as long as a CTA's stretch."""
     _check(n, kv, 4, 2, 64, 16, seed=91)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_waits_of_chunks_that_run_out(fmt, dim):
+    """A limit of zero makes waits run out for some lanes of a warp and not for
+    others, again and again: each call ends, reports it, and leaves a workspace
+    with which the next one is right."""
+    n, kv = [90, 300], [2700, 333]
+    batch, q, cache = _setup(n, kv, 8, 2, dim, 16, fmt, seed=73)
+    want, want_l, status, ws = _call(batch, q, cache)
+    assert status == 0
+    out, lse = torch.empty_like(want), torch.empty_like(want_l)
+    for _ in range(5):
+        try:
+            mx.mx_debug_set_wait_limit_ns(0)
+            mx.mx_paged_attention(q, cache, *batch.device(), out, ws, max_q_len=max(n), lse=lse)
+            assert mx.moe_get_status(ws) == mx.MX_ERR_TIMEOUT
+        finally:
+            mx.mx_debug_set_wait_limit_ns(2_000_000_000)
+        mx.mx_paged_attention(q, cache, *batch.device(), out, ws, max_q_len=max(n), lse=lse)
+        assert mx.moe_get_status(ws) == 0
+        assert torch.equal(out, want) and torch.equal(lse, want_l)
