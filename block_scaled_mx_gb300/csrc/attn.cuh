@@ -387,14 +387,17 @@ __device__ __forceinline__ unsigned attn_arrive(unsigned* counter) {
 
 // A wait for an mbarrier's phase.  One that runs out sets the status word and
 // makes every later wait of the CTA (`failed` in its shared memory) give up at
-// once.
-__device__ __noinline__ inline bool attn_wait_long(volatile int* failed, uint32_t bar, uint32_t parity, uint64_t limit_ns,
+// once.  With kNow a limit of zero waits for nothing: a try suspends the thread for
+// longer than the few-rows kernel's ordinary waits, which would never run out.
+template <bool kNow>
+__device__ __noinline__ bool attn_wait_long(volatile int* failed, uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                                    int* status) {
   const uint64_t t0 = globaltimer_ns();
-  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
-    if (n & 15u) continue;
+  const bool now = kNow && limit_ns == 0;
+  for (uint32_t n = 1; now || !mbar_try_wait(bar, parity); ++n) {
+    if (!now && (n & 15u)) continue;
     if (*failed) return false;
-    if (globaltimer_ns() - t0 > limit_ns) {
+    if (now || globaltimer_ns() - t0 > limit_ns) {
       *failed = 1;
       set_status(status, MX_ERR_TIMEOUT);
       return false;
@@ -402,10 +405,12 @@ __device__ __noinline__ inline bool attn_wait_long(volatile int* failed, uint32_
   }
   return true;
 }
+template <bool kNow>
 __device__ __forceinline__ bool attn_wait(volatile int* failed, uint64_t* bar, uint32_t parity, const AttnArgs& a) {
   const uint32_t b = smem_u32(bar);
-  if (__builtin_expect(mbar_try_wait(b, parity), 1)) return true;
-  return attn_wait_long(failed, b, parity, a.wait_limit_ns, a.status);
+  const bool there = kNow && a.wait_limit_ns == 0 ? mbar_test_wait(b, parity) : mbar_try_wait(b, parity);
+  if (__builtin_expect(there, 1)) return true;
+  return attn_wait_long<kNow>(failed, b, parity, a.wait_limit_ns, a.status);
 }
 
 // A stage of a ring and the parity of its current round.

@@ -147,7 +147,7 @@ struct Shared {
 // code of up to 8 KB each at full speed, and at a quarter of it past 32 KB), so
 // what a unit seldom needs lies outside of them.
 __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity, const AttnArgs& a) {
-  return attn_wait(&sh.failed, bar, parity, a);
+  return attn_wait<false>(&sh.failed, bar, parity, a);
 }
 
 // The 128 threads of a tile's softmax meet.

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         uint32_t here, bad;
         const int row = walk.box(a, cur.head, group, here, bad);
         const uint32_t boxes = __ballot_sync(0xffffffffu, leads && row >= 0) & ((1u << kGroups) - 1);
-        ok = attn_wait(&failed, &empty[ring.stage], ring.phase ^ 1u, a);
+        ok = attn_wait<true>(&failed, &empty[ring.stage], ring.phase ^ 1u, a);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t bar = smem_u32(&full[ring.stage]);
@@ -339,9 +339,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll 1
     for (int i = 0; i < take; ++i, ring.next()) {
       const int key = t.first + (place + i) * kUnit + warp * 16;
-      if (ok) ok = attn_wait(&failed, &full[ring.stage], ring.phase, a);
+      if (ok) ok = attn_wait<true>(&failed, &full[ring.stage], ring.phase, a);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok || !(s_here[ring.stage] >> warp & 1u)) {
+      // Behind a wait that ran out a warp releases nothing: stages that it never saw
+      // full would be filled again over copies in flight, and their barriers get an
+      // arrival too many.  The fetching warp's next wait then gives up too.
+      if (!ok) continue;
+      if (!(s_here[ring.stage] >> warp & 1u)) {
         warp_arrive(&empty[ring.stage]);
         continue;
       }

@@ -333,3 +333,24 @@ def test_waits_of_chunks_that_run_out(fmt, dim):
         mx.mx_paged_attention(q, cache, *batch.device(), out, ws, max_q_len=max(n), lse=lse)
         assert mx.moe_get_status(ws) == 0
         assert torch.equal(out, want) and torch.equal(lse, want_l)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("n,kv", [([1] * 9, [900] * 9), ([1] * 24, [9000] * 24), ([3] * 70, [150] * 70)])
+def test_waits_of_few_rows_that_run_out(n, kv, fmt):
+    """The same of the few-rows kernel, with fewer units a CTA than it fetches ahead,
+    with many, and with many short segments."""
+    batch, q, cache = _setup(n, kv, 8, 2, 128, 16, fmt, seed=74)
+    want, want_l, status, ws = _call(batch, q, cache)
+    assert status == 0
+    out, lse = torch.empty_like(want), torch.empty_like(want_l)
+    for _ in range(5):
+        try:
+            mx.mx_debug_set_wait_limit_ns(0)
+            mx.mx_paged_attention(q, cache, *batch.device(), out, ws, max_q_len=max(n), lse=lse)
+            assert mx.moe_get_status(ws) == mx.MX_ERR_TIMEOUT
+        finally:
+            mx.mx_debug_set_wait_limit_ns(2_000_000_000)
+        mx.mx_paged_attention(q, cache, *batch.device(), out, ws, max_q_len=max(n), lse=lse)
+        assert mx.moe_get_status(ws) == 0
+        assert torch.equal(out, want) and torch.equal(lse, want_l)
