@@ -83,6 +83,11 @@ __device__ __noinline__ AttnTile attn_tile(const AttnArgs& a, const AttnSeq& s, 
   return t;
 }
 
+// The first key that a row at position `at` sees with a window.  The position may be
+// negative (more new tokens than keys) and the window as large as an int, so they are
+// compared before the difference is taken.
+__device__ __forceinline__ int attn_row_lo(const AttnArgs& a, int at) { return at >= a.window ? at - a.window + 1 : 0; }
+
 // Places on the line of one KV head of a sequence; kWarp: the lanes of a warp
 // (all with the same sequence) take the tiles in turn.
 template <int kRows, int kUnit, int kCost, bool kWarp>

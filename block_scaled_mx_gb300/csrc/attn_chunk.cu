@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
         const int at = cur.s.kv - cur.s.n + tok;
         // rows past the last see everything: their queries are zero
         const int hi = !valid ? INT_MAX : a.causal ? min(cur.s.kv, max(at + 1, 0)) : cur.s.kv;
-        const int lo = valid && a.window > 0 ? max(at - a.window + 1, 0) : 0;
+        const int lo = valid && a.window > 0 ? attn_row_lo(a, at) : 0;
         const int all_hi = __reduce_min_sync(0xffffffffu, hi), all_lo = __reduce_max_sync(0xffffffffu, lo);
         const bool warp_valid = row0 + 32 * (warp & 3) < rows;
         const float scale = a.scale_log2;

@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       row_fac[k] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(max(127 + s_e[2 * c + k] - 14, 1)) << 23);
       // rows past the tile's are zeros that nobody reads
       row_hi[k] = R >= rows ? INT_MAX : a.causal ? min(s.kv, at + 1) : s.kv;
-      row_lo[k] = R < rows && a.window > 0 ? max(at - a.window + 1, 0) : 0;
+      row_lo[k] = R < rows && a.window > 0 ? attn_row_lo(a, at) : 0;
     }
     // keys in [all_lo, all_hi) need no mask
     const int all_hi = __reduce_min_sync(0xffffffffu, min(row_hi[0], row_hi[1]));

@@ -354,3 +354,11 @@ def test_waits_of_few_rows_that_run_out(n, kv, fmt):
         mx.mx_paged_attention(q, cache, *batch.device(), out, ws, max_q_len=max(n), lse=lse)
         assert mx.moe_get_status(ws) == 0
         assert torch.equal(out, want) and torch.equal(lse, want_l)
+
+
+@pytest.mark.parametrize("window", [1, 3, 2 ** 31 - 1])
+@pytest.mark.parametrize("n,kv", [([5, 1, 3], [2, 0, 3]), ([90, 70, 40], [30, 0, 100])])
+def test_windows_over_more_new_tokens_than_keys(n, kv, window):
+    """The first new tokens lie at negative positions, the window is up to an int's largest."""
+    for dim in (64, 128):
+        _check(n, kv, 4, 2, dim, 16, window=window, seed=101)
