@@ -139,12 +139,16 @@ def _ptr(t) -> Optional[int]:
     raise ValueError(f"expected a CUDA tensor, got one on {t.device}")
 
 
-# the handle itself, without a torch.cuda.Stream object around it: 0.2 us a call instead of 3
-_current_device, _current_raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# The handle itself, without a torch.cuda.Stream object around it: 0.2 us a call
+# instead of 3.  A torch that lacks the names (a build without CUDA) takes the object.
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _current_device is None or _current_raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
         return _current_raw_stream(_current_device())
     if isinstance(stream, int):
         return stream

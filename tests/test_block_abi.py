@@ -151,3 +151,21 @@ def test_attention_refuses_work_that_its_counters_cannot_hold(L):
     assert attend(2 ** 20, 32, 2, 2 ** 20) == 4        # 1.07e9 of each of two
     assert attend(2 ** 19, 32, 1, 2 ** 20) == 4
     assert attend(2 ** 20, 32, 8, 2 ** 22) == 2        # 8.6e9 in all
+
+
+def test_binding_imports_on_a_torch_without_cuda():
+    """The binding takes the current stream's handle from names that only a CUDA
+    build of torch has; without them it imports, and falls back to torch's objects."""
+    import os
+    import subprocess
+    import sys
+
+    code = ("import torch\n"
+            "for name in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n"
+            "    if hasattr(torch._C, name): delattr(torch._C, name)\n"
+            "from block_scaled_mx_gb300 import mxmoe as mx\n"
+            "torch.cuda.current_stream = lambda: type('S', (), {'cuda_stream': 77})()\n"
+            "assert mx._stream(None) == 77 and mx._stream(5) == 5\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
