@@ -314,6 +314,13 @@ def _dense(t, dtype, shape, what) -> Optional[int]:
     return t.data_ptr() if t.is_cuda and t.is_contiguous() else _ptr(t)
 
 
+def _int32(n, what) -> int:
+    """n, refused where a C int cannot hold it (ctypes would drop its high bits)."""
+    if not -0x80000000 <= n <= 0x7FFFFFFF:
+        raise ValueError(f"{what}: {n} does not fit 32 bits")
+    return n
+
+
 def mx_add_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, codes=None, scales=None, fmt="e4m3",
                    stream=None):
     """z = x + residual; residual_out = z; y = RMSNorm(z) * weight; codes, scales = MX(y),
@@ -423,7 +430,7 @@ def mx_kv_read(cache, block_table, kv_lens, q_starts, k_out, v_out, ws, stream=N
 
 def mx_paged_attention_workspace_size(T, n_seqs, n_heads, n_kv_heads, head_dim, max_q_len=None) -> int:
     return lib().mx_paged_attention_workspace_size(T, n_seqs, n_heads, n_kv_heads, head_dim,
-                                                   T if max_q_len is None else max_q_len)
+                                                   T if max_q_len is None else _int32(max_q_len, "max_q_len"))
 
 
 def mx_paged_attention(q, cache, block_table, kv_lens, q_starts, out, ws, scale=None, causal=True, window=0,
@@ -435,8 +442,9 @@ def mx_paged_attention(q, cache, block_table, kv_lens, q_starts, out, ws, scale=
     shape = T, heads, dim = q.shape
     qp, qs = _rows(q, heads, cache.head_dim, "q")
     st = lib().mx_paged_attention(cache._address, qp, qs, heads, table, lens, starts, n, pages, T,
-                                  T if max_q_len is None else max_q_len, dim ** -0.5 if scale is None else scale,
-                                  1 if causal else 0, window, _dense(out, torch.bfloat16, shape, "out"),
+                                  T if max_q_len is None else _int32(max_q_len, "max_q_len"),
+                                  dim ** -0.5 if scale is None else scale, 1 if causal else 0,
+                                  _int32(window, "window"), _dense(out, torch.bfloat16, shape, "out"),
                                   _dense(lse, torch.float32, (T, heads), "lse"), _ptr(ws), ws.nbytes, _stream(stream))
     if st:
         raise MxError(st, "mx_paged_attention")

@@ -169,3 +169,35 @@ def test_binding_imports_on_a_torch_without_cuda():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_binding_refuses_numbers_that_do_not_fit(L, monkeypatch):
+    """ctypes drops the high bits of an int: a window of 2^32 + 5 would be one of 5."""
+    from block_scaled_mx_gb300 import mxmoe as mx
+
+    seen = []
+
+    class Recorder:   # in the library's place, as no call may reach a device
+        def __getattr__(self, name):
+            return lambda *a: seen.append(name) or 0
+
+    monkeypatch.setattr(mx, "_lib", Recorder())
+    monkeypatch.setattr(mx, "_ptr", lambda t: 0)
+    monkeypatch.setattr(mx, "_rows", lambda *a: (0, 0))
+    monkeypatch.setattr(mx, "_dense", lambda *a: 0)
+    cache = type("Cache", (), {"head_dim": 64, "_address": 0})()
+    q, t = torch.empty(0, 8, 64), torch.empty(1, 1)
+
+    def attend(**kw):
+        mx.mx_paged_attention(q, cache, t, t, t, None, t, stream=0, **kw)
+
+    for bad in (2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="window"):
+            attend(window=bad)
+        with pytest.raises(ValueError, match="max_q_len"):
+            attend(max_q_len=bad)
+        with pytest.raises(ValueError, match="max_q_len"):
+            mx.mx_paged_attention_workspace_size(4, 2, 8, 2, 64, bad)
+    assert not seen
+    attend(window=2 ** 31 - 1, max_q_len=3)
+    assert seen == ["mx_paged_attention"]
