@@ -170,7 +170,8 @@ int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride
   if (st != MX_OK) return st;
   st = check_attention(T, n_seqs, n_heads, cache->n_kv_heads, cache->head_dim, max_q_len);
   if (st != MX_OK) return st;
-  if (!finite_positive(scale) || window < 0 || (window > 0 && !causal)) return MX_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!finite_positive(scale) || !finite_positive(scale_log2) || window < 0 || (window > 0 && !causal)) return MX_ERR_INVALID_ARG;
   if (q_stride < static_cast<int64_t>(n_heads) * cache->head_dim) return MX_ERR_INVALID_ARG;
   if (cache->page_size % 16) return MX_ERR_UNSUPPORTED;
   // cache rows are counted in ints
@@ -213,7 +214,7 @@ int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride
   a.max_q_len = max_q_len;
   a.causal = causal != 0;
   a.window = window;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.out = out;
   a.lse = lse;
   a.status = static_cast<int*>(ws);

@@ -436,8 +436,8 @@ MX_API size_t mx_paged_attention_workspace_size(int T, int n_seqs, int n_heads, 
  * some new token sees may reach the sequence's other new tokens of the call.
  * Deterministic: the same call gives the same bits.  Two launches at most: one
  * for sequences with few rows, one for chunks.
- * Errors: MX_ERR_INVALID_ARG (null, sizes, n_heads % n_kv_heads, scale not
- * positive and finite, window < 0 or without causal, stride),
+ * Errors: MX_ERR_INVALID_ARG (null, sizes, n_heads % n_kv_heads, scale or
+ * scale * log2(e) not positive and finite, window < 0 or without causal, stride),
  * MX_ERR_UNSUPPORTED (head_dim other than 64 and 128, page_size % 16, more
  * than 2^30 rows of q or 2^31 of a cache table, or 2^31 (256 query rows x 64
  * keys) of work for one KV head, 4e9 in all, by the sizes given),

@@ -201,3 +201,14 @@ def test_binding_refuses_numbers_that_do_not_fit(L, monkeypatch):
     assert not seen
     attend(window=2 ** 31 - 1, max_q_len=3)
     assert seen == ["mx_paged_attention"]
+
+
+def test_attention_refuses_a_scale_that_overflows_with_log2_e(L):
+    """The kernels work in powers of two: scale * log2(e) has to be finite too."""
+    c = _cache()
+
+    def attend(scale):   # with too small a workspace, so that nothing is launched
+        return L.mx_paged_attention(ctypes.addressof(c), fake, 512, 8, fake, fake, fake, 2, 4, 4, 4, scale, 1, 0, fake, fake,
+                                    fake, 256, None)
+
+    assert attend(2.3e38) == 4 and attend(2.4e38) == 1 and attend(3.4e38) == 1
