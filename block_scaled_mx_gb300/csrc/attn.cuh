@@ -14,6 +14,7 @@
 // at a segment joins its parts, always in key order, so results do not depend on
 // which one that is.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -445,7 +446,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // Tensor map of a code table, a.box_keys rows a box, swizzled so that 16-byte
 // pieces of neighbouring rows lie in different banks (or not at all).
 inline cudaError_t attn_code_map(CUtensorMap* map, const AttnArgs& a, const uint8_t* codes, int row_bytes, bool swizzle) {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  // atomic: the first calls may come from several threads, which find the same
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 encode = known.load(std::memory_order_relaxed);
   if (!encode) {
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -453,6 +456,7 @@ inline cudaError_t attn_code_map(CUtensorMap* map, const AttnArgs& a, const uint
         q != cudaDriverEntryPointSuccess)
       return cudaErrorNotSupported;
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    known.store(encode, std::memory_order_relaxed);
   }
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(a.num_pages) * a.n_kv_heads * a.page_size};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
