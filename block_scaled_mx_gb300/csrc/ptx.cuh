@@ -214,19 +214,9 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// 16-bit MMAs (kind::f16; f16 or bf16 by the instruction descriptor, the same
-// for A and B), fp32 accumulation, K = 16: A and B from shared memory, or A
-// from tensor memory (two K elements to a 32-bit column).
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t desc_hi,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 ad, {%1, %5};\n\t"
-      "mov.b64 bd, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(desc_hi));
-}
+// 16-bit MMA (kind::f16; f16 or bf16 by the instruction descriptor, the same for A
+// and B), fp32 accumulation, K = 16: A from tensor memory (two K elements to a
+// 32-bit column), B from shared memory.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t desc_hi,
                                            uint32_t idesc, uint32_t accumulate) {
   asm volatile(
