@@ -30,10 +30,10 @@ __device__ __forceinline__ int64_t token_row(const KvArgs& a, int t, int lane) {
     lo += (n - 1) * step;
     hi = min(lo + step, hi);
   }
-  const int end = a.q_starts[lo + 1];
+  const int start = a.q_starts[lo], end = a.q_starts[lo + 1], kv = a.kv_lens[lo];
   if (t >= end) return -1;
-  const int64_t pos = static_cast<int64_t>(a.kv_lens[lo]) - (end - t);
-  if (a.q_starts[lo] > t || pos < 0 || pos >= static_cast<int64_t>(a.max_pages) * a.page_size) {
+  const int64_t pos = static_cast<int64_t>(kv) - (end - t);
+  if (start < 0 || start > t || end > a.T || pos < 0 || kv > static_cast<int64_t>(a.max_pages) * a.page_size) {
     if (lane == 0) set_status(a.status, MX_ERR_DEVICE_ARG);
     return -1;
   }

@@ -392,9 +392,10 @@ typedef struct mx_kv_cache {
 /* Quantises T new keys and values and writes them to their places in the cache:
  * token t of sequence b goes to position kv_lens[b] - q_starts[b+1] + t.
  *   k, v: bf16, token t's [n_kv_heads, head_dim] at t * stride elements.
- * The codes are mx_quantize_act's of the same row, bit for bit.  Tokens with a
- * bad length, start or page are skipped.  Two tokens with the same place leave
- * either one.
+ * The codes are mx_quantize_act's of the same row, bit for bit.  Skipped are the
+ * tokens of a sequence whose start, end or length is out of range, and those
+ * without a position (more new tokens than kv_lens counts) or a page.  Two
+ * tokens with the same place leave either one.
  * Errors: MX_ERR_INVALID_ARG (null, negative or zero sizes, unknown format, a
  * stride below n_kv_heads * head_dim), MX_ERR_UNSUPPORTED (head_dim % 32),
  * MX_ERR_ALIGNMENT (k, v or a stride not a multiple of 16 bytes, a table),

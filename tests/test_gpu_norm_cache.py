@@ -249,3 +249,34 @@ def test_kv_bad_metadata_is_reported_and_skipped():
             assert float(ko[t].abs().sum()) > 0
         else:
             assert float(ko[t].abs().sum()) == 0 and float(vo[t].abs().sum()) == 0
+
+
+@pytest.mark.parametrize("starts,kv,good", [
+    ([0, 2, 50], [20, 48], [0, 1]),        # the second sequence's end lies past the tokens
+    ([-3, 2, 5], [20, 30], [2, 3, 4]),     # the first one's start is negative
+    ([0, 2, 5], [33, 30], [2, 3, 4]),      # a length past the table, by one token
+    ([0, 2, 5], [20, -1], [0, 1])])
+def test_kv_starts_and_lengths_out_of_range(starts, kv, good):
+    """A sequence whose start, end or length is out of range is left out as a whole,
+    as the attention leaves it out: nothing of it is written, read or kept."""
+    T, page = 5, 16
+    k, v = _kv_inputs(T, 2, 64, 11, False)
+    table = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
+    batch = (table, torch.tensor(kv, dtype=torch.int32, device="cuda"), torch.tensor(starts, dtype=torch.int32, device="cuda"))
+    cache = mx.KVCache(4, page, 2, 64)
+    ws = mx.alloc_workspace(256)
+    mx.mx_kv_append(cache, k, v, *batch, ws)
+    assert mx.moe_get_status(ws) == mx.MX_ERR_DEVICE_ARG
+    ko, vo = torch.full_like(k, 7.0), torch.full_like(v, 7.0)
+    mx.mx_kv_read(cache, *batch, ko, vo, ws)
+    assert mx.moe_get_status(ws) == mx.MX_ERR_DEVICE_ARG
+    written = cache.k_scales.amax(dim=(1, 3)) > 0
+    assert int(written.sum()) == len(good)
+    for t in range(T):
+        for x, o in ((k, ko), (v, vo)):
+            if t in good:
+                # half a step of e4m3 (2^-4), or of the smallest of the block
+                assert torch.all((o[t] - x[t]).abs().float() <= 2.0 ** -4 * x[t].abs().float() + 2.0 ** -3 * x[t].abs().amax().float())
+                assert float(o[t].abs().sum()) > 0
+            else:
+                assert float(o[t].abs().sum()) == 0
