@@ -87,10 +87,11 @@ __device__ __forceinline__ int units_of(Cursor& c, const AttnArgs& a) {
 }
 
 // What the softmax and the MMA issuer need to know of a unit.
-struct UnitMeta {
+struct alignas(16) UnitMeta {
   int v_exp;  // exponent of its largest V scale
   int wide;   // V and P in bf16
   uint32_t bad;  // UnitKeys::bad
+  float back;    // 2^-v_exp, or NaN where a V scale is
 };
 // A unit's keys to read, counted from its first, and its 16-key groups that are
 // not there (a bit each).
@@ -679,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
             if (__builtin_expect(meta.wide, 0)) weights([](float2 w) { return pack_bf16(w.x, w.y); });
             else weights([](float2 w) { return pack_f16(w.x, w.y); });
             const float2 all = add2(sum[0], sum[1]);
-            l = fmaf(all.x + all.y, __uint_as_float(static_cast<uint32_t>(127 - meta.v_exp) << 23), l);
+            l = fmaf(all.x + all.y, meta.back, l);
             wait_values();
             tmem_st_32x32b_x32(p_col, reinterpret_cast<uint32_t(&)[32]>(v[0]));
             tmem_st_wait();
@@ -962,6 +963,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk(const __grid_constan
           UnitMeta meta;
           meta.v_exp = min(max(static_cast<int>(top) - 127, -100), 126);
           meta.bad = keys.bad;
+          meta.back = __uint_as_float(top == 255u ? 0x7FC00000u : static_cast<uint32_t>(127 - meta.v_exp) << 23);
           meta.wide = meta.v_exp - (static_cast<int>(low) - 127) > 15;
           sh.meta[static_cast<uint32_t>(i) % kMetaRing] = meta;
         }

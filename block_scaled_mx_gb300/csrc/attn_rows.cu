@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       {
         const uint32_t ks = load_scales<Sh::kBlocks>(k_scales, warp * 16 + (lane & 15));
         const uint32_t vs = load_scales<Sh::kBlocks>(v_scales, warp * 16 + (lane & 15));
-        const int k_top = max_scale<Sh::kBlocks>(ks), e = min(max(max_scale<Sh::kBlocks>(vs) - 127, -100), 126);
+        const int k_top = max_scale<Sh::kBlocks>(ks), v_top = max_scale<Sh::kBlocks>(vs), e = min(max(v_top - 127, -100), 126);
         constexpr int kHalf = Sh::kBlocks / 2, kShift = E2M1 ? kE2m1Shift : 0;
         const uint32_t kh = ks >> (8 * kHalf * half), vh = vs >> (8 * kHalf * half);
 #pragma unroll
@@ -374,8 +374,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           table.v_rel[kHalf * half + b][lane & 15] =
               __float2half_rn(pow2_or_zero(min(static_cast<int>((vh >> (8 * b)) & 0xFFu) - 127 - e, 1) + kShift));
         }
+        // a scale that is NaN: K's makes the score NaN, V's the row's sum
         table.key[lane & 15] = make_float4(e8m0_value(k_top), static_cast<float>(e),
-                                           __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 0.0f);
+                                           __uint_as_float(v_top == 255 ? 0x7FC00000u : static_cast<uint32_t>(127 - e) << 23), 0.0f);
         __syncwarp();
       }
       // scores of keys g and g + 8 for the lane's rows
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         mma_f16(x, ka, qb[st].x, qb[st].y);
       }
-      const float4 key4[2] = {table.key[g], table.key[g + 8]};
+      float4 key4[2] = {table.key[g], table.key[g + 8]};
       // x[2 j + k]: key g + 8 j, row 2 c + k
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = fmaf(x[i], row_fac[i & 1] * key4[i >> 1].x, key4[i >> 1].y);
@@ -419,6 +420,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             for (int i = 0; i < Sh::kVWords; ++i) vw[j][i] = 0u;
           }
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (key + g + 8 * j >= t.hi || key + g + 8 * j < t.lo) key4[j].z = 0.0f;
       }
       // running maximum
       const bool above = fmaxf(x[0], x[2]) > m[0] + 8.0f || fmaxf(x[1], x[3]) > m[1] + 8.0f;

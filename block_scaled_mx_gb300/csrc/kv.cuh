@@ -25,9 +25,9 @@ __device__ __forceinline__ uint32_t f16x2_of_e2m1x2(uint32_t codes) {
   return r;
 }
 
-// 2^(code - 127) as fp32 (code 0 is the subnormal 2^-127).
+// 2^(code - 127) as fp32 (code 0 is the subnormal 2^-127, 255 is NaN).
 __device__ __forceinline__ float e8m0_value(int code) {
-  return __uint_as_float(code > 0 ? static_cast<uint32_t>(code) << 23 : 1u << 22);
+  return __uint_as_float(code > 0 && code < 255 ? static_cast<uint32_t>(code) << 23 : code == 0 ? 1u << 22 : 0x7FC00000u);
 }
 
 }  // namespace mxk

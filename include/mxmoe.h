@@ -364,7 +364,9 @@ MX_API int mx_add_rmsnorm(const void* x, int x_type, const void* residual, int r
  * dense, [num_pages, n_kv_heads, page_size, row] with row = head_dim bytes of
  * codes (MX_E4M3; head_dim / 2 for MX_E2M1, element 2i in the low nibble) or
  * head_dim / 32 scale bytes: a page holds page_size tokens of one sequence,
- * head by head.  The tables are 16-byte aligned. */
+ * head by head.  The tables are 16-byte aligned.  A scale byte of 255 is E8M0's
+ * NaN: mx_kv_append never writes it, mx_kv_read gives NaN for its block, and the
+ * attention a NaN row where a row sees such a key or value. */
 typedef struct mx_kv_cache {
   uint8_t* k_codes;
   uint8_t* k_scales;

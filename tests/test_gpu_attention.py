@@ -362,3 +362,28 @@ def test_windows_over_more_new_tokens_than_keys(n, kv, window):
     """The first new tokens lie at negative positions, the window is up to an int's largest."""
     for dim in (64, 128):
         _check(n, kv, 4, 2, dim, 16, window=window, seed=101)
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("n,kv,dim", [([1, 2], [90, 300], 128), ([3], [70], 64), ([70], [260], 128), ([90, 80], [90, 200], 64)])
+def test_scales_that_are_nan(n, kv, dim, fmt, which):
+    """A scale byte of 255 in one block of one key or value: the rows that see it are
+    NaN in both kernels, those of other heads and sequences keep their bits, and, for
+    a key's, those that do not see it."""
+    batch, q, cache = _setup(n, kv, 8, 2, dim, 16, fmt, seed=111)
+    want, want_l, status, _ = _call(batch, q, cache)
+    assert status == 0
+    pos = kv[0] - (n[0] + 1) // 2          # some new tokens of sequence 0 see it, in a chunk some do not
+    (page,), (at,) = batch.places(0, torch.tensor([pos]))
+    scales = {"k": cache.k_scales, "v": cache.v_scales}[which]
+    scales[page, 1, at, dim // 32 - 1] = 255
+    out, lse, status, _ = _call(batch, q, cache)
+    assert status == 0
+    seen = torch.zeros(batch.T, 8, dtype=torch.bool, device="cuda")
+    seen[n[0] - (kv[0] - pos): n[0], 4:] = True
+    assert torch.all(torch.isnan(out[seen])) and torch.all(torch.isnan(lse[seen]))
+    same = ~seen
+    if which == "v":
+        same[: n[0], 4:] = False           # what a masked value holds may reach them
+    assert torch.equal(out[same], want[same]) and torch.equal(lse[same], want_l[same])

@@ -280,3 +280,22 @@ def test_kv_starts_and_lengths_out_of_range(starts, kv, good):
                 assert float(o[t].abs().sum()) > 0
             else:
                 assert float(o[t].abs().sum()) == 0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_kv_read_of_a_scale_that_is_nan(fmt):
+    """A scale byte of 255 reads as NaN whatever the codes, zero among them."""
+    batch = ref.make_batch([3], [3], 16, 1)
+    k, v = _kv_inputs(3, 1, 64, 3, False)
+    k[1, 0, 40] = 0.0
+    cache = mx.KVCache(batch.pages, 16, 1, 64, fmt)
+    ws = mx.alloc_workspace(256)
+    mx.mx_kv_append(cache, k, v, *batch.device(), ws)
+    ko, vo, ko2, vo2 = (torch.empty_like(k) for _ in range(4))
+    mx.mx_kv_read(cache, *batch.device(), ko, vo, ws)
+    page, at = batch.places(0, torch.tensor([1]))
+    cache.k_scales[page[0], 0, at[0], 1] = 255
+    mx.mx_kv_read(cache, *batch.device(), ko2, vo2, ws)
+    hit = torch.zeros(3, 1, 64, dtype=torch.bool, device="cuda")
+    hit[1, 0, 32:] = True
+    assert torch.all(torch.isnan(ko2[hit])) and torch.equal(ko2[~hit], ko[~hit]) and torch.equal(vo2, vo)
