@@ -30,7 +30,7 @@
 
 namespace {
 
-// Enough for T <= 8192 tokens, E <= 512 experts, k <= 8 (393,728 bytes needed).
+// Enough for T <= 8192 tokens, E <= 512 experts, k <= 8 (393,472 bytes needed).
 constexpr size_t kNoAllocScratchBytes = 400 * 1024;
 constexpr int kMaxDevices = 64;
 

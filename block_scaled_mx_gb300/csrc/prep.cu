@@ -255,7 +255,7 @@ cudaError_t launch_topk(const float* logits, int T, int E, int k, int32_t* ids, 
 size_t permute_scratch_bytes(int T, int E, int k) {
   const size_t nchunks = static_cast<size_t>((T + kPermuteChunk - 1) / kPermuteChunk);
   auto al = [](size_t b) { return (b + 255) & ~static_cast<size_t>(255); };
-  return al(256) + al(nchunks * E * 4) * 2 + al(static_cast<size_t>(T) * k * 4) + al(256);
+  return al(256) + al(nchunks * E * 4) * 2 + al(static_cast<size_t>(T) * k * 4);
 }
 
 PermuteScratch permute_scratch_carve(void* ws, int T, int E, int k) {
@@ -263,15 +263,16 @@ PermuteScratch permute_scratch_carve(void* ws, int T, int E, int k) {
   auto al = [](size_t b) { return (b + 255) & ~static_cast<size_t>(255); };
   uint8_t* p = static_cast<uint8_t*>(ws);
   PermuteScratch sc;
+  // What a call expects as another left it lies in front, where the sizes do not
+  // move it: the next call on the workspace may have other ones.
   sc.status = reinterpret_cast<int*>(p);
+  sc.done = reinterpret_cast<unsigned*>(p) + 1;
   p += al(256);
   sc.chunk_counts = reinterpret_cast<int*>(p);
   p += al(nchunks * E * 4);
   sc.chunk_base = reinterpret_cast<int*>(p);
   p += al(nchunks * E * 4);
   sc.local_rank = reinterpret_cast<int*>(p);
-  p += al(static_cast<size_t>(T) * k * 4);
-  sc.done = reinterpret_cast<unsigned*>(p);
   return sc;
 }
 

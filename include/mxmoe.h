@@ -34,7 +34,8 @@
  *    range) are OR-ed into a status word at the start of the caller's
  *    workspace; read and clear it with moe_get_status.
  *  - Workspaces must be zero-filled once before their first use (the library
- *    leaves them ready for the next call).
+ *    leaves them ready for the next call of the same function, of any size that
+ *    they are large enough for).
  *  - Formats: MX_E4M3 (MXFP8, one byte per element) and MX_E2M1 (MXFP4, two
  *    elements per byte, element 2i in the low nibble).  Every 32 consecutive
  *    elements along K share one E8M0 scale byte (value 2^(code-127)).
