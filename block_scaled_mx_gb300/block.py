@@ -18,11 +18,17 @@ from . import mxmoe as mx
 class DecoderBlock:
     """Weights (bf16): ``w_qkv`` [(n_heads + 2 n_kv_heads) head_dim, H], ``w_o``
     [H, n_heads head_dim], the norms' ``g_attn`` and ``g_mlp`` [H], ``w_router``
-    [E, H]; ``experts`` is a prepared MoELayer."""
+    [E, H]; ``experts`` is a prepared MoELayer.
 
-    def __init__(self, w_qkv, w_o, g_attn, g_mlp, w_router, experts, n_heads, n_kv_heads, head_dim, eps=1e-6, window=0):
+    With ``keep_last`` the block holds what its last call computed on the way in
+    ``last`` (q and with it the whole projection, att, y, codes, scales) until the
+    next call."""
+
+    def __init__(self, w_qkv, w_o, g_attn, g_mlp, w_router, experts, n_heads, n_kv_heads, head_dim, eps=1e-6, window=0,
+                 keep_last=False):
         self.w_qkv, self.w_o, self.g_attn, self.g_mlp, self.w_router, self.experts = w_qkv, w_o, g_attn, g_mlp, w_router, experts
         self.n_heads, self.n_kv_heads, self.head_dim, self.eps, self.window = n_heads, n_kv_heads, head_dim, eps, window
+        self.keep_last, self.last = keep_last, None
         self._ws = {}
 
     def _workspace(self, name, nbytes):
@@ -70,7 +76,8 @@ class DecoderBlock:
         mx.moe_grouped_gemm_swiglu(codes, scales, offsets, order, e.w1, *sizes, h_codes, h_scales, ws)
         out = torch.zeros(T, H, dtype=torch.float32, device=dev)
         mx.moe_grouped_gemm_down_combine(h_codes, h_scales, offsets, order, weights, e.w2, *sizes, out, ws)
-        self.last = dict(q=q, att=att, y=y, codes=codes, scales=scales)  # of this call, for a look at it
+        if self.keep_last:
+            self.last = dict(q=q, att=att, y=y, codes=codes, scales=scales)
         return out, after
 
     def status(self):
@@ -78,8 +85,9 @@ class DecoderBlock:
         return max((mx.moe_get_status(ws) for name, ws in self._ws.items() if name != "permute"), default=0)
 
 
-def random_block(H, I, E, k, n_heads, n_kv_heads, head_dim, fmt="e4m3", window=0, seed=0, device="cuda"):
-    """A block of random weights."""
+def random_block(H, I, E, k, n_heads, n_kv_heads, head_dim, fmt="e4m3", window=0, seed=0, device="cuda", keep_last=True):
+    """A block of random weights, which keeps what its last call computed unless told
+    not to."""
     g = torch.Generator(device=device).manual_seed(seed)
 
     def normal(*shape, fan_in):
@@ -98,11 +106,12 @@ def random_block(H, I, E, k, n_heads, n_kv_heads, head_dim, fmt="e4m3", window=0
     return DecoderBlock(normal((n_heads + 2 * n_kv_heads) * head_dim, H, fan_in=H).to(bf16),
                         normal(H, n_heads * head_dim, fan_in=n_heads * head_dim).to(bf16),
                         torch.ones(H, dtype=bf16, device=device), torch.ones(H, dtype=bf16, device=device),
-                        normal(E, H, fan_in=H).to(bf16), experts, n_heads, n_kv_heads, head_dim, window=window)
+                        normal(E, H, fan_in=H).to(bf16), experts, n_heads, n_kv_heads, head_dim, window=window,
+                        keep_last=keep_last)
 
 
 def main(prompts=(700, 33, 1), steps=4, H=2048, I=512, E=16, k=4, n_heads=16, n_kv_heads=2, head_dim=128, page=64):
-    blocks = [random_block(H, I, E, k, n_heads, n_kv_heads, head_dim, seed=s) for s in range(2)]
+    blocks = [random_block(H, I, E, k, n_heads, n_kv_heads, head_dim, seed=s, keep_last=False) for s in range(2)]
     n = len(prompts)
     per = -(-(max(prompts) + steps) // page)
     table = torch.randperm(n * per, device="cuda").to(torch.int32).view(n, per)

@@ -68,3 +68,25 @@ def test_block_over_a_ragged_batch(fmt, cache_fmt, window):
 def test_example_runs(capsys):
     B.main(prompts=(40, 3), steps=2, H=256, I=128, E=4, k=2, n_heads=4, n_kv_heads=1, head_dim=64, page=16)
     assert "step 2" in capsys.readouterr().out
+
+
+def test_block_keeps_nothing_of_a_call():
+    """Unless it is asked to: a call's activations are free once it has returned."""
+    args = (256, 128, 8, 2, 8, 2, 64)
+    blk = B.random_block(*args, keep_last=False)
+    batch = ref.make_batch([2000], [2000], 16, 1)
+    x = torch.randn(2000, 256, device="cuda")
+    res = torch.zeros(2000, 256, dtype=torch.bfloat16, device="cuda")
+    cache = mx.KVCache(batch.pages, 16, 2, 64)
+    dev = batch.device()
+    out, after = blk.forward(x, res, cache, *dev, 2000)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    out, after = blk.forward(x, res, cache, *dev, 2000)
+    torch.cuda.synchronize()
+    assert blk.last is None and torch.cuda.memory_allocated() == before
+    w = blk.__dict__
+    plain = B.DecoderBlock(*(w[n] for n in ("w_qkv", "w_o", "g_attn", "g_mlp", "w_router", "experts", "n_heads", "n_kv_heads",
+                                            "head_dim")))
+    plain.forward(x, res, cache, *dev, 2000)
+    assert plain.last is None
