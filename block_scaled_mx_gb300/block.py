@@ -34,7 +34,10 @@ class DecoderBlock:
     def _workspace(self, name, nbytes):
         ws = self._ws.get(name)
         if ws is None or ws.nbytes < nbytes:
-            ws = self._ws[name] = mx.alloc_workspace(nbytes)
+            old, ws = ws, mx.alloc_workspace(nbytes)
+            if old is not None:
+                ws[:4] = old[:4]  # an error that status() has not read yet
+            self._ws[name] = ws
         return ws
 
     def forward(self, x, residual, cache, block_table, kv_lens, q_starts, max_q_len):
@@ -82,7 +85,7 @@ class DecoderBlock:
 
     def status(self):
         """The first error that a kernel reported (synchronises), 0 for none."""
-        return max((mx.moe_get_status(ws) for name, ws in self._ws.items() if name != "permute"), default=0)
+        return max((mx.moe_get_status(ws) for ws in self._ws.values()), default=0)
 
 
 def random_block(H, I, E, k, n_heads, n_kv_heads, head_dim, fmt="e4m3", window=0, seed=0, device="cuda", keep_last=True):
