@@ -20,6 +20,10 @@ class DecoderBlock:
     [H, n_heads head_dim], the norms' ``g_attn`` and ``g_mlp`` [H], ``w_router``
     [E, H]; ``experts`` is a prepared MoELayer.
 
+    Calls on different streams may overlap: each stream has workspaces of its own,
+    which the block keeps (at most 41 MB for the attention, and what the experts'
+    GEMMs need).  An object is for one host thread at a time.
+
     With ``keep_last`` the block holds what its last call computed on the way in
     ``last`` (q and with it the whole projection, att, y, codes, scales) until the
     next call."""
@@ -29,15 +33,16 @@ class DecoderBlock:
         self.w_qkv, self.w_o, self.g_attn, self.g_mlp, self.w_router, self.experts = w_qkv, w_o, g_attn, g_mlp, w_router, experts
         self.n_heads, self.n_kv_heads, self.head_dim, self.eps, self.window = n_heads, n_kv_heads, head_dim, eps, window
         self.keep_last, self.last = keep_last, None
-        self._ws = {}
+        self._ws = {}  # by name and stream
 
     def _workspace(self, name, nbytes):
-        ws = self._ws.get(name)
+        key = name, mx.current_stream()
+        ws = self._ws.get(key)
         if ws is None or ws.nbytes < nbytes:
             old, ws = ws, mx.alloc_workspace(nbytes)
             if old is not None:
                 ws[:4] = old[:4]  # an error that status() has not read yet
-            self._ws[name] = ws
+            self._ws[key] = ws
         return ws
 
     def forward(self, x, residual, cache, block_table, kv_lens, q_starts, max_q_len):
@@ -84,8 +89,9 @@ class DecoderBlock:
         return out, after
 
     def status(self):
-        """The first error that a kernel reported (synchronises), 0 for none."""
-        return max((mx.moe_get_status(ws) for ws in self._ws.values()), default=0)
+        """The first error that a kernel reported (waits for the device), 0 for none."""
+        torch.cuda.synchronize()
+        return max((mx.moe_get_status(ws, stream) for (_, stream), ws in self._ws.items()), default=0)
 
 
 def random_block(H, I, E, k, n_heads, n_kv_heads, head_dim, fmt="e4m3", window=0, seed=0, device="cuda", keep_last=True):

@@ -155,6 +155,11 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def current_stream() -> int:
+    """The handle of torch's current stream, which a call without ``stream`` uses."""
+    return _stream(None)
+
+
 def _check(st: int, what: str):
     if st != MX_OK:
         raise MxError(st, what)

@@ -19,6 +19,7 @@ def blk(monkeypatch):
     monkeypatch.setattr(mx, "alloc_workspace", lambda n, device="cpu": torch.zeros(n, dtype=torch.uint8))
     monkeypatch.setattr(mx, "moe_get_status", status)
     monkeypatch.setattr(torch.cuda, "synchronize", lambda *a: None)
+    monkeypatch.setattr(mx, "current_stream", lambda: 1, raising=False)
     return B.DecoderBlock(*[None] * 6, 8, 2, 64)
 
 
@@ -31,3 +32,14 @@ def test_an_error_is_kept_when_a_workspace_grows(blk, name):
     assert grown.nbytes == 1024 and int(grown[4:].max()) == 0
     assert blk.status() == 6
     assert blk.status() == 0
+
+
+def test_streams_have_workspaces_of_their_own(blk, monkeypatch):
+    one = blk._workspace("attention", 256)
+    monkeypatch.setattr(mx, "current_stream", lambda: 2, raising=False)
+    two = blk._workspace("attention", 256)
+    assert two is not one and blk._workspace("attention", 256) is two
+    monkeypatch.setattr(mx, "current_stream", lambda: 1, raising=False)
+    assert blk._workspace("attention", 256) is one
+    one[:4] = 3                             # an error on either stream is found
+    assert blk.status() == 3

@@ -90,3 +90,30 @@ def test_block_keeps_nothing_of_a_call():
                                             "head_dim")))
     plain.forward(x, res, cache, *dev, 2000)
     assert plain.last is None
+
+
+def test_calls_of_one_block_on_two_streams():
+    """Steps of different batches that overlap give what they give one after the other."""
+    blk = B.random_block(256, 128, 8, 2, 8, 2, 64, keep_last=False)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    steps = []
+    for new in ([700, 60], [1] * 40):
+        batch = ref.make_batch(new, [n + 300 for n in new], 16, 1)
+        cache = mx.KVCache(batch.pages, 16, 2, 64)
+        steps.append((torch.randn(batch.T, 256, generator=g, device="cuda"),
+                      torch.randn(batch.T, 256, generator=g, device="cuda").to(torch.bfloat16), cache, *batch.device(), max(new)))
+    want = [[blk.forward(*s) for s in steps] for _ in range(2)][1]
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got[i].append(blk.forward(*steps[i]))
+    assert blk.status() == 0
+    for i in range(2):
+        for out, after in got[i]:
+            assert torch.equal(after, want[i][1])
+            # a token's k + 1 = 3 slots in pieces, added in any order: at most 16
+            # additions of 2^-24 each, of terms that sum to four times their sum's size
+            assert float((out - want[i][0]).norm()) <= 2.0 ** -18 * float(want[i][0].norm())
