@@ -433,9 +433,16 @@ MX_API size_t mx_paged_attention_workspace_size(int T, int n_seqs, int n_heads, 
  *   out [T, n_heads, head_dim] bf16, lse [T, n_heads] fp32 or NULL, dense.
  *   max_q_len: no sequence has more new tokens (one that has is reported and
  *     its rows are not written).
- * Scores, softmax statistics and sums are fp32.  Rows of padding and of bad
- * metadata are not written; a bad page's keys are left out.  Cache places that
- * no row sees may hold anything, also pages behind the window may be gone.
+ * Scores, softmax statistics and sums are fp32.  For the second product a weight
+ * is rounded to f16 (2^-11), or, in chunks where the V scales of 64 keys spread over
+ * more than 2^15, to bf16 (2^-8); a weight times its value's largest block scale is
+ * held to 2^-25 of the row's largest such product: next to a value 2^25 larger, the
+ * others fade.  For few rows an element of a key or value is held to 2^-25 of its
+ * token's largest block scale, and is zero where its own block's scale lies 2^25
+ * below (MX_E2M1: 2^31).
+ * Rows of padding and of bad metadata are not written; a bad page's keys are left
+ * out.  Cache places that no row sees may hold anything, also pages behind the
+ * window may be gone.
  * A NaN or infinity in a query makes its row NaN; a NaN among the values that
  * some new token sees may reach the sequence's other new tokens of the call.
  * Deterministic: the same call gives the same bits.  Two launches at most: one

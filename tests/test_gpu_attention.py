@@ -387,3 +387,100 @@ def test_scales_that_are_nan(n, kv, dim, fmt, which):
     if which == "v":
         same[: n[0], 4:] = False           # what a masked value holds may reach them
     assert torch.equal(out[same], want[same]) and torch.equal(lse[same], want_l[same])
+
+
+def _bounded(q, tables, fmt, batch, scale):
+    """(out, lse, their bounds), fp64, causal, with what the header states of the
+    second product's roundings, element by element:
+    out goes to bf16 (2^-8); a weight to f16 (2^-11), or to bf16 (2^-8) where the V scales of a
+    64-key unit spread over more than 2^15; a weight times its value's largest block
+    scale is held to 2^-25 of the row's largest such product (f16's smallest step,
+    halved).  For few rows a key's or value's element is held to 2^-25 of its token's
+    largest block scale and is zero where its own block's scale lies 2^25 below (E2M1:
+    2^31).  A score sums D products in fp32 (2^-24 each of the sum of their sizes); a
+    query's element is held to 2^-22 of its block's largest.  Exponents are taken in
+    fp32: 2^-22 of the scores' sizes, and 2^-20 for the rest.  Only the scores' errors
+    against the largest weight's count; a weight that is off by r moves out by r (v - o)
+    and at most twice that once all are normalised, while they add up to less than 1/2."""
+    two = torch.tensor(2.0, dtype=torch.float64)
+    gone = 25 if fmt == "e4m3" else 31
+
+    def held(x, scales):
+        """How far each element of x [kv, Hk, D] may be off for its token's other blocks."""
+        top = scales.double().amax(-1, keepdim=True)
+        far = (scales.double() <= top - gone).repeat_interleave(32, -1)
+        return torch.where(far, x.abs(), torch.minimum(x.abs(), 2.0 ** -25 * torch.pow(two, top - 127)))
+
+    T, Hq, D = q.shape
+    Hk = tables[0].shape[1]
+    out, tol = (torch.zeros(T, Hq, D, dtype=torch.float64) for _ in range(2))
+    lse, tol_lse = (torch.zeros(T, Hq, dtype=torch.float64) for _ in range(2))
+    for b, (n, kv) in enumerate(zip(batch.n, batch.kv)):
+        page, at = batch.places(b, torch.arange(kv))
+        kc, ks, vc, vs = (t[page, :, at] for t in tables)
+        K, V = ref.decode(kc, ks, fmt), ref.decode(vc, vs, fmt)
+        v_top = vs.double().amax(-1) - 127          # [kv, Hk]
+        K_off, V_off = held(K, ks), held(V, vs)
+        for i in range(n):
+            hi = kv - n + i + 1
+            unit = torch.arange(hi) // 64
+            for h in range(Hq):
+                g = h * Hk // Hq
+                k, v, e = K[:hi, g], V[:hi, g], v_top[:hi, g]
+                x = q[batch.starts[b] + i, h].double()
+                block = x.abs().unflatten(0, (-1, 32)).amax(1).repeat_interleave(32)
+                s = k @ x * scale
+                ds = scale * (D * 2.0 ** -24 * (k.abs() @ x.abs()) + K_off[:hi, g] @ x.abs() + 2.0 ** -22 * (k.abs() @ block))
+                ds = ds + 2.0 ** -22 * (s.abs() + s.abs().max()) + 2.0 ** -20
+                p, star = torch.softmax(s, 0), int(s.argmax())
+                o = p @ v
+                r = torch.exp(torch.log_softmax(s, 0) + ds + ds[star]) - p   # of each weight
+                r[star] = 0
+                assert float(r.sum()) < 0.5
+                tops = torch.stack([v_top[u * 64: (u + 1) * 64, g].max() for u in range(int(unit[-1]) + 1)])
+                lows = torch.stack([vs[u * 64: (u + 1) * 64, g].double().min() - 127 for u in range(int(unit[-1]) + 1)])
+                half = torch.where(tops - lows > 15, 2.0 ** -8, 2.0 ** -11)[unit]
+                most = (p * torch.pow(two, tops[unit])).max()
+                err = (2 * r @ (v - o).abs() + (p * half) @ v.abs() + p @ V_off[:hi, g]
+                       + 2.0 ** -25 * most * (torch.pow(two, -e) @ v.abs()))
+                t = batch.starts[b] + i
+                out[t, h], tol[t, h] = o, 2.0 ** -8 * (o.abs() + err) + err
+                lse[t, h] = torch.logsumexp(s, 0)
+                tol_lse[t, h] = ds[star] + 2 * r.sum() + 2.0 ** -22 * (1 + lse[t, h].abs()) + 2.0 ** -20
+    return out, lse, tol, tol_lse
+
+
+@pytest.mark.parametrize("spread", [4, 8, 12, 16])
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("n,kv,dim", [([2, 1], [150, 40], 128), ([3], [90], 64), ([50], [150], 128), ([70], [100], 64)])
+def test_tokens_that_are_large_in_one_block(n, kv, dim, fmt, spread):
+    """One token of each sequence has keys and values 2^spread larger in one block of
+    32; half of the query heads have zeros there, so that their scores are ordinary."""
+    heads, kv_heads, page = 4, 2, 16
+    batch = ref.make_batch(n, kv, page, 121)
+    full = ref.Batch(list(kv), list(kv), page, batch.pages, batch.table)
+    g = torch.Generator().manual_seed(122)
+    k, v = (torch.randn(full.T, kv_heads, dim, generator=g) for _ in range(2))
+    for b in range(len(n)):
+        at = full.starts[b] + kv[b] // 3
+        k[at, :, 32:] *= 2.0 ** spread
+        v[at, :, 32:] *= 2.0 ** spread
+    q = torch.randn(batch.T, heads, dim, generator=g)
+    q[:, ::2, 32:] = 0
+    q = q.to(torch.bfloat16)
+    cache = mx.KVCache(batch.pages, page, kv_heads, dim, fmt)
+    ws = mx.alloc_workspace(256)
+    mx.mx_kv_append(cache, k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda(), *full.device(), ws)
+    out, lse, status, _ = _call(batch, q.cuda(), cache)
+    assert status == 0
+    tables = [t.cpu() for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)]
+    o, l, tol, tol_l = _bounded(q, tables, fmt, batch, dim ** -0.5)
+    assert torch.all((out.cpu().double() - o).abs() <= tol)
+    assert torch.all((lse.cpu().double() - l).abs() <= tol_l)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("n,kv,page", [([1, 2], [70001, 40003], 16), ([1], [140000], 64), ([40], [66007], 16)])
+def test_long_contexts(n, kv, page, fmt):
+    """Thousands of pages of one sequence."""
+    _check(n, kv, 2, 1, 64, page, fmt, seed=131)

@@ -299,3 +299,41 @@ def test_kv_read_of_a_scale_that_is_nan(fmt):
     hit = torch.zeros(3, 1, 64, dtype=torch.bool, device="cuda")
     hit[1, 0, 32:] = True
     assert torch.all(torch.isnan(ko2[hit])) and torch.equal(ko2[~hit], ko[~hit]) and torch.equal(vo2, vo)
+
+
+def test_add_rmsnorm_e2m1_codes_feed_the_grouped_gemms():
+    """MXFP4 codes of the norm through both grouped GEMMs, against the layer in one call
+    on the values that the codes stand for, which it quantises to the same codes."""
+    from block_scaled_mx_gb300 import block as B
+
+    T, H, I, E, k = 37, 256, 128, 8, 2
+    layer = B.random_block(H, I, E, k, 4, 2, 64, fmt="e2m1", seed=5).experts
+    opts = mx.layer_opts(act_fmt="e2m1")
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    w = (1 + 0.2 * torch.randn(H, generator=g, device="cuda")).to(torch.bfloat16)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    codes = torch.empty(T, H // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(T, H // 32, dtype=torch.uint8, device="cuda")
+    mx.mx_add_rmsnorm(x, w, 1e-6, codes=codes, scales=scales, fmt="e2m1")
+    values = ref.decode(codes.cpu(), scales.cpu(), "e2m1").to(torch.bfloat16).cuda()
+    again, again_s = torch.empty_like(codes), torch.empty_like(scales)
+    mx.mx_quantize_act(values, again, again_s, fmt="e2m1")
+    assert torch.equal(again, codes) and torch.equal(again_s, scales)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ids, weights = torch.empty(T, k, **i32), torch.empty(T, k, dtype=torch.float32, device="cuda")
+    mx.moe_route_topk(logits, k, ids, weights)
+    counts, offsets, order = torch.empty(E + 1, **i32), torch.empty(E + 2, **i32), torch.empty(T * (k + 1), **i32)
+    mx.moe_permute(ids, E, counts, offsets, order, mx.alloc_workspace(mx.moe_permute_workspace_size(T, E, k)))
+    h = torch.empty(T * (k + 1), I // 2, dtype=torch.uint8, device="cuda")
+    hs = torch.empty(T * (k + 1), I // 32, dtype=torch.uint8, device="cuda")
+    ws = mx.alloc_workspace(mx.moe_gemm_workspace_size(T, H, I, E, k))
+    sizes = (layer.fmt, T, H, I, E, k)
+    mx.moe_grouped_gemm_swiglu_ex(codes, scales, offsets, order, layer.w1, *sizes, h, hs, ws, opts)
+    out = torch.zeros(T, H, dtype=torch.float32, device="cuda")
+    mx.moe_grouped_gemm_down_combine(h, hs, offsets, order, weights, layer.w2, *sizes, out, ws, opts=opts)
+    assert mx.moe_get_status(ws) == 0
+    one = layer.forward(values, logits, opts=opts)
+    # an h next to a border may take either code, a step of at most 2^-1: one in 1000 of
+    # them moves the output by 2^-1 / 1000^0.5 = 0.016 (relative, L2)
+    assert float(one.norm()) > 0 and float((out - one).norm()) <= 0.016 * float(one.norm())
