@@ -24,9 +24,8 @@
 // (8 sequences of 8192 and 4 KV heads, 16 rows: 53 us, as two tiles 35).  P^T goes
 // from the layout of S^T's results to that of an operand by a transposing move.
 // The contraction order of an MMA is free, so a lane feeds it the 16-byte pieces
-// that it reads from shared memory.  (The register-level MMAs on 8-bit codes are
-// no way around the widening: they compile to conversions and MMAs on f16; with
-// them 32 sequences took 84 us.)
+// that it reads from shared memory.  (Register-level MMAs on the 8-bit codes were
+// slower than widening them for f16 ones: 32 sequences took 84 us against 77.)
 //
 // Arithmetic.  Codes are exact in f16.  A key's blocks are scaled relative to
 // the key's largest block scale (a power of two: exact down to 2^-24 of the
@@ -81,9 +80,8 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 // A word's four even or odd E2M1 codes as E4M3 codes of 2^-6 their size, by moving
-// their bits; from those the conversion takes an instruction for two, which from
-// E2M1 itself takes two, and for half of the bytes three (3 sequences of up to
-// 65536: 83 us from E2M1, 82 moving its bits into f16, 79 this way).
+// their bits; the conversion to f16 then starts from E4M3 (3 sequences of up to
+// 65536: 83 us converting from E2M1 itself, 82 moving its bits into f16, 79 this way).
 constexpr int kE2m1Shift = 6;
 __device__ __forceinline__ uint32_t e4m3_of_even(uint32_t w) { return (w << 4 & 0x80808080u) | (w << 2 & 0x1C1C1C1Cu); }
 __device__ __forceinline__ uint32_t e4m3_of_odd(uint32_t w) { return (w & 0x80808080u) | (w >> 2 & 0x1C1C1C1Cu); }

@@ -200,9 +200,8 @@ __device__ __forceinline__ void mma_mxf4_lo(uint32_t d_tmem, uint32_t a_lo, uint
       "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem), "r"(desc_hi));
 }
 
-// One lane of a converged warp.  Code under it, unlike code under lane == 0, is
-// compiled for one thread with its operands in uniform registers: an MMA then
-// issues in the 32 cycles that its tile takes (128 x 64 x 16) instead of 55.
+// One lane of a converged warp.  Timed: MMAs issued under it take the 32 cycles of
+// their tile (128 x 64 x 16) each, under lane == 0 they took 55.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
