@@ -1,6 +1,7 @@
 // C ABI of the operators around the expert layer (residual norm, paged MX cache,
 // attention): argument checks and workspace carving (see include/mxmoe.h).
 #include <cuda_runtime.h>
+#include <algorithm>
 #include <climits>
 #include <cstdint>
 
@@ -66,15 +67,37 @@ KvArgs kv_args(const mx_kv_cache* c, const int32_t* block_table, const int32_t* 
 constexpr size_t kArrivedOffset = 256;
 constexpr size_t kArrivedBytes = sizeof(unsigned) * kAttnMaxCtas;
 
-// Sequences of up to this many rows (new tokens x query heads of a KV head) are
-// the few-rows kernel's, others the chunk kernel's.  The few-rows kernel works
-// through the keys again for every 8 rows, the chunk kernel takes as long for
-// 256 as for one but starts and ends slower: over 8 sequences of 8192 tokens and
-// 4 KV heads, 16 rows took 35 us against 52, 24 46 against 52, 32 58 against 52.
-// With few (sequence, KV head) pairs the start weighs more: over 2 pairs of 2051
-// keys, 128 rows took 24 us against 41, 192 37 against 45.
+// Sequences of up to few_rows() rows (new tokens x query heads of a KV head) are the
+// few-rows kernel's, others the chunk kernel's.  The few-rows kernel goes through the
+// keys again for every 8 rows; the chunk kernel takes as long for 256 as for one, but
+// starts and ends slower, the more so the fewer the (sequence, KV head) pairs among
+// which its 152 CTAs share out and join the keys.  Count a batch's work in 64-key
+// units, and 8 more for each pair.  Without the start the chunk kernel's time is that
+// of two or three tiles of 8 rows; every further tile costs the few-rows kernel 2.5 ns
+// a unit (heads of 128 in MXFP8; 1.6 to 2.8 in the other three forms), and the start is
+// worth 10 us and 200 us over the number of pairs, less where a pair has few units.
+// In us, few rows / chunk, heads of 128 in MXFP8, on either side of the rule:
+//   pairs x keys     rows and times
+//   2 x 2048         128: 23 / 40
+//   2 x 131072       64: 102 / 167     96: 140 / 169     128: 180 / 170
+//   16 x 2048        96: 35 / 41       128: 42 / 41
+//   16 x 8192        32: 36 / 47       48: 47 / 47       64: 57 / 47
+//   16 x 131072      16: 182 / 191     24: 255 / 192     128: 1293 / 204
+//   32 x 2048        48: 32 / 39       64: 39 / 39       96: 52 / 41
+//   64 x 8192        16: 59 / 69       24: 80 / 71
+// Over 1056 combinations of 1 to 64 pairs, 512 to 131072 keys, 8 to 128 rows, both head
+// sizes and both formats the rule takes 0.2% longer than always the faster kernel, and
+// 28% at worst (2 pairs of 131072 keys, heads of 64, 128 rows: 152 us where 119 would do).
+// The lengths are on the device, so the keys are counted by what bounds them: the
+// block table's width and the window.
 constexpr int kMostFewRows = 128;
-int few_rows(int n_seqs, int n_kv_heads) { return static_cast<int64_t>(n_seqs) * n_kv_heads <= 16 ? kMostFewRows : 24; }
+int few_rows(int n_seqs, int n_kv_heads, int head_dim, bool e2m1, int64_t keys) {
+  const int even = head_dim == 128 && !e2m1 ? 2 : 3;
+  const int64_t pairs = static_cast<int64_t>(n_seqs) * n_kv_heads, units = (keys + 63) / 64;
+  const int64_t start = std::min<int64_t>(260 * units, 4000 + 80000 / pairs);  // of the chunk kernel, in units of one tile
+  return static_cast<int>(std::min<int64_t>(kMostFewRows, 8 * (even + start / (pairs * (units + 8)))));
+}
+constexpr int kLeastFewRows = 16;  // that few_rows() gives
 
 int check_attention(int T, int n_seqs, int n_heads, int n_kv_heads, int head_dim, int max_q_len) {
   if (T < 0 || n_seqs < 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || max_q_len < 0) return MX_ERR_INVALID_ARG;
@@ -158,7 +181,8 @@ int mx_kv_read(const mx_kv_cache* cache, const int32_t* block_table, const int32
 size_t mx_paged_attention_workspace_size(int T, int n_seqs, int n_heads, int n_kv_heads, int head_dim, int max_q_len) {
   if (check_attention(T, n_seqs, n_heads, n_kv_heads, head_dim, max_q_len) != MX_OK) return 0;
   size_t part = attn_rows_part_bytes(head_dim);
-  if (static_cast<int64_t>(max_q_len) * (n_heads / n_kv_heads) > few_rows(n_seqs, n_kv_heads) && attn_chunk_part_bytes(head_dim) > part) part = attn_chunk_part_bytes(head_dim);
+  // either kernel may take more rows than these: the lengths are not known here
+  if (static_cast<int64_t>(max_q_len) * (n_heads / n_kv_heads) > kLeastFewRows) part = std::max(part, attn_chunk_part_bytes(head_dim));
   return kArrivedOffset + al256(kArrivedBytes) + part;
 }
 
@@ -225,7 +249,9 @@ int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   a.rows_above = 0;
   a.rows_upto = INT_MAX;
-  const int few = few_rows(n_seqs, a.n_kv_heads);
+  int64_t keys = static_cast<int64_t>(max_pages) * a.page_size;
+  if (window > 0) keys = std::min(keys, static_cast<int64_t>(window) + max_q_len);
+  const int few = few_rows(n_seqs, a.n_kv_heads, a.head_dim, a.e2m1 != 0, keys);
   if (static_cast<int64_t>(max_q_len) * a.group <= few) return cuda_status(launch_attn_rows(a, cs));
   // Where all sequences are as long as the longest (T has room for it), one
   // launch takes them all; a shorter one among them is right there too.

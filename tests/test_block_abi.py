@@ -212,3 +212,14 @@ def test_attention_refuses_a_scale_that_overflows_with_log2_e(L):
                                     fake, 256, None)
 
     assert attend(2.3e38) == 4 and attend(2.4e38) == 1 and attend(3.4e38) == 1
+
+
+def test_workspace_holds_either_kernels_parts(L):
+    """Which kernel takes a sequence of a few tiles of rows depends on the length that
+    its block table allows, which the workspace's size does not ask for."""
+    f = L.mx_paged_attention_workspace_size
+    for dim in (64, 128):
+        chunks = f(4096, 1, 8, 1, dim, 4096)
+        for n, rows in ((16, 128), (16, 24), (1, 40), (64, 17)):
+            assert f(n * rows, n, 1, 1, dim, rows) >= chunks, (n, rows)
+        assert f(16 * 16, 16, 1, 1, dim, 16) < chunks

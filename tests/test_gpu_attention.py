@@ -484,3 +484,20 @@ def test_tokens_that_are_large_in_one_block(n, kv, dim, fmt, spread):
 def test_long_contexts(n, kv, page, fmt):
     """Thousands of pages of one sequence."""
     _check(n, kv, 2, 1, 64, page, fmt, seed=131)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n,window", [([6, 3, 10, 1], 0), ([12] * 4, 0), ([12] * 4, 70), ([4, 12, 0, 9], 0)])
+def test_narrow_and_wide_block_tables(n, window, dim, fmt):
+    """A wider table moves sequences of a few tiles of rows from the few-rows kernel to
+    the chunk kernel; what lies beyond the lengths is not looked at."""
+    kv = [a + 40 + 30 * b for b, a in enumerate(n)]
+    batch, q, cache = _setup(n, kv, 32, 4, dim, 16, fmt, seed=141)
+    table, lens, starts = batch.device()
+    wide = torch.full((len(n), 12000), -5, dtype=torch.int32, device="cuda")
+    wide[:, : table.shape[1]] = table
+    for t in (table, wide):
+        out, lse, status, _ = _call(batch, q, cache, dev=(t, lens, starts), window=window)
+        assert status == 0
+        _compare(batch, q, cache, out, lse, fmt, dim ** -0.5, True, window)
