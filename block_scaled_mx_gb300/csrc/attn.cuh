@@ -127,7 +127,7 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, uint32_t* uni
   const int tid = threadIdx.x, lane = tid & 31;
   constexpr int kPer = kAttnScan / 32;
   AttnShare r;
-  r.total = 0;
+  uint64_t all_of_them = 0;
   r.seq = 0;
   r.in_seq = r.u = r.end = 0;
   uint32_t v[kPer], mine = 0, before = 0;
@@ -164,6 +164,14 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, uint32_t* uni
 #pragma unroll
         for (int i = 0; i < kPer; ++i) mine += v[i] = units[lane * kPer + i];
         __syncthreads();
+        if (pass == 0) {
+          // in two halves, which a warp's sums hold
+          uint32_t lo = 0, hi = 0;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) lo += v[i] & 0xFFFFu, hi += v[i] >> 16;
+          all_of_them += __reduce_add_sync(0xffffffffu, lo) + (static_cast<uint64_t>(__reduce_add_sync(0xffffffffu, hi)) << 16);
+          continue;
+        }
       }
       uint32_t incl = mine;
 #pragma unroll
@@ -172,10 +180,6 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, uint32_t* uni
         if (lane >= d) incl += o;
       }
       const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
-      if (pass == 0) {
-        r.total += all;
-        continue;
-      }
       uint32_t from = before + incl - mine;
       int at = -1;
       uint32_t in = 0;
@@ -196,6 +200,13 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, uint32_t* uni
       }
     }
     if (pass == 0) {
+      // The host has refused what the sizes allow to be more than the line holds;
+      // starts that fall and rise again may give the same tokens to many sequences.
+      r.total = static_cast<uint32_t>(all_of_them);
+      if (all_of_them > 4000000000ull) {
+        r.total = 0;
+        if (blockIdx.x == 0) set_status(a.status, MX_ERR_DEVICE_ARG);
+      }
       const uint32_t n = (r.total + a.min_units - 1) / a.min_units;
       r.ctas = static_cast<int>(min(n, gridDim.x));
       r.each = r.ctas > 0 ? r.total / r.ctas : 1;

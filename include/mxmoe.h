@@ -441,7 +441,8 @@ MX_API size_t mx_paged_attention_workspace_size(int T, int n_seqs, int n_heads, 
  * token's largest block scale, and is zero where its own block's scale lies 2^25
  * below (MX_E2M1: 2^31).
  * Rows of padding and of bad metadata are not written; a bad page's keys are left
- * out.  Cache places that no row sees may hold anything, also pages behind the
+ * out.  Starts that are not ascending and ask for more work than the sizes allow are
+ * reported, and no row is written.  Cache places that no row sees may hold anything, also pages behind the
  * window may be gone.
  * A NaN or infinity in a query makes its row NaN; a NaN among the values that
  * some new token sees may reach the sequence's other new tokens of the call.

@@ -501,3 +501,28 @@ def test_narrow_and_wide_block_tables(n, window, dim, fmt):
         out, lse, status, _ = _call(batch, q, cache, dev=(t, lens, starts), window=window)
         assert status == 0
         _compare(batch, q, cache, out, lse, fmt, dim ** -0.5, True, window)
+
+
+@pytest.mark.parametrize("max_q_len,causal", [(4096, False), (1, True)])
+def test_starts_that_give_the_same_tokens_to_many_sequences(max_q_len, causal):
+    """Starts that fall and rise again may ask for more work than the kernels' 32-bit
+    line holds: 50000 sequences of 4096 new tokens here, or, with one new token, none.
+    The call is reported and writes nothing."""
+    n, T, page = 100001, 4096, 65536
+    starts = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    starts[1::2] = T
+    cache = mx.KVCache(1, page, 1, 64)
+    q = torch.randn(T, 16, 64, device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, 3.0)
+    lse = torch.full((T, 16), 3.0, device="cuda")
+    ws = mx.alloc_workspace(mx.mx_paged_attention_workspace_size(T, n, 16, 1, 64, max(max_q_len, 2)))
+    table = torch.zeros(n, 1, dtype=torch.int32, device="cuda")
+    lens = torch.full((n,), page, dtype=torch.int32, device="cuda")
+    mx.mx_paged_attention(q, cache, table, lens, starts, out, ws, causal=causal, max_q_len=max_q_len, lse=lse)
+    assert mx.moe_get_status(ws) == mx.MX_ERR_DEVICE_ARG
+    assert torch.all(out == 3.0) and torch.all(lse == 3.0)
+    # and the workspace is ready for a call that is right
+    lens[0], starts[1:] = 300, 2
+    mx.mx_paged_attention(q, cache, table, lens, starts, out, ws, causal=causal, max_q_len=max(max_q_len, 2), lse=lse)
+    assert mx.moe_get_status(ws) == 0
+    assert torch.all(out[:2] == 0) and torch.all(out[2:] == 3.0) and torch.all(lse[:2] != 3.0)   # a cache of zeros
