@@ -167,11 +167,16 @@ int mx_kv_read(const mx_kv_cache* cache, const int32_t* block_table, const int32
                mx_stream_t stream) {
   int st = check_cache(cache, n_seqs, max_pages, T);
   if (st != MX_OK) return st;
-  if (T == 0 || n_seqs == 0) return MX_OK;
+  if (T == 0) return MX_OK;
   if (!k_out || !v_out) return MX_ERR_INVALID_ARG;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return MX_ERR_ALIGNMENT;
+  if (n_seqs == 0) {  // all rows are padding
+    const size_t bytes = static_cast<size_t>(T) * cache->n_kv_heads * cache->head_dim * 2;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return cudaMemsetAsync(k_out, 0, bytes, s) == cudaSuccess ? cuda_status(cudaMemsetAsync(v_out, 0, bytes, s)) : MX_ERR_CUDA;
+  }
   st = check_cache_pointers(cache, block_table, kv_lens, q_starts, ws, ws_bytes);
   if (st != MX_OK) return st;
-  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return MX_ERR_ALIGNMENT;
   KvArgs a = kv_args(cache, block_table, kv_lens, q_starts, n_seqs, max_pages, T, ws);
   a.k_out = k_out;
   a.v_out = v_out;

@@ -337,3 +337,15 @@ def test_add_rmsnorm_e2m1_codes_feed_the_grouped_gemms():
     # an h next to a border may take either code, a step of at most 2^-1: one in 1000 of
     # them moves the output by 2^-1 / 1000^0.5 = 0.016 (relative, L2)
     assert float(one.norm()) > 0 and float((out - one).norm()) <= 0.016 * float(one.norm())
+
+
+def test_kv_read_without_sequences():
+    """All rows are padding then, and padding reads as zeros."""
+    cache = mx.KVCache(2, 16, 1, 64)
+    ko, vo = (torch.full((5, 1, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    none = torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    lens, starts = torch.empty(0, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = mx.alloc_workspace(256)
+    mx.mx_kv_read(cache, none, lens, starts, ko, vo, ws)
+    assert mx.moe_get_status(ws) == 0
+    assert float(ko.abs().sum()) == 0 and float(vo.abs().sum()) == 0
