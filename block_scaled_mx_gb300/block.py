@@ -56,6 +56,8 @@ class DecoderBlock:
         bf16 = dict(dtype=torch.bfloat16, device=dev)
         i32 = dict(dtype=torch.int32, device=dev)
 
+        if T == 0:  # no sequence has a new token
+            return torch.empty(0, H, dtype=torch.float32, device=dev), torch.empty(0, H, **bf16)
         y, mid, after = torch.empty(T, H, **bf16), torch.empty(T, H, **bf16), torch.empty(T, H, **bf16)
         mx.mx_add_rmsnorm(x, self.g_attn, self.eps, residual=residual, residual_out=mid, y=y)
         qkv = (y @ self.w_qkv.t()).view(T, hq + 2 * hk, d)

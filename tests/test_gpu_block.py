@@ -118,3 +118,12 @@ def test_calls_of_one_block_on_two_streams():
             # a token's k + 1 = 3 slots in pieces, added in any order: at most 16
             # additions of 2^-24 each, of terms that sum to four times their sum's size
             assert float((out - want[i][0]).norm()) <= 2.0 ** -18 * float(want[i][0].norm())
+
+
+def test_block_without_tokens():
+    """A step in which no sequence has a new token."""
+    blk = B.random_block(256, 128, 8, 2, 8, 2, 64, keep_last=False)
+    batch = ref.Batch([0, 0], [7, 0], 16, 4, torch.tensor([[0], [1]], dtype=torch.int32))
+    x = torch.empty(0, 256, device="cuda")
+    out, after = blk.forward(x, x.to(torch.bfloat16), mx.KVCache(4, 16, 2, 64), *batch.device(), 0)
+    assert out.shape == after.shape == (0, 256) and blk.status() == 0
