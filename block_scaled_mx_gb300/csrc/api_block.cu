@@ -67,16 +67,21 @@ KvArgs kv_args(const mx_kv_cache* c, const int32_t* block_table, const int32_t* 
 constexpr size_t kArrivedOffset = 256;
 constexpr size_t kArrivedBytes = sizeof(unsigned) * kAttnMaxCtas;
 
-// Sequences of up to few_rows() rows (new tokens x query heads of a KV head) are the
-// few-rows kernel's, others the chunk kernel's.  The few-rows kernel goes through the
-// keys again for every 8 rows; the chunk kernel takes as long for 256 as for one, but
-// starts and ends slower, the more so the fewer the (sequence, KV head) pairs among
-// which its 152 CTAs share out and join the keys.  Count a batch's work in 64-key
-// units, and 8 more for each pair.  Without the start the chunk kernel's time is that
-// of two or three tiles of 8 rows; every further tile costs the few-rows kernel 2.5 ns
-// a unit (heads of 128 in MXFP8; 1.6 to 2.8 in the other three forms), and the start is
-// worth 10 us and 200 us over the number of pairs, less where a pair has few units.
-// In us, few rows / chunk, heads of 128 in MXFP8, on either side of the rule:
+// Which kernel takes which sequences: all go to the few-rows kernel, all to the chunk
+// kernel, or those of up to `split` rows (new tokens x query heads of a KV head) to the
+// one and the others to the other, in two launches.
+//
+// The few-rows kernel goes through the keys again for every 8 rows; the chunk kernel
+// takes as long for 256 as for one, but starts and ends slower, the more so the fewer
+// the (sequence, KV head) pairs among which its 152 CTAs share out and join the keys.
+// Count a batch's work in 64-key units, and 8 more for each pair.  Without the start the
+// chunk kernel's time is that of two or three tiles of 8 rows; every further tile costs
+// the few-rows kernel 2.5 ns a unit (heads of 128 in MXFP8; 1.6 to 2.8 in the other
+// three forms), and the start is worth 10 us and 200 us over the number of pairs, less
+// where a pair has few units.  Two launches start and end twice; they pay where many
+// pairs have one tile, by which the few-rows kernel is ahead as a chunk's segment costs
+// 16 units beside its keys.
+// In us, few rows / chunk, heads of 128 in MXFP8, equal sequences:
 //   pairs x keys     rows and times
 //   2 x 2048         128: 23 / 40
 //   2 x 131072       64: 102 / 167     96: 140 / 169     128: 180 / 170
@@ -85,19 +90,39 @@ constexpr size_t kArrivedBytes = sizeof(unsigned) * kAttnMaxCtas;
 //   16 x 131072      16: 182 / 191     24: 255 / 192     128: 1293 / 204
 //   32 x 2048        48: 32 / 39       64: 39 / 39       96: 52 / 41
 //   64 x 8192        16: 59 / 69       24: 80 / 71
-// Over 1056 combinations of 1 to 64 pairs, 512 to 131072 keys, 8 to 128 rows, both head
-// sizes and both formats the rule takes 0.2% longer than always the faster kernel, and
-// 28% at worst (2 pairs of 131072 keys, heads of 64, 128 rows: 152 us where 119 would do).
-// The lengths are on the device, so the keys are counted by what bounds them: the
-// block table's width and the window.
+// and few rows / chunk / two launches, lengths of a quarter to all of the keys:
+//   16 x 32768, 3 to 6 tokens of 8 rows         75 / 82 / 118
+//   64 x 8192, one of 6 tokens, others of one    33 / 62 / 75
+//   16 x 2048, one of 512 tokens, others of one  - / 45 / 59
+//   512 x 2048, the same                         - / 146 / 91
+//   192 x 5000, heads of 64, window of 2048,
+//     12 of 24 sequences of 139 to 700 tokens    - / 274 / 272
+// Over 1326 batches (1 to 512 pairs, 512 to 131072 keys, both head sizes and formats) the
+// rule takes 0.3% longer than the fastest of the three, and 38% at worst.
+//
+// The lengths are on the device.  Keys are counted by what bounds them, the block
+// table's width and the window; rows by the average over the sequences; and for two
+// launches the batch is taken to be of single tokens and of as many of max_q_len as T
+// has room for.
 constexpr int kMostFewRows = 128;
-int few_rows(int n_seqs, int n_kv_heads, int head_dim, bool e2m1, int64_t keys) {
+struct AttnChoice {
+  bool few;   // all to the few-rows kernel
+  int split;  // else those of up to this many rows
+};
+AttnChoice choose_kernel(int T, int n_seqs, int n_kv_heads, int group, int max_q_len, int head_dim, bool e2m1, int64_t keys) {
   const int even = head_dim == 128 && !e2m1 ? 2 : 3;
-  const int64_t pairs = static_cast<int64_t>(n_seqs) * n_kv_heads, units = (keys + 63) / 64;
-  const int64_t start = std::min<int64_t>(260 * units, 4000 + 80000 / pairs);  // of the chunk kernel, in units of one tile
-  return static_cast<int>(std::min<int64_t>(kMostFewRows, 8 * (even + start / (pairs * (units + 8)))));
+  const double pairs = static_cast<double>(n_seqs) * n_kv_heads, units = static_cast<double>((keys + 63) / 64);
+  const int64_t most = static_cast<int64_t>(max_q_len) * group;
+  if (most <= kMostFewRows) {
+    const double tiles = std::min(static_cast<double>((most + 7) / 8), static_cast<double>(T) * group / n_seqs / 8);
+    const double start = std::min(260 * units, 4000 + 80000 / pairs);  // of the chunk kernel, in units of one tile
+    if (tiles <= even || (tiles - even) * pairs * (units + 8) <= start) return {true, 0};
+  }
+  if (T >= static_cast<int64_t>(n_seqs) * max_q_len) return {false, 0};  // room for max_q_len in all of them
+  const double single = n_seqs - static_cast<double>(T - n_seqs) / std::max(max_q_len - 1, 1);
+  const bool pays = single * n_kv_heads * ((units + 16) * even - (units + 8)) > 16000;  // ahead by a second start
+  return {false, pays ? 8 * (even - 1) : 0};
 }
-constexpr int kLeastFewRows = 16;  // that few_rows() gives
 
 int check_attention(int T, int n_seqs, int n_heads, int n_kv_heads, int head_dim, int max_q_len) {
   if (T < 0 || n_seqs < 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || max_q_len < 0) return MX_ERR_INVALID_ARG;
@@ -186,8 +211,8 @@ int mx_kv_read(const mx_kv_cache* cache, const int32_t* block_table, const int32
 size_t mx_paged_attention_workspace_size(int T, int n_seqs, int n_heads, int n_kv_heads, int head_dim, int max_q_len) {
   if (check_attention(T, n_seqs, n_heads, n_kv_heads, head_dim, max_q_len) != MX_OK) return 0;
   size_t part = attn_rows_part_bytes(head_dim);
-  // either kernel may take more rows than these: the lengths are not known here
-  if (static_cast<int64_t>(max_q_len) * (n_heads / n_kv_heads) > kLeastFewRows) part = std::max(part, attn_chunk_part_bytes(head_dim));
+  // up to 16 rows are the few-rows kernel's whatever the lengths, which are not known here
+  if (static_cast<int64_t>(max_q_len) * (n_heads / n_kv_heads) > 16) part = std::max(part, attn_chunk_part_bytes(head_dim));
   return kArrivedOffset + al256(kArrivedBytes) + part;
 }
 
@@ -256,16 +281,15 @@ int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q_stride
   a.rows_upto = INT_MAX;
   int64_t keys = static_cast<int64_t>(max_pages) * a.page_size;
   if (window > 0) keys = std::min(keys, static_cast<int64_t>(window) + max_q_len);
-  const int few = few_rows(n_seqs, a.n_kv_heads, a.head_dim, a.e2m1 != 0, keys);
-  if (static_cast<int64_t>(max_q_len) * a.group <= few) return cuda_status(launch_attn_rows(a, cs));
-  // Where all sequences are as long as the longest (T has room for it), one
-  // launch takes them all; a shorter one among them is right there too.
-  if (T >= static_cast<int64_t>(n_seqs) * max_q_len) return cuda_status(launch_attn_chunk(a, cs));
-  a.rows_upto = few;
-  st = cuda_status(launch_attn_rows(a, cs));
-  if (st != MX_OK) return st;
-  a.rows_above = few;
-  a.rows_upto = INT_MAX;
+  const AttnChoice choice = choose_kernel(T, n_seqs, a.n_kv_heads, a.group, max_q_len, a.head_dim, a.e2m1 != 0, keys);
+  if (choice.few) return cuda_status(launch_attn_rows(a, cs));
+  if (choice.split > 0) {
+    a.rows_upto = choice.split;
+    st = cuda_status(launch_attn_rows(a, cs));
+    if (st != MX_OK) return st;
+    a.rows_above = choice.split;
+    a.rows_upto = INT_MAX;
+  }
   return cuda_status(launch_attn_chunk(a, cs));
 }
 

@@ -446,10 +446,10 @@ MX_API size_t mx_paged_attention_workspace_size(int T, int n_seqs, int n_heads, 
  * window may be gone.
  * A NaN or infinity in a query makes its row NaN; a NaN among the values that
  * some new token sees may reach the sequence's other new tokens of the call.
- * Deterministic: the same call gives the same bits.  Two launches at most: one
- * for sequences with few rows, one for chunks; what few rows are depends on how many
- * keys a sequence may have, by max_pages * page_size and the window, so a block table
- * should be no wider than the batch needs.
+ * Deterministic: the same call gives the same bits.  One kernel for few rows, one
+ * for chunks, or both in two launches: the choice goes by the sizes, among them how
+ * many keys a sequence may have by max_pages * page_size and the window, so a block
+ * table should be no wider than the batch needs.
  * Errors: MX_ERR_INVALID_ARG (null, sizes, n_heads % n_kv_heads, scale or
  * scale * log2(e) not positive and finite, window < 0 or without causal, stride),
  * MX_ERR_UNSUPPORTED (head_dim other than 64 and 128, page_size % 16, more
