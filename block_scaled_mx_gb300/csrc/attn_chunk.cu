@@ -10,7 +10,8 @@
 // two parts, the accumulator written out, the first keys of the next on their
 // way through empty stages.  2048 new tokens behind 14336 take 414 us (1245
 // TFLOP/s of 4 head_dim flops for each visible (row, key) pair, 64% of a plain
-// bf16 product's), a prompt of 8192 509 us (1078).
+// bf16 product's), a prompt of 8192 510 us (1078).  Over an MXFP4 cache they take
+// 574 and 689: V's warps turn K's codes into 8-bit ones as well.
 //
 // A tile is 256 rows (new tokens x the query heads of one KV head) as two MMA
 // tiles of 128, A and B, that take turns: while the tensor cores work for one,
@@ -60,12 +61,14 @@ constexpr int kRows = 256;
 constexpr int kThreads = 512;
 constexpr int kMaxCtas = 152;
 constexpr int kMinUnits = 20;  // places of a CTA's stretch at least
-// A segment's queries and output, in units (a prompt of 8192: 518 us with 16, 539
-// with 12, 527 with 20).
+// A segment's queries and output, in units (a prompt of 8192: 510 us with 16, 515 with
+// 12, 520 with 20).  Heads of 64, whose segments cost 10, take the same: 8 prompts of up
+// to 500: 35 us with 16, 41 with 10; a prompt of 8192: 445 and 431.
 constexpr int kCost = 16;
 // Least units of a split segment's part: a part costs queries and an output again
-// (6 prompts of up to 662: 70 us with 1, 46 with 4, 44 with 8 and 12; 256 new
-// tokens over 4096, whose 8 segments are all there is to share out: 52, 51, 54, 59).
+// (6 prompts of up to 662 with 10 KV heads: 55 us with 1, 32 with 4, 30 with 8 and 12;
+// 256 new tokens over 4096, whose 32 segments are all there is to share out: 50, 50, 53,
+// 57).
 constexpr int kSnap = 8;
 constexpr int kStages = 4;     // of K and of V
 constexpr int kRawStages = 4;  // of codes on their way to V
@@ -312,8 +315,8 @@ __device__ __noinline__ void load_queries(const AttnArgs& a, Shared& sh, uint8_t
   constexpr int kPieces = D / 8;     // sixteen bytes of bf16
   constexpr int kStep = 128 / kPieces;  // rows of the 128 threads
   // Pieces converted side by side, and on their way behind them (a prompt of 8192:
-  // 506 us; 1 and 4: 517; 4 and 4: 512; with more on their way the unit loop's
-  // registers spill: 530 and worse).
+  // 510 us; 1 and 4: 516; 4 and 4: 513; with 2 and 8 the unit loop's registers spill:
+  // 554).
   constexpr int kTogether = 2, kAhead = 4;
   const int p = threadIdx.x % kPieces, r0 = (threadIdx.x & 127) / kPieces;
   uint8_t* hi_base = base + Sh::kQ + 2 * x * Sh::kQTile;

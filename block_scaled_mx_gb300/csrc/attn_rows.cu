@@ -1,6 +1,7 @@
 // Attention of few new tokens over the paged MX cache (decoding, verifying
 // drafts): the keys split over all SMs, one pass with a running softmax, on
-// register-level MMAs (with 8 rows a tensor-memory tile of 128 would be 94% empty).
+// register-level MMAs (with the rows as M a tensor-memory tile of 128 would be 94%
+// empty; one with the keys as M was not built).
 //
 // A tile is 8 rows (new tokens x the query heads of one KV head), so the
 // cache is read once for all heads that share it.  A fifth warp fetches units of
@@ -9,13 +10,14 @@
 // the CTA's stretch of a segment ends.
 //
 // What bounds it.  With MXFP8 the cache's bytes: of what 64 instead of 32
-// sequences of 8192 add, 6.5 TB/s (96% of a copy's).  A call has 18 us beside
+// sequences of 8192 add, 6.6 TB/s (98% of a copy's).  A call has 17 us beside
 // that: 4 until every CTA knows its stretch, 2 until the first keys are there, 4
 // to join, launch and uneven ends; so 32 ragged sequences of up to 8192 (300 MB)
-// take 64 us where a copy of the bytes takes 44, and 6 drafts over 2051 keys 18.
-// With MXFP4 the instructions: half the bytes a key and 504 instructions for 16
-// keys of a warp, with the pipe of conversions and bit operations busy for 63% of
-// the cycles: 3.2 TB/s; 3 sequences of up to 65536 take 79 us (copy: 32).
+// take 62 us where a copy of the bytes takes 44, and 6 drafts over 2051 keys 17.
+// With MXFP4 the instructions: half the bytes a key and 514 instructions for 16
+// keys of a warp (a whole call's, by the counter), with the pipe of conversions and
+// bit operations busy for 63% of the cycles: 3.2 TB/s; 3 sequences of up to 65536
+// take 79 us (copy: 32).
 //
 // Both products are transposed, S^T = K Q^T and O^T += V^T P^T, so that the query
 // rows are the MMAs' columns, of which there are 8 where there are 16 rows of
@@ -56,11 +58,11 @@ constexpr int kUnit = 64;
 constexpr int kWarps = 4;                  // that compute
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kCtasPerSm = 3;              // what the registers allow: 160 threads of 128
-// Places of a CTA's stretch at least (6 drafts over 2051 keys: 18.4 us with 4, 20.1
-// with 2, 19.6 with 6).
+// Places of a CTA's stretch at least (6 drafts over 2051 keys: 17.0 us with 4, 16.7
+// with 2, 16.8 with 6).
 constexpr int kMinUnits = 4;
-// A segment's queries and output, in units (32 sequences of up to 8192: 76 us with
-// 1, 68 with 4, 65 with 8).
+// A segment's queries and output, in units (32 sequences of up to 8192: 72 us with
+// 1, 63 with 4, 62 with 8, 66 with 16).
 constexpr int kCost = 8;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {

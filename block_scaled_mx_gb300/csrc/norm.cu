@@ -163,8 +163,8 @@ cudaError_t launch_nc(const NormArgs& a, int threads, cudaStream_t s) {
 }
 
 // Threads of a row up to which each takes one group of eight.  8192 rows of 4096
-// bf16: 53.5 us with at most 128 threads, 51.2 with 256, 47.0 with 512 (the bytes
-// at copy rate: 44.7); 2048 rows of 16384: 57.3 with 512, 67.4 with 1024, whose
+// bf16: 53.7 us with at most 128 threads, 51.0 with 256, 47.2 with 512 (the bytes
+// at copy rate: 44.7); 2048 rows of 16384: 57.9 with 512, 67.9 with 1024, whose
 // block leaves no room for another row's loads while it waits for its sum.
 constexpr int kMostThreads = 512;
 
