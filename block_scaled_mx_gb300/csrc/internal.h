@@ -113,6 +113,25 @@ struct NormArgs {
 };
 cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s);
 
+// ---- sandwich.cu
+struct SandwichArgs {
+  const void* x;            // [T, H] bf16 or fp32
+  const void* post_weight;  // [H], or null: no norm behind the block
+  const void* gate;         // by gate_kind
+  const void* residual;     // [T, H] bf16 or fp32
+  const void* weight;       // [H], or null: residual_out alone
+  int x_f32, post_weight_f32, gate_f32, residual_f32, weight_f32;
+  int gate_kind, gate_act;  // MX_GATE_*, MX_GATE_ACT_*
+  float residual_scale, block_scale, eps;
+  int T, H;
+  void* residual_out;       // the residual's type
+  void* y;                  // [T, H] bf16, or null
+  int e2m1;                 // codes as MXFP4 instead of MXFP8
+  uint8_t* codes;           // or null
+  uint8_t* scales;
+};
+cudaError_t launch_sandwich_rmsnorm(const SandwichArgs& a, cudaStream_t s);
+
 // ---- kvcache.cu
 struct KvArgs {
   uint8_t *k_codes, *k_scales, *v_codes, *v_scales;  // [num_pages, n_heads, page_size, row]
@@ -128,6 +147,36 @@ struct KvArgs {
 };
 cudaError_t launch_kv_append(const KvArgs& a, cudaStream_t s);
 cudaError_t launch_kv_read(const KvArgs& a, cudaStream_t s);
+
+// ---- rope.cu
+struct RopeArgs {
+  KvArgs kv;
+  const void* q;             // bf16 [T, n_q_heads, head_dim], or null with n_q_heads = 0
+  void* q_out;               // the same rotated (may be q)
+  int64_t q_stride, q_out_stride;
+  int n_q_heads;
+  const int32_t* positions;  // [T], or null: places in the sequences
+  const uint64_t* turns;     // [rot / 2] turns of a pair's angle for one position, in units of 2^-64
+  int rot, interleaved;
+  float amplitude;
+};
+cudaError_t launch_rope_kv_append(const RopeArgs& r, cudaStream_t s);
+
+// ---- sample.cu
+struct SampleArgs {
+  const void* logits;        // [T, V] bf16 or fp32
+  int64_t stride;            // elements between rows
+  int bf16, T, V;
+  const float* temperature;  // [T] each, or null
+  const int32_t* top_k;
+  const float *top_p, *min_p;
+  const float* u;            // [T]
+  int32_t* tokens;           // [T]
+  float* logp;               // [T], or null
+  int* status;
+};
+bool sample_supported(int V, bool bf16);
+cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
 
 // ---- attn_rows.cu, attn_chunk.cu
 constexpr int kAttnMaxCtas = 608;                    // 152 SMs x 4: partial slots and counters of the workspace

@@ -16,36 +16,6 @@ namespace {
 constexpr int kWarps = 4;   // tokens of a block
 constexpr int kUnroll = 4;  // groups of eight elements of K, and of V, that a lane loads before it uses one
 
-// Cache row (page, place) of token t: the sequence that holds it by a 32-way
-// search of q_starts, its position counted back from the sequence's length.
-// Returns the row index (page * n_kv_heads) * page_size + place of head 0, or
-// -1 for a token past the last sequence; bad metadata sets the status word.
-__device__ __forceinline__ int64_t token_row(const KvArgs& a, int t, int lane) {
-  int lo = 0, hi = a.n_seqs;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int i = lo + lane * step;
-    const bool le = i < hi && a.q_starts[i] <= t;
-    const int n = max(__popc(__ballot_sync(0xffffffffu, le)), 1);
-    lo += (n - 1) * step;
-    hi = min(lo + step, hi);
-  }
-  const int start = a.q_starts[lo], end = a.q_starts[lo + 1], kv = a.kv_lens[lo];
-  if (t >= end) return -1;
-  const int64_t pos = static_cast<int64_t>(kv) - (end - t);
-  if (start < 0 || start > t || end > a.T || pos < 0 || kv > static_cast<int64_t>(a.max_pages) * a.page_size) {
-    if (lane == 0) set_status(a.status, MX_ERR_DEVICE_ARG);
-    return -1;
-  }
-  const int p = static_cast<int>(pos / a.page_size);
-  const int page = a.block_table[static_cast<int64_t>(lo) * a.max_pages + p];
-  if (page < 0 || page >= a.num_pages) {
-    if (lane == 0) set_status(a.status, MX_ERR_DEVICE_ARG);
-    return -1;
-  }
-  return static_cast<int64_t>(page) * a.n_heads * a.page_size + (pos - static_cast<int64_t>(p) * a.page_size);
-}
-
 // Lane items are groups of eight elements of K, then of V; four consecutive
 // lanes hold one MX block (head_dim is a multiple of 32, so blocks and heads
 // start at multiples of four lanes).  All of a lane's loads are under way before
@@ -68,7 +38,8 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_append(const KvArgs a) {
     w[0][u] = __ldg(k + i);
     w[1][u] = __ldg(v + i);
   }
-  const int64_t row0 = token_row(a, t, lane);
+  int64_t pos;
+  const int64_t row0 = token_row(a, t, lane, pos);
   if (row0 < 0) return;
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
@@ -114,7 +85,8 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_read(const KvArgs a) {
   if (t >= a.T) return;
   const int per_head = a.head_dim / 8, n = a.n_heads * per_head;
   const int i0 = blockIdx.y * 32 * kUnroll + lane;
-  const int64_t row0 = token_row(a, t, lane);
+  int64_t pos;
+  const int64_t row0 = token_row(a, t, lane, pos);
   uint2 c[2][kUnroll];
   int s[2][kUnroll];
 #pragma unroll

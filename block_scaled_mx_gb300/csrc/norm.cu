@@ -4,45 +4,16 @@
 // One CTA holds one row of z in registers between the sum of squares and the
 // scaling, so every input is read once and every output written once; the
 // bound is HBM for many rows and launch latency for few.
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
 #include "common.cuh"
 #include "internal.h"
+#include "rows.cuh"
 
 namespace mxk {
 
 namespace {
-
-// Eight consecutive elements as fp32; `i` counts groups of eight.
-template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
-  if (F32) {
-    const float4* q = static_cast<const float4*>(p) + 2 * i;
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 a = static_cast<const uint4*>(p)[i];
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      v[2 * m] = __uint_as_float(w[m] << 16);
-      v[2 * m + 1] = __uint_as_float(w[m] & 0xFFFF0000u);
-    }
-  }
-}
-
-__device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * m], v[2 * m + 1]);
-    w[m] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // NC groups of eight elements a thread; XF32: x is fp32, else bf16; RES: 0 no
 // residual, 1 bf16, 2 fp32.  Four consecutive lanes hold one MX block of 32.

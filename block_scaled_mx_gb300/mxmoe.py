@@ -34,6 +34,10 @@ MX_ACT_SWIGLU = 0
 MX_ACT_SWIGLU_OAI = 1
 MX_SHARED_FOLDED = 0
 MX_SHARED_DENSE = 1
+MX_GATE_NONE, MX_GATE_CHANNEL, MX_GATE_TOKEN, MX_GATE_FULL = range(4)
+GATE_ACTS = {"none": 0, "sigmoid": 1}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
 
 class KVCacheTables(ctypes.Structure):
@@ -57,7 +61,7 @@ def layer_opts(activation="swiglu", alpha=1.0, limit=7.0, shared="folded", act_f
 
 # every entry point of the C ABI: name -> (restype, argtypes)
 _P, _I, _I64, _SZ, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_uint64
-_F = ctypes.c_float
+_F, _D = ctypes.c_float, ctypes.c_double
 SIGNATURES = {
     "mx_status_string": (ctypes.c_char_p, [_I]),
     "mx_quantize_act": (_I, [_P, _I, _I, _P, _P, _P]),
@@ -81,10 +85,16 @@ SIGNATURES = {
     "moe_forward_launches_ex": (_I, [_I, _I, _I, _I, _I, _I, _P]),
     "moe_forward_launches": (_I, [_I, _I, _I, _I, _I, _I]),
     "mx_add_rmsnorm": (_I, [_P, _I, _P, _I, _P, _I, _I, _I, _F, _P, _P, _I, _P, _P, _P]),
+    "mx_sandwich_rmsnorm": (_I, [_P, _I, _P, _I, _P, _I, _I, _I, _P, _I, _F, _F, _P, _I, _I, _I, _F, _P, _P, _I, _P, _P, _P]),
+    "mx_rope_table": (_I, [_I, _D, _I, _D, _D, _D, _I, _P, _P]),
+    "mx_rope_kv_append": (_I, [_P, _P, _I64, _I, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I, _I, _F, _P, _P, _P, _I, _I, _I, _P, _SZ,
+                               _P]),
     "mx_kv_append": (_I, [_P, _P, _I64, _P, _I64, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
     "mx_kv_read": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _SZ, _P]),
     "mx_paged_attention_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "mx_paged_attention": (_I, [_P, _P, _I64, _I, _P, _P, _P, _I, _I, _I, _I, _F, _I, _I, _P, _P, _P, _SZ, _P]),
+    "mx_sample_workspace_size": (_SZ, [_I, _I]),
+    "mx_sample": (_I, [_P, _I, _I64, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_get_status": (_I, [_P, _P, _P]),
     "mx_debug_set_wait_limit_ns": (None, [_U64]),
     "mx_debug_time_gemms": (None, [_I]),
@@ -349,6 +359,37 @@ def mx_add_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, cod
         raise MxError(st, "mx_add_rmsnorm")
 
 
+def mx_sandwich_rmsnorm(x, post_weight, eps, residual, residual_out, gate=None, gate_act="none", block_scale=1.0,
+                        residual_scale=1.0, weight=None, y=None, codes=None, scales=None, fmt="e4m3", stream=None):
+    """n = RMSNorm(x) * post_weight (x itself without one); z = residual_scale * residual
+    + block_scale * act(gate) * n; residual_out = z; y = RMSNorm(z) * weight; codes,
+    scales = MX(y), written where tensors are given.  ``gate``: [H], [T, 1] or [T, H];
+    ``gate_act`` "none" or "sigmoid"; types as mx_add_rmsnorm's."""
+    shape = T, H = x.shape
+    f, act = _fmt(fmt), GATE_ACTS[gate_act]
+    pt = wt = gt = MX_BF16
+    pp = wp = gp = None
+    if post_weight is not None:
+        pt, pp = _type(post_weight), _dense(post_weight, post_weight.dtype, (H,), "post_weight")
+    if weight is not None:
+        wt, wp = _type(weight), _dense(weight, weight.dtype, (H,), "weight")
+    kind = MX_GATE_NONE
+    if gate is not None:
+        g = gate.shape
+        kind = MX_GATE_CHANNEL if g == (H,) else MX_GATE_FULL if g == shape else MX_GATE_TOKEN if g == (T, 1) else None
+        if kind is None:
+            raise ValueError(f"gate: expected shape {(H,)}, {(T, 1)} or {tuple(shape)}, got {tuple(g)}")
+        gt, gp = _type(gate), _ptr(gate)
+    st = lib().mx_sandwich_rmsnorm(_ptr(x), _type(x), pp, pt, gp, gt, kind, act,
+                                   _dense(residual, residual.dtype, shape, "residual"), _type(residual), residual_scale,
+                                   block_scale, wp, wt, T, H, eps, _dense(residual_out, residual.dtype, shape, "residual_out"),
+                                   _dense(y, torch.bfloat16, shape, "y"), f,
+                                   _dense(codes, torch.uint8, (T, H // 2) if f == MX_E2M1 else shape, "codes"),
+                                   _dense(scales, torch.uint8, (T, H // 32), "scales"), _stream(stream))
+    if st:
+        raise MxError(st, "mx_sandwich_rmsnorm")
+
+
 class KVCache:
     """A paged key/value cache in MX form (mx_kv_cache): ``num_pages`` pages of
     ``page_size`` tokens, "e4m3" (MXFP8) or "e2m1" (MXFP4) with an E8M0 scale for
@@ -422,6 +463,56 @@ def mx_kv_append(cache, k, v, block_table, kv_lens, q_starts, ws, stream=None):
         raise MxError(st, "mx_kv_append")
 
 
+class Rope:
+    """Rotary positions (mx_rope_table): the first ``rot_dim`` elements of a head, paired
+    "half" (i, i + rot_dim / 2) or "interleaved" (2i, 2i + 1), with frequencies
+    base^(-2i / rot_dim), for contexts ``factor`` times the ``original_length`` by
+    ``scaling`` "none", "linear", "ntk", "yarn" or "bands".  ``low`` and ``high`` are the
+    turns in the original length between which yarn (1, 32) and bands (1, 4) go over
+    from scaled to unscaled pairs.  ``turns`` is the table on the device."""
+
+    def __init__(self, rot_dim, base=10000.0, layout="half", scaling="none", factor=1.0, original_length=0, low=None, high=None,
+                 device="cuda"):
+        kind = ROPE_SCALINGS[scaling]
+        low = 1.0 if low is None else low
+        high = {"yarn": 32.0}.get(scaling, 4.0) if high is None else high
+        if not 0 < rot_dim <= 1 << 16:
+            raise ValueError(f"rot_dim: {rot_dim}")
+        table, amplitude = (ctypes.c_uint64 * (rot_dim // 2))(), ctypes.c_float()
+        _check(lib().mx_rope_table(rot_dim, base, kind, factor, low, high, _int32(original_length, "original_length"),
+                                   ctypes.addressof(table), ctypes.addressof(amplitude)), "mx_rope_table")
+        self.rot_dim, self.layout, self.amplitude = rot_dim, ROPE_LAYOUTS[layout], amplitude.value
+        # as the signed numbers of the same bits
+        self.turns = torch.frombuffer(table, dtype=torch.int64).clone().to(device)
+
+
+def mx_rope_kv_append(cache, rope, q, k, v, block_table, kv_lens, q_starts, ws, q_out=None, positions=None, stream=None):
+    """mx_kv_append with the rotation of ``rope`` on the way: k is rotated into its places
+    in the cache, q (bf16 [T, n_heads, head_dim], token stride free; or None) into q_out,
+    which may be q itself.  ``positions`` int32 [T]: the angles' positions, where they are
+    not the places in the sequences."""
+    n, pages, table, lens, starts = _batch(block_table, kv_lens, q_starts)
+    kp, ks = _rows(k, cache.n_kv_heads, cache.head_dim, "k")
+    vp, vs = _rows(v, cache.n_kv_heads, cache.head_dim, "v")
+    T, heads, qp, qs, op, os_ = k.shape[0], 0, None, 0, None, 0
+    if v.shape[0] != T:
+        raise ValueError(f"k and v differ in shape: {tuple(k.shape)}, {tuple(v.shape)}")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out: both or neither")
+    if q is not None:
+        heads = q.shape[1]
+        qp, qs = _rows(q, heads, cache.head_dim, "q")
+        op, os_ = _rows(q_out, heads, cache.head_dim, "q_out")
+        if q.shape[0] != T or q_out.shape[0] != T:
+            raise ValueError(f"q, q_out: expected {T} tokens, got {q.shape[0]} and {q_out.shape[0]}")
+    st = lib().mx_rope_kv_append(cache._address, qp, qs, heads, op, os_, kp, ks, vp, vs,
+                                 _dense(positions, torch.int32, (T,), "positions"),
+                                 _dense(rope.turns, torch.int64, (rope.rot_dim // 2,), "turns"), rope.rot_dim, rope.layout,
+                                 rope.amplitude, table, lens, starts, n, pages, T, _ptr(ws), ws.nbytes, _stream(stream))
+    if st:
+        raise MxError(st, "mx_rope_kv_append")
+
+
 def mx_kv_read(cache, block_table, kv_lens, q_starts, k_out, v_out, ws, stream=None):
     """The last q_starts[b+1] - q_starts[b] tokens of each sequence as bf16."""
     n, pages, table, lens, starts = _batch(block_table, kv_lens, q_starts)
@@ -453,6 +544,29 @@ def mx_paged_attention(q, cache, block_table, kv_lens, q_starts, out, ws, scale=
                                   _dense(lse, torch.float32, (T, heads), "lse"), _ptr(ws), ws.nbytes, _stream(stream))
     if st:
         raise MxError(st, "mx_paged_attention")
+
+
+def mx_sample_workspace_size(T, V) -> int:
+    return lib().mx_sample_workspace_size(T, V)
+
+
+def mx_sample(logits, u, tokens, ws, temperature=None, top_k=None, top_p=None, min_p=None, logp=None, stream=None):
+    """A token for each row of logits (bf16 or fp32 [T, V], row stride free) by its random
+    number u (fp32 [T], in [0, 1)) and, where given, its temperature (0: the largest logit),
+    top_k (int32), top_p and min_p (fp32, [T] each) -> tokens int32 [T], logp fp32 [T]."""
+    T, V = logits.shape
+    row, element = logits.stride()
+    if element != 1 and V > 1:
+        raise ValueError(f"logits: a row is dense, got strides {logits.stride()}")
+    if not logits.is_cuda:
+        raise ValueError(f"expected a CUDA tensor, got one on {logits.device}")
+    f32, i32, n = torch.float32, torch.int32, (T,)
+    st = lib().mx_sample(logits.data_ptr(), _type(logits), row if T > 1 else V, T, V, _dense(temperature, f32, n, "temperature"),
+                         _dense(top_k, i32, n, "top_k"), _dense(top_p, f32, n, "top_p"), _dense(min_p, f32, n, "min_p"),
+                         _dense(u, f32, n, "u"), _dense(tokens, i32, n, "tokens"), _dense(logp, f32, n, "logp"), _ptr(ws), ws.nbytes,
+                         _stream(stream))
+    if st:
+        raise MxError(st, "mx_sample")
 
 
 def moe_get_status(ws, stream=None) -> int:

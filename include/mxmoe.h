@@ -361,6 +361,38 @@ MX_API int mx_add_rmsnorm(const void* x, int x_type, const void* residual, int r
                           int weight_type, int T, int H, float eps, void* residual_out, void* y, int fmt,
                           uint8_t* codes, uint8_t* scales, mx_stream_t stream);
 
+/* ---- gates of mx_sandwich_rmsnorm ---- */
+#define MX_GATE_NONE 0
+#define MX_GATE_CHANNEL 1 /* gate [H] */
+#define MX_GATE_TOKEN 2   /* gate [T] */
+#define MX_GATE_FULL 3    /* gate [T, H] */
+#define MX_GATE_ACT_NONE 0
+#define MX_GATE_ACT_SIGMOID 1
+
+/* Norm behind a block, its gate and scale, the residual, and the norm ahead of the
+ * next block with MX quantisation, in one pass:
+ *   n = x / sqrt(mean(x^2) + eps) * post_weight   (n = x where post_weight is NULL)
+ *   z = residual_scale * residual + block_scale * act(gate) * n,  residual_out = z,
+ *   y = z / sqrt(mean(z^2) + eps) * weight,  (codes, scales) = MX(y)
+ * in fp32; residual_out, y and the codes are each rounded once from fp32.
+ *   x [T, H] of x_type, residual [T, H] of residual_type, post_weight and weight
+ *     [H] (each MX_BF16 or MX_F32).
+ *   gate: NULL with MX_GATE_NONE, else by gate_kind, of gate_type; act by gate_act.
+ *   residual_out [T, H] of residual_type; it may be residual itself, or x where the
+ *     types are equal.
+ *   weight NULL: residual_out is the only output (y, codes and scales are NULL);
+ *     else y [T, H] bf16 or NULL, codes and scales as mx_add_rmsnorm's, and y or
+ *     codes is given.
+ * Errors: MX_ERR_INVALID_ARG (null, T < 0, H <= 0, eps not positive and finite, a
+ * scale that is not finite, an unknown type, gate or format), MX_ERR_UNSUPPORTED
+ * (H % 32, H > 32768), MX_ERR_ALIGNMENT (a tensor other than scales and a token's
+ * gate not 16-byte aligned). */
+MX_API int mx_sandwich_rmsnorm(const void* x, int x_type, const void* post_weight, int post_weight_type,
+                               const void* gate, int gate_type, int gate_kind, int gate_act, const void* residual,
+                               int residual_type, float residual_scale, float block_scale, const void* weight,
+                               int weight_type, int T, int H, float eps, void* residual_out, void* y, int fmt,
+                               uint8_t* codes, uint8_t* scales, mx_stream_t stream);
+
 /* A paged cache of keys and values in MX form.  Each of the four tables is
  * dense, [num_pages, n_kv_heads, page_size, row] with row = head_dim bytes of
  * codes (MX_E4M3; head_dim / 2 for MX_E2M1, element 2i in the low nibble) or
@@ -406,6 +438,59 @@ typedef struct mx_kv_cache {
 MX_API int mx_kv_append(const mx_kv_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                         const int32_t* block_table, const int32_t* kv_lens, const int32_t* q_starts, int n_seqs,
                         int max_pages, int T, void* ws, size_t ws_bytes, mx_stream_t stream);
+
+/* ---- rotary positions ---- */
+#define MX_ROPE_HALF 0        /* pairs (i, i + rot_dim / 2) */
+#define MX_ROPE_INTERLEAVED 1 /* pairs (2i, 2i + 1) */
+#define MX_ROPE_SCALING_NONE 0
+#define MX_ROPE_SCALING_LINEAR 1
+#define MX_ROPE_SCALING_NTK 2
+#define MX_ROPE_SCALING_YARN 3
+#define MX_ROPE_SCALING_BANDS 4
+
+/* The table that mx_rope_kv_append rotates by (host only: plain memory, no GPU).
+ * Pair i of rot_dim / 2 turns by f_i = base^(-2i / rot_dim) radians a position:
+ *   turns[i] = the fraction of f_i / 2 pi, in units of 2^-64; *amplitude = 1;
+ * scaled for contexts `factor` times as long as the original_length:
+ *   NONE    as it is (factor, low, high and original_length are not used)
+ *   LINEAR  f_i / factor
+ *   NTK     base * factor^(rot_dim / (rot_dim - 2)) in the place of base
+ *   YARN    with d(t) = rot_dim ln(original_length / (2 pi t)) / (2 ln base), the pair
+ *           that turns t times in the original length: f_i for i up to floor(d(high)),
+ *           f_i / factor from ceil(d(low)) on, a linear ramp between them (the two
+ *           held to [0, rot_dim - 1]); *amplitude = 0.1 ln(factor) + 1
+ *   BANDS   by t_i, pair i's turns in the original length: f_i for t_i >= high,
+ *           f_i / factor for t_i <= low, and s f_i + (1 - s) f_i / factor with
+ *           s = (t_i - low) / (high - low) between them
+ * (YARN after "YaRN: Efficient Context Window Extension of Large Language Models".)
+ * Errors: MX_ERR_INVALID_ARG (null, rot_dim not positive and even, an unknown
+ * scaling; base <= 1, and where they are used factor < 1, original_length <= 0, not
+ * 0 < low < high, or not finite; NTK with rot_dim 2). */
+MX_API int mx_rope_table(int rot_dim, double base, int scaling, double factor, double low, double high,
+                         int original_length, uint64_t* turns, float* amplitude);
+
+/* mx_kv_append with rotary positions: of each token that mx_kv_append would write,
+ * the first rot_dim elements of every head of q and k are rotated,
+ *   (a, b) -> amplitude * (a cos t - b sin t, a sin t + b cos t),  t = position * f_i,
+ * the others pass; the rotated k (from its fp32 values: one rounding) and v go to their
+ * places in the cache, the rotated q goes to q_out as bf16.
+ *   q: bf16, token t's [n_q_heads, head_dim] at t * q_stride elements, or NULL with
+ *     n_q_heads 0 (then no q_out).  q_out the same at t * q_out_stride; it may be q
+ *     with the same stride, and else does not overlap q, k or v.
+ *   positions [T] int32 or NULL: the angles' positions; without them a token's place in
+ *     its sequence.  They do not move the place that is written.
+ *   turns [rot_dim / 2] on the device, amplitude: mx_rope_table's.  An angle is exact
+ *     to 2^-25 turns at any position.
+ * Tokens that are skipped leave their rows of q_out as they were.
+ * Errors: as mx_kv_append (with q, q_out and their strides), plus MX_ERR_INVALID_ARG (an
+ * unknown layout, rot_dim < 0 or > head_dim, amplitude not finite, q without q_out) and
+ * MX_ERR_UNSUPPORTED (rot_dim % 16, head_dim > 256). */
+MX_API int mx_rope_kv_append(const mx_kv_cache* cache, const void* q, int64_t q_stride, int n_q_heads, void* q_out,
+                             int64_t q_out_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const int32_t* positions, const uint64_t* turns, int rot_dim, int layout,
+                             float amplitude, const int32_t* block_table, const int32_t* kv_lens,
+                             const int32_t* q_starts, int n_seqs, int max_pages, int T, void* ws, size_t ws_bytes,
+                             mx_stream_t stream);
 
 /* The reverse: the last q_starts[b+1] - q_starts[b] tokens of each sequence
  * (all of them where q_starts counts kv_lens) as bf16 [T, n_kv_heads, head_dim],
@@ -460,6 +545,35 @@ MX_API int mx_paged_attention(const mx_kv_cache* cache, const void* q, int64_t q
                               const int32_t* block_table, const int32_t* kv_lens, const int32_t* q_starts, int n_seqs,
                               int max_pages, int T, int max_q_len, float scale, int causal, int window, void* out,
                               float* lse, void* ws, size_t ws_bytes, mx_stream_t stream);
+
+/* Bytes of workspace mx_sample needs (0 for sizes that it rejects). */
+MX_API size_t mx_sample_workspace_size(int T, int V);
+
+/* One token for each row of logits, drawn by a given random number.  With the row's
+ * tokens in the order of their logits (descending; the same logit: ascending number):
+ *   weights  w_i = exp((logit_i - max) / temperature)
+ *   top_k    the first top_k tokens are kept (top_k <= 0 or >= V: all)
+ *   top_p    of those, token i is kept while the weight of those before it is below
+ *            top_p times the weight of all those (top_p >= 1: all; the first always)
+ *   min_p    of those, the ones with w_i >= min_p (of the largest; above 1 counts as 1)
+ *   token    the first, by number, at which the sum of the kept weights exceeds u
+ *            times their whole sum; logp = log of its weight's share in that sum.
+ * temperature 0 or top_k 1: the largest logit (of the lowest number), logp 0.
+ *   logits [T, V] bf16 or fp32 (type), row t at t * stride elements.
+ *   temperature, top_p, min_p fp32, top_k int32: [T] each, or NULL for 1, 1, 0, 0.
+ *   u [T] fp32 in [0, 1) (held to it).  tokens [T] int32, logp [T] fp32 or NULL.
+ * Weights are held as whole multiples of 2^-43 (those below 2^-44 are never drawn),
+ * 2^-30 off, and summed exactly: the same call gives the same tokens, and one next to a
+ * border may differ from exact arithmetic.  Logits of -inf are never drawn; of +inf, the
+ * only ones drawn.  A row with a NaN, without a finite or infinite maximum, or with a
+ * negative or NaN temperature gives token -1 and logp NaN and sets MX_ERR_DEVICE_ARG in
+ * the workspace status.
+ * Errors: MX_ERR_INVALID_ARG (null, T < 0, V <= 0, an unknown type, stride < V),
+ * MX_ERR_UNSUPPORTED (V > 800000 in bf16, V > 400000 in fp32), MX_ERR_ALIGNMENT (a tensor
+ * not aligned to its elements, ws), MX_ERR_WORKSPACE, MX_ERR_CUDA. */
+MX_API int mx_sample(const void* logits, int type, int64_t stride, int T, int V, const float* temperature,
+                     const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* tokens,
+                     float* logp, void* ws, size_t ws_bytes, mx_stream_t stream);
 
 /* Copy the workspace status word to *host_status (synchronising `stream`) and
  * clear it.  0 = no device-side error; otherwise an MX_ERR_* code. */

@@ -1,0 +1,147 @@
+"""Host-side argument checks of the operators that close a decoding step: every call
+below is refused, or has nothing to do, before any device work (no GPU needed)."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import serve_reference as srv
+
+
+@pytest.fixture(scope="module")
+def L():
+    from block_scaled_mx_gb300 import build as B
+    from block_scaled_mx_gb300 import mxmoe as mx
+
+    B.build()
+    return mx.lib()
+
+
+P = ctypes.c_void_p
+fake = P(4096)   # never dereferenced
+odd = P(4098)
+
+
+# ------------------------------------------------------------------ sandwich norm
+def test_sandwich_refusals(L):
+    def call(x=fake, xt=0, pw=fake, pt=0, gate=None, gt=0, kind=0, act=0, res=fake, rt=0, rs=1.0, bs=1.0, w=fake, wt=0, T=4, H=64,
+             eps=1e-6, ro=fake, y=fake, fmt=0, codes=fake, scales=fake):
+        return L.mx_sandwich_rmsnorm(x, xt, pw, pt, gate, gt, kind, act, res, rt, rs, bs, w, wt, T, H, eps, ro, y, fmt, codes, scales, None)
+
+    assert call(T=0) == 0
+    for bad in (dict(x=None), dict(res=None), dict(ro=None), dict(T=-1), dict(H=0), dict(xt=2), dict(rt=-1), dict(wt=5), dict(pt=3), dict(eps=0.0),
+                dict(eps=math.nan), dict(rs=math.inf), dict(bs=math.nan), dict(fmt=2), dict(scales=None), dict(codes=None),
+                dict(y=None, codes=None, scales=None), dict(w=None), dict(w=None, y=None), dict(kind=4, gate=fake), dict(kind=1), dict(gate=fake),
+                dict(kind=-1), dict(act=2), dict(kind=3, gate=fake, gt=2)):
+        assert call(**bad) == 1, bad
+    for bad in (dict(H=48), dict(H=32800)):
+        assert call(**bad) == 2, bad
+    for bad in (dict(x=odd), dict(res=odd), dict(w=odd), dict(pw=odd), dict(ro=odd), dict(y=odd), dict(codes=odd), dict(kind=1, gate=odd),
+                dict(kind=3, gate=odd), dict(kind=2, gate=odd, gt=1), dict(kind=2, gate=P(4097))):
+        assert call(**bad) == 3, bad
+
+
+# ------------------------------------------------------------------ rotary positions
+def _table(L, R=64, base=10000.0, scaling=0, factor=1.0, low=1.0, high=4.0, length=4096):
+    out, amp = (ctypes.c_uint64 * max(R // 2, 1))(), ctypes.c_float()
+    st = L.mx_rope_table(R, base, scaling, factor, low, high, length, ctypes.addressof(out), ctypes.addressof(amp))
+    return st, list(out), amp.value
+
+
+def test_rope_table_refusals(L):
+    out = ctypes.addressof((ctypes.c_uint64 * 32)())
+    assert L.mx_rope_table(64, 1e4, 0, 1.0, 1.0, 4.0, 0, None, out) == 1 and L.mx_rope_table(64, 1e4, 0, 1.0, 1.0, 4.0, 0, out, None) == 1
+    for bad in (dict(R=0), dict(R=-2), dict(R=3), dict(base=1.0), dict(base=math.nan), dict(base=math.inf), dict(scaling=5), dict(scaling=-1),
+                dict(scaling=1, factor=0.5), dict(scaling=2, factor=math.nan), dict(scaling=2, R=2, factor=2.0), dict(scaling=3, length=0),
+                dict(scaling=4, length=-1), dict(scaling=3, low=0.0), dict(scaling=3, low=4.0), dict(scaling=4, high=math.inf)):
+        assert _table(L, **bad)[0] == 1, bad
+    for fine in (dict(), dict(factor=math.nan, low=math.nan), dict(scaling=1, factor=1.0, length=0), dict(R=2)):
+        assert _table(L, **fine)[0] == 0, fine
+
+
+@pytest.mark.parametrize("scaling,name", list(enumerate(["none", "linear", "ntk", "yarn", "bands"])))
+@pytest.mark.parametrize("R,base,factor,length,low,high", [(64, 10000.0, 8.0, 4096, 1.0, 32.0), (128, 500000.0, 16.0, 8192, 1.0, 4.0), (32, 10000.0, 1.0, 2048, 0.5, 2.0)])
+def test_rope_table_values(L, scaling, name, R, base, factor, length, low, high):
+    st, turns, amp = _table(L, R, base, scaling, factor, low, high, length)
+    f, want_amp = srv.frequencies(R, base, name, factor, length, low, high)
+    assert st == 0 and abs(amp - want_amp) <= 2.0 ** -24 * want_amp
+    for got, x in zip(turns, f):
+        x = x / (2 * math.pi)
+        # a handful of roundings in 64 bits, each 2^-53; the exponent of a power by up to 14 of
+        # them; the table holds whole multiples of 2^-64, rounded down
+        assert abs(got / 2.0 ** 64 - x) <= 64 * 2.0 ** -53 * x + 2.0 ** -64
+
+
+def _cache(**kw):
+    from block_scaled_mx_gb300 import mxmoe as mx
+
+    f = dict(k_codes=4096, k_scales=4096, v_codes=4096, v_scales=4096, num_pages=8, page_size=16, n_kv_heads=2, head_dim=64, fmt=0)
+    f.update(kw)
+    return mx.KVCacheTables(*(f[n] for n, _ in mx.KVCacheTables._fields_))
+
+
+def test_rope_append_refusals(L):
+    def call(c=None, q=fake, qs=512, nq=8, qo=fake, os=512, k=fake, ks=512, v=fake, vs=512, pos=None, turns=fake, R=64, layout=0, amp=1.0, bt=fake,
+             kv=fake, st=fake, n=2, mp=4, T=4, ws=fake, wb=256):
+        c = _cache() if c is None else c
+        return L.mx_rope_kv_append(ctypes.addressof(c), q, qs, nq, qo, os, k, ks, v, vs, pos, turns, R, layout, amp, bt, kv, st, n, mp, T, ws, wb, None)
+
+    assert call(T=0) == 0 and call(n=0) == 0
+    for bad in (dict(q=None), dict(qo=None), dict(k=None), dict(v=None), dict(turns=None), dict(bt=None), dict(kv=None), dict(st=None), dict(ws=None),
+                dict(nq=-1), dict(nq=0), dict(qs=511), dict(os=100), dict(ks=127), dict(vs=1), dict(R=-16), dict(R=80), dict(layout=2),
+                dict(amp=math.nan), dict(amp=math.inf), dict(T=-1), dict(n=-1), dict(mp=0), dict(c=_cache(fmt=2)), dict(c=_cache(num_pages=0))):
+        assert call(**bad) == 1, bad
+    for bad in (dict(R=24), dict(c=_cache(head_dim=288), qs=4096, os=4096, ks=4096, vs=4096), dict(c=_cache(head_dim=80), R=16, qs=4096, os=4096, ks=4096, vs=4096),
+                dict(nq=20000, qs=2 ** 21, os=2 ** 21), dict(c=_cache(page_size=2 ** 30))):
+        assert call(**bad) == 2, bad
+    for bad in (dict(q=odd), dict(qo=odd), dict(k=odd), dict(v=odd), dict(qs=516), dict(os=516), dict(ks=516), dict(vs=516), dict(pos=P(4097)),
+                dict(turns=P(4100)), dict(ws=P(4112)), dict(bt=odd)):
+        assert call(**bad) == 3, bad
+    assert call(wb=255) == 4
+
+
+# ------------------------------------------------------------------ sampling
+def test_sample_refusals(L):
+    def call(x=fake, type=0, stride=100, T=4, V=100, tau=None, k=None, p=None, m=None, u=fake, tok=fake, lp=None, ws=fake, wb=256):
+        return L.mx_sample(x, type, stride, T, V, tau, k, p, m, u, tok, lp, ws, wb, None)
+
+    assert call(T=0) == 0
+    for bad in (dict(x=None), dict(u=None), dict(tok=None), dict(ws=None), dict(type=2), dict(stride=99), dict(T=-1), dict(V=0)):
+        assert call(**bad) == 1, bad
+    for bad in (dict(V=800001, stride=10 ** 6), dict(V=400001, stride=10 ** 6, type=1), dict(T=2 ** 30)):
+        assert call(**bad) == 2, bad
+    for bad in (dict(x=P(4097)), dict(x=odd, type=1), dict(tau=odd), dict(k=odd), dict(p=odd), dict(m=odd), dict(u=odd), dict(tok=odd), dict(lp=odd),
+                dict(ws=P(4112))):
+        assert call(**bad) == 3, bad
+    assert call(wb=255) == 4
+    assert L.mx_sample_workspace_size(-1, 5) == 0 and L.mx_sample_workspace_size(3, 0) == 0 and L.mx_sample_workspace_size(0, 5) == 256
+
+
+# ------------------------------------------------------------------ the binding
+def test_binding_checks_tensors(L):
+    from block_scaled_mx_gb300 import mxmoe as mx
+
+    meta = dict(device="meta")
+    x, row = torch.empty(4, 64, **meta), torch.empty(64, **meta)
+    with pytest.raises(ValueError, match="gate"):
+        mx.mx_sandwich_rmsnorm(x, None, 1e-6, x, x, gate=torch.empty(4, **meta))
+    with pytest.raises(ValueError, match="post_weight"):
+        mx.mx_sandwich_rmsnorm(x, torch.empty(32, **meta), 1e-6, x, x)
+    with pytest.raises(KeyError):
+        mx.mx_sandwich_rmsnorm(x, None, 1e-6, x, x, gate_act="relu")
+    with pytest.raises(KeyError):
+        mx.Rope(64, layout="other", device="cpu")
+    with pytest.raises(KeyError):
+        mx.Rope(64, scaling="other", device="cpu")
+    with pytest.raises(mx.MxError):
+        mx.Rope(63, device="cpu")
+    with pytest.raises(ValueError):
+        mx.Rope(0, device="cpu")
+    rope = mx.Rope(64, scaling="yarn", factor=4.0, original_length=4096, device="cpu")
+    assert rope.turns.dtype == torch.int64 and rope.turns.shape == (32,) and abs(rope.amplitude - 1.138629436) < 1e-6
+    logits = torch.empty(4, 50, **meta)
+    with pytest.raises(ValueError, match="CUDA"):
+        mx.mx_sample(logits, row, row, row)
+    with pytest.raises(ValueError, match="dense"):
+        mx.mx_sample(logits.t(), row, row, row)
