@@ -12,7 +12,73 @@
 
 using namespace mxk;
 
+namespace {
+
+// sizes whose products and grids fit their types
+int check_linear(int T, int N, int K, int act_fmt, int w_fmt) {
+  if (T < 0 || N <= 0 || K <= 0) return MX_ERR_INVALID_ARG;
+  if ((act_fmt != MX_E4M3 && act_fmt != MX_E2M1) || (w_fmt != MX_E4M3 && w_fmt != MX_E2M1)) return MX_ERR_INVALID_ARG;
+  if (K % 32 || K > (1 << 20) || N > (1 << 22) || T > (1 << 22) || (act_fmt == MX_E2M1 && w_fmt != MX_E2M1)) return MX_ERR_UNSUPPORTED;
+  return MX_OK;
+}
+
+// Workspace of mx_linear: the status word, the tokens' tiled scales, their codes.
+size_t linear_scales_bytes(int T, int K) { return static_cast<size_t>((T + 127) / 128) * ((K + 127) / 128) * 512; }
+
+}  // namespace
+
 extern "C" {
+
+size_t mx_linear_prepared_bytes(int N, int K, int fmt) {
+  return check_linear(0, N, K, MX_E4M3, fmt) == MX_OK ? linear_layout(N, K, fmt).total_bytes : 0;
+}
+
+int mx_linear_prepare(const uint8_t* codes, const uint8_t* scales, int N, int K, int fmt, void* dst, size_t dst_bytes,
+                      mx_stream_t stream) {
+  const int st = check_linear(0, N, K, MX_E4M3, fmt);
+  if (st != MX_OK) return st;
+  if (!codes || !scales || !dst) return MX_ERR_INVALID_ARG;
+  if (!aligned(codes, 16) || !aligned(dst, 256)) return MX_ERR_ALIGNMENT;
+  const LinearLayout L = linear_layout(N, K, fmt);
+  if (dst_bytes < L.total_bytes) return MX_ERR_WORKSPACE;
+  return cuda_status(launch_linear_prepare(codes, scales, L, static_cast<uint8_t*>(dst), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mx_linear_workspace_size(int T, int N, int K, int act_fmt) {
+  if (check_linear(T, N, K, act_fmt, MX_E2M1) != MX_OK) return 0;
+  return 256 + al256(linear_scales_bytes(T, K)) + al256(static_cast<size_t>(T) * (act_fmt == MX_E2M1 ? K / 2 : K));
+}
+
+int mx_linear(const void* x_bf16, const uint8_t* codes, const uint8_t* scales, int act_fmt, const void* w_prep, int w_fmt,
+              const float* bias, int T, int N, int K, void* out, int out_type, void* ws, size_t ws_bytes,
+              mx_stream_t stream) {
+  const int st = check_linear(T, N, K, act_fmt, w_fmt);
+  if (st != MX_OK) return st;
+  if (!type_ok(out_type)) return MX_ERR_INVALID_ARG;
+  if (T == 0) return MX_OK;
+  if (!w_prep || !out || !ws || !codes != !scales || !x_bf16 != (codes != nullptr)) return MX_ERR_INVALID_ARG;
+  if (!aligned(x_bf16, 16) || !aligned(codes, 16) || !aligned(w_prep, 256) || !aligned(bias, 4) || !aligned(out, 16) || !aligned(ws, 256))
+    return MX_ERR_ALIGNMENT;
+  if (ws_bytes < mx_linear_workspace_size(T, N, K, act_fmt)) return MX_ERR_WORKSPACE;
+  uint8_t* const w = static_cast<uint8_t*>(ws);
+  LinearArgs a{};
+  a.w_prep = static_cast<const uint8_t*>(w_prep);
+  a.w_fmt = w_fmt;
+  a.act_fmt = act_fmt;
+  a.x = x_bf16;
+  a.scales = scales;
+  a.t_scales = w + 256;
+  a.t_codes = codes ? codes : w + 256 + al256(linear_scales_bytes(T, K));
+  a.bias = bias;
+  a.out = out;
+  a.out_f32 = out_type == MX_F32;
+  a.T = T;
+  a.N = N;
+  a.K = K;
+  a.status = static_cast<int*>(ws);
+  a.wait_limit_ns = wait_limit_ns();
+  return cuda_status(launch_linear(a, reinterpret_cast<cudaStream_t>(stream)));
+}
 
 int mx_sandwich_rmsnorm(const void* x, int x_type, const void* post_weight, int post_weight_type, const void* gate,
                         int gate_type, int gate_kind, int gate_act, const void* residual, int residual_type,

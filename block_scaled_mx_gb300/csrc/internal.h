@@ -162,6 +162,30 @@ struct RopeArgs {
 };
 cudaError_t launch_rope_kv_append(const RopeArgs& r, cudaStream_t s);
 
+// ---- linear.cu
+// Laid-out weights: blocks of 128 rows x 128 elements, block (rb, kc) at rb * NK + kc,
+// then their scales in 512-byte blocks in the order of tensor memory.
+struct LinearLayout {
+  int N, K, e2m1, RB, NK, row_bytes;  // bytes of a block's row
+  size_t scales_offset, total_bytes;
+};
+LinearLayout linear_layout(int N, int K, int fmt);
+cudaError_t launch_linear_prepare(const uint8_t* codes, const uint8_t* scales, const LinearLayout& L, uint8_t* dst, cudaStream_t s);
+struct LinearArgs {
+  const uint8_t* w_prep;
+  int w_fmt, act_fmt;
+  const void* x;           // [T, K] bf16 to be quantised to t_codes, or null:
+  const uint8_t* scales;   // [T, K / 32] of the given t_codes
+  const uint8_t* t_codes;  // [T, K] or [T, K / 2]
+  uint8_t* t_scales;       // workspace: tiled scales, 512 bytes for 128 tokens x 128 elements
+  const float* bias;       // [N] or null
+  void* out;               // [T, N]
+  int out_f32, T, N, K;
+  int* status;
+  uint64_t wait_limit_ns;
+};
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
+
 // ---- sample.cu
 struct SampleArgs {
   const void* logits;        // [T, V] bf16 or fp32

@@ -1,0 +1,691 @@
+// Dense products with MX weights: out[t, n] = bias[n] + sum_k A[t, k] W[n, k] for MX
+// activations A (E4M3 or E2M1) and MX weights W, as block-scaled tcgen05 MMAs with fp32
+// accumulators in tensor memory.
+//
+// Weights are the MMA's A operand (128 rows of N a block), tokens its B operand (`bn` of
+// them a tile), so a decoding step of a few tokens still runs full-width MMAs while the
+// weights stream.  All operands come by TMA, the scales too: they lie in 512-byte blocks
+// of 128 rows x 4 scales in the order that tcgen05.cp copies to tensor memory, the
+// weights' laid out once (mx_linear_prepare), the tokens' by a first launch, which also
+// quantises bf16 activations.  The MMAs' launch is a dependent one: its set-up and its
+// first weights come while the first launch runs.
+//
+// Warps: 0 TMA, 1 tensor memory and MMAs (one thread), 2..9 epilogue (two to a quarter of
+// tensor memory's lanes).  Accumulators are double-buffered where tensor memory holds
+// two.  Three forms:
+//   split  clusters of S CTAs share a tile's K; the parts are added in rank order
+//          through distributed shared memory (the same bits every time)
+//   whole  a CTA goes through tiles of all of K
+//   pair   two CTAs share a 256-row tile: cta_group::2 MMAs, each loads half the tokens
+// Every wait is bounded; one that runs out sets MX_ERR_TIMEOUT and all roles unwind.
+#include <cooperative_groups.h>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+#include "common.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+#include "rows.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace mxk {
+
+namespace {
+
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kMaxStages = 12;
+
+struct Params {
+  int T, N, NK, RB, TT;
+  int bn, brows;       // tokens of a tile, of this CTA's loads (half in a pair)
+  int splits, units;   // CTAs that share a tile's K; tiles (of pairs in a pair)
+  int kps, stages, acc_bufs;
+  int TB;              // blocks of 128 tokens
+  int a_fmt, b_fmt, out_f32, slice;
+  uint32_t a_tx;       // bytes that a weight block's copy counts for
+  uint32_t a_slot, b_slot, sb_slot;  // shared memory of a chunk
+  uint32_t off_a, off_b, off_sa, off_sb, off_bar;
+  uint32_t tmem_cols, acc_cols, sf_col0, sfc;
+  const uint8_t* w_scales;
+  const uint8_t* t_scales;
+  const float* bias;
+  void* out;
+  int* status;
+  unsigned long long wait_limit_ns;
+};
+
+struct Bars {
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
+  uint32_t tmem;
+  int abort;
+};
+
+template <bool PAIR>
+struct Waiter {
+  Bars* b;
+  uint32_t peer_abort;  // the peer's flag in a pair
+  unsigned long long limit_ns;
+  int* status;
+  __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, bool sleep) const {
+    if (PAIR) return sleep ? mbar_try_wait_cluster_sleep(bar, parity, 20000u) : mbar_try_wait_cluster(bar, parity);
+    return sleep ? mbar_try_wait_sleep(bar, parity, 20000u) : mbar_try_wait(bar, parity);
+  }
+  // False when the wait ran out or another role gave up.
+  __device__ __forceinline__ bool operator()(uint64_t* bar64, uint32_t parity, bool sleep = true) const {
+    const uint32_t bar = smem_u32(bar64);
+    if (poll(bar, parity, false)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+      if (poll(bar, parity, sleep)) return true;
+      if (*static_cast<volatile int*>(&b->abort)) return false;
+      if (globaltimer_ns() - t0 > limit_ns) {
+        set_status(status, MX_ERR_TIMEOUT);
+        *static_cast<volatile int*>(&b->abort) = 1;
+        if (PAIR) st_shared_cluster_u32(peer_abort, 1u);
+        return false;
+      }
+    }
+  }
+  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, (*this)(bar, parity)) != 0;
+  }
+};
+
+__device__ __forceinline__ void store_out(const Params& p, int64_t at, float v) {
+  if (p.out_f32) static_cast<float*>(p.out)[at] = v;
+  else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+}
+
+// A4: both operands packed E2M1 (kind::mxf4), else kind::mxf8f6f4 (E2M1 weights are
+// widened to bytes by the TMA).
+template <bool PAIR, bool A4>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_linear(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+             const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Bars* const bars = reinterpret_cast<Bars*>(base + p.off_bar);
+  const int S = p.stages, kps = p.kps;
+  const uint32_t rank = PAIR || p.splits > 1 ? cluster_ctarank() : 0u;
+  const int group = PAIR ? 2 : p.splits;
+  const int unit0 = blockIdx.x / group, unit_step = gridDim.x / group;
+  const int k0 = PAIR ? 0 : static_cast<int>(static_cast<int64_t>(p.NK) * rank / p.splits);
+  const int k1 = PAIR ? p.NK : static_cast<int>(static_cast<int64_t>(p.NK) * (rank + 1) / p.splits);
+  const int rbs = PAIR ? (p.RB + 1) / 2 : p.RB;  // tiles along N
+  constexpr int kEl = A4 ? 64 : 128;             // bytes of a token's chunk
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&bars->full[s]), PAIR ? 2 : 1);  // one arrival with bytes from each CTA's TMA warp
+      mbar_init(smem_u32(&bars->empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&bars->acc_full[a]), 1);
+      mbar_init(smem_u32(&bars->acc_empty[a]), PAIR ? 2 * kEpiWarps : kEpiWarps);
+    }
+    mbar_init(smem_u32(&bars->drain), 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    if (PAIR) {
+      tmem_alloc_pair(smem_u32(&bars->tmem), p.tmem_cols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(&bars->tmem), p.tmem_cols);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync_all();  // barriers are ready before the peer arrives on them
+  tc_fence_after();
+  const uint32_t tbase = bars->tmem;
+  const Waiter<PAIR> wait{bars, PAIR ? mapa_shared(smem_u32(&bars->abort), rank ^ 1u) : 0u, p.wait_limit_ns, p.status};
+
+  if (warp == 0) {
+    // ================================================================ TMA
+    if (lane == 0) {
+      uint32_t fills = 0, s = 0, ph = 0;
+      bool ok = true, ready = false;
+      // weights of one stage; its barrier is armed for everything that lands there
+      auto weights = [&](uint32_t slot, int unit, int kc) {
+        const int tt = unit / rbs, rb = PAIR ? 2 * (unit - tt * rbs) + static_cast<int>(rank) : unit - tt * rbs;
+        const int n0 = tt * p.bn, nk = min(kps, k1 - kc);
+        const int tb0 = n0 / 128, nb = min((n0 % 128 + p.bn + 127) / 128, p.TB - tb0);
+        const uint32_t full = smem_u32(&bars->full[slot]);
+        const uint32_t sa = smem_u32(base + p.off_sa) + slot * kps * 512u;
+        const uint32_t a = smem_u32(base + p.off_a) + slot * kps * p.a_slot;
+        const uint32_t b_bytes = static_cast<uint32_t>(nk * p.brows * kEl);
+        if (PAIR) {
+          // both CTAs' copies land on rank 0's barrier, whose thread issues the MMAs
+          const uint32_t bar = mapa_shared(full, 0u);
+          mbar_arrive_expect_tx_cluster(bar, kps * p.a_tx + b_bytes + static_cast<uint32_t>(kps) * 512u * static_cast<uint32_t>(1 + p.sb_slot / 512));
+          tma_load_4d_pair(a, &tm_a, 0, 0, kc, rb, bar);
+          tma_load_3d_pair(sa, &tm_sa, 0, kc, rb, bar);
+        } else {
+          mbar_arrive_expect_tx(full, kps * p.a_tx + b_bytes + static_cast<uint32_t>(nk) * 512u * static_cast<uint32_t>(1 + nb));
+          tma_load_4d(a, &tm_a, 0, 0, kc, rb, full);
+          bulk_load(sa, p.w_scales + (static_cast<size_t>(rb) * p.NK + kc) * 512, static_cast<uint32_t>(nk) * 512u, full);
+        }
+      };
+      auto tokens = [&](uint32_t slot, int unit, int kc) {
+        const int tt = unit / rbs;
+        const int n0 = tt * p.bn, nk = min(kps, k1 - kc);
+        const int tb0 = n0 / 128, nb = min((n0 % 128 + p.bn + 127) / 128, p.TB - tb0);
+        const uint32_t full = smem_u32(&bars->full[slot]);
+        const uint32_t b = smem_u32(base + p.off_b) + slot * kps * p.b_slot;
+        const uint32_t sb = smem_u32(base + p.off_sb) + slot * kps * p.sb_slot;
+        if (PAIR) {
+          const uint32_t bar = mapa_shared(full, 0u);
+          for (int u = 0; u < nk; ++u)
+            tma_load_2d_pair(b + u * p.b_slot, &tm_b, (kc + u) * kEl, n0 + static_cast<int>(rank) * p.brows, bar);
+          for (int i = 0; i < static_cast<int>(p.sb_slot / 512); ++i) tma_load_3d_pair(sb + i * kps * 512u, &tm_sb, 0, kc, tb0 + i, bar);
+        } else {
+          for (int u = 0; u < nk; ++u) tma_load_2d(b + u * p.b_slot, &tm_b, (kc + u) * kEl, n0, full);
+          for (int i = 0; i < nb; ++i)
+            bulk_load(sb + i * kps * 512u, p.t_scales + (static_cast<size_t>(tb0 + i) * p.NK + kc) * 512, static_cast<uint32_t>(nk) * 512u, full);
+        }
+      };
+      prefetch_tensormap(&tm_a);
+      prefetch_tensormap(&tm_b);
+      for (int unit = unit0; unit < p.units && ok; unit += unit_step) {
+        int kc = k0;
+        if (!ready) {
+          // the first launch's results are awaited behind the weights of all stages
+          int n = 0;
+          for (int k = k0; n < S && k < k1; ++n, k += kps) weights(n, unit, k);
+          asm volatile("griddepcontrol.wait;" ::: "memory");
+          ready = true;
+          for (int i = 0; i < n; ++i, kc += kps) tokens(i, unit, kc);
+          fills = n;
+          s = n % S;
+          ph = n / S;
+        }
+        for (; kc < k1; kc += kps) {
+          if (!wait(&bars->empty[s], ph ^ 1u)) {
+            ok = false;
+            break;
+          }
+          weights(s, unit, kc);
+          tokens(s, unit, kc);
+          ++fills;
+          if (++s == static_cast<uint32_t>(S)) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // what this thread asked for has landed before the CTA leaves (in a pair rank 0's
+      // barriers count both CTAs' copies)
+      if (!PAIR || rank == 0) {
+        for (int i = 0; i < S && static_cast<uint32_t>(i) < fills; ++i) {
+          const uint32_t last = fills - 1 - ((fills - 1 - i) % S);
+          mbar_wait(smem_u32(&bars->full[i]), (last / S) & 1u, 100000000ull);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ================================================================ MMAs
+    if ((!PAIR || rank == 0) && elect_one()) {
+      const uint32_t a0 = desc_lo_sw128(smem_u32(base + p.off_a)), b0 = desc_lo_sw128(smem_u32(base + p.off_b));
+      const uint32_t sa0 = smem_u32(base + p.off_sa), sb0 = smem_u32(base + p.off_sb);
+      constexpr uint32_t kM = PAIR ? 256u : 128u;
+      uint32_t s = 0, ph = 0, ab = 0, aph = 0, slot = 0;
+      bool ok = true;
+      for (int unit = unit0; unit < p.units && ok; unit += unit_step) {
+        const int tt = unit / rbs, n0 = tt * p.bn;
+        const int nsb = (n0 % 128 + p.bn + 127) / 128;
+        const uint32_t sb_col = static_cast<uint32_t>(n0 % 128) / 32;
+        uint32_t n_mma = static_cast<uint32_t>((min(p.bn, p.T - n0) + 15) & ~15);
+        // a pair's CTAs hold the two halves of a whole tile
+        if (PAIR) n_mma = static_cast<uint32_t>(p.bn);
+        uint32_t idesc[A4 ? 2 : 4];
+#pragma unroll
+        for (int i = 0; i < (A4 ? 2 : 4); ++i)
+          idesc[i] = A4 ? idesc_mxf4(kM, n_mma, 2 * i) : idesc_mx(p.a_fmt, p.b_fmt, kM, n_mma, i, i);
+        if (!wait(&bars->acc_empty[ab], aph ^ 1u)) break;
+        tc_fence_after();
+        const uint32_t d = tbase + ab * p.acc_cols;
+        uint32_t accum = 0;
+        for (int kc = k0; kc < k1; kc += kps) {
+          if (!wait(&bars->full[s], ph, false)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int nk = min(kps, k1 - kc);
+          for (int u = 0; u < nk; ++u) {
+            const uint32_t c = s * kps + u;
+            const uint32_t sf = tbase + p.sf_col0 + slot * p.sfc;
+            slot = slot + 1 == 4 ? 0 : slot + 1;  // four sets of columns in turn
+            if (PAIR) tmem_copy_scales_pair(sf, sa0 + c * 512u);
+            else tmem_copy_scales(sf, sa0 + c * 512u);
+            for (int i = 0; i < nsb; ++i) {
+              const uint32_t at = sb0 + s * kps * p.sb_slot + (i * kps + u) * 512u;
+              if (PAIR) tmem_copy_scales_pair(sf + 4u + 4u * i, at);
+              else tmem_copy_scales(sf + 4u + 4u * i, at);
+            }
+            const uint32_t a = a0 + c * (p.a_slot >> 4), b = b0 + c * (p.b_slot >> 4);
+#pragma unroll
+            for (int i = 0; i < (A4 ? 2 : 4); ++i) {
+              if (A4) {
+                if (PAIR) mma_mxf4_pair_lo(d, a + 2u * i, b + 2u * i, kDescHiSw64, idesc[i], sf, sf + 4u + sb_col, accum);
+                else mma_mxf4_lo(d, a + 2u * i, b + 2u * i, kDescHiSw64, idesc[i], sf, sf + 4u + sb_col, accum);
+              } else {
+                if (PAIR) mma_mxf8f6f4_pair_lo(d, a + 2u * i, b + 2u * i, kDescHiSw128, idesc[i], sf, sf + 4u + sb_col, accum);
+                else mma_mxf8f6f4_lo(d, a + 2u * i, b + 2u * i, kDescHiSw128, idesc[i], sf, sf + 4u + sb_col, accum);
+              }
+              accum = 1;
+            }
+          }
+          if (PAIR) mma_commit_pair(smem_u32(&bars->empty[s]), 3);
+          else mma_commit(smem_u32(&bars->empty[s]));
+          if (++s == static_cast<uint32_t>(S)) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (PAIR) mma_commit_pair(smem_u32(&bars->acc_full[ab]), 3);
+        else mma_commit(smem_u32(&bars->acc_full[ab]));
+        if (++ab == static_cast<uint32_t>(p.acc_bufs)) {
+          ab = 0;
+          aph ^= 1u;
+        }
+      }
+      // every MMA has completed before tensor memory is given back
+      if (PAIR) mma_commit_pair(smem_u32(&bars->drain), 1);
+      else mma_commit(smem_u32(&bars->drain));
+      mbar_wait(smem_u32(&bars->drain), 0, 100000000ull);
+    }
+    __syncwarp();
+  } else if (PAIR || p.splits == 1) {
+    // ================================================================ epilogue
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    uint32_t ab = 0, aph = 0;
+    for (int unit = unit0; unit < p.units; unit += unit_step) {
+      const int tt = unit / rbs, rb = PAIR ? 2 * (unit - tt * rbs) + static_cast<int>(rank) : unit - tt * rbs;
+      const int n0 = tt * p.bn, cols = min(p.bn, p.T - n0);
+      const int n = rb * 128 + 32 * q + lane;
+      const float bias = p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;
+      if (!wait.warp(&bars->acc_full[ab], aph)) break;
+      tc_fence_after();
+      const uint32_t d = tbase + (static_cast<uint32_t>(32 * q) << 16) + ab * p.acc_cols;
+      for (int c0 = 32 * half; c0 < cols; c0 += 64) {
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(d + c0, r);
+        tmem_ld_wait();
+        const int64_t at = static_cast<int64_t>(n0 + c0) * p.N + n;
+        if (!p.out_f32 && p.N % 2 == 0) {
+          // two lanes exchange a token each, so that a lane stores two neighbours of one
+          const bool odd = lane & 1;
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float v0 = __uint_as_float(r[c]) + bias, v1 = __uint_as_float(r[c + 1]) + bias;
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+            const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(other, v1) : __floats2bfloat162_rn(v0, other);
+            if (c0 + c + odd < cols && n < p.N)
+              *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at + static_cast<int64_t>(c + odd) * p.N - odd) = w;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c0 + c < cols && n < p.N) store_out(p, at + static_cast<int64_t>(c) * p.N, __uint_as_float(r[c]) + bias);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&bars->acc_empty[ab]), 0u));
+        else mbar_arrive(smem_u32(&bars->acc_empty[ab]));
+      }
+      if (++ab == static_cast<uint32_t>(p.acc_bufs)) {
+        ab = 0;
+        aph ^= 1u;
+      }
+    }
+  } else {
+    // split: one tile a cluster; its parts are added below
+    wait.warp(&bars->acc_full[0], 0);
+    tc_fence_after();
+  }
+
+  if (!PAIR && p.splits > 1) {
+    // Rank r adds up columns [r * slice, (r + 1) * slice) of the tile: every CTA stores its
+    // part of them in r's shared memory (the stages', which all CTAs have read by now).
+    __syncthreads();
+    cluster_sync_all();
+    float* const parts = reinterpret_cast<float*>(base + p.off_a);  // [source][column of the slice][128 rows]
+    const int tt = unit0 / rbs, rb = unit0 - tt * rbs, n0 = tt * p.bn, cols = min(p.bn, p.T - n0);
+    if (warp >= 2) {
+      const int q = warp & 3, half = (warp - 2) >> 2;
+      const uint32_t d = tbase + (static_cast<uint32_t>(32 * q) << 16);
+      for (int c0 = 8 * half; c0 < cols; c0 += 16) {
+        uint32_t r[8];
+        __syncwarp();
+        tmem_ld_32x32b_x8(d + c0, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          if (c0 + c < cols) {
+            const int owner = (c0 + c) / p.slice, col = c0 + c - owner * p.slice;
+            const uint32_t at = smem_u32(parts + (static_cast<int>(rank) * p.slice + col) * 128 + 32 * q + lane);
+            st_shared_cluster_u32(mapa_shared(at, static_cast<uint32_t>(owner)), r[c]);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();
+    const int first = static_cast<int>(rank) * p.slice, mine = min(p.slice, cols - first);
+    if (!bars->abort) {
+      for (int i = tid; i < mine * 64; i += kThreads) {
+        const int col = i >> 6, row = (i & 63) * 2, n = rb * 128 + row;
+        float2 v = make_float2(0.0f, 0.0f);
+        for (int s = 0; s < p.splits; ++s) {
+          const float2 w = *reinterpret_cast<const float2*>(parts + (s * p.slice + col) * 128 + row);
+          v.x += w.x;
+          v.y += w.y;
+        }
+        if (p.bias) {
+          if (n < p.N) v.x += __ldg(p.bias + n);
+          if (n + 1 < p.N) v.y += __ldg(p.bias + n + 1);
+        }
+        const int64_t at = static_cast<int64_t>(n0 + first + col) * p.N + n;
+        if (!p.out_f32 && p.N % 2 == 0) {
+          if (n < p.N) *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at) = __floats2bfloat162_rn(v.x, v.y);
+        } else {
+          if (n < p.N) store_out(p, at, v.x);
+          if (n + 1 < p.N) store_out(p, at + 1, v.y);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR && bars->abort) {
+    // where a wait ran out nobody counts rank 1's last copies: they get a millisecond
+    if (tid == 0) {
+      for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000ull;) {
+      }
+    }
+    __syncthreads();
+  }
+  if (PAIR) cluster_sync_all();  // neither leaves while the other's MMAs or copies may reach it
+  tc_fence_after();
+  if (warp == 1) {
+    if (PAIR) tmem_dealloc_pair(tbase, p.tmem_cols);
+    else tmem_dealloc(tbase, p.tmem_cols);
+  }
+}
+
+// ------------------------------------------------------------------ tokens
+// bf16 rows to MX codes and tiled scales, or (x null) row-major scales to tiled ones.  A
+// lane has eight elements, four lanes a block of 32; scale blocks behind K are 1.
+// Tiled: block (t / 128, k / 128) of 512 bytes, word [t % 32][t % 128 / 32] its row's four.
+template <bool E2M1>
+__global__ void __launch_bounds__(256) k_linear_tokens(const uint4* __restrict__ x, const uint8_t* __restrict__ scales, int T, int K, int NK,
+                                                       uint8_t* __restrict__ codes, uint8_t* __restrict__ tiled) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int per_row = NK * 16;  // groups of eight
+  const int64_t n = static_cast<int64_t>(T) * per_row, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  if (!x) {
+    const int64_t blocks = static_cast<int64_t>(T) * NK * 4;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < blocks; i += stride) {
+      const int t = static_cast<int>(i / (NK * 4)), b = static_cast<int>(i - static_cast<int64_t>(t) * NK * 4);
+      tiled[(static_cast<size_t>(t / 128) * NK + b / 4) * 512 + (t % 32) * 16 + (t % 128 / 32) * 4 + b % 4] =
+          b < K / 32 ? scales[static_cast<size_t>(t) * (K / 32) + b] : 127;
+    }
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i - lane < n; i += stride) {
+    const int t = static_cast<int>(i / per_row), g = static_cast<int>(i - static_cast<int64_t>(t) * per_row);
+    const bool in = i < n && g < K / 8;
+    const int64_t at = static_cast<int64_t>(t) * (K / 8) + g;
+    const uint4 w = in ? __ldg(x + at) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t b[4] = {w.x, w.y, w.z, w.w};
+    float v[8];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      v[2 * m] = __uint_as_float(b[m] << 16);
+      v[2 * m + 1] = __uint_as_float(b[m] & 0xFFFF0000u);
+    }
+    uint8_t scale;
+    const uint2 c = mx_codes8(v, E2M1, scale);
+    if (in) {
+      if (E2M1) reinterpret_cast<uint32_t*>(codes)[at] = c.x;
+      else reinterpret_cast<uint2*>(codes)[at] = c;
+    }
+    if (i < n && (g & 3) == 0)
+      tiled[(static_cast<size_t>(t / 128) * NK + g / 16) * 512 + (t % 32) * 16 + (t % 128 / 32) * 4 + (g >> 2) % 4] =
+          in ? scale : 127;
+  }
+}
+
+// Weights to blocks of 128 rows x 128 elements and their scales to tiled ones; rows
+// behind N and elements behind K are zeros of scale 1.
+__global__ void __launch_bounds__(256) k_linear_prepare(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, LinearLayout L,
+                                                        uint8_t* __restrict__ dst) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x, i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int row16 = L.row_bytes / 16;                               // 16-byte pieces of a block's row
+  const int src16 = (L.e2m1 ? L.K / 2 : L.K) / 16;                  // of a weight's row
+  const int64_t blocks = static_cast<int64_t>(L.RB) * L.NK, pieces = blocks * 128 * row16;
+  for (int64_t i = i0; i < pieces; i += stride) {
+    const int64_t b = i / (128 * row16);
+    const int in = static_cast<int>(i - b * (128 * row16)), r = in / row16, c = in - r * row16;
+    const int rb = static_cast<int>(b / L.NK), kc = static_cast<int>(b - static_cast<int64_t>(rb) * L.NK);
+    const int64_t n = static_cast<int64_t>(rb) * 128 + r;
+    const int k = kc * row16 + c;
+    reinterpret_cast<uint4*>(dst)[i] = n < L.N && k < src16 ? __ldg(reinterpret_cast<const uint4*>(codes) + n * src16 + k) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  for (int64_t i = i0; i < blocks * 512; i += stride) {
+    const int64_t b = i / 512;
+    const int in = static_cast<int>(i - b * 512);
+    const int rb = static_cast<int>(b / L.NK), kc = static_cast<int>(b - static_cast<int64_t>(rb) * L.NK);
+    const int64_t n = static_cast<int64_t>(rb) * 128 + (in / 4 % 4) * 32 + in / 16;
+    const int k = kc * 4 + in % 4;
+    dst[L.scales_offset + i] = n < L.N && k < L.K / 32 ? scales[n * (L.K / 32) + k] : 127;
+  }
+}
+
+// ------------------------------------------------------------------ host side
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess) {
+      f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+      fn.store(f, std::memory_order_release);
+    }
+  }
+  return f;
+}
+
+constexpr uint32_t kSmem = 227 * 1024;
+
+struct Plan {
+  bool pair, a4;
+  int ctas;  // of the launch
+  uint32_t smem;
+};
+
+// Shared and tensor memory of a form; false where it does not fit.
+bool lay_out(Params& p, bool pair, bool a4, uint32_t budget, uint32_t* smem) {
+  const int sb = p.TT == 1 ? (p.bn + 127) / 128 : p.bn % 128 ? p.bn / 128 + 1 : p.bn / 128;  // token blocks that a tile touches
+  p.brows = pair ? p.bn / 2 : p.bn;
+  p.a_slot = a4 ? 8192u : 16384u;
+  p.b_slot = (static_cast<uint32_t>(p.brows) * (a4 ? 64u : 128u) + 1023u) & ~1023u;
+  p.sb_slot = static_cast<uint32_t>(sb) * 512u;
+  p.sfc = (4u + 4u * sb + 3u) & ~3u;
+  p.acc_cols = static_cast<uint32_t>(p.bn + 31) & ~31u;
+  p.acc_bufs = p.splits == 1 && 2 * p.acc_cols + 4 * p.sfc <= 512 ? 2 : 1;
+  p.sf_col0 = p.acc_bufs * p.acc_cols;
+  const uint32_t cols = p.sf_col0 + 4 * p.sfc;
+  if (cols > 512) return false;
+  for (p.tmem_cols = 32; p.tmem_cols < cols;) p.tmem_cols *= 2;
+  const uint32_t chunk = p.a_slot + p.b_slot + 512u + p.sb_slot;
+  const uint32_t fixed = 1024u + static_cast<uint32_t>((sizeof(Bars) + 127) & ~size_t(127));
+  p.stages = std::min<int>(kMaxStages, static_cast<int>((budget - fixed) / (chunk * p.kps)));
+  if (p.stages < 2) return false;
+  const uint32_t n = static_cast<uint32_t>(p.stages * p.kps);
+  p.off_a = 0;
+  p.off_b = n * p.a_slot;
+  p.off_sa = p.off_b + n * p.b_slot;
+  p.off_sb = p.off_sa + n * 512u;
+  p.off_bar = p.off_sb + n * p.sb_slot;
+  *smem = p.off_bar + fixed;
+  p.slice = (p.bn + p.splits - 1) / p.splits;
+  // the parts of a split tile lie where the stages were
+  return p.splits == 1 || static_cast<uint32_t>(p.splits * p.slice) * 512u <= p.off_bar;
+}
+
+}  // namespace
+
+LinearLayout linear_layout(int N, int K, int fmt) {
+  LinearLayout L{};
+  L.N = N;
+  L.K = K;
+  L.e2m1 = fmt == MX_E2M1;
+  L.RB = (N + 127) / 128;
+  L.NK = (K + 127) / 128;
+  L.row_bytes = L.e2m1 ? 64 : 128;
+  const size_t blocks = static_cast<size_t>(L.RB) * L.NK;
+  L.scales_offset = blocks * 128 * L.row_bytes;
+  L.total_bytes = L.scales_offset + blocks * 512;
+  return L;
+}
+
+cudaError_t launch_linear_prepare(const uint8_t* codes, const uint8_t* scales, const LinearLayout& L, uint8_t* dst, cudaStream_t s) {
+  const int64_t pieces = static_cast<int64_t>(L.scales_offset) / 16;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((pieces + 255) / 256, 152 * 8));
+  k_linear_prepare<<<grid, 256, 0, s>>>(codes, scales, L, dst);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
+  auto encode = encode_fn();
+  if (!encode) return cudaErrorNotSupported;
+  const LinearLayout L = linear_layout(a.N, a.K, a.w_fmt);
+  Params p{};
+  p.T = a.T;
+  p.N = a.N;
+  p.NK = L.NK;
+  p.RB = L.RB;
+  p.TB = (a.T + 127) / 128;
+  p.a_fmt = a.w_fmt == MX_E4M3 ? kFmtE4M3 : kFmtE2M1;
+  p.b_fmt = kFmtE4M3;
+  p.out_f32 = a.out_f32;
+  p.a_tx = a.w_fmt == MX_E4M3 ? 16384u : 8192u;
+  p.w_scales = a.w_prep + L.scales_offset;
+  p.t_scales = a.t_scales;
+  p.bias = a.bias;
+  p.out = a.out;
+  p.status = a.status;
+  p.wait_limit_ns = a.wait_limit_ns;
+  const bool a4 = a.act_fmt == MX_E2M1;
+
+  bool pair = false;
+  uint32_t smem = 0, ctas = 0;
+  p.splits = 1;
+  p.kps = 1;
+  if (a.T <= 256) {
+    p.bn = (a.T + 15) & ~15;
+    p.TT = 1;
+    // K is shared by as many CTAs as fill the SMs, of four chunks each at least
+    while (p.splits < 8 && p.RB * (p.splits + 1) <= 152 && p.NK / (p.splits + 1) >= 4) ++p.splits;
+    p.units = p.RB;
+    if (!lay_out(p, false, a4, kSmem, &smem)) return cudaErrorInvalidConfiguration;
+    ctas = p.splits > 1 ? p.units * p.splits : std::min(p.units, 152);
+  } else {
+    pair = true;
+    p.bn = 192;
+    p.TT = (a.T + p.bn - 1) / p.bn;
+    p.units = p.TT * ((p.RB + 1) / 2);
+    p.kps = a4 ? 2 : 1;
+    if (!lay_out(p, true, a4, kSmem, &smem)) return cudaErrorInvalidConfiguration;
+    ctas = 2 * std::min(p.units, 76);
+  }
+
+  CUtensorMap tm_a, tm_b, tm_sa{}, tm_sb{};
+  const bool bytes = a.w_fmt == MX_E4M3 || a4;
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  {
+    const cuuint64_t inner = a4 ? 64 : 128, row = static_cast<cuuint64_t>(L.row_bytes);
+    const cuuint64_t dims[4] = {inner, 128, static_cast<cuuint64_t>(L.NK), static_cast<cuuint64_t>(L.RB)};
+    const cuuint64_t strides[3] = {row, row * 128, row * 128 * L.NK};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(inner), 128, static_cast<cuuint32_t>(p.kps), 1};
+    if (encode(&tm_a, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 4, const_cast<uint8_t*>(a.w_prep), dims, strides,
+               box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, a4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  {
+    const cuuint64_t row = static_cast<cuuint64_t>(a4 ? a.K / 2 : a.K);
+    const cuuint64_t dims[2] = {row, static_cast<cuuint64_t>(a.T)};
+    const cuuint64_t strides[1] = {row};
+    const cuuint32_t box[2] = {a4 ? 64u : 128u, static_cast<cuuint32_t>(p.brows)};
+    if (encode(&tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.t_codes), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               a4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  if (pair) {
+    // scales as [block of 128 rows][chunk][128 words]
+    for (int i = 0; i < 2; ++i) {
+      const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(L.NK), static_cast<cuuint64_t>(i ? p.TB : L.RB)};
+      const cuuint64_t strides[2] = {512, 512 * static_cast<cuuint64_t>(L.NK)};
+      const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(p.kps), 1};
+      if (encode(i ? &tm_sb : &tm_sa, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(i ? p.t_scales : p.w_scales), dims, strides, box, es,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    }
+  }
+
+  {
+    const int64_t groups = a.x ? static_cast<int64_t>(a.T) * L.NK * 16 : static_cast<int64_t>(a.T) * L.NK * 4;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((groups + 255) / 256, 152 * 8));
+    const uint4* x = static_cast<const uint4*>(a.x);
+    uint8_t* codes = const_cast<uint8_t*>(a.t_codes);
+    if (a4) k_linear_tokens<true><<<grid, 256, 0, s>>>(x, a.scales, a.T, a.K, L.NK, codes, a.t_scales);
+    else k_linear_tokens<false><<<grid, 256, 0, s>>>(x, a.scales, a.T, a.K, L.NK, codes, a.t_scales);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  void (*kernel)(Params, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap) =
+      pair ? (a4 ? k_linear<true, true> : k_linear<true, false>) : (a4 ? k_linear<false, true> : k_linear<false, false>);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = pair ? 2 : p.splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p, tm_a, tm_b, tm_sa, tm_sb);
+}
+
+}  // namespace mxk

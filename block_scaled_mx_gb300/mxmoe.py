@@ -85,6 +85,10 @@ SIGNATURES = {
     "moe_forward_launches_ex": (_I, [_I, _I, _I, _I, _I, _I, _P]),
     "moe_forward_launches": (_I, [_I, _I, _I, _I, _I, _I]),
     "mx_add_rmsnorm": (_I, [_P, _I, _P, _I, _P, _I, _I, _I, _F, _P, _P, _I, _P, _P, _P]),
+    "mx_linear_prepared_bytes": (_SZ, [_I, _I, _I]),
+    "mx_linear_prepare": (_I, [_P, _P, _I, _I, _I, _P, _SZ, _P]),
+    "mx_linear_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "mx_linear": (_I, [_P, _P, _P, _I, _P, _I, _P, _I, _I, _I, _P, _I, _P, _SZ, _P]),
     "mx_sandwich_rmsnorm": (_I, [_P, _I, _P, _I, _P, _I, _I, _I, _P, _I, _F, _F, _P, _I, _I, _I, _F, _P, _P, _I, _P, _P, _P]),
     "mx_rope_table": (_I, [_I, _D, _I, _D, _D, _D, _I, _P, _P]),
     "mx_rope_kv_append": (_I, [_P, _P, _I64, _I, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I, _I, _F, _P, _P, _P, _I, _I, _I, _P, _SZ,
@@ -357,6 +361,37 @@ def mx_add_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, cod
                               _dense(scales, torch.uint8, (T, H // 32), "scales"), _stream(stream))
     if st:
         raise MxError(st, "mx_add_rmsnorm")
+
+
+class LinearWeights:
+    """An MX weight [N, K] ("e4m3" codes [N, K] or "e2m1" [N, K/2], scales [N, K/32], uint8)
+    laid out for mx_linear."""
+
+    def __init__(self, codes, scales, fmt, stream=None):
+        self.fmt = _fmt(fmt)
+        N, row = codes.shape
+        self.N, self.K = N, row * 2 if self.fmt == MX_E2M1 else row
+        cp, sp = _dense(codes, torch.uint8, (N, row), "codes"), _dense(scales, torch.uint8, (N, self.K // 32), "scales")
+        need = lib().mx_linear_prepared_bytes(N, self.K, self.fmt)
+        self.data = torch.empty(need, dtype=torch.uint8, device=codes.device)
+        _check(lib().mx_linear_prepare(cp, sp, N, self.K, self.fmt, self.data.data_ptr(), need, _stream(stream)), "mx_linear_prepare")
+
+
+def mx_linear_workspace_size(T, N, K, act_fmt="e4m3") -> int:
+    return lib().mx_linear_workspace_size(T, N, K, _fmt(act_fmt))
+
+
+def mx_linear(w, out, ws, x=None, codes=None, scales=None, act_fmt="e4m3", bias=None, stream=None):
+    """out [T, N] (bf16 or fp32) = A . W^T + bias (fp32 [N]) for laid-out weights ``w`` and A
+    either x (bf16 [T, K], quantised to ``act_fmt`` here) or codes and scales."""
+    f, T = _fmt(act_fmt), out.shape[0]
+    st = lib().mx_linear(_dense(x, torch.bfloat16, (T, w.K), "x"),
+                         _dense(codes, torch.uint8, (T, w.K // 2 if f == MX_E2M1 else w.K), "codes"),
+                         _dense(scales, torch.uint8, (T, w.K // 32), "scales"), f, w.data.data_ptr(), w.fmt,
+                         _dense(bias, torch.float32, (w.N,), "bias"), T, w.N, w.K, _dense(out, out.dtype, (T, w.N), "out"), _type(out),
+                         _ptr(ws), ws.nbytes, _stream(stream))
+    if st:
+        raise MxError(st, "mx_linear")
 
 
 def mx_sandwich_rmsnorm(x, post_weight, eps, residual, residual_out, gate=None, gate_act="none", block_scale=1.0,

@@ -361,6 +361,36 @@ MX_API int mx_add_rmsnorm(const void* x, int x_type, const void* residual, int r
                           int weight_type, int T, int H, float eps, void* residual_out, void* y, int fmt,
                           uint8_t* codes, uint8_t* scales, mx_stream_t stream);
 
+/* Bytes of a weight [N, K] laid out for mx_linear (0 for sizes that it rejects). */
+MX_API size_t mx_linear_prepared_bytes(int N, int K, int fmt);
+
+/* Load-time layout of an MX weight for mx_linear, once for each weight.
+ *   codes [N, K] (MX_E4M3) or [N, K/2] bytes (MX_E2M1), scales [N, K/32];
+ *   dst: mx_linear_prepared_bytes bytes, 256-byte aligned.
+ * Errors: MX_ERR_INVALID_ARG (null, sizes, format), MX_ERR_UNSUPPORTED (K % 32, K > 2^20,
+ * N > 2^22), MX_ERR_ALIGNMENT (codes 16 bytes, dst 256), MX_ERR_WORKSPACE. */
+MX_API int mx_linear_prepare(const uint8_t* codes, const uint8_t* scales, int N, int K, int fmt, void* dst,
+                             size_t dst_bytes, mx_stream_t stream);
+
+/* Bytes of workspace mx_linear needs for at most T tokens (0 for sizes that it rejects). */
+MX_API size_t mx_linear_workspace_size(int T, int N, int K, int act_fmt);
+
+/* A dense projection in MX:
+ *   out[t, n] = bias[n] + sum_k A[t, k] * W[n, k]
+ * with W the weight laid out by mx_linear_prepare and A the activations in act_fmt
+ * (MX_E4M3, or with MX_E2M1 weights MX_E2M1): either x_bf16 [T, K], quantised within the
+ * call as mx_quantize_act_ex does, or codes [T, K] (MX_E2M1: [T, K/2]) with scales
+ * [T, K/32], as the norms and quantisers give them.  Products are exact, sums fp32, out
+ * [T, N] (bf16 or fp32 by out_type) is rounded once.  bias [N] fp32 or NULL.
+ * Deterministic.  ws: mx_linear_workspace_size bytes, its first word the status word.
+ * Errors: MX_ERR_INVALID_ARG (null, sizes, an unknown format or type, both or neither of
+ * x_bf16 and codes), MX_ERR_UNSUPPORTED (K % 32, K > 2^20, N or T > 2^22, MX_E2M1
+ * activations with MX_E4M3 weights), MX_ERR_ALIGNMENT (x_bf16, codes, out 16 bytes,
+ * w_prep, ws 256), MX_ERR_WORKSPACE, MX_ERR_CUDA. */
+MX_API int mx_linear(const void* x_bf16, const uint8_t* codes, const uint8_t* scales, int act_fmt, const void* w_prep,
+                     int w_fmt, const float* bias, int T, int N, int K, void* out, int out_type, void* ws,
+                     size_t ws_bytes, mx_stream_t stream);
+
 /* ---- gates of mx_sandwich_rmsnorm ---- */
 #define MX_GATE_NONE 0
 #define MX_GATE_CHANNEL 1 /* gate [H] */

@@ -23,6 +23,34 @@ fake = P(4096)   # never dereferenced
 odd = P(4098)
 
 
+# ------------------------------------------------------------------ projections
+def test_linear_refusals(L):
+    size = L.mx_linear_workspace_size(4, 100, 256, 0)
+    assert size > 256 + 4 * 256 and L.mx_linear_workspace_size(0, 100, 256, 0) == 256
+
+    def call(x=fake, c=None, sc=None, act=0, w=fake, wf=0, bias=None, T=4, N=100, K=256, out=fake, ot=0, ws=fake, wb=size):
+        return L.mx_linear(x, c, sc, act, w, wf, bias, T, N, K, out, ot, ws, wb, None)
+
+    assert call(T=0) == 0
+    for bad in (dict(x=None), dict(c=fake, sc=fake), dict(x=None, c=fake), dict(x=None, sc=fake), dict(sc=fake), dict(w=None), dict(out=None), dict(ws=None),
+                dict(T=-1), dict(N=0), dict(K=0), dict(act=2), dict(wf=-1), dict(ot=3)):
+        assert call(**bad) == 1, bad
+    for bad in (dict(K=48), dict(K=2 ** 20 + 32), dict(N=2 ** 22 + 1), dict(T=2 ** 22 + 1), dict(act=1, wf=0)):
+        assert call(**bad) == 2, bad
+    for bad in (dict(x=P(4104)), dict(x=None, c=P(4104), sc=fake), dict(w=P(4112)), dict(bias=odd), dict(out=P(4104)), dict(ws=P(4112))):
+        assert call(**bad) == 3, bad
+    assert call(wb=size - 1) == 4
+    need = L.mx_linear_prepared_bytes(100, 96, 1)
+    assert need == 128 * 64 + 512 and L.mx_linear_prepared_bytes(100, 100, 1) == 0 and L.mx_linear_prepared_bytes(129, 160, 0) == 4 * (16384 + 512)
+
+    def lay(c=fake, sc=fake, N=100, K=96, f=1, d=fake, db=need):
+        return L.mx_linear_prepare(c, sc, N, K, f, d, db, None)
+
+    for bad, want in ((dict(c=None), 1), (dict(sc=None), 1), (dict(d=None), 1), (dict(N=0), 1), (dict(f=2), 1), (dict(K=100), 2), (dict(c=P(4104)), 3),
+                      (dict(d=P(4112)), 3), (dict(db=need - 1), 4)):
+        assert lay(**bad) == want, bad
+
+
 # ------------------------------------------------------------------ sandwich norm
 def test_sandwich_refusals(L):
     def call(x=fake, xt=0, pw=fake, pt=0, gate=None, gt=0, kind=0, act=0, res=fake, rt=0, rs=1.0, bs=1.0, w=fake, wt=0, T=4, H=64,
