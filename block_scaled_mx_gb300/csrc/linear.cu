@@ -41,6 +41,7 @@ namespace {
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kMaxStages = 12;
+constexpr int kBand = 8;
 
 struct Params {
   int T, N, NK, RB, TT;
@@ -106,7 +107,7 @@ __device__ __forceinline__ void store_out(const Params& p, int64_t at, float v) 
 // A4: both operands packed E2M1 (kind::mxf4), else kind::mxf8f6f4 (E2M1 weights are
 // widened to bytes by the TMA).
 template <bool PAIR, bool A4>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
     k_linear(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
              const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb) {
   extern __shared__ uint8_t smem_raw[];
@@ -120,6 +121,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int k0 = PAIR ? 0 : static_cast<int>(static_cast<int64_t>(p.NK) * rank / p.splits);
   const int k1 = PAIR ? p.NK : static_cast<int>(static_cast<int64_t>(p.NK) * (rank + 1) / p.splits);
   const int rbs = PAIR ? (p.RB + 1) / 2 : p.RB;  // tiles along N
+  // Tile of a unit: bands of kBand tiles along N, each through all tokens, so that the
+  // CTAs at work share both operands' rows.
+  auto tile_of = [&](int unit, int& tt, int& rb) {
+    const int band = unit / (kBand * p.TT), in = unit - band * kBand * p.TT, wide = min(kBand, rbs - band * kBand);
+    tt = in / wide;
+    rb = band * kBand + in - tt * wide;
+    if (PAIR) rb = 2 * rb + static_cast<int>(rank);
+  };
   constexpr int kEl = A4 ? 64 : 128;             // bytes of a token's chunk
 
   if (tid == 0) {
@@ -153,59 +162,70 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ================================================================ TMA
-    if (lane == 0) {
+    if (elect_one()) {
+      // A single thread feeds the MMAs, so what it does for a stage is MMA time: all that
+      // does not change from stage to stage is worked out once a tile.
       uint32_t fills = 0, s = 0, ph = 0;
       bool ok = true, ready = false;
+      const uint32_t full0 = smem_u32(bars->full), a0 = smem_u32(base + p.off_a), sa0 = smem_u32(base + p.off_sa);
+      const uint32_t b0 = smem_u32(base + p.off_b), sb0 = smem_u32(base + p.off_sb);
+      const uint32_t a_stage = kps * p.a_slot, b_slot = p.b_slot, sb_chunks = kps * 512u, sb_stage = kps * p.sb_slot;
+      const uint32_t b_bytes = static_cast<uint32_t>(p.brows * kEl);
+      const uint32_t bar0 = PAIR ? mapa_shared(full0, 0u) : full0;  // in a pair all copies land on rank 0's barriers
+      const int most = static_cast<int>(p.sb_slot / 512), NK = p.NK, TB = p.TB, bn = p.bn, units = p.units;
+      const uint8_t* const w_scales = p.w_scales;
+      const uint8_t* const t_scales = p.t_scales;
+      int rb = 0, n0 = 0, row0 = 0, tb0 = 0, nb = 0;  // of the tile
+      const uint8_t *sa_src = nullptr, *sb_src = nullptr;
+      auto tile = [&](int unit) {
+        int tt;
+        tile_of(unit, tt, rb);
+        n0 = tt * bn;
+        row0 = PAIR ? n0 + static_cast<int>(rank) * p.brows : n0;
+        tb0 = n0 / 128;
+        nb = min((n0 % 128 + bn + 127) / 128, TB - tb0);
+        sa_src = w_scales + static_cast<size_t>(rb) * NK * 512;
+        sb_src = t_scales + static_cast<size_t>(tb0) * NK * 512;
+      };
       // weights of one stage; its barrier is armed for everything that lands there
-      auto weights = [&](uint32_t slot, int unit, int kc) {
-        const int tt = unit / rbs, rb = PAIR ? 2 * (unit - tt * rbs) + static_cast<int>(rank) : unit - tt * rbs;
-        const int n0 = tt * p.bn, nk = min(kps, k1 - kc);
-        const int tb0 = n0 / 128, nb = min((n0 % 128 + p.bn + 127) / 128, p.TB - tb0);
-        const uint32_t full = smem_u32(&bars->full[slot]);
-        const uint32_t sa = smem_u32(base + p.off_sa) + slot * kps * 512u;
-        const uint32_t a = smem_u32(base + p.off_a) + slot * kps * p.a_slot;
-        const uint32_t b_bytes = static_cast<uint32_t>(nk * p.brows * kEl);
+      auto weights = [&](uint32_t slot, int kc) {
+        const int nk = min(kps, k1 - kc);
+        const uint32_t bar = bar0 + slot * 8u, a = a0 + slot * a_stage, sa = sa0 + slot * sb_chunks;
         if (PAIR) {
-          // both CTAs' copies land on rank 0's barrier, whose thread issues the MMAs
-          const uint32_t bar = mapa_shared(full, 0u);
-          mbar_arrive_expect_tx_cluster(bar, kps * p.a_tx + b_bytes + static_cast<uint32_t>(kps) * 512u * static_cast<uint32_t>(1 + p.sb_slot / 512));
+          mbar_arrive_expect_tx_cluster_relaxed(bar, kps * (p.a_tx + 512u * static_cast<uint32_t>(1 + most)) + nk * b_bytes);
           tma_load_4d_pair(a, &tm_a, 0, 0, kc, rb, bar);
           tma_load_3d_pair(sa, &tm_sa, 0, kc, rb, bar);
         } else {
-          mbar_arrive_expect_tx(full, kps * p.a_tx + b_bytes + static_cast<uint32_t>(nk) * 512u * static_cast<uint32_t>(1 + nb));
-          tma_load_4d(a, &tm_a, 0, 0, kc, rb, full);
-          bulk_load(sa, p.w_scales + (static_cast<size_t>(rb) * p.NK + kc) * 512, static_cast<uint32_t>(nk) * 512u, full);
+          mbar_arrive_expect_tx(bar, kps * p.a_tx + nk * (b_bytes + 512u * static_cast<uint32_t>(1 + nb)));
+          tma_load_4d(a, &tm_a, 0, 0, kc, rb, bar);
+          bulk_load(sa, sa_src + kc * 512, static_cast<uint32_t>(nk) * 512u, bar);
         }
       };
-      auto tokens = [&](uint32_t slot, int unit, int kc) {
-        const int tt = unit / rbs;
-        const int n0 = tt * p.bn, nk = min(kps, k1 - kc);
-        const int tb0 = n0 / 128, nb = min((n0 % 128 + p.bn + 127) / 128, p.TB - tb0);
-        const uint32_t full = smem_u32(&bars->full[slot]);
-        const uint32_t b = smem_u32(base + p.off_b) + slot * kps * p.b_slot;
-        const uint32_t sb = smem_u32(base + p.off_sb) + slot * kps * p.sb_slot;
+      auto tokens = [&](uint32_t slot, int kc) {
+        const int nk = min(kps, k1 - kc);
+        const uint32_t bar = bar0 + slot * 8u;
+        uint32_t b = b0 + slot * kps * b_slot, sb = sb0 + slot * sb_stage;
         if (PAIR) {
-          const uint32_t bar = mapa_shared(full, 0u);
-          for (int u = 0; u < nk; ++u)
-            tma_load_2d_pair(b + u * p.b_slot, &tm_b, (kc + u) * kEl, n0 + static_cast<int>(rank) * p.brows, bar);
-          for (int i = 0; i < static_cast<int>(p.sb_slot / 512); ++i) tma_load_3d_pair(sb + i * kps * 512u, &tm_sb, 0, kc, tb0 + i, bar);
+          for (int u = 0; u < nk; ++u, b += b_slot) tma_load_2d_pair(b, &tm_b, (kc + u) * kEl, row0, bar);
+          for (int i = 0; i < most; ++i, sb += sb_chunks) tma_load_3d_pair(sb, &tm_sb, 0, kc, tb0 + i, bar);
         } else {
-          for (int u = 0; u < nk; ++u) tma_load_2d(b + u * p.b_slot, &tm_b, (kc + u) * kEl, n0, full);
-          for (int i = 0; i < nb; ++i)
-            bulk_load(sb + i * kps * 512u, p.t_scales + (static_cast<size_t>(tb0 + i) * p.NK + kc) * 512, static_cast<uint32_t>(nk) * 512u, full);
+          for (int u = 0; u < nk; ++u, b += b_slot) tma_load_2d(b, &tm_b, (kc + u) * kEl, row0, bar);
+          const uint8_t* src = sb_src + kc * 512;
+          for (int i = 0; i < nb; ++i, sb += sb_chunks, src += static_cast<size_t>(NK) * 512) bulk_load(sb, src, static_cast<uint32_t>(nk) * 512u, bar);
         }
       };
       prefetch_tensormap(&tm_a);
       prefetch_tensormap(&tm_b);
-      for (int unit = unit0; unit < p.units && ok; unit += unit_step) {
+      for (int unit = unit0; unit < units && ok; unit += unit_step) {
+        tile(unit);
         int kc = k0;
         if (!ready) {
           // the first launch's results are awaited behind the weights of all stages
           int n = 0;
-          for (int k = k0; n < S && k < k1; ++n, k += kps) weights(n, unit, k);
+          for (int k = k0; n < S && k < k1; ++n, k += kps) weights(n, k);
           asm volatile("griddepcontrol.wait;" ::: "memory");
           ready = true;
-          for (int i = 0; i < n; ++i, kc += kps) tokens(i, unit, kc);
+          for (int i = 0; i < n; ++i, kc += kps) tokens(i, kc);
           fills = n;
           s = n % S;
           ph = n / S;
@@ -215,8 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          weights(s, unit, kc);
-          tokens(s, unit, kc);
+          weights(s, kc);
+          tokens(s, kc);
           ++fills;
           if (++s == static_cast<uint32_t>(S)) {
             s = 0;
@@ -239,16 +259,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if ((!PAIR || rank == 0) && elect_one()) {
       const uint32_t a0 = desc_lo_sw128(smem_u32(base + p.off_a)), b0 = desc_lo_sw128(smem_u32(base + p.off_b));
       const uint32_t sa0 = smem_u32(base + p.off_sa), sb0 = smem_u32(base + p.off_sb);
+      const uint32_t a_slot = p.a_slot >> 4, b_slot = p.b_slot >> 4, sb_stage = kps * p.sb_slot, sb_chunks = kps * 512u;
+      const uint32_t sf0 = tbase + p.sf_col0, sf_end = sf0 + 4u * p.sfc, sfc = p.sfc;
+      const int units = p.units, bn = p.bn, T = p.T;
       constexpr uint32_t kM = PAIR ? 256u : 128u;
-      uint32_t s = 0, ph = 0, ab = 0, aph = 0, slot = 0;
+      uint32_t s = 0, ph = 0, ab = 0, aph = 0, sf = sf0;
       bool ok = true;
-      for (int unit = unit0; unit < p.units && ok; unit += unit_step) {
-        const int tt = unit / rbs, n0 = tt * p.bn;
-        const int nsb = (n0 % 128 + p.bn + 127) / 128;
-        const uint32_t sb_col = static_cast<uint32_t>(n0 % 128) / 32;
-        uint32_t n_mma = static_cast<uint32_t>((min(p.bn, p.T - n0) + 15) & ~15);
+      for (int unit = unit0; unit < units && ok; unit += unit_step) {
+        int tt, rb;
+        tile_of(unit, tt, rb);
+        const int n0 = tt * bn;
+        const int nsb = (n0 % 128 + bn + 127) / 128;
+        const uint32_t sb_col = 4u + static_cast<uint32_t>(n0 % 128) / 32;
+        uint32_t n_mma = static_cast<uint32_t>((min(bn, T - n0) + 15) & ~15);
         // a pair's CTAs hold the two halves of a whole tile
-        if (PAIR) n_mma = static_cast<uint32_t>(p.bn);
+        if (PAIR) n_mma = static_cast<uint32_t>(bn);
         uint32_t idesc[A4 ? 2 : 4];
 #pragma unroll
         for (int i = 0; i < (A4 ? 2 : 4); ++i)
@@ -264,29 +289,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const int nk = min(kps, k1 - kc);
-          for (int u = 0; u < nk; ++u) {
-            const uint32_t c = s * kps + u;
-            const uint32_t sf = tbase + p.sf_col0 + slot * p.sfc;
-            slot = slot + 1 == 4 ? 0 : slot + 1;  // four sets of columns in turn
-            if (PAIR) tmem_copy_scales_pair(sf, sa0 + c * 512u);
-            else tmem_copy_scales(sf, sa0 + c * 512u);
+          uint32_t a = a0 + s * kps * a_slot, b = b0 + s * kps * b_slot, sa = sa0 + s * sb_chunks, sb = sb0 + s * sb_stage;
+          for (int u = 0; u < nk; ++u, a += a_slot, b += b_slot, sa += 512u, sb += 512u) {
+            if (PAIR) tmem_copy_scales_pair(sf, sa);
+            else tmem_copy_scales(sf, sa);
             for (int i = 0; i < nsb; ++i) {
-              const uint32_t at = sb0 + s * kps * p.sb_slot + (i * kps + u) * 512u;
-              if (PAIR) tmem_copy_scales_pair(sf + 4u + 4u * i, at);
-              else tmem_copy_scales(sf + 4u + 4u * i, at);
+              if (PAIR) tmem_copy_scales_pair(sf + 4u + 4u * i, sb + i * sb_chunks);
+              else tmem_copy_scales(sf + 4u + 4u * i, sb + i * sb_chunks);
             }
-            const uint32_t a = a0 + c * (p.a_slot >> 4), b = b0 + c * (p.b_slot >> 4);
 #pragma unroll
             for (int i = 0; i < (A4 ? 2 : 4); ++i) {
               if (A4) {
-                if (PAIR) mma_mxf4_pair_lo(d, a + 2u * i, b + 2u * i, kDescHiSw64, idesc[i], sf, sf + 4u + sb_col, accum);
-                else mma_mxf4_lo(d, a + 2u * i, b + 2u * i, kDescHiSw64, idesc[i], sf, sf + 4u + sb_col, accum);
+                if (PAIR) mma_mxf4_pair_lo(d, a + 2u * i, b + 2u * i, kDescHiSw64, idesc[i], sf, sf + sb_col, accum);
+                else mma_mxf4_lo(d, a + 2u * i, b + 2u * i, kDescHiSw64, idesc[i], sf, sf + sb_col, accum);
               } else {
-                if (PAIR) mma_mxf8f6f4_pair_lo(d, a + 2u * i, b + 2u * i, kDescHiSw128, idesc[i], sf, sf + 4u + sb_col, accum);
-                else mma_mxf8f6f4_lo(d, a + 2u * i, b + 2u * i, kDescHiSw128, idesc[i], sf, sf + 4u + sb_col, accum);
+                if (PAIR) mma_mxf8f6f4_pair_lo(d, a + 2u * i, b + 2u * i, kDescHiSw128, idesc[i], sf, sf + sb_col, accum);
+                else mma_mxf8f6f4_lo(d, a + 2u * i, b + 2u * i, kDescHiSw128, idesc[i], sf, sf + sb_col, accum);
               }
               accum = 1;
             }
+            sf += sfc;  // four sets of columns in turn
+            if (sf == sf_end) sf = sf0;
           }
           if (PAIR) mma_commit_pair(smem_u32(&bars->empty[s]), 3);
           else mma_commit(smem_u32(&bars->empty[s]));
@@ -314,7 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, half = (warp - 2) >> 2;
     uint32_t ab = 0, aph = 0;
     for (int unit = unit0; unit < p.units; unit += unit_step) {
-      const int tt = unit / rbs, rb = PAIR ? 2 * (unit - tt * rbs) + static_cast<int>(rank) : unit - tt * rbs;
+      int tt, rb;
+      tile_of(unit, tt, rb);
       const int n0 = tt * p.bn, cols = min(p.bn, p.T - n0);
       const int n = rb * 128 + 32 * q + lane;
       const float bias = p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;
@@ -366,48 +390,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     // part of them in r's shared memory (the stages', which all CTAs have read by now).
     __syncthreads();
     cluster_sync_all();
-    float* const parts = reinterpret_cast<float*>(base + p.off_a);  // [source][column of the slice][128 rows]
-    const int tt = unit0 / rbs, rb = unit0 - tt * rbs, n0 = tt * p.bn, cols = min(p.bn, p.T - n0);
+    float* const parts = reinterpret_cast<float*>(base + p.off_a);  // [source][128 rows][pitch]
+    const int slice = p.slice, pitch = slice + 4;                   // rows 16 bytes apart modulo 128: no bank conflicts
+    int tt, rb;
+    tile_of(unit0, tt, rb);
+    const int n0 = tt * p.bn, cols = min(p.bn, p.T - n0);
     if (warp >= 2) {
       const int q = warp & 3, half = (warp - 2) >> 2;
       const uint32_t d = tbase + (static_cast<uint32_t>(32 * q) << 16);
+      const uint32_t mine = smem_u32(parts + (static_cast<int>(rank) * 128 + 32 * q + lane) * pitch);
       for (int c0 = 8 * half; c0 < cols; c0 += 16) {
         uint32_t r[8];
         __syncwarp();
         tmem_ld_32x32b_x8(d + c0, r);
+        const int owner = c0 / slice;  // eight columns have one: slice is a multiple of eight
+        const uint32_t at = mapa_shared(mine + static_cast<uint32_t>(c0 - owner * slice) * 4u, static_cast<uint32_t>(owner));
         tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (c0 + c < cols) {
-            const int owner = (c0 + c) / p.slice, col = c0 + c - owner * p.slice;
-            const uint32_t at = smem_u32(parts + (static_cast<int>(rank) * p.slice + col) * 128 + 32 * q + lane);
-            st_shared_cluster_u32(mapa_shared(at, static_cast<uint32_t>(owner)), r[c]);
-          }
-        }
+        st_shared_cluster_v4(at, r[0], r[1], r[2], r[3]);
+        st_shared_cluster_v4(at + 16u, r[4], r[5], r[6], r[7]);
       }
     }
     __syncwarp();
     cluster_sync_all();
-    const int first = static_cast<int>(rank) * p.slice, mine = min(p.slice, cols - first);
+    const int first = static_cast<int>(rank) * slice, left = min(slice, cols - first);
     if (!bars->abort) {
-      for (int i = tid; i < mine * 64; i += kThreads) {
-        const int col = i >> 6, row = (i & 63) * 2, n = rb * 128 + row;
-        float2 v = make_float2(0.0f, 0.0f);
+      for (int i = tid; i < 128 * ((left + 3) / 4); i += kThreads) {
+        const int row = i & 127, c0 = (i >> 7) * 4, n = rb * 128 + row;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int s = 0; s < p.splits; ++s) {
-          const float2 w = *reinterpret_cast<const float2*>(parts + (s * p.slice + col) * 128 + row);
-          v.x += w.x;
-          v.y += w.y;
+          const float4 w = *reinterpret_cast<const float4*>(parts + (s * 128 + row) * pitch + c0);
+          v[0] += w.x;
+          v[1] += w.y;
+          v[2] += w.z;
+          v[3] += w.w;
         }
-        if (p.bias) {
-          if (n < p.N) v.x += __ldg(p.bias + n);
-          if (n + 1 < p.N) v.y += __ldg(p.bias + n + 1);
-        }
-        const int64_t at = static_cast<int64_t>(n0 + first + col) * p.N + n;
-        if (!p.out_f32 && p.N % 2 == 0) {
-          if (n < p.N) *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at) = __floats2bfloat162_rn(v.x, v.y);
-        } else {
-          if (n < p.N) store_out(p, at, v.x);
-          if (n + 1 < p.N) store_out(p, at + 1, v.y);
+        if (n < p.N) {
+          const float bias = p.bias ? __ldg(p.bias + n) : 0.0f;
+          const int64_t at = static_cast<int64_t>(n0 + first + c0) * p.N + n;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c0 + c < left) store_out(p, at + static_cast<int64_t>(c) * p.N, v[c] + bias);
         }
       }
     }
@@ -549,9 +571,9 @@ bool lay_out(Params& p, bool pair, bool a4, uint32_t budget, uint32_t* smem) {
   p.off_sb = p.off_sa + n * 512u;
   p.off_bar = p.off_sb + n * p.sb_slot;
   *smem = p.off_bar + fixed;
-  p.slice = (p.bn + p.splits - 1) / p.splits;
+  p.slice = ((p.bn + p.splits - 1) / p.splits + 7) & ~7;
   // the parts of a split tile lie where the stages were
-  return p.splits == 1 || static_cast<uint32_t>(p.splits * p.slice) * 512u <= p.off_bar;
+  return p.splits == 1 || static_cast<uint32_t>(p.splits * (p.slice + 4)) * 512u <= p.off_bar;
 }
 
 }  // namespace
@@ -609,7 +631,8 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
     // K is shared by as many CTAs as fill the SMs, of four chunks each at least
     while (p.splits < 8 && p.RB * (p.splits + 1) <= 152 && p.NK / (p.splits + 1) >= 4) ++p.splits;
     p.units = p.RB;
-    if (!lay_out(p, false, a4, kSmem, &smem)) return cudaErrorInvalidConfiguration;
+    if (!(p.splits > 1 && p.bn <= 64 && lay_out(p, false, a4, kSmem / 2 - 1024, &smem)) && !lay_out(p, false, a4, kSmem, &smem))
+      return cudaErrorInvalidConfiguration;
     ctas = p.splits > 1 ? p.units * p.splits : std::min(p.units, 152);
   } else {
     pair = true;

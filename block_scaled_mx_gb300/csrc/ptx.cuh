@@ -340,6 +340,13 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_a
                "r"(bytes)
                : "memory");
 }
+// The same without a release, for a thread that has written nothing the barrier's waiters
+// read (TMA producers): a release at cluster scope costs some 1000 cycles.
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster_relaxed(uint32_t cluster_addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
+               "r"(bytes)
+               : "memory");
+}
 // Polls of a barrier that receives arrivals from the peer CTA (cluster-scope acquire).
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
