@@ -23,7 +23,8 @@ int check_linear(int T, int N, int K, int act_fmt, int w_fmt) {
 }
 
 // Workspace of mx_linear: the status word, the tokens' tiled scales, their codes.
-size_t linear_scales_bytes(int T, int K) { return static_cast<size_t>((T + 127) / 128) * ((K + 127) / 128) * 512; }
+// (tokens' scales have as many blocks along K as the weights', an even number with E2M1)
+size_t linear_scales_bytes(int T, int K) { return static_cast<size_t>((T + 127) / 128) * ((K + 255) / 256 * 2) * 512; }
 
 }  // namespace
 

@@ -163,10 +163,11 @@ struct RopeArgs {
 cudaError_t launch_rope_kv_append(const RopeArgs& r, cudaStream_t s);
 
 // ---- linear.cu
-// Laid-out weights: blocks of 128 rows x 128 elements, block (rb, kc) at rb * NK + kc,
-// then their scales in 512-byte blocks in the order of tensor memory.
+// Laid-out weights: blocks of 128 rows x 128 bytes, block (rb, kb) at rb * NB + kb, then
+// their scales in 512-byte blocks (128 rows x 128 elements) in the order of tensor memory,
+// block (rb, k) at rb * NK + k.
 struct LinearLayout {
-  int N, K, e2m1, RB, NK, row_bytes;  // bytes of a block's row
+  int N, K, e2m1, RB, NB, NK;
   size_t scales_offset, total_bytes;
 };
 LinearLayout linear_layout(int N, int K, int fmt);

@@ -44,18 +44,15 @@ constexpr int kMaxStages = 12;
 constexpr int kBand = 8;
 
 struct Params {
-  int T, N, NK, RB, TT;
-  int bn, brows;       // tokens of a tile, of this CTA's loads (half in a pair)
-  int splits, units;   // CTAs that share a tile's K; tiles (of pairs in a pair)
-  int kps, stages, acc_bufs;
-  int TB;              // blocks of 128 tokens
-  int a_fmt, b_fmt, out_f32, slice;
-  uint32_t a_tx;       // bytes that a weight block's copy counts for
-  uint32_t a_slot, b_slot, sb_slot;  // shared memory of a chunk
-  uint32_t off_a, off_b, off_sa, off_sb, off_bar;
-  uint32_t tmem_cols, acc_cols, sf_col0, sfc;
-  const uint8_t* w_scales;
-  const uint8_t* t_scales;
+  int T, N, RB, TT, KS;  // KS: stages of all of K (128 bytes of every row each)
+  int bn, brows;         // tokens of a tile, of this CTA's loads (half in a pair)
+  int splits, units;     // CTAs that share a tile's K; tiles (of pairs in a pair)
+  int stages, acc_bufs;
+  int a_fmt, out_f32, slice, half_blocks;  // half_blocks: a stage is half of a weight block (E2M1 widened to bytes)
+  uint32_t a_tx;         // bytes that a stage's weights count for
+  uint32_t b_slot;       // shared memory of a stage's tokens
+  uint32_t off_b, off_sa, off_sb, off_bar;
+  uint32_t tmem_cols, acc_cols, sf_col0;
   const float* bias;
   void* out;
   int* status;
@@ -104,9 +101,10 @@ __device__ __forceinline__ void store_out(const Params& p, int64_t at, float v) 
   else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
 }
 
-// A4: both operands packed E2M1 (kind::mxf4), else kind::mxf8f6f4 (E2M1 weights are
-// widened to bytes by the TMA).
-template <bool PAIR, bool A4>
+// A4: both operands packed E2M1 (kind::mxf4, 256 elements a stage), else kind::mxf8f6f4
+// (128 elements; E2M1 weights are widened to bytes by the TMA).  NSB: blocks of 128 tokens
+// that a tile touches.
+template <bool PAIR, bool A4, int NSB>
 __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
     k_linear(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
              const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb) {
@@ -114,12 +112,15 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
   uint8_t* const base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   Bars* const bars = reinterpret_cast<Bars*>(base + p.off_bar);
-  const int S = p.stages, kps = p.kps;
+  constexpr int kSub = A4 ? 2 : 1;                      // scale blocks of a stage along K
+  constexpr uint32_t kSa = kSub * 512u, kSb = NSB * kSub * 512u;
+  constexpr uint32_t kSfCols = 4u + 4u * NSB;           // tensor-memory columns of a scale block's set
+  const int S = p.stages;
   const uint32_t rank = PAIR || p.splits > 1 ? cluster_ctarank() : 0u;
   const int group = PAIR ? 2 : p.splits;
   const int unit0 = blockIdx.x / group, unit_step = gridDim.x / group;
-  const int k0 = PAIR ? 0 : static_cast<int>(static_cast<int64_t>(p.NK) * rank / p.splits);
-  const int k1 = PAIR ? p.NK : static_cast<int>(static_cast<int64_t>(p.NK) * (rank + 1) / p.splits);
+  const int k0 = PAIR ? 0 : static_cast<int>(static_cast<int64_t>(p.KS) * rank / p.splits);
+  const int k1 = PAIR ? p.KS : static_cast<int>(static_cast<int64_t>(p.KS) * (rank + 1) / p.splits);
   const int rbs = PAIR ? (p.RB + 1) / 2 : p.RB;  // tiles along N
   // Tile of a unit: bands of kBand tiles along N, each through all tokens, so that the
   // CTAs at work share both operands' rows.
@@ -129,7 +130,6 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
     rb = band * kBand + in - tt * wide;
     if (PAIR) rb = 2 * rb + static_cast<int>(rank);
   };
-  constexpr int kEl = A4 ? 64 : 128;             // bytes of a token's chunk
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -167,76 +167,64 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
       // does not change from stage to stage is worked out once a tile.
       uint32_t fills = 0, s = 0, ph = 0;
       bool ok = true, ready = false;
-      const uint32_t full0 = smem_u32(bars->full), a0 = smem_u32(base + p.off_a), sa0 = smem_u32(base + p.off_sa);
-      const uint32_t b0 = smem_u32(base + p.off_b), sb0 = smem_u32(base + p.off_sb);
-      const uint32_t a_stage = kps * p.a_slot, b_slot = p.b_slot, sb_chunks = kps * 512u, sb_stage = kps * p.sb_slot;
-      const uint32_t b_bytes = static_cast<uint32_t>(p.brows * kEl);
+      const uint32_t full0 = smem_u32(bars->full), a0 = smem_u32(base);
+      const uint32_t b0 = a0 + p.off_b, sa0 = a0 + p.off_sa, sb0 = a0 + p.off_sb, b_slot = p.b_slot;
       const uint32_t bar0 = PAIR ? mapa_shared(full0, 0u) : full0;  // in a pair all copies land on rank 0's barriers
-      const int most = static_cast<int>(p.sb_slot / 512), NK = p.NK, TB = p.TB, bn = p.bn, units = p.units;
-      const uint8_t* const w_scales = p.w_scales;
-      const uint8_t* const t_scales = p.t_scales;
-      int rb = 0, n0 = 0, row0 = 0, tb0 = 0, nb = 0;  // of the tile
-      const uint8_t *sa_src = nullptr, *sb_src = nullptr;
-      auto tile = [&](int unit) {
-        int tt;
-        tile_of(unit, tt, rb);
-        n0 = tt * bn;
-        row0 = PAIR ? n0 + static_cast<int>(rank) * p.brows : n0;
-        tb0 = n0 / 128;
-        nb = min((n0 % 128 + bn + 127) / 128, TB - tb0);
-        sa_src = w_scales + static_cast<size_t>(rb) * NK * 512;
-        sb_src = t_scales + static_cast<size_t>(tb0) * NK * 512;
-      };
+      const uint32_t bytes = p.a_tx + static_cast<uint32_t>(p.brows) * 128u + kSa + kSb;
+      const int units = p.units;
+      const bool half_blocks = p.half_blocks != 0;
+      int tt, rb = 0, row0 = 0, tb0 = 0;  // of the tile
       // weights of one stage; its barrier is armed for everything that lands there
-      auto weights = [&](uint32_t slot, int kc) {
-        const int nk = min(kps, k1 - kc);
-        const uint32_t bar = bar0 + slot * 8u, a = a0 + slot * a_stage, sa = sa0 + slot * sb_chunks;
+      auto weights = [&](uint32_t slot, int k) {
+        const uint32_t bar = bar0 + slot * 8u, a = a0 + slot * 16384u, sa = sa0 + slot * kSa;
+        const int x = half_blocks ? (k & 1) * 128 : 0, kb = half_blocks ? k >> 1 : k;
         if (PAIR) {
-          mbar_arrive_expect_tx_cluster_relaxed(bar, kps * (p.a_tx + 512u * static_cast<uint32_t>(1 + most)) + nk * b_bytes);
-          tma_load_4d_pair(a, &tm_a, 0, 0, kc, rb, bar);
-          tma_load_3d_pair(sa, &tm_sa, 0, kc, rb, bar);
+          mbar_arrive_expect_tx_cluster_relaxed(bar, bytes);
+          tma_load_4d_pair(a, &tm_a, x, 0, kb, rb, bar);
+          tma_load_3d_pair(sa, &tm_sa, 0, k * kSub, rb, bar);
         } else {
-          mbar_arrive_expect_tx(bar, kps * p.a_tx + nk * (b_bytes + 512u * static_cast<uint32_t>(1 + nb)));
-          tma_load_4d(a, &tm_a, 0, 0, kc, rb, bar);
-          bulk_load(sa, sa_src + kc * 512, static_cast<uint32_t>(nk) * 512u, bar);
+          mbar_arrive_expect_tx(bar, bytes);
+          tma_load_4d(a, &tm_a, x, 0, kb, rb, bar);
+          tma_load_3d(sa, &tm_sa, 0, k * kSub, rb, bar);
         }
       };
-      auto tokens = [&](uint32_t slot, int kc) {
-        const int nk = min(kps, k1 - kc);
-        const uint32_t bar = bar0 + slot * 8u;
-        uint32_t b = b0 + slot * kps * b_slot, sb = sb0 + slot * sb_stage;
+      auto tokens = [&](uint32_t slot, int k) {
+        const uint32_t bar = bar0 + slot * 8u, b = b0 + slot * b_slot, sb = sb0 + slot * kSb;
         if (PAIR) {
-          for (int u = 0; u < nk; ++u, b += b_slot) tma_load_2d_pair(b, &tm_b, (kc + u) * kEl, row0, bar);
-          for (int i = 0; i < most; ++i, sb += sb_chunks) tma_load_3d_pair(sb, &tm_sb, 0, kc, tb0 + i, bar);
+          tma_load_2d_pair(b, &tm_b, k * 128, row0, bar);
+          tma_load_3d_pair(sb, &tm_sb, 0, k * kSub, tb0, bar);
         } else {
-          for (int u = 0; u < nk; ++u, b += b_slot) tma_load_2d(b, &tm_b, (kc + u) * kEl, row0, bar);
-          const uint8_t* src = sb_src + kc * 512;
-          for (int i = 0; i < nb; ++i, sb += sb_chunks, src += static_cast<size_t>(NK) * 512) bulk_load(sb, src, static_cast<uint32_t>(nk) * 512u, bar);
+          tma_load_2d(b, &tm_b, k * 128, row0, bar);
+          tma_load_3d(sb, &tm_sb, 0, k * kSub, tb0, bar);
         }
       };
       prefetch_tensormap(&tm_a);
+      prefetch_tensormap(&tm_sa);
       prefetch_tensormap(&tm_b);
+      prefetch_tensormap(&tm_sb);
       for (int unit = unit0; unit < units && ok; unit += unit_step) {
-        tile(unit);
-        int kc = k0;
+        tile_of(unit, tt, rb);
+        tb0 = tt * p.bn / 128;
+        row0 = tt * p.bn + (PAIR ? static_cast<int>(rank) * p.brows : 0);
+        int k = k0;
         if (!ready) {
           // the first launch's results are awaited behind the weights of all stages
           int n = 0;
-          for (int k = k0; n < S && k < k1; ++n, k += kps) weights(n, k);
+          for (; n < S && k0 + n < k1; ++n) weights(n, k0 + n);
           asm volatile("griddepcontrol.wait;" ::: "memory");
           ready = true;
-          for (int i = 0; i < n; ++i, kc += kps) tokens(i, kc);
+          for (int i = 0; i < n; ++i) tokens(i, k++);
           fills = n;
           s = n % S;
           ph = n / S;
         }
-        for (; kc < k1; kc += kps) {
+        for (; k < k1; ++k) {
           if (!wait(&bars->empty[s], ph ^ 1u)) {
             ok = false;
             break;
           }
-          weights(s, kc);
-          tokens(s, kc);
+          weights(s, k);
+          tokens(s, k);
           ++fills;
           if (++s == static_cast<uint32_t>(S)) {
             s = 0;
@@ -257,65 +245,72 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
   } else if (warp == 1) {
     // ================================================================ MMAs
     if ((!PAIR || rank == 0) && elect_one()) {
-      const uint32_t a0 = desc_lo_sw128(smem_u32(base + p.off_a)), b0 = desc_lo_sw128(smem_u32(base + p.off_b));
-      const uint32_t sa0 = smem_u32(base + p.off_sa), sb0 = smem_u32(base + p.off_sb);
-      const uint32_t a_slot = p.a_slot >> 4, b_slot = p.b_slot >> 4, sb_stage = kps * p.sb_slot, sb_chunks = kps * 512u;
-      const uint32_t sf0 = tbase + p.sf_col0, sf_end = sf0 + 4u * p.sfc, sfc = p.sfc;
+      const uint32_t smem0 = smem_u32(base);
+      const uint32_t a0 = desc_lo_sw128(smem0), b0 = desc_lo_sw128(smem0 + p.off_b), b_step = p.b_slot >> 4;
+      const uint32_t sa0 = scales_desc_lo(smem0 + p.off_sa), sb0 = scales_desc_lo(smem0 + p.off_sb);
+      const uint32_t sf0 = tbase + p.sf_col0, sf_end = sf0 + 4u * kSfCols;  // four sets of scale columns in turn
       const int units = p.units, bn = p.bn, T = p.T;
       constexpr uint32_t kM = PAIR ? 256u : 128u;
       uint32_t s = 0, ph = 0, ab = 0, aph = 0, sf = sf0;
+      uint32_t a = a0, b = b0, sa = sa0, sb = sb0;
       bool ok = true;
       for (int unit = unit0; unit < units && ok; unit += unit_step) {
         int tt, rb;
         tile_of(unit, tt, rb);
         const int n0 = tt * bn;
-        const int nsb = (n0 % 128 + bn + 127) / 128;
         const uint32_t sb_col = 4u + static_cast<uint32_t>(n0 % 128) / 32;
-        uint32_t n_mma = static_cast<uint32_t>((min(bn, T - n0) + 15) & ~15);
         // a pair's CTAs hold the two halves of a whole tile
-        if (PAIR) n_mma = static_cast<uint32_t>(bn);
+        const uint32_t n_mma = static_cast<uint32_t>(PAIR ? bn : (min(bn, T - n0) + 15) & ~15);
         uint32_t idesc[A4 ? 2 : 4];
 #pragma unroll
         for (int i = 0; i < (A4 ? 2 : 4); ++i)
-          idesc[i] = A4 ? idesc_mxf4(kM, n_mma, 2 * i) : idesc_mx(p.a_fmt, p.b_fmt, kM, n_mma, i, i);
+          idesc[i] = A4 ? idesc_mxf4(kM, n_mma, 2 * i) : idesc_mx(p.a_fmt, kFmtE4M3, kM, n_mma, i, i);
         if (!wait(&bars->acc_empty[ab], aph ^ 1u)) break;
         tc_fence_after();
         const uint32_t d = tbase + ab * p.acc_cols;
-        uint32_t accum = 0;
-        for (int kc = k0; kc < k1; kc += kps) {
+        for (int k = k0; k < k1; ++k) {
           if (!wait(&bars->full[s], ph, false)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const int nk = min(kps, k1 - kc);
-          uint32_t a = a0 + s * kps * a_slot, b = b0 + s * kps * b_slot, sa = sa0 + s * sb_chunks, sb = sb0 + s * sb_stage;
-          for (int u = 0; u < nk; ++u, a += a_slot, b += b_slot, sa += 512u, sb += 512u) {
-            if (PAIR) tmem_copy_scales_pair(sf, sa);
-            else tmem_copy_scales(sf, sa);
-            for (int i = 0; i < nsb; ++i) {
-              if (PAIR) tmem_copy_scales_pair(sf + 4u + 4u * i, sb + i * sb_chunks);
-              else tmem_copy_scales(sf + 4u + 4u * i, sb + i * sb_chunks);
-            }
+          const uint32_t accum = k > k0;
 #pragma unroll
-            for (int i = 0; i < (A4 ? 2 : 4); ++i) {
-              if (A4) {
-                if (PAIR) mma_mxf4_pair_lo(d, a + 2u * i, b + 2u * i, kDescHiSw64, idesc[i], sf, sf + sb_col, accum);
-                else mma_mxf4_lo(d, a + 2u * i, b + 2u * i, kDescHiSw64, idesc[i], sf, sf + sb_col, accum);
-              } else {
-                if (PAIR) mma_mxf8f6f4_pair_lo(d, a + 2u * i, b + 2u * i, kDescHiSw128, idesc[i], sf, sf + sb_col, accum);
-                else mma_mxf8f6f4_lo(d, a + 2u * i, b + 2u * i, kDescHiSw128, idesc[i], sf, sf + sb_col, accum);
-              }
-              accum = 1;
+          for (int c = 0; c < kSub; ++c) {
+            if (PAIR) tmem_copy_scales_pair(sf + c * kSfCols, sa + c * 32u);
+            else tmem_copy_scales_lo(sf + c * kSfCols, sa + c * 32u);
+#pragma unroll
+            for (int i = 0; i < NSB; ++i) {
+              if (PAIR) tmem_copy_scales_pair(sf + c * kSfCols + 4u + 4u * i, sb + (i * kSub + c) * 32u);
+              else tmem_copy_scales_lo(sf + c * kSfCols + 4u + 4u * i, sb + (i * kSub + c) * 32u);
             }
-            sf += sfc;  // four sets of columns in turn
-            if (sf == sf_end) sf = sf0;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t f = sf + (A4 ? i / 2 : 0) * kSfCols;
+            if (A4) {
+              if (PAIR) mma_mxf4_pair_lo(d, a + 2u * i, b + 2u * i, kDescHiSw128, idesc[i & 1], f, f + sb_col, i ? 1u : accum);
+              else mma_mxf4_lo(d, a + 2u * i, b + 2u * i, kDescHiSw128, idesc[i & 1], f, f + sb_col, i ? 1u : accum);
+            } else {
+              if (PAIR) mma_mxf8f6f4_pair_lo(d, a + 2u * i, b + 2u * i, kDescHiSw128, idesc[A4 ? 0 : i], f, f + sb_col, i ? 1u : accum);
+              else mma_mxf8f6f4_lo(d, a + 2u * i, b + 2u * i, kDescHiSw128, idesc[A4 ? 0 : i], f, f + sb_col, i ? 1u : accum);
+            }
           }
           if (PAIR) mma_commit_pair(smem_u32(&bars->empty[s]), 3);
           else mma_commit(smem_u32(&bars->empty[s]));
+          sf += kSub * kSfCols;
+          if (sf == sf_end) sf = sf0;
+          a += 16384u >> 4;
+          b += b_step;
+          sa += kSa >> 4;
+          sb += kSb >> 4;
           if (++s == static_cast<uint32_t>(S)) {
             s = 0;
             ph ^= 1u;
+            a = a0;
+            b = b0;
+            sa = sa0;
+            sb = sb0;
           }
         }
         if (!ok) break;
@@ -390,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
     // part of them in r's shared memory (the stages', which all CTAs have read by now).
     __syncthreads();
     cluster_sync_all();
-    float* const parts = reinterpret_cast<float*>(base + p.off_a);  // [source][128 rows][pitch]
+    float* const parts = reinterpret_cast<float*>(base);  // [source][128 rows][pitch]
     const int slice = p.slice, pitch = slice + 4;                   // rows 16 bytes apart modulo 128: no bank conflicts
     int tt, rb;
     tile_of(unit0, tt, rb);
@@ -496,23 +491,23 @@ __global__ void __launch_bounds__(256) k_linear_tokens(const uint4* __restrict__
   }
 }
 
-// Weights to blocks of 128 rows x 128 elements and their scales to tiled ones; rows
+// Weights to blocks of 128 rows x 128 bytes and their scales to tiled ones; rows
 // behind N and elements behind K are zeros of scale 1.
 __global__ void __launch_bounds__(256) k_linear_prepare(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, LinearLayout L,
                                                         uint8_t* __restrict__ dst) {
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x, i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int row16 = L.row_bytes / 16;                               // 16-byte pieces of a block's row
+  constexpr int row16 = 8;                                          // 16-byte pieces of a block's row
   const int src16 = (L.e2m1 ? L.K / 2 : L.K) / 16;                  // of a weight's row
-  const int64_t blocks = static_cast<int64_t>(L.RB) * L.NK, pieces = blocks * 128 * row16;
+  const int64_t blocks = static_cast<int64_t>(L.RB) * L.NB, pieces = blocks * 128 * row16;
   for (int64_t i = i0; i < pieces; i += stride) {
     const int64_t b = i / (128 * row16);
     const int in = static_cast<int>(i - b * (128 * row16)), r = in / row16, c = in - r * row16;
-    const int rb = static_cast<int>(b / L.NK), kc = static_cast<int>(b - static_cast<int64_t>(rb) * L.NK);
+    const int rb = static_cast<int>(b / L.NB), kc = static_cast<int>(b - static_cast<int64_t>(rb) * L.NB);
     const int64_t n = static_cast<int64_t>(rb) * 128 + r;
     const int k = kc * row16 + c;
     reinterpret_cast<uint4*>(dst)[i] = n < L.N && k < src16 ? __ldg(reinterpret_cast<const uint4*>(codes) + n * src16 + k) : make_uint4(0u, 0u, 0u, 0u);
   }
-  for (int64_t i = i0; i < blocks * 512; i += stride) {
+  for (int64_t i = i0; i < static_cast<int64_t>(L.RB) * L.NK * 512; i += stride) {
     const int64_t b = i / 512;
     const int in = static_cast<int>(i - b * 512);
     const int rb = static_cast<int>(b / L.NK), kc = static_cast<int>(b - static_cast<int64_t>(rb) * L.NK);
@@ -540,40 +535,37 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 constexpr uint32_t kSmem = 227 * 1024;
 
-struct Plan {
-  bool pair, a4;
-  int ctas;  // of the launch
-  uint32_t smem;
-};
-
 // Shared and tensor memory of a form; false where it does not fit.
-bool lay_out(Params& p, bool pair, bool a4, uint32_t budget, uint32_t* smem) {
-  const int sb = p.TT == 1 ? (p.bn + 127) / 128 : p.bn % 128 ? p.bn / 128 + 1 : p.bn / 128;  // token blocks that a tile touches
+bool lay_out(Params& p, bool pair, bool a4, int nsb, uint32_t budget, uint32_t* smem) {
+  const uint32_t sa = a4 ? 1024u : 512u, sb = sa * nsb, sf_cols = 4u + 4u * nsb;
   p.brows = pair ? p.bn / 2 : p.bn;
-  p.a_slot = a4 ? 8192u : 16384u;
-  p.b_slot = (static_cast<uint32_t>(p.brows) * (a4 ? 64u : 128u) + 1023u) & ~1023u;
-  p.sb_slot = static_cast<uint32_t>(sb) * 512u;
-  p.sfc = (4u + 4u * sb + 3u) & ~3u;
+  p.b_slot = static_cast<uint32_t>(p.brows) * 128u;
   p.acc_cols = static_cast<uint32_t>(p.bn + 31) & ~31u;
-  p.acc_bufs = p.splits == 1 && 2 * p.acc_cols + 4 * p.sfc <= 512 ? 2 : 1;
+  p.acc_bufs = p.splits == 1 && 2 * p.acc_cols + 4 * sf_cols <= 512 ? 2 : 1;
   p.sf_col0 = p.acc_bufs * p.acc_cols;
-  const uint32_t cols = p.sf_col0 + 4 * p.sfc;
+  const uint32_t cols = p.sf_col0 + 4 * sf_cols;
   if (cols > 512) return false;
   for (p.tmem_cols = 32; p.tmem_cols < cols;) p.tmem_cols *= 2;
-  const uint32_t chunk = p.a_slot + p.b_slot + 512u + p.sb_slot;
+  const uint32_t stage = 16384u + p.b_slot + sa + sb;
   const uint32_t fixed = 1024u + static_cast<uint32_t>((sizeof(Bars) + 127) & ~size_t(127));
-  p.stages = std::min<int>(kMaxStages, static_cast<int>((budget - fixed) / (chunk * p.kps)));
+  p.stages = std::min<int>(kMaxStages, static_cast<int>((budget - fixed) / stage));
   if (p.stages < 2) return false;
-  const uint32_t n = static_cast<uint32_t>(p.stages * p.kps);
-  p.off_a = 0;
-  p.off_b = n * p.a_slot;
+  const uint32_t n = static_cast<uint32_t>(p.stages);
+  p.off_b = n * 16384u;
   p.off_sa = p.off_b + n * p.b_slot;
-  p.off_sb = p.off_sa + n * 512u;
-  p.off_bar = p.off_sb + n * p.sb_slot;
+  p.off_sb = p.off_sa + n * sa;
+  p.off_bar = p.off_sb + n * sb;
   *smem = p.off_bar + fixed;
   p.slice = ((p.bn + p.splits - 1) / p.splits + 7) & ~7;
   // the parts of a split tile lie where the stages were
   return p.splits == 1 || static_cast<uint32_t>(p.splits * (p.slice + 4)) * 512u <= p.off_bar;
+}
+
+using Kernel = void (*)(Params, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap);
+Kernel kernel_of(bool pair, bool a4, int nsb) {
+  if (pair) return a4 ? k_linear<true, true, 2> : k_linear<true, false, 2>;
+  if (nsb == 1) return a4 ? k_linear<false, true, 1> : k_linear<false, false, 1>;
+  return a4 ? k_linear<false, true, 2> : k_linear<false, false, 2>;
 }
 
 }  // namespace
@@ -584,11 +576,10 @@ LinearLayout linear_layout(int N, int K, int fmt) {
   L.K = K;
   L.e2m1 = fmt == MX_E2M1;
   L.RB = (N + 127) / 128;
-  L.NK = (K + 127) / 128;
-  L.row_bytes = L.e2m1 ? 64 : 128;
-  const size_t blocks = static_cast<size_t>(L.RB) * L.NK;
-  L.scales_offset = blocks * 128 * L.row_bytes;
-  L.total_bytes = L.scales_offset + blocks * 512;
+  L.NB = L.e2m1 ? (K + 255) / 256 : (K + 127) / 128;
+  L.NK = L.e2m1 ? 2 * L.NB : L.NB;
+  L.scales_offset = static_cast<size_t>(L.RB) * L.NB * 16384;
+  L.total_bytes = L.scales_offset + static_cast<size_t>(L.RB) * L.NK * 512;
   return L;
 }
 
@@ -603,35 +594,34 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   auto encode = encode_fn();
   if (!encode) return cudaErrorNotSupported;
   const LinearLayout L = linear_layout(a.N, a.K, a.w_fmt);
+  const bool a4 = a.act_fmt == MX_E2M1;
+  const int TB = (a.T + 127) / 128;
   Params p{};
   p.T = a.T;
   p.N = a.N;
-  p.NK = L.NK;
   p.RB = L.RB;
-  p.TB = (a.T + 127) / 128;
+  p.KS = a4 ? L.NB : (a.K + 127) / 128;
   p.a_fmt = a.w_fmt == MX_E4M3 ? kFmtE4M3 : kFmtE2M1;
-  p.b_fmt = kFmtE4M3;
+  p.half_blocks = a.w_fmt == MX_E2M1 && !a4;
+  p.a_tx = p.half_blocks ? 8192u : 16384u;
   p.out_f32 = a.out_f32;
-  p.a_tx = a.w_fmt == MX_E4M3 ? 16384u : 8192u;
-  p.w_scales = a.w_prep + L.scales_offset;
-  p.t_scales = a.t_scales;
   p.bias = a.bias;
   p.out = a.out;
   p.status = a.status;
   p.wait_limit_ns = a.wait_limit_ns;
-  const bool a4 = a.act_fmt == MX_E2M1;
 
   bool pair = false;
+  int nsb = 2;
   uint32_t smem = 0, ctas = 0;
   p.splits = 1;
-  p.kps = 1;
   if (a.T <= 256) {
     p.bn = (a.T + 15) & ~15;
     p.TT = 1;
-    // K is shared by as many CTAs as fill the SMs, of four chunks each at least
-    while (p.splits < 8 && p.RB * (p.splits + 1) <= 152 && p.NK / (p.splits + 1) >= 4) ++p.splits;
+    nsb = a.T <= 128 ? 1 : 2;
+    // K is shared by as many CTAs as fill the SMs, of four stages each at least
+    while (p.splits < 8 && p.RB * (p.splits + 1) <= 152 && p.KS / (p.splits + 1) >= (a4 ? 2 : 4)) ++p.splits;
     p.units = p.RB;
-    if (!(p.splits > 1 && p.bn <= 64 && lay_out(p, false, a4, kSmem / 2 - 1024, &smem)) && !lay_out(p, false, a4, kSmem, &smem))
+    if (!(p.splits > 1 && p.bn <= 64 && lay_out(p, false, a4, nsb, kSmem / 2 - 1024, &smem)) && !lay_out(p, false, a4, nsb, kSmem, &smem))
       return cudaErrorInvalidConfiguration;
     ctas = p.splits > 1 ? p.units * p.splits : std::min(p.units, 152);
   } else {
@@ -639,45 +629,41 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
     p.bn = 192;
     p.TT = (a.T + p.bn - 1) / p.bn;
     p.units = p.TT * ((p.RB + 1) / 2);
-    p.kps = a4 ? 2 : 1;
-    if (!lay_out(p, true, a4, kSmem, &smem)) return cudaErrorInvalidConfiguration;
+    if (!lay_out(p, true, a4, nsb, kSmem, &smem)) return cudaErrorInvalidConfiguration;
     ctas = 2 * std::min(p.units, 76);
   }
 
-  CUtensorMap tm_a, tm_b, tm_sa{}, tm_sb{};
-  const bool bytes = a.w_fmt == MX_E4M3 || a4;
+  CUtensorMap tm_a, tm_b, tm_sa, tm_sb;
   const cuuint32_t es[4] = {1, 1, 1, 1};
   {
-    const cuuint64_t inner = a4 ? 64 : 128, row = static_cast<cuuint64_t>(L.row_bytes);
-    const cuuint64_t dims[4] = {inner, 128, static_cast<cuuint64_t>(L.NK), static_cast<cuuint64_t>(L.RB)};
-    const cuuint64_t strides[3] = {row, row * 128, row * 128 * L.NK};
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(inner), 128, static_cast<cuuint32_t>(p.kps), 1};
-    if (encode(&tm_a, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 4, const_cast<uint8_t*>(a.w_prep), dims, strides,
-               box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, a4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    // blocks of 128 rows x 128 bytes; as elements where E2M1 is widened
+    const cuuint64_t inner = p.half_blocks ? 256 : 128;
+    const cuuint64_t dims[4] = {inner, 128, static_cast<cuuint64_t>(L.NB), static_cast<cuuint64_t>(L.RB)};
+    const cuuint64_t strides[3] = {128, 16384, 16384 * static_cast<cuuint64_t>(L.NB)};
+    const cuuint32_t box[4] = {128, 128, 1, 1};
+    if (encode(&tm_a, p.half_blocks ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(a.w_prep), dims,
+               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
   {
     const cuuint64_t row = static_cast<cuuint64_t>(a4 ? a.K / 2 : a.K);
     const cuuint64_t dims[2] = {row, static_cast<cuuint64_t>(a.T)};
     const cuuint64_t strides[1] = {row};
-    const cuuint32_t box[2] = {a4 ? 64u : 128u, static_cast<cuuint32_t>(p.brows)};
+    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(p.brows)};
     if (encode(&tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.t_codes), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               a4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  if (pair) {
-    // scales as [block of 128 rows][chunk][128 words]
-    for (int i = 0; i < 2; ++i) {
-      const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(L.NK), static_cast<cuuint64_t>(i ? p.TB : L.RB)};
-      const cuuint64_t strides[2] = {512, 512 * static_cast<cuuint64_t>(L.NK)};
-      const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(p.kps), 1};
-      if (encode(i ? &tm_sb : &tm_sa, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(i ? p.t_scales : p.w_scales), dims, strides, box, es,
-                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
-    }
+  for (int i = 0; i < 2; ++i) {
+    // scales as [block of 128 rows][scale block along K][128 words]
+    const uint8_t* src = i ? a.t_scales : a.w_prep + L.scales_offset;
+    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(L.NK), static_cast<cuuint64_t>(i ? TB : L.RB)};
+    const cuuint64_t strides[2] = {512, 512 * static_cast<cuuint64_t>(L.NK)};
+    const cuuint32_t box[3] = {128, a4 ? 2u : 1u, i ? static_cast<cuuint32_t>(nsb) : 1u};
+    if (encode(i ? &tm_sb : &tm_sa, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(src), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
   }
 
   {
@@ -690,8 +676,7 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  void (*kernel)(Params, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap) =
-      pair ? (a4 ? k_linear<true, true> : k_linear<true, false>) : (a4 ? k_linear<false, true> : k_linear<false, false>);
+  const Kernel kernel = kernel_of(pair, a4, nsb);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

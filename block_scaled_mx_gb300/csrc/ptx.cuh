@@ -228,14 +228,18 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
 
 // 32 rows of 16 bytes (512 bytes of shared memory, 128-byte aligned, unswizzled)
 // to four columns of tensor memory, lane i of every lane quarter from row i:
-// block-scale words, ordered before the MMAs that this thread issues next.
-__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t smem) {
-  const uint32_t lo = ((smem >> 4) & 0x3FFFu) | (8u << 16);
+// block-scale words, ordered before the MMAs that this thread issues next.  The low half
+// of its shared-memory descriptor grows by 32 from one 512-byte block to the next.
+__device__ __forceinline__ uint32_t scales_desc_lo(uint32_t smem) { return ((smem >> 4) & 0x3FFFu) | (8u << 16); }
+__device__ __forceinline__ void tmem_copy_scales_lo(uint32_t taddr, uint32_t lo) {
   asm volatile(
       "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
       "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
       "r"(lo), "r"((128u >> 4) | (1u << 14))
       : "memory");
+}
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t smem) {
+  tmem_copy_scales_lo(taddr, scales_desc_lo(smem));
 }
 
 // Arrive (once) on an mbarrier when every previously issued tcgen05 async
@@ -450,10 +454,9 @@ __device__ __forceinline__ void mma_mxf4_pair_lo(uint32_t d_tmem, uint32_t a_lo,
       "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], ad, bd, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
       "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem), "r"(desc_hi));
 }
-// tmem_copy_scales in both CTAs of the pair, each from its own shared memory at the same
-// offset to its own tensor memory (issued by rank 0 only).
-__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint32_t smem) {
-  const uint32_t lo = ((smem >> 4) & 0x3FFFu) | (8u << 16);
+// tmem_copy_scales_lo in both CTAs of the pair, each from its own shared memory at the
+// same offset to its own tensor memory (issued by rank 0 only).
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint32_t lo) {
   asm volatile(
       "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
       "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),

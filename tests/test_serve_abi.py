@@ -41,7 +41,7 @@ def test_linear_refusals(L):
         assert call(**bad) == 3, bad
     assert call(wb=size - 1) == 4
     need = L.mx_linear_prepared_bytes(100, 96, 1)
-    assert need == 128 * 64 + 512 and L.mx_linear_prepared_bytes(100, 100, 1) == 0 and L.mx_linear_prepared_bytes(129, 160, 0) == 4 * (16384 + 512)
+    assert need == 128 * 128 + 2 * 512 and L.mx_linear_prepared_bytes(100, 100, 1) == 0 and L.mx_linear_prepared_bytes(129, 160, 0) == 4 * (16384 + 512)
 
     def lay(c=fake, sc=fake, N=100, K=96, f=1, d=fake, db=need):
         return L.mx_linear_prepare(c, sc, N, K, f, d, db, None)
