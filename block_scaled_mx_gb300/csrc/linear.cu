@@ -561,8 +561,48 @@ bool lay_out(Params& p, bool pair, bool a4, int nsb, uint32_t budget, uint32_t* 
   return p.splits == 1 || static_cast<uint32_t>(p.splits * (p.slice + 4)) * 512u <= p.off_bar;
 }
 
+struct Form {
+  bool pair, half;  // half: two CTAs share an SM
+  int bn, splits;
+};
+
+// Which form a call takes, by sizes.  A call's time is its weights' stream and a start of
+// some 6 us; in us, MXFP8 on both sides, K -> N:
+//   few tokens: two CTAs an SM, K split so that some 200 CTAs stream (a cluster of three
+//     with an SM to each CTA leaves SMs that no cluster fits)
+//       1 token, 4096 -> 6144      whole 12.4, split in 2 / 3 / 4 / 5: 11.9 / 11.8 / 11.1 / 11.4
+//       1 token, 4096 -> 20000     whole with an SM to each CTA 24.4, two an SM 19.5
+//   more: pairs, whose wave of tiles takes about 94 + bn
+//       96 tokens, 4096 -> 6144    pair 13.0, split in 2: 15.4    160: 13.5 and 17
+//       700 tokens, 4096 -> 6144   bn 64 / 128 / 192: 32.5 / 24.0 / 26.2
+//       700 tokens, 4096 -> 20000  75 / 51.8 / 48.8
+//   but a long K over few tiles is split all the same
+//       96 tokens, 16384 -> 4096   pair 27, tiles of 64 tokens split in 4: 24.6
+Form choose_form(int T, int RB, int KS) {
+  const int rbs = (RB + 1) / 2;
+  auto split = [&](int bn) {
+    const int tiles = RB * ((T + bn - 1) / bn);
+    Form f{false, true, bn, 1};
+    while (f.splits < 8 && tiles * (f.splits + 1) <= 228 && KS / (f.splits + 1) >= 4) ++f.splits;
+    return f;
+  };
+  if (T <= 32 || (T <= 64 && RB <= 24)) return split((T + 15) & ~15);
+  if (T <= 256 && KS >= 64 && rbs * ((T + 63) / 64) <= 38) return split(64);
+  Form best{true, false, 64, 1};
+  int64_t least = INT64_MAX;
+  for (int bn = 64; bn <= 192; bn += 64) {
+    const int64_t waves = (static_cast<int64_t>((T + bn - 1) / bn) * rbs + 75) / 76, time = waves * (94 + bn);
+    if (time < least) {
+      least = time;
+      best.bn = bn;
+    }
+  }
+  return best;
+}
+
 using Kernel = void (*)(Params, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap);
 Kernel kernel_of(bool pair, bool a4, int nsb) {
+  if (pair && nsb == 1) return a4 ? k_linear<true, true, 1> : k_linear<true, false, 1>;
   if (pair) return a4 ? k_linear<true, true, 2> : k_linear<true, false, 2>;
   if (nsb == 1) return a4 ? k_linear<false, true, 1> : k_linear<false, false, 1>;
   return a4 ? k_linear<false, true, 2> : k_linear<false, false, 2>;
@@ -610,28 +650,18 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   p.status = a.status;
   p.wait_limit_ns = a.wait_limit_ns;
 
-  bool pair = false;
-  int nsb = 2;
-  uint32_t smem = 0, ctas = 0;
-  p.splits = 1;
-  if (a.T <= 256) {
-    p.bn = (a.T + 15) & ~15;
-    p.TT = 1;
-    nsb = a.T <= 128 ? 1 : 2;
-    // K is shared by as many CTAs as fill the SMs, of four stages each at least
-    while (p.splits < 8 && p.RB * (p.splits + 1) <= 152 && p.KS / (p.splits + 1) >= (a4 ? 2 : 4)) ++p.splits;
-    p.units = p.RB;
-    if (!(p.splits > 1 && p.bn <= 64 && lay_out(p, false, a4, nsb, kSmem / 2 - 1024, &smem)) && !lay_out(p, false, a4, nsb, kSmem, &smem))
-      return cudaErrorInvalidConfiguration;
-    ctas = p.splits > 1 ? p.units * p.splits : std::min(p.units, 152);
-  } else {
-    pair = true;
-    p.bn = 192;
-    p.TT = (a.T + p.bn - 1) / p.bn;
-    p.units = p.TT * ((p.RB + 1) / 2);
-    if (!lay_out(p, true, a4, nsb, kSmem, &smem)) return cudaErrorInvalidConfiguration;
-    ctas = 2 * std::min(p.units, 76);
-  }
+  const Form f = choose_form(a.T, p.RB, p.KS);
+  const bool pair = f.pair;
+  p.bn = f.bn;
+  p.splits = f.splits;
+  p.TT = (a.T + p.bn - 1) / p.bn;
+  p.units = p.TT * (pair ? (p.RB + 1) / 2 : p.RB);
+  // token tiles start at multiples of 64 of their blocks of 128
+  const int nsb = p.TT == 1 ? (p.bn + 127) / 128 : p.bn % 128 == 0 || p.bn == 64 ? (p.bn + 127) / 128 : p.bn / 128 + 1;
+  uint32_t smem = 0;
+  if (!(f.half && lay_out(p, pair, a4, nsb, kSmem / 2 - 1024, &smem)) && !lay_out(p, pair, a4, nsb, kSmem, &smem)) return cudaErrorInvalidConfiguration;
+  const int fit = 152 * (f.half ? 2 : 1);
+  const uint32_t ctas = p.splits > 1 ? p.units * p.splits : pair ? 2 * std::min(p.units, fit / 2) : std::min(p.units, fit);
 
   CUtensorMap tm_a, tm_b, tm_sa, tm_sb;
   const cuuint32_t es[4] = {1, 1, 1, 1};
