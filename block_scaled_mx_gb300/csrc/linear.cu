@@ -451,28 +451,44 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
 // bf16 rows to MX codes and tiled scales, or (x null) row-major scales to tiled ones.  A
 // lane has eight elements, four lanes a block of 32; scale blocks behind K are 1.
 // Tiled: block (t / 128, k / 128) of 512 bytes, word [t % 32][t % 128 / 32] its row's four.
+// Memory-bound: four 16-byte loads a thread are on their way before the first is used, and
+// places are found by products (8192 x 4096: 30 us with divisions and one load at a time).
+constexpr int kTokenUnroll = 4;
+
+// Byte of a token's scale of block b (of 32 elements) among the tiled ones.
+__device__ __forceinline__ size_t tiled_at(int t, int b, int NK) {
+  return (static_cast<size_t>(t / 128) * NK + b / 4) * 512 + (t % 32) * 16 + (t % 128 / 32) * 4 + b % 4;
+}
+
 template <bool E2M1>
-__global__ void __launch_bounds__(256) k_linear_tokens(const uint4* __restrict__ x, const uint8_t* __restrict__ scales, int T, int K, int NK,
-                                                       uint8_t* __restrict__ codes, uint8_t* __restrict__ tiled) {
+__global__ void __launch_bounds__(256) k_linear_tokens(const uint4* __restrict__ x, const uint8_t* __restrict__ scales, int t0, int n, int K, int NK,
+                                                       FastDiv per_row_div, uint8_t* __restrict__ codes, uint8_t* __restrict__ tiled) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int per_row = NK * 16;  // groups of eight
-  const int64_t n = static_cast<int64_t>(T) * per_row, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  if (!x) {
-    const int64_t blocks = static_cast<int64_t>(T) * NK * 4;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < blocks; i += stride) {
-      const int t = static_cast<int>(i / (NK * 4)), b = static_cast<int>(i - static_cast<int64_t>(t) * NK * 4);
-      tiled[(static_cast<size_t>(t / 128) * NK + b / 4) * 512 + (t % 32) * 16 + (t % 128 / 32) * 4 + b % 4] =
-          b < K / 32 ? scales[static_cast<size_t>(t) * (K / 32) + b] : 127;
+  if (!x) {  // n scales, per_row of a token
+    const int per_row = NK * 4;
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
+      const int r = per_row_div.of(i), b = i - r * per_row, t = t0 + r;
+      tiled[tiled_at(t, b, NK)] = b < K / 32 ? scales[static_cast<size_t>(t) * (K / 32) + b] : 127;
     }
     return;
   }
-  const int lane = threadIdx.x & 31;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i - lane < n; i += stride) {
-    const int t = static_cast<int>(i / per_row), g = static_cast<int>(i - static_cast<int64_t>(t) * per_row);
-    const bool in = i < n && g < K / 8;
-    const int64_t at = static_cast<int64_t>(t) * (K / 8) + g;
-    const uint4 w = in ? __ldg(x + at) : make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t b[4] = {w.x, w.y, w.z, w.w};
+  const int per_row = NK * 16, lane = threadIdx.x & 31;  // n groups of eight, per_row of a token
+  const int i0 = blockIdx.x * (256 * kTokenUnroll) + threadIdx.x;
+  uint4 w[kTokenUnroll];
+  int t[kTokenUnroll], g[kTokenUnroll];
+#pragma unroll
+  for (int u = 0; u < kTokenUnroll; ++u) {
+    const int i = min(i0 + u * 256, n - 1);
+    const int r = per_row_div.of(i);
+    g[u] = i - r * per_row;
+    t[u] = t0 + r;
+    w[u] = g[u] < K / 8 ? __ldcs(x + static_cast<int64_t>(t[u]) * (K / 8) + g[u]) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int u = 0; u < kTokenUnroll; ++u) {
+    if (i0 - lane + u * 256 >= n) break;
+    const bool in = i0 + u * 256 < n && g[u] < K / 8;
+    const uint32_t b[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
     float v[8];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -481,13 +497,12 @@ __global__ void __launch_bounds__(256) k_linear_tokens(const uint4* __restrict__
     }
     uint8_t scale;
     const uint2 c = mx_codes8(v, E2M1, scale);
+    const int64_t at = static_cast<int64_t>(t[u]) * (K / 8) + g[u];
     if (in) {
       if (E2M1) reinterpret_cast<uint32_t*>(codes)[at] = c.x;
       else reinterpret_cast<uint2*>(codes)[at] = c;
     }
-    if (i < n && (g & 3) == 0)
-      tiled[(static_cast<size_t>(t / 128) * NK + g / 16) * 512 + (t % 32) * 16 + (t % 128 / 32) * 4 + (g >> 2) % 4] =
-          in ? scale : 127;
+    if (i0 + u * 256 < n && (g[u] & 3) == 0) tiled[tiled_at(t[u], g[u] >> 2, NK)] = in ? scale : 127;
   }
 }
 
@@ -697,14 +712,19 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   }
 
   {
-    const int64_t groups = a.x ? static_cast<int64_t>(a.T) * L.NK * 16 : static_cast<int64_t>(a.T) * L.NK * 4;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((groups + 255) / 256, 152 * 8));
-    const uint4* x = static_cast<const uint4*>(a.x);
-    uint8_t* codes = const_cast<uint8_t*>(a.t_codes);
-    if (a4) k_linear_tokens<true><<<grid, 256, 0, s>>>(x, a.scales, a.T, a.K, L.NK, codes, a.t_scales);
-    else k_linear_tokens<false><<<grid, 256, 0, s>>>(x, a.scales, a.T, a.K, L.NK, codes, a.t_scales);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    const int per_row = L.NK * (a.x ? 16 : 4);
+    const int most = (1 << 30) / per_row;  // tokens of a launch: places are ints
+    for (int t0 = 0; t0 < a.T; t0 += most) {
+      const int n = std::min(most, a.T - t0) * per_row;
+      const unsigned grid = a.x ? static_cast<unsigned>((n + 256 * kTokenUnroll - 1) / (256 * kTokenUnroll)) : static_cast<unsigned>(std::min((n + 255) / 256, 152 * 8));
+      const uint4* x = static_cast<const uint4*>(a.x);
+      uint8_t* codes = const_cast<uint8_t*>(a.t_codes);
+      const FastDiv div = FastDiv::by(per_row);
+      if (a4) k_linear_tokens<true><<<grid, 256, 0, s>>>(x, a.scales, t0, n, a.K, L.NK, div, codes, a.t_scales);
+      else k_linear_tokens<false><<<grid, 256, 0, s>>>(x, a.scales, t0, n, a.K, L.NK, div, codes, a.t_scales);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
   }
   const Kernel kernel = kernel_of(pair, a4, nsb);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));

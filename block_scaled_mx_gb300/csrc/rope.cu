@@ -6,7 +6,7 @@
 // for the pairs (i, i + R/2) or (2i, 2i + 1).  Angles of far positions lose their
 // fraction of a turn in fp32, so f_i is kept as the 64-bit fraction of a turn a
 // position, p * f_i is a product modulo 2^64, which is exact but for f_i's own rounding
-// (2^-53), and its upper 32 bits are the angle in [-1/2, 1/2) turns.
+// (2^-53), and its upper 32 bits are the angle in [-1/2, 1/2) turns (2^-33 of a turn off).
 //
 // Memory-bound: every input is read once and every output written once.  A warp
 // takes one token, or a part of one; a lane holds eight elements of a head, so that
@@ -74,10 +74,15 @@ __global__ void __launch_bounds__(32 * kWarps) k_rope_kv_append(const RopeArgs r
       sn[i] = 0.0f;
       if (turns) {
         const uint64_t turn = static_cast<uint64_t>(pos) * __ldg(r.turns + i0 + i);
-        // half turns, in [-1, 1): the product's upper word, rounded to 24 bits
-        sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn[i], &cs[i]);
-        cs[i] *= r.amplitude;
-        sn[i] *= second ? -r.amplitude : r.amplitude;
+        // half turns, in [-1, 1): the product's upper word, its first 24 bits as a float and
+        // the others by the derivative
+        const uint32_t word = static_cast<uint32_t>(turn >> 32);
+        const float h = static_cast<float>(static_cast<int32_t>(word & 0xFFFFFF00u));
+        const float left = static_cast<float>(word & 0xFFu) * (3.14159274f * 0x1p-31f);
+        float sine, cosine;
+        sincospif(h * 0x1p-31f, &sine, &cosine);
+        cs[i] = fmaf(-sine, left, cosine) * r.amplitude;
+        sn[i] = fmaf(cosine, left, sine) * (second ? -r.amplitude : r.amplitude);
       }
     }
   }

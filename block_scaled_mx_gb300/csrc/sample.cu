@@ -5,13 +5,14 @@
 // A cluster of CTAs holds the row in its shared memory (read once) and goes over it a
 // few times from there:
 //   1. the row's maximum m;
-//   2. with top-k or top-p, a histogram of counts and weights over bins of m - logit,
-//      merged across the cluster slice by slice.  The bin in which the kept prefix ends
-//      holds few tokens as a rule; they are ranked one against the other.  Where it
-//      holds many, it is divided by the bits of the logit until few are left or all of
-//      them are equal (then the first ones by number are kept);
-//   3. the kept weights, by warp; the warp in which the random number falls goes over
-//      its stretch once more.
+//   2. with top-k or top-p, a histogram of counts (and weights) over bins of m - logit,
+//      merged across the cluster slice by slice, which tells the bin where the kept prefix
+//      ends.  As a rule the tokens up to there are few: one CTA gathers them and does the
+//      rest alone, by radix selections over what its threads hold in registers;
+//   3. where they are many, the end is found in its bin alone (by a CTA if that is small,
+//      else by further histograms over the bits of the logit); then the kept weights are
+//      added up by warp, and the warp in which the random number falls goes over its
+//      stretch once more.  So are rows without top-k and top-p.
 //
 // Weights are whole numbers, 2^43 e^((logit - m) / temperature) rounded down, so sums
 // are exact in any order (no atomic changes a result) and two calls agree.  A draw next
@@ -26,6 +27,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -35,7 +37,8 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 1024, kDigit = 10;  // bins of a histogram, bits of the logit that one divides by
-constexpr int kCandidates = 256;          // ranked one against the other
+constexpr int kItems = 3;                 // tokens that a thread holds of those gathered in one CTA
+constexpr int kCandidates = 1280;         // most of those: their list lies where the histogram was
 constexpr int kMaxCluster = 8;
 constexpr int kOneBits = 43;
 constexpr unsigned long long kOne = 1ull << kOneBits;  // the largest weight; 2^20 of them fit 64 bits
@@ -88,6 +91,12 @@ struct End {
   unsigned long long mass;  // of all of them
 };
 
+// Where a selection ends: items above `key`, and some of the `count` with it.
+struct Selected {
+  uint32_t key, before, count;
+  unsigned long long before_mass;
+};
+
 struct Control {
   float c_hi, c_lo;
   float max[kMaxCluster];
@@ -99,8 +108,13 @@ struct Control {
   End end;
   uint32_t key_min[kMaxCluster], key_max[kMaxCluster];
   uint32_t n;  // candidates (rank 0)
-  uint32_t cand_key[kCandidates], cand_at[kCandidates];
-  unsigned long long cand_mass[kCandidates];
+  uint32_t local_n, local_base, local_at[kCandidates];  // this CTA's
+  Selected sel;
+  uint32_t sel_digit;
+  uint32_t sel_count[256], sel_lo[256], sel_hi[256];
+  uint32_t rank_n;
+  unsigned long long rank_order[128], rank_w[128], near_before, near_order;
+  int near_bin;
   uint32_t warp_eq[kMaxCluster * kWarps];
   unsigned long long warp_mass[kMaxCluster * kWarps];
   int hit_warp;
@@ -109,8 +123,16 @@ struct Control {
   uint32_t red[kWarps], red2[kWarps];
   unsigned long long red64[kWarps];
   float2 exp2_table[64];
-  uint32_t hist_count[kBins], hist_lo[kBins], hist_hi[kBins];
+  union {
+    struct {
+      uint32_t hist_count[kBins], hist_lo[kBins], hist_hi[kBins];
+    };
+    struct {
+      uint32_t cand_key[kCandidates], cand_at[kCandidates];  // (rank 0) behind the histogram's merge
+    };
+  };
 };
+static_assert(kCandidates <= kItems * kThreads && 2 * kCandidates <= 3 * kBins, "");
 
 // Logits in their order as unsigned numbers (both zeros the same), and back.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -121,12 +143,24 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
 
+// x in (0, 1] times 2^bits as a whole number, rounded down, without the slow 64-bit floats
+// (24-bit significands: nothing is lost above 2^-40).
+__device__ __forceinline__ unsigned long long fixed_of(float x, int bits) {
+  if (!(x > 0.0f)) return 0ull;
+  const uint32_t b = __float_as_uint(x);
+  const int e = max(static_cast<int>(b >> 23), 1);  // subnormals give 0 below
+  const unsigned long long m = (b & 0x7FFFFFu) | (b >> 23 ? 0x800000u : 0u);
+  const int up = bits + e - 150;
+  return up >= 0 ? m << up : up > -24 ? m >> -up : 0ull;
+}
+
 // 2^43 e^((x - max) / temperature), rounded down; c_hi + c_lo = log2(e) / temperature.
-__device__ __forceinline__ unsigned long long weight_of(float x, float max, float c_hi, float c_lo, const float2* table) {
-  if (x == max) return kOne;
+// Without branches, so that a thread's weights go side by side.
+__device__ __forceinline__ unsigned long long weight_of(float x, float max, float c_hi, float c_lo, uint32_t table) {
   const float s = x - max;
-  const float t = s * c_hi;
-  if (!(t > -44.0f)) return 0ull;  // also -inf, and NaN of an infinite maximum
+  const float t0 = s * c_hi;
+  const bool some = t0 > -44.0f;  // not for -inf, nor for NaN of an infinite maximum
+  const float t = some ? t0 : 0.0f;
   // x - max = s + e exactly (the error of a sum of two floats), its product likewise
   const float v = s - x;
   const float e = (x - (s - v)) - (max + v);
@@ -136,11 +170,14 @@ __device__ __forceinline__ unsigned long long weight_of(float x, float max, floa
   const float f = (t - (shifted - 196608.0f)) + t_lo;
   // 2^f - 1 for |f| <= 2^-7: the next term is below 2^-44
   const float q = f * fmaf(f, fmaf(f, fmaf(f, 9.6181291e-3f, 5.5504109e-2f), 0.24022651f), 0.69314718f);
-  const float2 p = table[j & 63];
-  const float lo = fmaf(p.x, q, p.y);  // below 2^-6 in size
-  const unsigned long long whole = static_cast<unsigned long long>((__float_as_uint(p.x) & 0x7FFFFFu) | 0x800000u) << (kOneBits - 23);
-  const long long part = static_cast<long long>(__float2int_rn(lo * 0x1p36f)) << (kOneBits - 36);
-  return (whole + part) >> -(j >> 6);
+  float2 p;
+  asm("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(p.x), "=f"(p.y) : "r"(table + (j & 63) * 8));
+  // (p.x + lo) 2^43 with p.x's 24 bits as they are, then down by whole powers of two
+  const uint32_t whole = (__float_as_uint(p.x) & 0x7FFFFFu) | 0x800000u;
+  const int part = __float2int_rn(fmaf(p.x, q, p.y) * 0x1p36f);  // below 2^-6 in size
+  const unsigned long long sum = (static_cast<unsigned long long>(whole) << (kOneBits - 23)) + (static_cast<long long>(part) << (kOneBits - 36));
+  const unsigned long long w = sum >> (-(j >> 6) & 63);
+  return x == max ? kOne : some ? w : 0ull;
 }
 
 template <bool BF16>
@@ -162,7 +199,7 @@ struct Row {
   int vecs;           // of the segment
   uint32_t at0;       // place of its first element
   float max, c_hi, c_lo, bin_scale;
-  const float2* table;
+  uint32_t table;     // shared-memory address of 2^(j/64)
   __device__ __forceinline__ unsigned long long weight(float x) const { return weight_of(x, max, c_hi, c_lo, table); }
   // Bins of the first histogram: more for lower logits, by a function that keeps order.
   __device__ __forceinline__ int bin(float x) const {
@@ -181,71 +218,43 @@ struct Subset {
   }
 };
 
-// Histogram of the whole row (level 0) or of a subset by the `kDigit` bits below its
-// shift, highest first; merged in slices of kBins / C bins, one a CTA, and the slices'
-// sums known to all.
-template <bool BF16>
-__device__ void histogram(const Row<BF16>& r, Control& ctl, uint32_t* slice_count, unsigned long long* slice_mass, bool masses,
-                          int level, const Subset& sub) {
+__device__ __forceinline__ void histogram_begin(Control& ctl) {
+  for (int b = threadIdx.x; b < kBins; b += kThreads) ctl.hist_count[b] = ctl.hist_lo[b] = ctl.hist_hi[b] = 0u;
+  __syncthreads();
+}
+
+// The CTAs' histograms merged in slices of kBins / C bins, one a CTA, and the slices' sums
+// known to all.
+__device__ void histogram_merge(Control& ctl, uint32_t* slice_count, unsigned long long* slice_mass, bool masses, int level) {
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = cluster.num_blocks(), R = cluster.block_rank();
-  for (int b = tid; b < kBins; b += kThreads) ctl.hist_count[b] = ctl.hist_lo[b] = ctl.hist_hi[b] = 0u;
-  __syncthreads();
-  const int low = sub.shift - kDigit;  // the digit's lowest bit (may be negative: fewer bits left)
-  // the last bin, which may hold nearly all of a row, is added up in registers
-  uint32_t last_count = 0;
-  unsigned long long last_mass = 0;
-  auto add = [&](int b, unsigned long long w) {
-    const uint32_t lo = static_cast<uint32_t>(w);
-    const uint32_t hi = static_cast<uint32_t>(w >> 32) + (atomicAdd(&ctl.hist_lo[b], lo) > ~lo ? 1u : 0u);
-    if (hi) atomicAdd(&ctl.hist_hi[b], hi);
-  };
-  for (int i = tid; i < r.vecs; i += kThreads) {
-    const uint4 v = r.seg[i];
-#pragma unroll
-    for (int m = 0; m < Row<BF16>::VE; ++m) {
-      const float x = element<BF16>(v, m);
-      int b;
-      if (level == 0) {
-        b = r.bin(x);
-      } else {
-        const uint32_t key = key_of(x);
-        if (!sub.holds(r, x, key)) continue;
-        const uint32_t digit = low >= 0 ? (key >> low) & (kBins - 1) : (key << -low) & (kBins - 1);
-        b = kBins - 1 - static_cast<int>(digit);
-      }
-      const unsigned long long w = masses ? r.weight(x) : 0ull;
-      if (b == kBins - 1) {
-        ++last_count;
-        last_mass += w;
-      } else {
-        atomicAdd(&ctl.hist_count[b], 1u);
-        if (w) add(b, w);
-      }
-    }
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    last_count += __shfl_xor_sync(0xffffffffu, last_count, d);
-    last_mass += __shfl_xor_sync(0xffffffffu, last_mass, d);
-  }
-  if (lane == 0 && last_count) {
-    atomicAdd(&ctl.hist_count[kBins - 1], last_count);
-    add(kBins - 1, last_mass);
-  }
   cluster.sync();
   const int S = kBins / C;
   uint32_t count = 0;
   unsigned long long mass = 0;
   for (int b = tid; b < S; b += kThreads) {
+    // all peers' bins are on their way before the first is added
+    const int at = R * S + b;
+    uint32_t ns[kMaxCluster], lo[kMaxCluster], hi[kMaxCluster];
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) {
+      ns[c] = lo[c] = hi[c] = 0u;
+      if (c < C) {
+        const Control* peer = cluster.map_shared_rank(&ctl, c);
+        ns[c] = peer->hist_count[at];
+        if (masses) {
+          lo[c] = peer->hist_lo[at];
+          hi[c] = peer->hist_hi[at];
+        }
+      }
+    }
     uint32_t n = 0;
     unsigned long long w = 0;
-    for (int c = 0; c < C; ++c) {
-      const Control* peer = cluster.map_shared_rank(&ctl, c);
-      const int at = R * S + b;
-      n += peer->hist_count[at];
-      if (masses) w += (static_cast<unsigned long long>(peer->hist_hi[at]) << 32) + peer->hist_lo[at];
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) {
+      n += ns[c];
+      w += (static_cast<unsigned long long>(hi[c]) << 32) + lo[c];
     }
     slice_count[b] = n;
     slice_mass[b] = w;
@@ -274,6 +283,60 @@ __device__ void histogram(const Row<BF16>& r, Control& ctl, uint32_t* slice_coun
     peer->slice_mass[level ? 1 : 0][R] = w;
   }
   cluster.sync();
+}
+
+// Histogram of the whole row (level 0) or of a subset by the `kDigit` bits below its
+// shift, highest first; merged.
+template <bool BF16>
+__device__ void histogram(const Row<BF16>& r, Control& ctl, uint32_t* slice_count, unsigned long long* slice_mass, bool masses,
+                          int level, const Subset& sub) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  histogram_begin(ctl);
+  const int low = sub.shift - kDigit;  // the digit's lowest bit (may be negative: fewer bits left)
+  // the last bin, which may hold nearly all of a row, is added up in registers
+  uint32_t last_count = 0;
+  unsigned long long last_mass = 0;
+  auto add = [&](int b, unsigned long long w) {
+    const uint32_t lo = static_cast<uint32_t>(w);
+    const uint32_t hi = static_cast<uint32_t>(w >> 32) + (atomicAdd(&ctl.hist_lo[b], lo) > ~lo ? 1u : 0u);
+    if (hi) atomicAdd(&ctl.hist_hi[b], hi);
+  };
+  for (int i = tid; i < r.vecs; i += kThreads) {
+    const uint4 v = r.seg[i];
+    unsigned long long w[Row<BF16>::VE];
+#pragma unroll
+    for (int m = 0; m < Row<BF16>::VE; ++m) w[m] = masses ? r.weight(element<BF16>(v, m)) : 0ull;
+#pragma unroll
+    for (int m = 0; m < Row<BF16>::VE; ++m) {
+      const float x = element<BF16>(v, m);
+      int b;
+      if (level == 0) {
+        b = r.bin(x);
+      } else {
+        const uint32_t key = key_of(x);
+        if (!sub.holds(r, x, key)) continue;
+        const uint32_t digit = low >= 0 ? (key >> low) & (kBins - 1) : (key << -low) & (kBins - 1);
+        b = kBins - 1 - static_cast<int>(digit);
+      }
+      if (b == kBins - 1) {
+        ++last_count;
+        last_mass += w[m];
+      } else {
+        atomicAdd(&ctl.hist_count[b], 1u);
+        if (w[m]) add(b, w[m]);
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    last_count += __shfl_xor_sync(0xffffffffu, last_count, d);
+    last_mass += __shfl_xor_sync(0xffffffffu, last_mass, d);
+  }
+  if (lane == 0 && last_count) {
+    atomicAdd(&ctl.hist_count[kBins - 1], last_count);
+    add(kBins - 1, last_mass);
+  }
+  histogram_merge(ctl, slice_count, slice_mass, masses, level);
 }
 
 // The bin in which the `target`th token, or unit of weight, lies; the sums of what is
@@ -339,97 +402,335 @@ __device__ Found find_bin(Control& ctl, const uint32_t* slice_count, const unsig
   return ctl.found;
 }
 
-// Where the prefix of `target` tokens (or of tokens until their weights reach target)
-// ends, from the level-0 histogram on.
-template <bool BF16>
-__device__ End find_end(const Row<BF16>& r, Control& ctl, uint32_t* const (&slice_count)[2], unsigned long long* const (&slice_mass)[2],
-                        bool by_mass, bool masses, unsigned long long target) {
-  cg::cluster_group cluster = cg::this_cluster();
+// Tokens gathered in one CTA, up to kItems a thread.
+struct Items {
+  uint32_t key[kItems], at[kItems];
+  unsigned long long w[kItems];
+  uint32_t kept;  // bit i: item i is there and still kept
+};
+
+// Sum over the CTA, the same in every thread.
+__device__ unsigned long long block_sum(Control& ctl, unsigned long long v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  __syncthreads();  // the slots may still be read from the call before
+  if ((threadIdx.x & 31) == 0) ctl.red64[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) v += ctl.red64[i];
+  return v;
+}
+
+// The key, in descending order, at which the `target`th of the kept items, or unit of their
+// weight, lies, beginning behind `before` items of `before_mass` (the weight before it is
+// told with `masses`).  Whole CTA.
+__device__ Selected select(Control& ctl, const uint32_t (&key)[kItems], const unsigned long long (&w)[kItems], uint32_t kept, bool by_mass, bool masses,
+                           unsigned long long target, uint32_t before, unsigned long long before_mass) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = cluster.num_blocks(), R = cluster.block_rank();
-  Found f = find_bin(ctl, slice_count[0], slice_mass[0], by_mass, target, 0, Found{});
-  Subset sub{f.bin, 32, 0u};
-  while (true) {
-    // the subset's least and largest key, and its tokens where they are few
-    uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-    Control* leader = cluster.map_shared_rank(&ctl, 0);
-    for (int i = tid; i < r.vecs; i += kThreads) {
-      const uint4 v = r.seg[i];
+  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    if (kept >> i & 1) {
+      lo = min(lo, key[i]);
+      hi = max(hi, key[i]);
+    }
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  const uint32_t mine = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(__popc(kept)));
+  __syncthreads();
+  if (lane == 0) {
+    ctl.red[warp] = lo;
+    ctl.red2[warp] = hi;
+    ctl.red64[warp] = mine;
+  }
+  __syncthreads();
+  Selected r{0u, before, 0u, before_mass};
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    lo = min(lo, ctl.red[i]);
+    hi = max(hi, ctl.red2[i]);
+    r.count += static_cast<uint32_t>(ctl.red64[i]);
+  }
+  r.key = hi;
+  if (lo >= hi) return r;  // all the same
+  int shift = 32 - __clz(lo ^ hi);
+  uint32_t prefix = shift < 32 ? hi >> shift : 0u;
+  while (shift > 0 && r.count > 1) {
+    const int low = max(shift - 8, 0), bits = shift - low;
+    for (int i = tid; i < 256; i += kThreads) ctl.sel_count[i] = ctl.sel_lo[i] = ctl.sel_hi[i] = 0u;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      if ((kept >> i & 1) && (shift >= 32 || (key[i] >> shift) == prefix)) {
+        const uint32_t d = (key[i] >> low) & ((1u << bits) - 1);
+        atomicAdd(&ctl.sel_count[d], 1u);
+        if (masses) {
+          const uint32_t l = static_cast<uint32_t>(w[i]);
+          const uint32_t h = static_cast<uint32_t>(w[i] >> 32) + (atomicAdd(&ctl.sel_lo[d], l) > ~l ? 1u : 0u);
+          if (h) atomicAdd(&ctl.sel_hi[d], h);
+        }
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // lane l: digits 255 - 8 l and the seven below
+      uint32_t n[8], run = 0;
+      unsigned long long m[8], run_mass = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int d = 255 - 8 * lane - i;
+        n[i] = ctl.sel_count[d];
+        m[i] = (static_cast<unsigned long long>(ctl.sel_hi[d]) << 32) + ctl.sel_lo[d];
+        run += n[i];
+        run_mass += m[i];
+      }
+      uint32_t in = run;
+      unsigned long long in_mass = run_mass;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, in, d);
+        const unsigned long long z = shfl_up64(in_mass, d);
+        if (lane >= d) {
+          in += y;
+          in_mass += z;
+        }
+      }
+      const bool reached = by_mass ? r.before_mass + in_mass >= target : r.before + in >= target;
+      const unsigned hits = __ballot_sync(0xffffffffu, reached);
+      if (lane == (hits ? __ffs(hits) - 1 : 31)) {
+        uint32_t b = r.before + in - run;
+        unsigned long long bm = r.before_mass + in_mass - run_mass;
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (!found) {
+            if ((by_mass ? bm + m[i] : static_cast<unsigned long long>(b + n[i])) >= target || i == 7) {
+              ctl.sel = Selected{0u, b, n[i], bm};
+              ctl.sel_digit = 255 - 8 * lane - i;
+              found = true;
+            } else {
+              b += n[i];
+              bm += m[i];
+            }
+          }
+        }
+      }
+    }
+    __syncthreads();
+    r = ctl.sel;
+    prefix = prefix << bits | ctl.sel_digit;
+    shift = low;
+  }
+  // the one item, or the equal ones, left
+#pragma unroll
+  for (int i = 0; i < kItems; ++i)
+    if ((kept >> i & 1) && (shift >= 32 || (key[i] >> shift) == prefix)) ctl.sel.key = key[i];
+  __syncthreads();
+  r.key = ctl.sel.key;
+  return r;
+}
+
+// The same by 1024 even bins of the items' range, and the few items of one bin ranked one
+// against the other: one pass where the radix selection takes one for each eight bits.
+// Items are in ascending `order`; the order of the item at which the target lies.  Whole CTA.
+constexpr int kRanked = 128;  // most items of that bin
+__device__ unsigned long long select_near(Control& ctl, const int (&bin)[kItems], const unsigned long long (&order)[kItems],
+                                          const unsigned long long (&w)[kItems], uint32_t kept, bool by_mass, unsigned long long target, bool& done) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kNear = 2 * kThreads;
+  static_assert(kNear == kBins, "the bins lie where the histogram and the list were");
+  __syncthreads();
+  for (int i = tid; i < kNear; i += kThreads) ctl.hist_count[i] = ctl.hist_lo[i] = ctl.hist_hi[i] = 0u;
+  if (tid == 0) ctl.rank_n = 0u;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    if (kept >> i & 1) {
+      atomicAdd(&ctl.hist_count[bin[i]], 1u);
+      if (by_mass) {
+        const uint32_t l = static_cast<uint32_t>(w[i]);
+        const uint32_t h = static_cast<uint32_t>(w[i] >> 32) + (atomicAdd(&ctl.hist_lo[bin[i]], l) > ~l ? 1u : 0u);
+        if (h) atomicAdd(&ctl.hist_hi[bin[i]], h);
+      }
+    }
+  }
+  __syncthreads();
+  // each thread two bins; what lies before them by warp and then over the warps
+  const unsigned long long v0 = by_mass ? (static_cast<unsigned long long>(ctl.hist_hi[2 * tid]) << 32) + ctl.hist_lo[2 * tid] : ctl.hist_count[2 * tid];
+  const unsigned long long v1 = by_mass ? (static_cast<unsigned long long>(ctl.hist_hi[2 * tid + 1]) << 32) + ctl.hist_lo[2 * tid + 1] : ctl.hist_count[2 * tid + 1];
+  unsigned long long in = v0 + v1;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned long long y = shfl_up64(in, d);
+    if (lane >= d) in += y;
+  }
+  if (lane == 31) ctl.red64[warp] = in;
+  __syncthreads();
+  unsigned long long before = in - v0 - v1;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) before += i < warp ? ctl.red64[i] : 0ull;
+  if (before < target && before + v0 + v1 >= target) {
+    const int second = before + v0 < target;
+    ctl.near_bin = 2 * tid + second;
+    ctl.near_before = second ? before + v0 : before;
+  }
+  __syncthreads();
+  const int b = ctl.near_bin;
+  done = ctl.hist_count[b] <= kRanked;
+  if (!done) return 0ull;
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    if ((kept >> i & 1) && bin[i] == b) {
+      const uint32_t at = atomicAdd(&ctl.rank_n, 1u);
+      ctl.rank_order[at] = order[i];
+      ctl.rank_w[at] = by_mass ? w[i] : 1ull;
+    }
+  }
+  __syncthreads();
+  const int n = static_cast<int>(ctl.rank_n);
+  if (tid < n) {
+    const unsigned long long mine = ctl.rank_order[tid], own = ctl.rank_w[tid];
+    unsigned long long sum = ctl.near_before;
+    for (int j = 0; j < n; ++j) sum += ctl.rank_order[j] < mine ? ctl.rank_w[j] : 0ull;
+    if (sum < target && sum + own >= target) ctl.near_order = mine;
+  }
+  __syncthreads();
+  return ctl.near_order;
+}
+
+// Keeps of the items the prefix, by logit and then number, of `target` items, or until
+// their weight reaches target.
+template <bool BF16>
+__device__ void keep_prefix(const Row<BF16>& r, Control& ctl, Items& it, float near_scale, bool by_mass, unsigned long long target) {
+  int bin[kItems];
+  unsigned long long order[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const float x = value_of(it.key[i]);
+    bin[i] = x == r.max ? 0 : min(2 * kThreads - 1, __float2int_rz((r.max - x) * near_scale));
+    order[i] = static_cast<unsigned long long>(~it.key[i]) << 32 | it.at[i];
+  }
+  bool done;
+  const unsigned long long last = select_near(ctl, bin, order, it.w, it.kept, by_mass, target, done);
+  if (done) {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+      if (order[i] > last) it.kept &= ~(1u << i);
+    return;
+  }
+  const Selected s = select(ctl, it.key, it.w, it.kept, by_mass, by_mass, target, 0u, 0ull);
+  uint32_t equal = 0, above = 0;
+  unsigned long long w = 0;
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    if (it.kept >> i & 1) {
+      if (it.key[i] > s.key) above |= 1u << i;
+      if (it.key[i] == s.key) {
+        equal |= 1u << i;
+        w = it.w[i];
+      }
+    }
+  }
+  if (s.count > 1) {
+    // of equal ones the first by number
+    if (by_mass) {
+      __syncthreads();
+      if (equal) ctl.total = w;
+      __syncthreads();
+      w = ctl.total;
+    }
+    unsigned long long quota = by_mass ? (w ? (target - s.before_mass + w - 1) / w : s.count) : target - s.before;
+    if (quota < s.count) {
+      uint32_t at[kItems];
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) at[i] = ~it.at[i];
+      const Selected last = select(ctl, at, it.w, equal, false, false, quota, 0u, 0ull);
+#pragma unroll
+      for (int i = 0; i < kItems; ++i)
+        if (at[i] < last.key) equal &= ~(1u << i);
+    }
+  }
+  it.kept = above | equal;
+}
+
+// The tokens of bins up to sub.bin0 (all_before), or of a subset, into rank 0's list: first
+// into one of this CTA's, then all of them with one reservation.  Whole CTA; the list's
+// length is in rank 0's n behind the next cluster barrier (more than kCandidates: it does
+// not hold them).
+template <bool BF16>
+__device__ void gather(const Row<BF16>& r, Control& ctl, const Subset& sub, bool all_before) {
+  const int tid = threadIdx.x;
+  if (tid == 0) ctl.local_n = 0u;
+  __syncthreads();
+  const float edge = static_cast<float>(sub.bin0 + 1);  // bin() is below it where its product is
+  for (int i = tid; i < r.vecs; i += kThreads) {
+    const uint4 v = r.seg[i];
+    if (all_before) {
 #pragma unroll
       for (int m = 0; m < Row<BF16>::VE; ++m) {
         const float x = element<BF16>(v, m);
-        if (r.bin(x) != sub.bin0) continue;
-        const uint32_t key = key_of(x);
-        if (sub.shift < 32 && (key >> sub.shift) != sub.prefix) continue;
-        lo = min(lo, key);
-        hi = max(hi, key);
-        if (f.count <= kCandidates) {
-          const uint32_t at = atomicAdd(&leader->n, 1u);
-          if (at < kCandidates) {
-            leader->cand_key[at] = key;
-            leader->cand_at[at] = r.at0 + static_cast<uint32_t>(i * Row<BF16>::VE + m);
-            leader->cand_mass[at] = masses ? r.weight(x) : 0ull;
-          }
+        if ((r.max - x) * r.bin_scale < edge || x == r.max || sub.bin0 >= kBins - 1) {
+          const uint32_t at = atomicAdd(&ctl.local_n, 1u);
+          if (at < kCandidates) ctl.local_at[at] = static_cast<uint32_t>(i * Row<BF16>::VE + m);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < Row<BF16>::VE; ++m) {
+        const float x = element<BF16>(v, m);
+        if (sub.holds(r, x, key_of(x))) {
+          const uint32_t at = atomicAdd(&ctl.local_n, 1u);
+          if (at < kCandidates) ctl.local_at[at] = static_cast<uint32_t>(i * Row<BF16>::VE + m);
         }
       }
     }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) {
-      ctl.red[warp] = lo;
-      ctl.red2[warp] = hi;
+  }
+  __syncthreads();
+  Control* leader = cg::this_cluster().map_shared_rank(&ctl, 0);
+  if (tid == 0) ctl.local_base = atomicAdd(&leader->n, ctl.local_n);
+  __syncthreads();
+  const uint32_t base = ctl.local_base;
+  for (uint32_t i = tid; i < min(ctl.local_n, static_cast<uint32_t>(kCandidates)); i += kThreads) {
+    if (base + i < kCandidates) {
+      const uint32_t at = ctl.local_at[i];
+      const uint32_t word = reinterpret_cast<const uint32_t*>(r.seg)[BF16 ? at / 2 : at];
+      const float x = __uint_as_float(!BF16 ? word : at & 1 ? word & 0xFFFF0000u : word << 16);
+      leader->cand_key[base + i] = key_of(x);
+      leader->cand_at[base + i] = r.at0 + at;
     }
-    __syncthreads();
-    if (tid < C) {
-      for (int i = 0; i < kWarps; ++i) {
-        lo = min(lo, ctl.red[i]);
-        hi = max(hi, ctl.red2[i]);
-      }
-      Control* peer = cluster.map_shared_rank(&ctl, tid);
-      peer->key_min[R] = lo;
-      peer->key_max[R] = hi;
+  }
+}
+
+template <bool BF16>
+__device__ Items take_items(const Row<BF16>& r, const Control& ctl, uint32_t n) {
+  Items it;
+  it.kept = 0;
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const uint32_t at = threadIdx.x + i * kThreads;
+    it.key[i] = it.at[i] = 0u;
+    it.w[i] = 0ull;
+    if (at < n) {
+      it.key[i] = ctl.cand_key[at];
+      it.at[i] = ctl.cand_at[at];
+      it.w[i] = r.weight(value_of(it.key[i]));
+      it.kept |= 1u << i;
     }
-    cluster.sync();
-    lo = 0xFFFFFFFFu;
-    hi = 0u;
-    for (int c = 0; c < C; ++c) {
-      lo = min(lo, ctl.key_min[c]);
-      hi = max(hi, ctl.key_max[c]);
-    }
-    if (lo == hi) {  // equal logits: the first ones by number
-      const unsigned long long w = masses ? r.weight(value_of(lo)) : 0ull;
-      unsigned long long quota = by_mass ? (w ? (target - f.before_mass + w - 1) / w : f.count) : target - f.before;
-      if (quota > f.count) quota = f.count;
-      return End{lo, static_cast<uint32_t>(quota), f.before_mass + quota * w};
-    }
-    if (f.count <= kCandidates) {
-      if (R == 0) {
-        // a token's rank among them: those of a larger logit, or of the same and a lower number
-        const int n = static_cast<int>(f.count);
-        if (tid < n) {
-          const uint32_t key = ctl.cand_key[tid], at = ctl.cand_at[tid];
-          uint32_t rank = 0, equal = 0;
-          unsigned long long mass = f.before_mass;
-          for (int j = 0; j < n; ++j) {
-            const uint32_t k2 = ctl.cand_key[j];
-            const bool same = k2 == key && ctl.cand_at[j] < at;
-            if (k2 > key || same) {
-              ++rank;
-              mass += ctl.cand_mass[j];
-            }
-            if (same) ++equal;
-          }
-          const unsigned long long w = ctl.cand_mass[tid];
-          const bool last = by_mass ? mass < target && mass + w >= target : f.before + rank + 1 == target;
-          if (last) {
-            for (int c = 0; c < C; ++c) cluster.map_shared_rank(&ctl, c)->end = End{key, equal + 1, mass + w};
-          }
-        }
-      }
-      cluster.sync();
-      return ctl.end;
-    }
-    // many, and not all equal: by the next bits of the key
+  }
+  return it;
+}
+
+// Where the prefix of `target` tokens (or of tokens until their weights reach target)
+// ends, from its bin `f` of the level-0 histogram on.
+template <bool BF16>
+__device__ End find_end(const Row<BF16>& r, Control& ctl, uint32_t* const (&slice_count)[2], unsigned long long* const (&slice_mass)[2],
+                        bool by_mass, bool masses, unsigned long long target, Found f) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = cluster.num_blocks(), R = cluster.block_rank();
+  Subset sub{f.bin, 32, 0u};
+  while (f.count > kCandidates && sub.shift > (BF16 ? 16 : 0)) {  // by the next bits of the logit
     histogram(r, ctl, slice_count[1], slice_mass[1], masses, 1, sub);
     const Found next = find_bin(ctl, slice_count[1], slice_mass[1], by_mass, target, 1, f);
     const int low = sub.shift - kDigit, digit = kBins - 1 - next.bin;
@@ -437,10 +738,35 @@ __device__ End find_end(const Row<BF16>& r, Control& ctl, uint32_t* const (&slic
     sub.shift = max(low, 0);
     f = next;
   }
+  if (f.count > kCandidates) {
+    // all bits are known: equal logits, the first ones by number (of bf16 the last bits are 0, but for
+    // the sign's complement)
+    uint32_t key = sub.prefix << sub.shift;
+    if (BF16 && !(key & 0x80000000u)) key |= 0xFFFFu;
+    const unsigned long long w = masses ? r.weight(value_of(key)) : 0ull;
+    unsigned long long quota = by_mass ? (w ? (target - f.before_mass + w - 1) / w : f.count) : target - f.before;
+    if (quota > f.count) quota = f.count;
+    return End{key, static_cast<uint32_t>(quota), f.before_mass + quota * w};
+  }
+  gather(r, ctl, sub, false);
+  cluster.sync();
+  if (R == 0) {
+    const Items it = take_items(r, ctl, f.count);
+    const Selected s = select(ctl, it.key, it.w, it.kept, by_mass, masses, target, f.before, f.before_mass);
+    if (threadIdx.x == 0) {
+      const unsigned long long w = masses ? r.weight(value_of(s.key)) : 0ull;
+      unsigned long long quota = by_mass ? (w ? (target - s.before_mass + w - 1) / w : s.count) : target - s.before;
+      if (quota > s.count) quota = s.count;
+      const End e{s.key, static_cast<uint32_t>(quota), s.before_mass + quota * w};
+      for (int c = 0; c < C; ++c) cluster.map_shared_rank(&ctl, c)->end = e;
+    }
+  }
+  cluster.sync();
+  return ctl.end;
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a, int chunk) {
+__global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int chunk) {
   extern __shared__ __align__(16) uint8_t smem[];
   cg::cluster_group cluster = cg::this_cluster();
   constexpr int VE = Row<BF16>::VE;
@@ -467,8 +793,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a, int chu
   const int end = mis + a.V;  // places of the row are [mis, end)
   const uint4* const base = reinterpret_cast<const uint4*>(row - (reinterpret_cast<uintptr_t>(row) & 15));
   const int v0 = R * per;
-  float mx = -INFINITY;
-  int nan = 0;
+  float mx = -INFINITY;  // NaN as soon as one is seen
   constexpr uint32_t kNone = BF16 ? 0xFF80FF80u : 0xFF800000u;
   constexpr int kUnroll = 8;
   for (int i0 = tid; i0 < per; i0 += kThreads * kUnroll) {
@@ -503,19 +828,19 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a, int chu
       if (i < per) seg[i] = v[u];
 #pragma unroll
       for (int m = 0; m < VE; ++m) {
-        const float x = element<BF16>(v[u], m);
-        nan |= x != x;
-        mx = fmaxf(mx, x);
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(mx) : "f"(element<BF16>(v[u], m)));
       }
     }
   }
+  const float own_max = mx;
   if (tid < 64) ctl.exp2_table[tid] = kExp2[tid];
   if (tid == 0) {
     const double c = 1.4426950408889634074 / static_cast<double>(temperature);
     ctl.c_hi = static_cast<float>(c);
     ctl.c_lo = static_cast<float>(c - static_cast<double>(ctl.c_hi));
   }
-  const int any_nan = __syncthreads_or(nan);
+  //@load
+  const int any_nan = __syncthreads_or(mx != mx);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
   if (lane == 0) ctl.red[warp] = __float_as_uint(mx);
@@ -527,6 +852,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a, int chu
     peer->nan[R] = any_nan;
   }
   cluster.sync();
+  //@maxsync
   bool bad = !(temperature >= 0.0f);
   mx = -INFINITY;
   for (int c = 0; c < C; ++c) {
@@ -574,49 +900,152 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a, int chu
   r.max = mx;
   r.c_hi = ctl.c_hi;
   r.c_lo = ctl.c_lo;
-  r.table = ctl.exp2_table;
+  r.table = smem_u32(ctl.exp2_table);
   // the first histogram spans what has weight (e^-30), and eight units of the logits at least
   r.bin_scale = kBins / fmaxf(30.0f * 1.4426950f / r.c_hi, 8.0f);
 
+  const unsigned long long least = fixed_of(fminf(min_p, 1.0f), kOneBits);
+  const float u = fminf(fmaxf(a.u[t], 0.0f), 0x1.fffffep-1f);
+  const unsigned long long u64 = fixed_of(u, 64);
+  auto log_share = [&](float x, unsigned long long w, unsigned long long total) {
+    // by the difference where the token has most of the weight, else by the logit
+    if (w > total / 4) return -log1pf(static_cast<float>(total - w) / static_cast<float>(w));
+    return (x - mx) * (r.c_hi * 0.69314718f) - logf(static_cast<float>(total) * 0x1p-43f);
+  };
+
   // ---- the kept prefix
   const bool by_k = top_k > 0 && top_k < a.V, by_p = top_p < 1.0f;
+  // a token is kept while the weight before it is below p times the whole: the whole
+  // numbers below that product are those below its ceiling
+  const unsigned long long p64 = by_p ? fixed_of(top_p, 64) : 0ull;
+  auto p_target = [&](unsigned long long mass) {
+    const unsigned long long target = __umul64hi(p64, mass) + (p64 * mass ? 1ull : 0ull);
+    return target ? target : 1ull;
+  };
   End kept{0u, UINT_MAX, 0ull};
   if (by_k || by_p) {
-    histogram(r, ctl, slice_count[0], slice_mass[0], by_p, 0, Subset{0, 32, 0u});
-    unsigned long long mass = 0;
-    for (int c = 0; c < C; ++c) mass += ctl.slice_mass[0][c];
-    if (by_k) {
-      kept = find_end(r, ctl, slice_count, slice_mass, false, by_p, static_cast<unsigned long long>(top_k));
-      mass = kept.mass;
+    unsigned long long target = static_cast<unsigned long long>(top_k);
+    // With a small top-k: where so many threads' own maxima lie, so many tokens do, and few
+    // others, so the histogram is one of maxima: one addition a thread, no weights.
+    const bool maxima = by_k && top_k <= kCandidates * 3 / 4 && top_k <= C * kThreads / 3;
+    bool masses = by_p && !maxima;
+    Found f;
+    if (maxima) {
+      histogram_begin(ctl);
+      if (own_max > -INFINITY) atomicAdd(&ctl.hist_count[r.bin(own_max)], 1u);
+      histogram_merge(ctl, slice_count[0], slice_mass[0], false, 0);
+      f = find_bin(ctl, slice_count[0], slice_mass[0], false, target, 0, Found{});
+    } else {
+      histogram(r, ctl, slice_count[0], slice_mass[0], masses, 0, Subset{0, 32, 0u});
+      if (!by_k) {
+        unsigned long long mass = 0;
+        for (int c = 0; c < C; ++c) mass += ctl.slice_mass[0][c];
+        target = p_target(mass);
+      }
+      f = find_bin(ctl, slice_count[0], slice_mass[0], !by_k, target, 0, Found{});
     }
-    if (by_p) {
-      // a token is kept while the weight before it is below p times the whole: the whole
-      // numbers below that product are those below its ceiling
-      const unsigned long long p = top_p > 0.0f ? static_cast<unsigned long long>(static_cast<double>(top_p) * 0x1p64) : 0ull;
-      unsigned long long target = __umul64hi(p, mass) + (p * mass ? 1ull : 0ull);
-      if (target == 0) target = 1;
-      kept = find_end(r, ctl, slice_count, slice_mass, true, true, target);
+    //@bin
+    if (maxima || f.before + f.count <= kCandidates) {
+      // ---- few tokens: one CTA does the rest
+      gather(r, ctl, Subset{f.bin, 32, 0u}, true);
+      cluster.sync();
+      const uint32_t n = *cluster.map_shared_rank(&ctl.n, 0);
+      if (n <= kCandidates && n >= static_cast<uint32_t>(by_k ? top_k : 1)) {
+        cluster.sync();  // from here on no CTA touches another's memory
+        if (R != 0) return;
+        //@gather
+        const float near_scale = r.bin_scale * (2 * kThreads) / static_cast<float>(f.bin + 1);
+        Items it = take_items(r, ctl, n);
+        keep_prefix(r, ctl, it, near_scale, !by_k, target);
+        //@prefix
+        if (by_k && by_p) {
+          unsigned long long mass = 0;
+#pragma unroll
+          for (int i = 0; i < kItems; ++i) mass += it.kept >> i & 1 ? it.w[i] : 0ull;
+          keep_prefix(r, ctl, it, near_scale, true, p_target(block_sum(ctl, mass)));
+        }
+        //@prefix2
+        unsigned long long mass = 0, order[kItems];
+        int bin[kItems];
+        const float places = (2 * kThreads) / (static_cast<float>(a.V) + 16.0f);
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+          if (it.w[i] < least) it.kept &= ~(1u << i);
+          mass += it.kept >> i & 1 ? it.w[i] : 0ull;
+          order[i] = it.at[i];
+          bin[i] = min(2 * kThreads - 1, __float2int_rz(static_cast<float>(it.at[i]) * places));
+        }
+        const unsigned long long total = block_sum(ctl, mass), draw = __umul64hi(u64, total) + 1;
+        bool done;
+        unsigned long long drawn = select_near(ctl, bin, order, it.w, it.kept, true, draw, done);
+        if (!done) {
+          uint32_t at[kItems];
+#pragma unroll
+          for (int i = 0; i < kItems; ++i) at[i] = ~it.at[i];
+          drawn = ~select(ctl, at, it.w, it.kept, true, true, draw, 0u, 0ull).key;
+        }
+        //!END
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+          if ((it.kept >> i & 1) && it.at[i] == static_cast<uint32_t>(drawn)) {
+            a.tokens[t] = static_cast<int32_t>(it.at[i]) - mis;
+            if (a.logp) a.logp[t] = log_share(value_of(it.key[i]), it.w[i], total);
+          }
+        }
+        return;
+      }
+      // more of them than the list holds (or, of maxima, fewer): the whole histogram
+      cluster.sync();
+      if (maxima) {
+        masses = by_p;
+        histogram(r, ctl, slice_count[0], slice_mass[0], masses, 0, Subset{0, 32, 0u});
+        f = find_bin(ctl, slice_count[0], slice_mass[0], false, target, 0, Found{});
+      }
+    }
+    kept = find_end(r, ctl, slice_count, slice_mass, !by_k, masses, target, f);
+    if (by_k && by_p) {
+      target = p_target(kept.mass);
+      f = find_bin(ctl, slice_count[0], slice_mass[0], true, target, 0, Found{});
+      kept = find_end(r, ctl, slice_count, slice_mass, true, true, target, f);
     }
   }
 
   // ---- kept weights by warp (runs of the row in order)
-  const unsigned long long least =
-      min_p > 0.0f ? static_cast<unsigned long long>(static_cast<double>(fminf(min_p, 1.0f)) * 0x1p43) : 0ull;
   const unsigned long long w_end = r.weight(value_of(kept.key));
   const uint32_t quota = w_end >= least ? kept.quota : 0u;
   unsigned long long mass = 0;
   uint32_t eq = 0;
-  for (int i = warp * chunk + lane; i < (warp + 1) * chunk; i += 32) {
-    const uint4 v = seg[i];
+  if (!by_k && !by_p && !least) {  // all of them
+#pragma unroll 2
+    for (int i = warp * chunk + lane; i < (warp + 1) * chunk; i += 32) {
+      const uint4 v = seg[i];
 #pragma unroll
-    for (int m = 0; m < VE; ++m) {
-      const float x = element<BF16>(v, m);
-      const uint32_t key = key_of(x);
-      if (key > kept.key) {
-        const unsigned long long w = r.weight(x);
-        mass += w >= least ? w : 0ull;
+      for (int m = 0; m < VE; ++m) mass += r.weight(element<BF16>(v, m));
+    }
+  } else {
+    // A piece's weights are worked out side by side, whether kept or not, unless the whole
+    // warp has none that is (what min-p drops lies below log2 of it, with some room).
+    const float low = least ? fmaf(log2f(fminf(min_p, 1.0f)), 1.0001f, -0.001f) : -INFINITY;
+    for (int i0 = warp * chunk; i0 < (warp + 1) * chunk; i0 += 32) {
+      const int i = i0 + lane;
+      uint4 v = make_uint4(kNone, kNone, kNone, kNone);
+      if (i < (warp + 1) * chunk) v = seg[i];
+      bool in[VE], any = false;
+#pragma unroll
+      for (int m = 0; m < VE; ++m) {
+        const float x = element<BF16>(v, m);
+        const uint32_t key = key_of(x);
+        in[m] = key > kept.key && !((x - mx) * r.c_hi < low);
+        any |= in[m];
+        eq += key == kept.key && i < (warp + 1) * chunk;
       }
-      eq += key == kept.key;
+      if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+        for (int m = 0; m < VE; ++m) {
+          const unsigned long long w = r.weight(element<BF16>(v, m));
+          mass += in[m] && w >= least ? w : 0ull;
+        }
+      }
     }
   }
 #pragma unroll
@@ -632,6 +1061,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a, int chu
   if (tid == 0) ctl.hit_warp = -1;
   cluster.sync();  // from here on no CTA touches another's memory
 
+  //@weights
   // ---- the warp in whose run the random number falls
   if (warp == 0) {
     constexpr int kPer = kMaxCluster * kWarps / 32;
@@ -668,8 +1098,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a, int chu
       if (lane >= d) in += y;
     }
     const unsigned long long total = __shfl_sync(0xffffffffu, in, 31);
-    const float u = fminf(fmaxf(a.u[t], 0.0f), 0x1.fffffep-1f);
-    const unsigned long long target = __umul64hi(static_cast<unsigned long long>(static_cast<double>(u) * 0x1p64), total);
+    const unsigned long long target = __umul64hi(u64, total);
     unsigned long long before = in - run;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -685,6 +1114,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a, int chu
     }
   }
   __syncthreads();
+  //!END
   if (warp != ctl.hit_warp) return;
 
   // ---- its run in order: 32 pieces at a time
@@ -735,11 +1165,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a, int chu
         const unsigned long long w = kept_weight(x, rank);
         if (at <= target && target < at + w) {
           a.tokens[t] = (v0 + i) * VE + m - mis;
-          if (a.logp) {
-            // by the difference where the token has most of the weight, else by the logit
-            if (w > total / 4) a.logp[t] = -log1pf(static_cast<float>(total - w) / static_cast<float>(w));
-            else a.logp[t] = (x - mx) * (r.c_hi * 0.69314718f) - logf(static_cast<float>(total) * 0x1p-43f);
-          }
+          if (a.logp) a.logp[t] = log_share(x, w, total);
         }
         at += w;
       }
@@ -750,11 +1176,15 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a, int chu
   }
 }
 
-// CTAs of a row: a power of two, so that a CTA has some 64 KB of it at most.
-int cluster_of(int V, bool bf16) {
+// CTAs of a row, a power of two.  Few rows are spread as wide as it goes, down to 16 KB a
+// CTA; with more rows than the SMs take at once a CTA has up to 64 KB, as what it does for a
+// cluster's sake is the same for less (in us, by 16 / 64 KB: one row of 5000 16.1 / 19.5; 256
+// rows of 131072 in bf16 167 / 151, 500 of 20000 in fp32 178 / 85).
+int cluster_of(int T, int V, bool bf16) {
   const int64_t bytes = static_cast<int64_t>(V) * (bf16 ? 2 : 4);
   int C = 1;
-  while (C < kMaxCluster && bytes > static_cast<int64_t>(C) * 16384) C *= 2;
+  while (C < kMaxCluster && (bytes > static_cast<int64_t>(C) * 65536 || (bytes > static_cast<int64_t>(C) * 16384 && static_cast<int64_t>(T) * C <= 152)))
+    C *= 2;
   return C;
 }
 
@@ -762,10 +1192,10 @@ struct Plan {
   int C, chunk;
   size_t smem;
 };
-Plan plan_of(int V, bool bf16) {
+Plan plan_of(int T, int V, bool bf16) {
   const int VE = bf16 ? 8 : 4;
   Plan p;
-  p.C = cluster_of(V, bf16);
+  p.C = cluster_of(T, V, bf16);
   const int64_t vecs = (static_cast<int64_t>(V) + 2 * (VE - 1)) / VE + 1;  // wherever the row starts
   p.chunk = static_cast<int>((vecs + p.C * kWarps - 1) / (p.C * kWarps));
   p.smem = static_cast<size_t>(p.chunk) * kWarps * 16 + sizeof(Control) + static_cast<size_t>(kBins / p.C) * 2 * 12;
@@ -775,10 +1205,10 @@ Plan plan_of(int V, bool bf16) {
 }  // namespace
 
 // what eight CTAs' shared memory holds
-bool sample_supported(int V, bool bf16) { return V <= (bf16 ? 800000 : 400000) && plan_of(V, bf16).smem <= 227 * 1024; }
+bool sample_supported(int V, bool bf16) { return V <= (bf16 ? 800000 : 400000) && plan_of(1, V, bf16).smem <= 227 * 1024; }
 
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s) {
-  const Plan p = plan_of(a.V, a.bf16 != 0);
+  const Plan p = plan_of(a.T, a.V, a.bf16 != 0);
   void (*kernel)(SampleArgs, int) = a.bf16 ? k_sample<true> : k_sample<false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return e;

@@ -510,7 +510,7 @@ MX_API int mx_rope_table(int rot_dim, double base, int scaling, double factor, d
  *   positions [T] int32 or NULL: the angles' positions; without them a token's place in
  *     its sequence.  They do not move the place that is written.
  *   turns [rot_dim / 2] on the device, amplitude: mx_rope_table's.  An angle is exact
- *     to 2^-25 turns at any position.
+ *     to 2^-32 turns at any position.
  * Tokens that are skipped leave their rows of q_out as they were.
  * Errors: as mx_kv_append (with q, q_out and their strides), plus MX_ERR_INVALID_ARG (an
  * unknown layout, rot_dim < 0 or > head_dim, amplitude not finite, q without q_out) and
