@@ -148,6 +148,19 @@ struct KvArgs {
 cudaError_t launch_kv_append(const KvArgs& a, cudaStream_t s);
 cudaError_t launch_kv_read(const KvArgs& a, cudaStream_t s);
 
+// Division by a number that the host knows, of 0 <= n < 2^31, in three
+// instructions: with 2^l >= d the error of m = 2^(31 + l) / d + 1 is below 1 / n.
+struct FastDiv {
+  uint32_t m;
+  int shift;
+  static FastDiv by(int d) {
+    int l = 0;
+    while ((1ll << l) < d) ++l;
+    return {static_cast<uint32_t>((1ull << (31 + l)) / d + 1), 31 + l};
+  }
+  __host__ __device__ int of(int n) const { return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * m) >> shift); }
+};
+
 // ---- rope.cu
 struct RopeArgs {
   KvArgs kv;
@@ -205,19 +218,6 @@ cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
 
 // ---- attn_rows.cu, attn_chunk.cu
 constexpr int kAttnMaxCtas = 608;                    // 152 SMs x 4: partial slots and counters of the workspace
-// Division by a number that the host knows, of 0 <= n < 2^31, in three
-// instructions: with 2^l >= d the error of m = 2^(31 + l) / d + 1 is below 1 / n.
-struct FastDiv {
-  uint32_t m;
-  int shift;
-  static FastDiv by(int d) {
-    int l = 0;
-    while ((1ll << l) < d) ++l;
-    return {static_cast<uint32_t>((1ull << (31 + l)) / d + 1), 31 + l};
-  }
-  __host__ __device__ int of(int n) const { return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * m) >> shift); }
-};
-
 struct AttnArgs {
   const void* q;                                     // bf16 [T, n_heads, head_dim]
   int64_t q_stride;                                  // elements between tokens

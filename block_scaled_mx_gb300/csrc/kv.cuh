@@ -55,7 +55,7 @@ __device__ __forceinline__ int64_t token_row(const KvArgs& a, int t, int lane, i
     if (lane == 0) set_status(a.status, MX_ERR_DEVICE_ARG);
     return -1;
   }
-  const int p = static_cast<int>(pos / a.page_size);
+  const int p = static_cast<int>(pos) / a.page_size;  // positions are ints: kv has been checked
   const int page = a.block_table[static_cast<int64_t>(lo) * a.max_pages + p];
   if (page < 0 || page >= a.num_pages) {
     if (lane == 0) set_status(a.status, MX_ERR_DEVICE_ARG);
