@@ -43,40 +43,40 @@ constexpr int kMaxCluster = 8;
 constexpr int kOneBits = 43;
 constexpr unsigned long long kOne = 1ull << kOneBits;  // the largest weight; 2^20 of them fit 64 bits
 
-// 2^(j/64) as the sum of two floats.
-__constant__ float2 kExp2[64] = {
-    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.02c9a40000000p+0f, -0x1.887fa00000000p-28f},
-    {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f}, {0x1.0874520000000p+0f, -0x1.e2990e0000000p-26f},
-    {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f}, {0x1.0e3ec40000000p+0f, -0x1.a585cc0000000p-25f},
-    {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f}, {0x1.1429aa0000000p+0f, 0x1.d525bc0000000p-25f},
-    {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.1a35be0000000p+0f, 0x1.6df96e0000000p-25f},
-    {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f}, {0x1.2063b80000000p+0f, 0x1.0c519a0000000p-25f},
-    {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}, {0x1.26b4560000000p+0f, 0x1.789f380000000p-26f},
-    {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f}, {0x1.2d285a0000000p+0f, 0x1.b900c20000000p-26f},
-    {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f}, {0x1.33c08c0000000p+0f, -0x1.b37d200000000p-25f},
-    {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f}, {0x1.3a7db40000000p+0f, -0x1.634c020000000p-25f},
-    {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}, {0x1.4160a20000000p+0f, 0x1.f72e2a0000000p-28f},
-    {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f}, {0x1.486a2c0000000p+0f, -0x1.47d8660000000p-25f},
-    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.4f9b280000000p+0f, -0x1.2c5a6c0000000p-25f},
-    {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f}, {0x1.56f4740000000p+0f, -0x1.295b040000000p-25f},
-    {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f}, {0x1.5e76f20000000p+0f, -0x1.4a5bd60000000p-25f},
-    {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f}, {0x1.6623880000000p+0f, 0x1.2a91120000000p-27f},
-    {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.6dfb240000000p+0f, -0x1.cd72e80000000p-27f},
-    {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f}, {0x1.75feb60000000p+0f, -0x1.37b3060000000p-25f},
-    {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}, {0x1.7e2f340000000p+0f, -0x1.2616340000000p-25f},
-    {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f}, {0x1.868d9a0000000p+0f, -0x1.2edb440000000p-26f},
-    {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f}, {0x1.8f1aea0000000p+0f, -0x1.baa2320000000p-26f},
-    {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f}, {0x1.97d82a0000000p+0f, -0x1.0d8d840000000p-31f},
-    {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}, {0x1.a0c6680000000p+0f, -0x1.2886a60000000p-26f},
-    {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f}, {0x1.a9e6b60000000p+0f, -0x1.50c0480000000p-25f},
-    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.b33a2c0000000p+0f, -0x1.ec3a820000000p-26f},
-    {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f}, {0x1.bcc1ea0000000p+0f, -0x1.f687c60000000p-25f},
-    {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f}, {0x1.c67f120000000p+0f, 0x1.cafa2a0000000p-25f},
-    {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f}, {0x1.d072d40000000p+0f, 0x1.40f1300000000p-25f},
-    {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.da9e600000000p+0f, 0x1.ed99420000000p-27f},
-    {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f}, {0x1.e502ee0000000p+0f, 0x1.e2cffe0000000p-26f},
-    {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.efa1be0000000p+0f, 0x1.cc2b440000000p-25f},
-    {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}, {0x1.fa7c180000000p+0f, 0x1.9e90d80000000p-28f},
+// 2^(j/64): 2^43 times it as a whole number (low word, high word), and as a float's bits.
+__constant__ uint4 kExp2[64] = {
+    {0x0u, 0x800u, 0x3f800000u, 0u}, {0x4d1f3bc0u, 0x816u, 0x3f8164d2u, 0u},
+    {0xd8698ac3u, 0x82cu, 0x3f82cd87u, 0u}, {0xa28c3aceu, 0x843u, 0x3f843a29u, 0u},
+    {0xac367cc5u, 0x85au, 0x3f85aac3u, 0u}, {0xf61969e9u, 0x871u, 0x3f871f62u, 0u},
+    {0x80e8092eu, 0x889u, 0x3f88980fu, 0u}, {0x4d575497u, 0x8a1u, 0x3f8a14d5u, 0u},
+    {0x5c1e3ea9u, 0x8b9u, 0x3f8b95c2u, 0u}, {0xadf5b7e6u, 0x8d1u, 0x3f8d1adfu, 0u},
+    {0x4398b45du, 0x8eau, 0x3f8ea43au, 0u}, {0x1dc43146u, 0x903u, 0x3f9031dcu, 0u},
+    {0x3d373ab1u, 0x91cu, 0x3f91c3d3u, 0u}, {0xa2b2f13eu, 0x935u, 0x3f935a2bu, 0u},
+    {0x4efa8fefu, 0x94fu, 0x3f94f4f0u, 0u}, {0x42d37202u, 0x969u, 0x3f96942du, 0u},
+    {0x7f0518dcu, 0x983u, 0x3f9837f0u, 0u}, {0x459320bu, 0x99eu, 0x3f99e046u, 0u},
+    {0xd39b9d55u, 0x9b8u, 0x3f9b8d3au, 0u}, {0xed9a72d0u, 0x9d3u, 0x3f9d3edau, 0u},
+    {0x5326091au, 0x9efu, 0x3f9ef532u, 0u}, {0x510fb97u, 0xa0bu, 0x3fa0b051u, 0u},
+    {0x43030c5u, 0xa27u, 0x3fa27043u, 0u}, {0x515ae09eu, 0xa43u, 0x3fa43516u, 0u},
+    {0xed6a9b15u, 0xa5fu, 0x3fa5fed7u, 0u}, {0xd93b4e96u, 0xa7cu, 0x3fa7cd94u, 0u},
+    {0x15ab4ea8u, 0xa9au, 0x3fa9a15bu, 0u}, {0xa39b5a94u, 0xab7u, 0x3fab7a3au, 0u},
+    {0x83eea42au, 0xad5u, 0x3fad583fu, 0u}, {0xb78ad691u, 0xaf3u, 0x3faf3b79u, 0u},
+    {0x3f581d2bu, 0xb12u, 0x3fb123f6u, 0u}, {0x1c412a91u, 0xb31u, 0x3fb311c4u, 0u},
+    {0x4f333f9eu, 0xb50u, 0x3fb504f3u, 0u}, {0xd91e328du, 0xb6fu, 0x3fb6fd92u, 0u},
+    {0xbaf47630u, 0xb8fu, 0x3fb8fbafu, 0u}, {0xf5ab2134u, 0xbafu, 0x3fbaff5bu, 0u},
+    {0x8a39f581u, 0xbd0u, 0x3fbd08a4u, 0u}, {0x799b67a7u, 0xbf1u, 0x3fbf179au, 0u},
+    {0xc4cca667u, 0xc12u, 0x3fc12c4du, 0u}, {0x6ccda249u, 0xc34u, 0x3fc346cdu, 0u},
+    {0x72a11550u, 0xc56u, 0x3fc5672au, 0u}, {0xd74c8abcu, 0xc78u, 0x3fc78d75u, 0u},
+    {0x9bd866e3u, 0xc9bu, 0x3fc9b9beu, 0u}, {0xc14fef27u, 0xcbeu, 0x3fcbec15u, 0u},
+    {0x48c151f8u, 0xce2u, 0x3fce248cu, 0u}, {0x333daef3u, 0xd06u, 0x3fd06334u, 0u},
+    {0x81d91f13u, 0xd2au, 0x3fd2a81eu, 0u}, {0x35aabcffu, 0xd4fu, 0x3fd4f35bu, 0u},
+    {0x4fccad6au, 0xd74u, 0x3fd744fdu, 0u}, {0xd15c278bu, 0xd99u, 0x3fd99d16u, 0u},
+    {0xbb797dafu, 0xdbfu, 0x3fdbfbb8u, 0u}, {0xf4825e1u, 0xde6u, 0x3fde60f5u, 0u},
+    {0xcdeec2a9u, 0xe0cu, 0x3fe0ccdfu, 0u}, {0xf8972be9u, 0xe33u, 0x3fe33f89u, 0u},
+    {0x906e77c8u, 0xe5bu, 0x3fe5b907u, 0u}, {0x96a503c5u, 0xe83u, 0x3fe8396au, 0u},
+    {0xc6e7dd2u, 0xeacu, 0x3feac0c7u, 0u}, {0xf301ed99u, 0xed4u, 0x3fed4f30u, 0u},
+    {0x4b99bdceu, 0xefeu, 0x3fefe4bau, 0u}, {0x1773c5a0u, 0xf28u, 0x3ff28177u, 0u},
+    {0x57d15248u, 0xf52u, 0x3ff5257du, 0u}, {0xdf730adu, 0xf7du, 0x3ff7d0dfu, 0u},
+    {0x3b2db723u, 0xfa8u, 0x3ffa83b3u, 0u}, {0xe0c0cf48u, 0xfd3u, 0x3ffd3e0cu, 0u},
 };
 
 // Where the kept prefix ends: the bin, what lies before it, what it holds.
@@ -122,7 +122,7 @@ struct Control {
   unsigned long long hit_before, total, target;
   uint32_t red[kWarps], red2[kWarps];
   unsigned long long red64[kWarps];
-  float2 exp2_table[64];
+  uint4 exp2_table[64];
   union {
     struct {
       uint32_t hist_count[kBins], hist_lo[kBins], hist_hi[kBins];
@@ -154,30 +154,22 @@ __device__ __forceinline__ unsigned long long fixed_of(float x, int bits) {
   return up >= 0 ? m << up : up > -24 ? m >> -up : 0ull;
 }
 
-// 2^43 e^((x - max) / temperature), rounded down; c_hi + c_lo = log2(e) / temperature.
-// Without branches, so that a thread's weights go side by side.
-__device__ __forceinline__ unsigned long long weight_of(float x, float max, float c_hi, float c_lo, uint32_t table) {
-  const float s = x - max;
-  const float t0 = s * c_hi;
-  const bool some = t0 > -44.0f;  // not for -inf, nor for NaN of an infinite maximum
-  const float t = some ? t0 : 0.0f;
-  // x - max = s + e exactly (the error of a sum of two floats), its product likewise
-  const float v = s - x;
-  const float e = (x - (s - v)) - (max + v);
-  const float t_lo = fmaf(s, c_hi, -t) + fmaf(s, c_lo, e * c_hi);
-  const float shifted = t + 196608.0f;  // 1.5 * 2^17: the sum's last place is 2^-6
-  const int j = __float_as_int(shifted) - 0x48400000;
-  const float f = (t - (shifted - 196608.0f)) + t_lo;
-  // 2^f - 1 for |f| <= 2^-7: the next term is below 2^-44
-  const float q = f * fmaf(f, fmaf(f, fmaf(f, 9.6181291e-3f, 5.5504109e-2f), 0.24022651f), 0.69314718f);
-  float2 p;
-  asm("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(p.x), "=f"(p.y) : "r"(table + (j & 63) * 8));
-  // (p.x + lo) 2^43 with p.x's 24 bits as they are, then down by whole powers of two
-  const uint32_t whole = (__float_as_uint(p.x) & 0x7FFFFFu) | 0x800000u;
-  const int part = __float2int_rn(fmaf(p.x, q, p.y) * 0x1p36f);  // below 2^-6 in size
-  const unsigned long long sum = (static_cast<unsigned long long>(whole) << (kOneBits - 23)) + (static_cast<long long>(part) << (kOneBits - 36));
-  const unsigned long long w = sum >> (-(j >> 6) & 63);
-  return x == max ? kOne : some ? w : 0ull;
+// mx = max(mx, the piece's elements), NaN where one is.
+template <bool BF16>
+__device__ __forceinline__ void piece_max(const uint4& v, float& mx) {
+  if (BF16) {
+    uint32_t a, b;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(mx) : "f"(__uint_as_float(a << 16)));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(mx) : "f"(__uint_as_float(a & 0xFFFF0000u)));
+  } else {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(mx) : "f"(__uint_as_float(v.x)));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(mx) : "f"(__uint_as_float(v.y)));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(mx) : "f"(__uint_as_float(v.z)));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(mx) : "f"(__uint_as_float(v.w)));
+  }
 }
 
 template <bool BF16>
@@ -198,9 +190,37 @@ struct Row {
   const uint4* seg;
   int vecs;           // of the segment
   uint32_t at0;       // place of its first element
-  float max, c_hi, c_lo, bin_scale;
-  uint32_t table;     // shared-memory address of 2^(j/64)
-  __device__ __forceinline__ unsigned long long weight(float x) const { return weight_of(x, max, c_hi, c_lo, table); }
+  float max, least;   // the row's largest logit; the least one with a weight
+  float c_hi, c_lo;   // log2(e) / temperature
+  float bin_scale;
+  uint32_t table;     // shared-memory address of kExp2
+  // 2^43 e^((x - max) / temperature), rounded down.  Without branches, so that a thread's
+  // weights go side by side.
+  __device__ __forceinline__ unsigned long long weight(float x) const {
+    if (max == INFINITY) return x == max ? kOne : 0ull;
+    const bool none = x < least;  // -inf among them
+    x = fmaxf(x, least);
+    const float s = x - max;
+    const float t = s * c_hi;
+    float t_lo = fmaf(s, c_lo, fmaf(s, c_hi, -t));
+    if (!BF16) {
+      // x - max = s + e exactly (the error of a sum of two floats); of 8-bit significands s is
+      // exact, but for logits below 2^-16 of the largest (there 2^-22 of a weight)
+      const float v = s - x;
+      t_lo = fmaf((x - (s - v)) - (max + v), c_hi, t_lo);
+    }
+    const float shifted = t + 196608.0f;  // 1.5 * 2^17: the sum's last place is 2^-6, its last bits t's
+    const uint32_t bits = __float_as_uint(shifted);
+    const float f = (t - (shifted - 196608.0f)) + t_lo;
+    // 2^36 (2^f - 1) for |f| <= 2^-7: the next term is below 2^-44 of the weight
+    const float q = f * fmaf(f, fmaf(f, fmaf(f, 9.6181291e-3f * 0x1p36f, 5.5504109e-2f * 0x1p36f), 0.24022651f * 0x1p36f), 0.69314718f * 0x1p36f);
+    uint32_t lo, hi, p, unused;
+    asm("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(lo), "=r"(hi), "=r"(p), "=r"(unused) : "r"(table + (bits & 63u) * 16u));
+    const unsigned long long whole = static_cast<unsigned long long>(hi) << 32 | lo;
+    const long long part = static_cast<long long>(__float2int_rn(__uint_as_float(p) * q)) * (1 << (kOneBits - 36));  // below 2^-6 in size
+    const unsigned long long w = (whole + part) >> ((0x4840003Fu - bits) >> 6);
+    return none ? 0ull : w;
+  }
   // Bins of the first histogram: more for lower logits, by a function that keeps order.
   __device__ __forceinline__ int bin(float x) const {
     return x == max ? 0 : min(kBins - 1, __float2int_rz((max - x) * bin_scale));
@@ -664,27 +684,23 @@ __device__ void gather(const Row<BF16>& r, Control& ctl, const Subset& sub, bool
   const int tid = threadIdx.x;
   if (tid == 0) ctl.local_n = 0u;
   __syncthreads();
-  const float edge = static_cast<float>(sub.bin0 + 1);  // bin() is below it where its product is
+  // some more than the bins' tokens do no harm: the list is ranked exactly
+  const float edge = sub.bin0 >= kBins - 1 ? -INFINITY : r.max - static_cast<float>(sub.bin0 + 1) / r.bin_scale * 1.00001f;
+  auto take = [&](int at) {
+    const uint32_t n = atomicAdd(&ctl.local_n, 1u);
+    if (n < kCandidates) ctl.local_at[n] = static_cast<uint32_t>(at);
+  };
   for (int i = tid; i < r.vecs; i += kThreads) {
     const uint4 v = r.seg[i];
     if (all_before) {
+      float top = -INFINITY;
+      piece_max<BF16>(v, top);
+      if (!(top >= edge)) continue;
+    }
 #pragma unroll
-      for (int m = 0; m < Row<BF16>::VE; ++m) {
-        const float x = element<BF16>(v, m);
-        if ((r.max - x) * r.bin_scale < edge || x == r.max || sub.bin0 >= kBins - 1) {
-          const uint32_t at = atomicAdd(&ctl.local_n, 1u);
-          if (at < kCandidates) ctl.local_at[at] = static_cast<uint32_t>(i * Row<BF16>::VE + m);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int m = 0; m < Row<BF16>::VE; ++m) {
-        const float x = element<BF16>(v, m);
-        if (sub.holds(r, x, key_of(x))) {
-          const uint32_t at = atomicAdd(&ctl.local_n, 1u);
-          if (at < kCandidates) ctl.local_at[at] = static_cast<uint32_t>(i * Row<BF16>::VE + m);
-        }
-      }
+    for (int m = 0; m < Row<BF16>::VE; ++m) {
+      const float x = element<BF16>(v, m);
+      if (all_before ? x >= edge : sub.holds(r, x, key_of(x))) take(i * Row<BF16>::VE + m);
     }
   }
   __syncthreads();
@@ -826,20 +842,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
     for (int u = 0; u < kUnroll; ++u) {
       const int i = i0 + u * kThreads;
       if (i < per) seg[i] = v[u];
-#pragma unroll
-      for (int m = 0; m < VE; ++m) {
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(mx) : "f"(element<BF16>(v[u], m)));
-      }
+      piece_max<BF16>(v[u], mx);
     }
   }
   const float own_max = mx;
   if (tid < 64) ctl.exp2_table[tid] = kExp2[tid];
   if (tid == 0) {
-    const double c = 1.4426950408889634074 / static_cast<double>(temperature);
+    const double c = 1.4426950408889634074 / static_cast<double>(fminf(temperature, 0x1p100f));
     ctl.c_hi = static_cast<float>(c);
     ctl.c_lo = static_cast<float>(c - static_cast<double>(ctl.c_hi));
   }
-  //@load
   const int any_nan = __syncthreads_or(mx != mx);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -852,7 +864,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
     peer->nan[R] = any_nan;
   }
   cluster.sync();
-  //@maxsync
   bool bad = !(temperature >= 0.0f);
   mx = -INFINITY;
   for (int c = 0; c < C; ++c) {
@@ -901,6 +912,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
   r.c_hi = ctl.c_hi;
   r.c_lo = ctl.c_lo;
   r.table = smem_u32(ctl.exp2_table);
+  r.least = fmaxf(mx - 45.0f / r.c_hi, -3.402823466e38f);
   // the first histogram spans what has weight (e^-30), and eight units of the logits at least
   r.bin_scale = kBins / fmaxf(30.0f * 1.4426950f / r.c_hi, 8.0f);
 
@@ -944,7 +956,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
       }
       f = find_bin(ctl, slice_count[0], slice_mass[0], !by_k, target, 0, Found{});
     }
-    //@bin
     if (maxima || f.before + f.count <= kCandidates) {
       // ---- few tokens: one CTA does the rest
       gather(r, ctl, Subset{f.bin, 32, 0u}, true);
@@ -953,18 +964,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
       if (n <= kCandidates && n >= static_cast<uint32_t>(by_k ? top_k : 1)) {
         cluster.sync();  // from here on no CTA touches another's memory
         if (R != 0) return;
-        //@gather
         const float near_scale = r.bin_scale * (2 * kThreads) / static_cast<float>(f.bin + 1);
         Items it = take_items(r, ctl, n);
         keep_prefix(r, ctl, it, near_scale, !by_k, target);
-        //@prefix
         if (by_k && by_p) {
           unsigned long long mass = 0;
 #pragma unroll
           for (int i = 0; i < kItems; ++i) mass += it.kept >> i & 1 ? it.w[i] : 0ull;
           keep_prefix(r, ctl, it, near_scale, true, p_target(block_sum(ctl, mass)));
         }
-        //@prefix2
         unsigned long long mass = 0, order[kItems];
         int bin[kItems];
         const float places = (2 * kThreads) / (static_cast<float>(a.V) + 16.0f);
@@ -984,7 +992,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
           for (int i = 0; i < kItems; ++i) at[i] = ~it.at[i];
           drawn = ~select(ctl, at, it.w, it.kept, true, true, draw, 0u, 0ull).key;
         }
-        //!END
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
           if ((it.kept >> i & 1) && it.at[i] == static_cast<uint32_t>(drawn)) {
@@ -1061,7 +1068,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
   if (tid == 0) ctl.hit_warp = -1;
   cluster.sync();  // from here on no CTA touches another's memory
 
-  //@weights
   // ---- the warp in whose run the random number falls
   if (warp == 0) {
     constexpr int kPer = kMaxCluster * kWarps / 32;
@@ -1114,7 +1120,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
     }
   }
   __syncthreads();
-  //!END
   if (warp != ctl.hit_warp) return;
 
   // ---- its run in order: 32 pieces at a time
