@@ -2,6 +2,7 @@
 // translation units.  Launchers only enqueue work; argument checks happen in
 // api.cu.
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -174,6 +175,20 @@ struct RopeArgs {
   float amplitude;
 };
 cudaError_t launch_rope_kv_append(const RopeArgs& r, cudaStream_t s);
+
+// Lets a kernel have `bytes` of dynamic shared memory: the driver is asked once for each
+// device (`done` has a bit for each of the first 64).
+template <class Kernel>
+cudaError_t allow_smem(Kernel* kernel, std::atomic<uint64_t>& done, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // ---- linear.cu
 // Laid-out weights: blocks of 128 rows x 128 bytes, block (rb, kb) at rb * NB + kb, then

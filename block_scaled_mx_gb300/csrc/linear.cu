@@ -619,8 +619,7 @@ using Kernel = void (*)(Params, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorM
 Kernel kernel_of(bool pair, bool a4, int nsb) {
   if (pair && nsb == 1) return a4 ? k_linear<true, true, 1> : k_linear<true, false, 1>;
   if (pair) return a4 ? k_linear<true, true, 2> : k_linear<true, false, 2>;
-  if (nsb == 1) return a4 ? k_linear<false, true, 1> : k_linear<false, false, 1>;
-  return a4 ? k_linear<false, true, 2> : k_linear<false, false, 2>;
+  return a4 ? k_linear<false, true, 1> : k_linear<false, false, 1>;  // at most 64 tokens a tile
 }
 
 }  // namespace
@@ -727,7 +726,8 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
     }
   }
   const Kernel kernel = kernel_of(pair, a4, nsb);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+  static std::atomic<uint64_t> allowed[6];
+  cudaError_t e = allow_smem(kernel, allowed[(pair ? nsb : 0) * 2 + a4], static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);

@@ -1215,7 +1215,8 @@ bool sample_supported(int V, bool bf16) { return V <= (bf16 ? 800000 : 400000) &
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s) {
   const Plan p = plan_of(a.T, a.V, a.bf16 != 0);
   void (*kernel)(SampleArgs, int) = a.bf16 ? k_sample<true> : k_sample<false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  static std::atomic<uint64_t> allowed[2];
+  cudaError_t e = allow_smem(kernel, allowed[a.bf16 ? 1 : 0], 227 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.T) * p.C);
