@@ -35,7 +35,7 @@ enum Kind { kQuery, kKey, kValue };
 // HALF: the pairs are (i, i + R/2).  `parts` warps share a token.
 template <bool E2M1, bool HALF>
 __global__ void __launch_bounds__(32 * kWarps) k_rope_kv_append(const RopeArgs r, int parts) {
-  __shared__ float2 turned_of[kWarps][kMostPairs];  // (cos, sin) of the warp's token's pairs, times the amplitude
+  __shared__ __align__(16) float2 turned_of[kWarps][kMostPairs];  // (cos, sin) of the warp's token's pairs, times the amplitude
   const KvArgs& a = r.kv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + warp;

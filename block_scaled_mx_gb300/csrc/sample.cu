@@ -109,6 +109,7 @@ struct Control {
   uint32_t key_min[kMaxCluster], key_max[kMaxCluster];
   uint32_t n;  // candidates (rank 0)
   uint32_t local_n, local_base, local_at[kCandidates];  // this CTA's
+  uint32_t gathered[kMaxCluster];
   Selected sel;
   uint32_t sel_digit;
   uint32_t sel_count[256], sel_lo[256], sel_hi[256];
@@ -676,9 +677,9 @@ __device__ void keep_prefix(const Row<BF16>& r, Control& ctl, Items& it, float n
 }
 
 // The tokens of bins up to sub.bin0 (all_before), or of a subset, into rank 0's list: first
-// into one of this CTA's, then all of them with one reservation.  Whole CTA; the list's
-// length is in rank 0's n behind the next cluster barrier (more than kCandidates: it does
-// not hold them).
+// into one of this CTA's, then all of them with one reservation.  Whole CTA; the CTAs'
+// numbers of them are in `gathered` behind the next cluster barrier (more than kCandidates
+// in all: the list does not hold them).
 template <bool BF16>
 __device__ void gather(const Row<BF16>& r, Control& ctl, const Subset& sub, bool all_before) {
   const int tid = threadIdx.x;
@@ -704,8 +705,10 @@ __device__ void gather(const Row<BF16>& r, Control& ctl, const Subset& sub, bool
     }
   }
   __syncthreads();
-  Control* leader = cg::this_cluster().map_shared_rank(&ctl, 0);
+  cg::cluster_group cluster = cg::this_cluster();
+  Control* leader = cluster.map_shared_rank(&ctl, 0);
   if (tid == 0) ctl.local_base = atomicAdd(&leader->n, ctl.local_n);
+  if (tid < static_cast<int>(cluster.num_blocks())) cluster.map_shared_rank(&ctl, tid)->gathered[cluster.block_rank()] = ctl.local_n;
   __syncthreads();
   const uint32_t base = ctl.local_base;
   for (uint32_t i = tid; i < min(ctl.local_n, static_cast<uint32_t>(kCandidates)); i += kThreads) {
@@ -845,7 +848,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
       piece_max<BF16>(v[u], mx);
     }
   }
-  const float own_max = mx;
   if (tid < 64) ctl.exp2_table[tid] = kExp2[tid];
   if (tid == 0) {
     const double c = 1.4426950408889634074 / static_cast<double>(fminf(temperature, 0x1p100f));
@@ -937,14 +939,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
   End kept{0u, UINT_MAX, 0ull};
   if (by_k || by_p) {
     unsigned long long target = static_cast<unsigned long long>(top_k);
-    // With a small top-k: where so many threads' own maxima lie, so many tokens do, and few
-    // others, so the histogram is one of maxima: one addition a thread, no weights.
-    const bool maxima = by_k && top_k <= kCandidates * 3 / 4 && top_k <= C * kThreads / 3;
+    // With a small top-k: where so many of the pieces' maxima lie, so many tokens do, and few
+    // others, so the histogram is one of maxima, an addition for four or eight tokens, without
+    // weights.
+    const bool maxima = by_k && top_k <= kCandidates * 7 / 8 && top_k <= a.V / (2 * VE);
     bool masses = by_p && !maxima;
     Found f;
     if (maxima) {
       histogram_begin(ctl);
-      if (own_max > -INFINITY) atomicAdd(&ctl.hist_count[r.bin(own_max)], 1u);
+      for (int i = tid; i < per; i += kThreads) {
+        float top = -INFINITY;
+        piece_max<BF16>(seg[i], top);
+        const int b = r.bin(top);
+        if (b < kBins - 1) atomicAdd(&ctl.hist_count[b], 1u);  // (the last bin's are found missing below)
+      }
       histogram_merge(ctl, slice_count[0], slice_mass[0], false, 0);
       f = find_bin(ctl, slice_count[0], slice_mass[0], false, target, 0, Found{});
     } else {
@@ -960,10 +968,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
       // ---- few tokens: one CTA does the rest
       gather(r, ctl, Subset{f.bin, 32, 0u}, true);
       cluster.sync();
-      const uint32_t n = *cluster.map_shared_rank(&ctl.n, 0);
+      uint32_t n = 0;
+      for (int c = 0; c < C; ++c) n += ctl.gathered[c];
       if (n <= kCandidates && n >= static_cast<uint32_t>(by_k ? top_k : 1)) {
-        cluster.sync();  // from here on no CTA touches another's memory
-        if (R != 0) return;
+        if (R != 0) return;  // from here on no CTA touches another's memory
         const float near_scale = r.bin_scale * (2 * kThreads) / static_cast<float>(f.bin + 1);
         Items it = take_items(r, ctl, n);
         keep_prefix(r, ctl, it, near_scale, !by_k, target);

@@ -333,6 +333,12 @@ def _dense(t, dtype, shape, what) -> Optional[int]:
     return t.data_ptr() if t.is_cuda and t.is_contiguous() else _ptr(t)
 
 
+def _here(t, what):
+    """Refuses a tensor of another GPU than the current one, whose stream the call would use."""
+    if _current_device is not None and t.is_cuda and t.get_device() != _current_device():
+        raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{_current_device()}")
+
+
 def _int32(n, what) -> int:
     """n, refused where a C int cannot hold it (ctypes would drop its high bits)."""
     if not -0x80000000 <= n <= 0x7FFFFFFF:
@@ -385,6 +391,7 @@ def mx_linear(w, out, ws, x=None, codes=None, scales=None, act_fmt="e4m3", bias=
     """out [T, N] (bf16 or fp32) = A . W^T + bias (fp32 [N]) for laid-out weights ``w`` and A
     either x (bf16 [T, K], quantised to ``act_fmt`` here) or codes and scales."""
     f, T = _fmt(act_fmt), out.shape[0]
+    _here(out, "out")
     st = lib().mx_linear(_dense(x, torch.bfloat16, (T, w.K), "x"),
                          _dense(codes, torch.uint8, (T, w.K // 2 if f == MX_E2M1 else w.K), "codes"),
                          _dense(scales, torch.uint8, (T, w.K // 32), "scales"), f, w.data.data_ptr(), w.fmt,
@@ -402,6 +409,7 @@ def mx_sandwich_rmsnorm(x, post_weight, eps, residual, residual_out, gate=None, 
     ``gate_act`` "none" or "sigmoid"; types as mx_add_rmsnorm's."""
     shape = T, H = x.shape
     f, act = _fmt(fmt), GATE_ACTS[gate_act]
+    _here(x, "x")
     pt = wt = gt = MX_BF16
     pp = wp = gp = None
     if post_weight is not None:
@@ -527,6 +535,7 @@ def mx_rope_kv_append(cache, rope, q, k, v, block_table, kv_lens, q_starts, ws, 
     which may be q itself.  ``positions`` int32 [T]: the angles' positions, where they are
     not the places in the sequences."""
     n, pages, table, lens, starts = _batch(block_table, kv_lens, q_starts)
+    _here(k, "k")
     kp, ks = _rows(k, cache.n_kv_heads, cache.head_dim, "k")
     vp, vs = _rows(v, cache.n_kv_heads, cache.head_dim, "v")
     T, heads, qp, qs, op, os_ = k.shape[0], 0, None, 0, None, 0
@@ -595,6 +604,7 @@ def mx_sample(logits, u, tokens, ws, temperature=None, top_k=None, top_p=None, m
         raise ValueError(f"logits: a row is dense, got strides {logits.stride()}")
     if not logits.is_cuda:
         raise ValueError(f"expected a CUDA tensor, got one on {logits.device}")
+    _here(logits, "logits")
     f32, i32, n = torch.float32, torch.int32, (T,)
     st = lib().mx_sample(logits.data_ptr(), _type(logits), row if T > 1 else V, T, V, _dense(temperature, f32, n, "temperature"),
                          _dense(top_k, i32, n, "top_k"), _dense(top_p, f32, n, "top_p"), _dense(min_p, f32, n, "min_p"),

@@ -169,11 +169,11 @@ def test_two_streams_and_a_graph():
 
 def test_a_wait_that_runs_out_is_reported():
     """A limit of a nanosecond: waits end, the status says so, and the next call is whole."""
-    codes, scales = _weights(2048, 4096, "e4m3", 1)
-    w = mx.LinearWeights(codes, scales, "e4m3")
-    for T in (8, 1000):
-        x, ws = torch.randn(T, 4096, device="cuda").to(torch.bfloat16), mx.alloc_workspace(mx.mx_linear_workspace_size(T, 2048, 4096))
-        out, again = torch.empty(T, 2048, device="cuda"), torch.empty(T, 2048, device="cuda")
+    for T, N in ((8, 2048), (8, 40000), (1000, 2048)):   # K shared by a cluster, whole, pairs
+        codes, scales = _weights(N, 4096, "e4m3", 1)
+        w = mx.LinearWeights(codes, scales, "e4m3")
+        x, ws = torch.randn(T, 4096, device="cuda").to(torch.bfloat16), mx.alloc_workspace(mx.mx_linear_workspace_size(T, N, 4096))
+        out, again = torch.empty(T, N, device="cuda"), torch.empty(T, N, device="cuda")
         mx.mx_linear(w, out, ws, x=x)
         mx.mx_debug_set_wait_limit_ns(1)
         try:

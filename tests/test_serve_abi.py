@@ -173,3 +173,20 @@ def test_binding_checks_tensors(L):
         mx.mx_sample(logits, row, row, row)
     with pytest.raises(ValueError, match="dense"):
         mx.mx_sample(logits.t(), row, row, row)
+
+
+def test_binding_refuses_tensors_of_another_device(L, monkeypatch):
+    """The stream is the current device's: a tensor that lies on another one is refused."""
+    from block_scaled_mx_gb300 import mxmoe as mx
+
+    class There:   # a tensor of cuda:1, of which a machine with one GPU has none
+        is_cuda, device = True, "cuda:1"
+
+        def get_device(self):
+            return 1
+
+    monkeypatch.setattr(mx, "_current_device", lambda: 0)
+    with pytest.raises(ValueError, match="current device is cuda:0"):
+        mx._here(There(), "x")
+    monkeypatch.setattr(mx, "_current_device", lambda: 1)
+    mx._here(There(), "x")
