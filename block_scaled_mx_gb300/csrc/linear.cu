@@ -18,7 +18,6 @@
 //   whole  a CTA goes through tiles of all of K
 //   pair   two CTAs share a 256-row tile: cta_group::2 MMAs, each loads half the tokens
 // Every wait is bounded; one that runs out sets MX_ERR_TIMEOUT and all roles unwind.
-#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -31,8 +30,6 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "rows.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace mxk {
 
