@@ -1009,7 +1009,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
         }
         return;
       }
-      // more of them than the list holds (or, of maxima, fewer): the whole histogram
+      // More of them than the list holds: some lie on the border behind the prefix's bin (or, of
+      // maxima, in the bins with it: then the whole histogram).  The list begins again.
+      if (R == 0 && tid == 0) ctl.n = 0u;
       cluster.sync();
       if (maxima) {
         masses = by_p;

@@ -202,3 +202,30 @@ def test_the_same_call_again_on_another_stream_and_in_a_graph():
     torch.cuda.synchronize()
     for tokens, logp in outs[1:]:
         assert torch.equal(tokens, outs[0][0]) and torch.equal(logp, outs[0][1])
+
+
+def _groups(V, groups, rest, T, dtype, seed):
+    """T rows of (count, logit) groups in shuffled places, the others at `rest`."""
+    x = torch.full((T, V), rest)
+    for t in range(T):
+        places, at = torch.randperm(V, generator=torch.Generator().manual_seed(seed + t)), 0
+        for n, v in groups:
+            x[t, places[at:at + n]] = v
+            at += n
+    return x.to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,groups,rest,rules", [
+    (5000, [(1000, 1.0), (200, 1 - 1 / 128), (100, 1 - 2 / 128)], -20.0, dict(top_p=0.87)),
+    (5000, [(1, 0.0), (1000, -1 / 128), (1000, -2 / 128)], -100.0, dict(top_p=0.3)),
+    (40000, [(1000, 1.0), (260, 1 - 1 / 128), (100, 1 - 2 / 128)], -20.0, dict(top_k=1250)),
+    (40000, [(1000, 1.0), (260, 1 - 1 / 128), (100, 1 - 2 / 128)], -20.0, dict(top_k=1250, top_p=0.93)),
+    (2000, [(900, 1.0), (300, 1 - 1 / 128), (700, 1 - 2 / 128)], -1.0, dict(top_k=1100)),
+])
+def test_prefixes_that_end_at_a_border_with_many_neighbours(V, groups, rest, rules, dtype):
+    """At this temperature the histogram's bins are 1/128 wide and these logits lie on their
+    borders: up to the prefix's end there are fewer tokens than a CTA's list holds (1280),
+    with those on the border more."""
+    T = 8
+    _check(_groups(V, groups, rest, T, dtype, V), [(t + 0.5) / T for t in range(T)], temperature=[0.25] * T, **{n: [v] * T for n, v in rules.items()})
