@@ -1022,6 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
     kept = find_end(r, ctl, slice_count, slice_mass, !by_k, masses, target, f);
     if (by_k && by_p) {
       target = p_target(kept.mass);
+      cluster.sync();  // find_end may come right from find_bin: every warp has read what it found before the next is told
       f = find_bin(ctl, slice_count[0], slice_mass[0], true, target, 0, Found{});
       kept = find_end(r, ctl, slice_count, slice_mass, true, true, target, f);
     }

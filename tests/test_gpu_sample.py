@@ -229,3 +229,20 @@ def test_prefixes_that_end_at_a_border_with_many_neighbours(V, groups, rest, rul
     with those on the border more."""
     T = 8
     _check(_groups(V, groups, rest, T, dtype, V), [(t + 0.5) / T for t in range(T)], temperature=[0.25] * T, **{n: [v] * T for n, v in rules.items()})
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_top_k_and_top_p_that_end_among_thousands_of_equal_logits(dtype):
+    """Both ends lie among equal logits, whose last bits the search never needs: two
+    selections one right behind the other, in the same bin or in two."""
+    V, T = 30011, 12
+    x = torch.randint(0, 3, (T, V), generator=torch.Generator().manual_seed(6)) * 0.5
+    u = [(t + 0.5) / T for t in range(T)]
+    x = x.to(dtype).cuda()
+    for rules in (dict(top_k=[25000] * T, top_p=[0.8] * T), dict(top_k=[9000 + 1700 * t for t in range(T)], top_p=[0.4 + 0.05 * t for t in range(T)])):
+        want = None
+        for _ in range(5):
+            if want is None:
+                _check(x, u, **rules)
+                want = _draw(x, u, **rules)
+            assert _draw(x, u, **rules) == want
