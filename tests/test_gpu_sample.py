@@ -246,3 +246,26 @@ def test_top_k_and_top_p_that_end_among_thousands_of_equal_logits(dtype):
                 _check(x, u, **rules)
                 want = _draw(x, u, **rules)
             assert _draw(x, u, **rules) == want
+
+
+@pytest.mark.parametrize("V,dtype", [(4100, torch.float32), (9001, torch.float32), (131072, torch.bfloat16)])
+def test_clusters_that_start_beside_other_work(V, dtype):
+    """Rows shared by two, four and eight CTAs, whose clusters start as another stream's leave:
+    a CTA tells its peers a maximum only once they run."""
+    T = 70
+    logits, u = _random(T, V, dtype, V)
+    rules = dict(temperature=[0.8] * T, top_k=[0, 40] * (T // 2), top_p=[0.9] * T)
+    want = _draw(logits, u, **rules)
+    kinds = dict(temperature=torch.float32, top_k=torch.int32, top_p=torch.float32)
+    kw = {n: torch.tensor(v, dtype=kinds[n], device="cuda") for n, v in rules.items()}
+    u = torch.tensor(u, device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [[(torch.empty(T, dtype=torch.int32, device="cuda"), torch.empty(T, device="cuda")) for _ in range(30)] for _ in streams]
+    ws = [mx.alloc_workspace(256) for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(30):
+        for s, w, o in zip(streams, ws, outs):
+            with torch.cuda.stream(s):
+                mx.mx_sample(logits, u, o[i][0], w, logp=o[i][1], **kw)
+    torch.cuda.synchronize()
+    assert all((tokens.tolist(), logp.tolist()) == want for o in outs for tokens, logp in o) and not any(mx.moe_get_status(w) for w in ws)
