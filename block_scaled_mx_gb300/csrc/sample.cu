@@ -564,7 +564,11 @@ __device__ unsigned long long select_near(Control& ctl, const int (&bin)[kItems]
   static_assert(kNear == kBins, "the bins lie where the histogram and the list were");
   __syncthreads();
   for (int i = tid; i < kNear; i += kThreads) ctl.hist_count[i] = ctl.hist_lo[i] = ctl.hist_hi[i] = 0u;
-  if (tid == 0) ctl.rank_n = 0u;
+  if (tid == 0) {
+    ctl.rank_n = 0u;
+    ctl.near_bin = 0;  // a bin, also where no bin reaches the target
+    ctl.near_before = 0ull;
+  }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
@@ -851,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
   }
   if (tid < 64) ctl.exp2_table[tid] = kExp2[tid];
   if (tid == 0) {
-    const double c = 1.4426950408889634074 / static_cast<double>(fminf(temperature, 0x1p100f));
+    const double c = 1.4426950408889634074 / static_cast<double>(fminf(fmaxf(temperature, 0x1p-126f), 0x1p100f));  // finite as a float
     ctl.c_hi = static_cast<float>(c);
     ctl.c_lo = static_cast<float>(c - static_cast<double>(ctl.c_hi));
   }

@@ -588,8 +588,8 @@ MX_API size_t mx_sample_workspace_size(int T, int V);
  *   min_p    of those, the ones with w_i >= min_p (of the largest; above 1 counts as 1)
  *   token    the first, by number, at which the sum of the kept weights exceeds u
  *            times their whole sum; logp = log of its weight's share in that sum.
- * temperature 0 or top_k 1: the largest logit (of the lowest number), logp 0; temperatures
- * above 2^100 count as that.
+ * temperature 0 or top_k 1: the largest logit (of the lowest number), logp 0; other
+ * temperatures are held to [2^-126, 2^100].
  *   logits [T, V] bf16 or fp32 (type), row t at t * stride elements.
  *   temperature, top_p, min_p fp32, top_k int32: [T] each, or NULL for 1, 1, 0, 0.
  *   u [T] fp32 in [0, 1) (held to it).  tokens [T] int32, logp [T] fp32 or NULL.

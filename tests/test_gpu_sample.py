@@ -269,3 +269,25 @@ def test_clusters_that_start_beside_other_work(V, dtype):
                 mx.mx_sample(logits, u, o[i][0], w, logp=o[i][1], **kw)
     torch.cuda.synchronize()
     assert all((tokens.tolist(), logp.tolist()) == want for o in outs for tokens, logp in o) and not any(mx.moe_get_status(w) for w in ws)
+
+
+@pytest.mark.parametrize("rules", [dict(), dict(top_p=0.9), dict(top_k=40), dict(top_k=1200, top_p=0.5), dict(min_p=0.1)])
+def test_the_smallest_temperatures(rules):
+    """Positive temperatures down to the smallest number; below 2^-126 they count as that."""
+    V, temperature = 1009, [2.0 ** -149, 1e-40, 4.1e-39, 2.0 ** -126, 1e-37, 1e-30]
+    T = len(temperature)
+    for dtype in (torch.float32, torch.bfloat16):
+        x = torch.randn(T, V, generator=torch.Generator().manual_seed(11)).to(dtype)
+        x[:, 500] = x[:, 7] = 6.0                      # the two largest share the draw
+        kw = {n: [v] * T for n, v in rules.items()}
+        for u, place in ((0.25, 7), (0.75, 500)):
+            tokens, logp = _draw(x.cuda(), [u] * T, temperature=temperature, **kw)
+            alone = rules.get("top_p", 1.0) <= 0.5     # the first of the two has half of the weight
+            assert tokens == [7 if alone else place] * T
+            assert all(abs(v - (0.0 if alone else math.log(0.5))) <= 2.0 ** -23 for v in logp)
+    x = torch.full((4, V), -1.0)
+    x[:, 3], x[:, 9] = 2.0 ** -126, 0.0                # one unit of 2^-126 apart: weights 1 and 1 / e
+    tokens, logp = _draw(x.cuda(), [0.7, 0.75, 0.7, 0.75], temperature=[2.0 ** -126, 2.0 ** -126, 2.0 ** -140, 2.0 ** -140])
+    share = 1 / (1 + math.exp(-1))                     # 0.731
+    assert tokens == [3, 9, 3, 9]
+    assert all(abs(v - w) <= 2.0 ** -20 * (1 + abs(w)) for v, w in zip(logp, [math.log(share), math.log(1 - share)] * 2))
