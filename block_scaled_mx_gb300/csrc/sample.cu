@@ -930,7 +930,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
   auto log_share = [&](float x, unsigned long long w, unsigned long long total) {
     // by the difference where the token has most of the weight, else by the logit
     if (w > total / 4) return -log1pf(static_cast<float>(total - w) / static_cast<float>(w));
-    return (x - mx) * (r.c_hi * 0.69314718f) - logf(static_cast<float>(total) * 0x1p-43f);
+    const float below = mx == INFINITY ? 0.0f : x - mx;  // of infinite logits only those of the maximum have a weight
+    return below * (r.c_hi * 0.69314718f) - logf(static_cast<float>(total) * 0x1p-43f);
   };
 
   // ---- the kept prefix

@@ -291,3 +291,20 @@ def test_the_smallest_temperatures(rules):
     share = 1 / (1 + math.exp(-1))                     # 0.731
     assert tokens == [3, 9, 3, 9]
     assert all(abs(v - w) <= 2.0 ** -20 * (1 + abs(w)) for v, w in zip(logp, [math.log(share), math.log(1 - share)] * 2))
+
+
+@pytest.mark.parametrize("n", [2, 4, 9, 300, 3000])
+def test_infinite_logits_share_the_draw(n):
+    """n logits of +inf are alike: each is drawn with 1 / n, and the log-probability is a number."""
+    V, T = 7001, 5
+    x = torch.randn(T, V, generator=torch.Generator().manual_seed(n))
+    places = torch.randperm(V, generator=torch.Generator().manual_seed(n))[:n].sort().values
+    x[:, places] = INF
+    u = [(t + 0.5) / T for t in range(T)]
+    for rules, kept in ((dict(), n), (dict(top_k=[50] * T), min(n, 50)), (dict(top_p=[0.7] * T), math.ceil(float(torch.tensor(0.7)) * n)), (dict(min_p=[0.5] * T), n)):
+        for dtype in (torch.float32, torch.bfloat16):
+            tokens, logp = _draw(x.to(dtype).cuda(), u, **rules)
+            # u as the call reads it: in fp32, where 0.7 and 0.9 lie below the borders 210 / 300 and 270 / 300
+            assert tokens == [int(places[int(float(v) * kept)]) for v in torch.tensor(u, dtype=torch.float32)], rules
+            # the logarithm of a whole number in fp32: its rounding and the function's, 2^-23 each
+            assert all(abs(v + math.log(kept)) <= 2.0 ** -22 * math.log(kept) for v in logp), rules
