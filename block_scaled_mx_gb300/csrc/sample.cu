@@ -872,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
     peer->nan[R] = any_nan;
   }
   cluster.sync();
-  bool bad = !(temperature >= 0.0f);
+  bool bad = !(temperature >= 0.0f) || isnan(top_p) || isnan(min_p);
   mx = -INFINITY;
   for (int c = 0; c < C; ++c) {
     mx = fmaxf(mx, ctl.max[c]);

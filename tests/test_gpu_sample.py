@@ -308,3 +308,13 @@ def test_infinite_logits_share_the_draw(n):
             assert tokens == [int(places[int(float(v) * kept)]) for v in torch.tensor(u, dtype=torch.float32)], rules
             # the logarithm of a whole number in fp32: its rounding and the function's, 2^-23 each
             assert all(abs(v + math.log(kept)) <= 2.0 ** -22 * math.log(kept) for v in logp), rules
+
+
+def test_rules_that_are_not_numbers():
+    """A NaN among a row's rules: no token, and the status says so; other rows are drawn."""
+    x = torch.randn(4, 300, generator=torch.Generator().manual_seed(8)).cuda()
+    fine = _draw(x, [0.3] * 4, top_p=[0.9] * 4, min_p=[0.01] * 4)
+    for kw in (dict(top_p=[0.9, math.nan, 0.9, 0.9], min_p=[0.01] * 4), dict(top_p=[0.9] * 4, min_p=[0.01, math.nan, 0.01, 0.01])):
+        tokens, logp = _draw(x, [0.3] * 4, status=mx.MX_ERR_DEVICE_ARG, **kw)
+        assert tokens[1] == -1 and math.isnan(logp[1])
+        assert [tokens[i] for i in (0, 2, 3)] == [fine[0][i] for i in (0, 2, 3)] and [logp[i] for i in (0, 2, 3)] == [fine[1][i] for i in (0, 2, 3)]
