@@ -427,8 +427,9 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
     }
   }
   tc_fence_before();
-  __syncthreads();
-  if (PAIR && bars->abort) {
+  // One answer for the whole CTA: the peer may still set the flag (it does so ahead of the
+  // cluster's barrier below), and threads that read it for themselves would part here.
+  if (__syncthreads_or(PAIR && *static_cast<volatile int*>(&bars->abort))) {
     // where a wait ran out nobody counts rank 1's last copies: they get a millisecond
     if (tid == 0) {
       for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000ull;) {

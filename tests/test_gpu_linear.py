@@ -183,3 +183,25 @@ def test_a_wait_that_runs_out_is_reported():
             mx.mx_debug_set_wait_limit_ns(2000000000)
         mx.mx_linear(w, again, ws, x=x)
         assert mx.moe_get_status(ws) == 0 and torch.equal(out, again)
+
+
+@pytest.mark.parametrize("T,N,wf,af", [(700, 6144, "e4m3", "e4m3"), (300, 2000, "e2m1", "e2m1"), (65, 30000, "e2m1", "e4m3")])
+def test_pairs_leave_together_where_waits_run_out(T, N, wf, af):
+    """In a pair either CTA's wait may be the one that runs out, at any point of the other's
+    way: limits from one that ends all waits to one that ends few, and whole calls between."""
+    K = 2048
+    w = mx.LinearWeights(*_weights(N, K, wf, 3), wf)
+    x, ws = torch.randn(T, K, device="cuda").to(torch.bfloat16), mx.alloc_workspace(mx.mx_linear_workspace_size(T, N, K, af))
+    out, again = torch.empty(T, N, device="cuda"), torch.empty(T, N, device="cuda")
+    mx.mx_linear(w, out, ws, x=x, act_fmt=af)
+    assert mx.moe_get_status(ws) == 0
+    for limit in (1, 1000, 4000, 12000):
+        mx.mx_debug_set_wait_limit_ns(limit)
+        try:
+            for _ in range(2):
+                mx.mx_linear(w, again, ws, x=x, act_fmt=af)
+            assert mx.moe_get_status(ws) in (0, mx.MX_ERR_TIMEOUT)
+        finally:
+            mx.mx_debug_set_wait_limit_ns(2000000000)
+        mx.mx_linear(w, again, ws, x=x, act_fmt=af)
+        assert mx.moe_get_status(ws) == 0 and torch.equal(out, again)
