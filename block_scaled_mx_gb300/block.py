@@ -37,18 +37,27 @@ def _norm(sandwich, x, weight, eps, residual, residual_out, **out):
 
 
 class _Workspaces:
-    """Workspaces by name and stream, which are kept: calls on different streams may overlap."""
+    """Workspaces by name and stream, which are kept: calls on different streams may overlap.
+    So may the graphs that calls are captured into: each has workspaces of its own, which
+    are kept as long as the object."""
 
     def __init__(self):
-        self._ws = {}
+        self._ws = {}        # by name, stream and capture
+        self._outgrown = []  # workspaces that earlier calls of a capture go on using, with their stream
 
     def _workspace(self, name, nbytes):
-        key = name, mx.current_stream()
+        key = name, mx.current_stream(), mx.current_capture()
         ws = self._ws.get(key)
         if ws is None or ws.nbytes < nbytes:
-            old, ws = ws, mx.alloc_workspace(nbytes)
-            if old is not None:
-                ws[:4] = old[:4]  # an error that status() has not read yet
+            old = ws
+            if key[2]:
+                ws = mx.alloc_captured_workspace(nbytes)
+                if old is not None:
+                    self._outgrown.append((key[1], old))
+            else:
+                ws = mx.alloc_workspace(nbytes)
+                if old is not None:
+                    ws[:4] = old[:4]  # an error that status() has not read yet
             self._ws[key] = ws
         return ws
 
@@ -65,7 +74,8 @@ class _Workspaces:
     def status(self):
         """The first error that a kernel reported (waits for the device), 0 for none."""
         torch.cuda.synchronize()
-        return max((mx.moe_get_status(ws, stream) for (_, stream), ws in self._ws.items()), default=0)
+        every = [(stream, ws) for (_, stream, _), ws in self._ws.items()] + self._outgrown
+        return max((mx.moe_get_status(ws, stream) for stream, ws in every), default=0)
 
 
 class DecoderBlock(_Workspaces):
@@ -75,9 +85,10 @@ class DecoderBlock(_Workspaces):
     queries and keys their positions; ``before`` and ``between`` are the Sandwich of the
     incoming x (the output of the block before) and of the attention's projection.
 
-    Calls on different streams may overlap: each stream has workspaces of its own,
-    which the block keeps (at most 41 MB for the attention, and what the experts'
-    GEMMs and the projections need).  An object is for one host thread at a time.
+    Calls on different streams may overlap, and so may graphs that calls are captured into:
+    each stream and each graph has workspaces of its own, which the block keeps (at most
+    41 MB for the attention, and what the experts' GEMMs and the projections need).  An
+    object is for one host thread at a time.
 
     With ``keep_last`` the block holds what its last call computed on the way in
     ``last`` (q and with it the whole projection, att, y, codes, scales) until the

@@ -609,6 +609,23 @@ int moe_get_status(void* ws, mx_stream_t stream, int* host_status) {
   return MX_OK;
 }
 
+int mx_capture_id(mx_stream_t stream, uint64_t* id) {
+  if (!id) return MX_ERR_INVALID_ARG;
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long n = 0;
+  if (cudaStreamGetCaptureInfo(reinterpret_cast<cudaStream_t>(stream), &status, &n) != cudaSuccess) return MX_ERR_CUDA;
+  *id = status == cudaStreamCaptureStatusNone ? 0 : n + 1;
+  return MX_OK;
+}
+
+int mx_exchange_capture_mode(int* mode) {
+  if (!mode || *mode < cudaStreamCaptureModeGlobal || *mode > cudaStreamCaptureModeRelaxed) return MX_ERR_INVALID_ARG;
+  cudaStreamCaptureMode m = static_cast<cudaStreamCaptureMode>(*mode);
+  const cudaError_t e = cudaThreadExchangeStreamCaptureMode(&m);
+  if (e == cudaSuccess) *mode = m;
+  return cuda_status(e);
+}
+
 void mx_debug_set_wait_limit_ns(uint64_t ns) { g_wait_limit_ns = ns; }
 
 void mx_debug_time_gemms(int enable) { gemm_timing_enable(enable != 0); }

@@ -100,6 +100,8 @@ SIGNATURES = {
     "mx_sample_workspace_size": (_SZ, [_I, _I]),
     "mx_sample": (_I, [_P, _I, _I64, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_get_status": (_I, [_P, _P, _P]),
+    "mx_capture_id": (_I, [_P, _P]),
+    "mx_exchange_capture_mode": (_I, [_P]),
     "mx_debug_set_wait_limit_ns": (None, [_U64]),
     "mx_debug_time_gemms": (None, [_I]),
     "mx_debug_gemm_times": (_I, [_P, _P, _I]),
@@ -177,6 +179,18 @@ def current_stream() -> int:
 def _check(st: int, what: str):
     if st != MX_OK:
         raise MxError(st, what)
+
+
+def capture_id(stream=None) -> int:
+    """A number of the graph capture that a stream (torch's current one) is part of, 0 for none."""
+    v = ctypes.c_uint64(0)
+    _check(lib().mx_capture_id(_stream(stream), ctypes.addressof(v)), "mx_capture_id")
+    return v.value
+
+
+def current_capture() -> int:
+    """capture_id of torch's current stream (0 where CUDA is not in use)."""
+    return capture_id() if torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing() else 0
 
 
 def _fmt(fmt) -> int:
@@ -650,6 +664,22 @@ def mx_build_stamp() -> str:
 def alloc_workspace(nbytes: int, device="cuda") -> torch.Tensor:
     """Zero-filled, 256-byte aligned workspace (the library requires zero on first use)."""
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+
+
+def alloc_captured_workspace(nbytes: int) -> torch.Tensor:
+    """alloc_workspace while torch's current stream is being captured into a graph: zero from
+    here on, not by a node of the graph, and none of the graph's memory, so that it is the
+    caller's to keep as long as the graph may run."""
+    side = next(s for s in iter(torch.cuda.Stream, None) if not capture_id(s))  # torch hands out its streams in turn
+    mode = ctypes.c_int(2)
+    _check(lib().mx_exchange_capture_mode(ctypes.addressof(mode)), "mx_exchange_capture_mode")
+    try:
+        with torch.cuda.stream(side):
+            ws = alloc_workspace(nbytes)
+        side.synchronize()
+    finally:
+        _check(lib().mx_exchange_capture_mode(ctypes.addressof(mode)), "mx_exchange_capture_mode")
+    return ws
 
 
 class MoELayer:

@@ -610,6 +610,18 @@ MX_API int mx_sample(const void* logits, int type, int64_t stride, int T, int V,
  * clear it.  0 = no device-side error; otherwise an MX_ERR_* code. */
 MX_API int moe_get_status(void* ws, mx_stream_t stream, int* host_status);
 
+/* *id = a number of the graph capture that `stream` is part of, 0 where it is part of none:
+ * for callers that keep a workspace for each graph.  (Two graphs that may run at once need
+ * one each, and a zero fill that was captured into one graph is none for the other.)
+ * Errors: MX_ERR_INVALID_ARG (null), MX_ERR_CUDA. */
+MX_API int mx_capture_id(mx_stream_t stream, uint64_t* id);
+
+/* Exchanges *mode with the calling thread's capture mode, as cudaThreadExchangeStreamCaptureMode
+ * does: 0 global, 1 this thread, 2 relaxed.  A thread that captures one stream into a graph may
+ * allocate, fill and wait for memory on another while its mode is relaxed.
+ * Errors: MX_ERR_INVALID_ARG (null, another mode), MX_ERR_CUDA. */
+MX_API int mx_exchange_capture_mode(int* mode);
+
 /* Test hook: the wall-clock limit, in nanoseconds, of every bounded wait inside
  * the GEMM kernels (default 2e9).  A tiny limit makes the waits run out, which
  * exercises the MX_ERR_TIMEOUT path without hanging the GPU. */

@@ -43,3 +43,25 @@ def test_streams_have_workspaces_of_their_own(blk, monkeypatch):
     assert blk._workspace("attention", 256) is one
     one[:4] = 3                             # an error on either stream is found
     assert blk.status() == 3
+
+
+def test_captured_graphs_have_workspaces_of_their_own(blk, monkeypatch):
+    """Captures on one stream, as torch's default capture stream, one after the other: what a
+    graph uses is neither another graph's nor an eager call's, and is never given up."""
+    monkeypatch.setattr(mx, "alloc_captured_workspace", lambda n: torch.zeros(n, dtype=torch.uint8), raising=False)
+    capture = 0
+    monkeypatch.setattr(mx, "current_capture", lambda: capture, raising=False)
+    eager = blk._workspace("attention", 256)
+    capture = 5
+    one = blk._workspace("attention", 256)
+    assert blk._workspace("attention", 200) is one
+    grown = blk._workspace("attention", 1024)
+    capture = 8
+    two = blk._workspace("attention", 256)
+    capture = 0
+    assert blk._workspace("attention", 256) is eager
+    larger = blk._workspace("attention", 512)
+    assert len({ws.data_ptr() for ws in (eager, one, grown, two, larger)}) == 5
+    for ws in (one, grown, two, larger):    # an error in any of them is found
+        ws[:4] = 3
+        assert blk.status() == 3 and blk.status() == 0

@@ -190,3 +190,15 @@ def test_binding_refuses_tensors_of_another_device(L, monkeypatch):
         mx._here(There(), "x")
     monkeypatch.setattr(mx, "_current_device", lambda: 1)
     mx._here(There(), "x")
+
+
+# ------------------------------------------------------------------ workspaces of captured graphs
+def test_capture_refusals(L):
+    from block_scaled_mx_gb300 import mxmoe as mx
+
+    assert L.mx_capture_id(None, None) == 1
+    assert L.mx_exchange_capture_mode(None) == 1
+    for bad in (-1, 3):
+        assert L.mx_exchange_capture_mode(ctypes.addressof(ctypes.c_int(bad))) == 1
+    if not torch.cuda.is_available():
+        assert mx.current_capture() == 0
