@@ -338,19 +338,38 @@ def _type(t) -> int:
     return code
 
 
-def _dense(t, dtype, shape, what) -> Optional[int]:
-    """_ptr of an optional tensor that has to have this dtype and shape."""
+def _dense(t, dtype, shape, what, here=None) -> Optional[int]:
+    """_ptr of an optional tensor that has to have this dtype and shape, and to lie on the
+    device ``here`` where one is given."""
     if t is None:
         return None
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
-    return t.data_ptr() if t.is_cuda and t.is_contiguous() else _ptr(t)
+    if here is None:
+        return t.data_ptr() if t.is_cuda and t.is_contiguous() else _ptr(t)
+    return t.data_ptr() if 0 <= here == t.get_device() and t.is_contiguous() else _at(t, what, here)
 
 
-def _here(t, what):
-    """Refuses a tensor of another GPU than the current one, whose stream the call would use."""
-    if _current_device is not None and t.is_cuda and t.get_device() != _current_device():
-        raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{_current_device()}")
+def _here(t, what) -> int:
+    """The device of a call's first tensor; one of another GPU than the current one, whose
+    stream the call would use, is refused."""
+    here = t.get_device()
+    if _current_device is not None and t.is_cuda and here != _current_device():
+        raise _elsewhere(t, what, _current_device())
+    return here
+
+
+def _elsewhere(t, what, here):
+    return ValueError(f"{what}: on {t.device}, but the current device is cuda:{here}")
+
+
+def _at(t, what, here) -> int:
+    """_ptr of a tensor that has to lie on the call's device."""
+    if 0 <= here == t.get_device() and t.is_contiguous():
+        return t.data_ptr()
+    if t.is_cuda and t.get_device() != here:
+        raise _elsewhere(t, what, here)
+    return _ptr(t)  # which says what is wrong with it
 
 
 def _int32(n, what) -> int:
@@ -391,7 +410,8 @@ class LinearWeights:
         self.fmt = _fmt(fmt)
         N, row = codes.shape
         self.N, self.K = N, row * 2 if self.fmt == MX_E2M1 else row
-        cp, sp = _dense(codes, torch.uint8, (N, row), "codes"), _dense(scales, torch.uint8, (N, self.K // 32), "scales")
+        here = _here(codes, "codes")
+        cp, sp = _dense(codes, torch.uint8, (N, row), "codes", here), _dense(scales, torch.uint8, (N, self.K // 32), "scales", here)
         need = lib().mx_linear_prepared_bytes(N, self.K, self.fmt)
         self.data = torch.empty(need, dtype=torch.uint8, device=codes.device)
         _check(lib().mx_linear_prepare(cp, sp, N, self.K, self.fmt, self.data.data_ptr(), need, _stream(stream)), "mx_linear_prepare")
@@ -405,12 +425,12 @@ def mx_linear(w, out, ws, x=None, codes=None, scales=None, act_fmt="e4m3", bias=
     """out [T, N] (bf16 or fp32) = A . W^T + bias (fp32 [N]) for laid-out weights ``w`` and A
     either x (bf16 [T, K], quantised to ``act_fmt`` here) or codes and scales."""
     f, T = _fmt(act_fmt), out.shape[0]
-    _here(out, "out")
-    st = lib().mx_linear(_dense(x, torch.bfloat16, (T, w.K), "x"),
-                         _dense(codes, torch.uint8, (T, w.K // 2 if f == MX_E2M1 else w.K), "codes"),
-                         _dense(scales, torch.uint8, (T, w.K // 32), "scales"), f, w.data.data_ptr(), w.fmt,
-                         _dense(bias, torch.float32, (w.N,), "bias"), T, w.N, w.K, _dense(out, out.dtype, (T, w.N), "out"), _type(out),
-                         _ptr(ws), ws.nbytes, _stream(stream))
+    here = _here(out, "out")
+    st = lib().mx_linear(_dense(x, torch.bfloat16, (T, w.K), "x", here),
+                         _dense(codes, torch.uint8, (T, w.K // 2 if f == MX_E2M1 else w.K), "codes", here),
+                         _dense(scales, torch.uint8, (T, w.K // 32), "scales", here), f, _at(w.data, "w", here), w.fmt,
+                         _dense(bias, torch.float32, (w.N,), "bias", here), T, w.N, w.K, _dense(out, out.dtype, (T, w.N), "out", here),
+                         _type(out), _at(ws, "ws", here), ws.nbytes, _stream(stream))
     if st:
         raise MxError(st, "mx_linear")
 
@@ -423,26 +443,26 @@ def mx_sandwich_rmsnorm(x, post_weight, eps, residual, residual_out, gate=None, 
     ``gate_act`` "none" or "sigmoid"; types as mx_add_rmsnorm's."""
     shape = T, H = x.shape
     f, act = _fmt(fmt), GATE_ACTS[gate_act]
-    _here(x, "x")
+    here = _here(x, "x")
     pt = wt = gt = MX_BF16
     pp = wp = gp = None
     if post_weight is not None:
-        pt, pp = _type(post_weight), _dense(post_weight, post_weight.dtype, (H,), "post_weight")
+        pt, pp = _type(post_weight), _dense(post_weight, post_weight.dtype, (H,), "post_weight", here)
     if weight is not None:
-        wt, wp = _type(weight), _dense(weight, weight.dtype, (H,), "weight")
+        wt, wp = _type(weight), _dense(weight, weight.dtype, (H,), "weight", here)
     kind = MX_GATE_NONE
     if gate is not None:
         g = gate.shape
         kind = MX_GATE_CHANNEL if g == (H,) else MX_GATE_FULL if g == shape else MX_GATE_TOKEN if g == (T, 1) else None
         if kind is None:
             raise ValueError(f"gate: expected shape {(H,)}, {(T, 1)} or {tuple(shape)}, got {tuple(g)}")
-        gt, gp = _type(gate), _ptr(gate)
-    st = lib().mx_sandwich_rmsnorm(_ptr(x), _type(x), pp, pt, gp, gt, kind, act,
-                                   _dense(residual, residual.dtype, shape, "residual"), _type(residual), residual_scale,
-                                   block_scale, wp, wt, T, H, eps, _dense(residual_out, residual.dtype, shape, "residual_out"),
-                                   _dense(y, torch.bfloat16, shape, "y"), f,
-                                   _dense(codes, torch.uint8, (T, H // 2) if f == MX_E2M1 else shape, "codes"),
-                                   _dense(scales, torch.uint8, (T, H // 32), "scales"), _stream(stream))
+        gt, gp = _type(gate), _at(gate, "gate", here)
+    st = lib().mx_sandwich_rmsnorm(_at(x, "x", here), _type(x), pp, pt, gp, gt, kind, act,
+                                   _dense(residual, residual.dtype, shape, "residual", here), _type(residual), residual_scale,
+                                   block_scale, wp, wt, T, H, eps, _dense(residual_out, residual.dtype, shape, "residual_out", here),
+                                   _dense(y, torch.bfloat16, shape, "y", here), f,
+                                   _dense(codes, torch.uint8, (T, H // 2) if f == MX_E2M1 else shape, "codes", here),
+                                   _dense(scales, torch.uint8, (T, H // 32), "scales", here), _stream(stream))
     if st:
         raise MxError(st, "mx_sandwich_rmsnorm")
 
@@ -479,19 +499,20 @@ class KVCache:
                 raise ValueError(f"{what}: expected uint8 {(pages, heads, size, r)}, got {t.dtype} {tuple(t.shape)}")
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.num_pages, self.page_size, self.n_kv_heads, self.head_dim, self.fmt = pages, size, heads, head_dim, fmt
+        self._devices = {t.get_device() for t in (k_codes, k_scales, v_codes, v_scales)}
         self._tables = KVCacheTables(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), pages, size, heads,
                                      head_dim, fmt)
         self._address = ctypes.addressof(self._tables)
 
 
-def _batch(block_table, kv_lens, q_starts):
+def _batch(block_table, kv_lens, q_starts, here=None):
     """Checked sizes and addresses of a batch's int32 tensors."""
     n, pages = block_table.shape
-    return (n, pages, _dense(block_table, torch.int32, (n, pages), "block_table"),
-            _dense(kv_lens, torch.int32, (n,), "kv_lens"), _dense(q_starts, torch.int32, (n + 1,), "q_starts"))
+    return (n, pages, _dense(block_table, torch.int32, (n, pages), "block_table", here),
+            _dense(kv_lens, torch.int32, (n,), "kv_lens", here), _dense(q_starts, torch.int32, (n + 1,), "q_starts", here))
 
 
-def _rows(t, heads, dim, what):
+def _rows(t, heads, dim, what, here=None):
     """Address and token stride of a bf16 [T, heads, dim] tensor whose tokens may
     lie apart (a slice of a wider projection)."""
     shape = t.shape
@@ -502,6 +523,8 @@ def _rows(t, heads, dim, what):
         raise ValueError(f"{what}: a token's heads are dense, got strides {t.stride()}")
     if not t.is_cuda:
         raise ValueError(f"expected a CUDA tensor, got one on {t.device}")
+    if here is not None and t.get_device() != here:
+        raise _elsewhere(t, what, here)
     return t.data_ptr(), token if shape[0] > 1 else heads * dim  # one token has no stride of its own
 
 
@@ -548,25 +571,27 @@ def mx_rope_kv_append(cache, rope, q, k, v, block_table, kv_lens, q_starts, ws, 
     in the cache, q (bf16 [T, n_heads, head_dim], token stride free; or None) into q_out,
     which may be q itself.  ``positions`` int32 [T]: the angles' positions, where they are
     not the places in the sequences."""
-    n, pages, table, lens, starts = _batch(block_table, kv_lens, q_starts)
-    _here(k, "k")
-    kp, ks = _rows(k, cache.n_kv_heads, cache.head_dim, "k")
-    vp, vs = _rows(v, cache.n_kv_heads, cache.head_dim, "v")
+    here = _here(k, "k")
+    n, pages, table, lens, starts = _batch(block_table, kv_lens, q_starts, here)
+    kp, ks = _rows(k, cache.n_kv_heads, cache.head_dim, "k", here)
+    vp, vs = _rows(v, cache.n_kv_heads, cache.head_dim, "v", here)
     T, heads, qp, qs, op, os_ = k.shape[0], 0, None, 0, None, 0
     if v.shape[0] != T:
         raise ValueError(f"k and v differ in shape: {tuple(k.shape)}, {tuple(v.shape)}")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out: both or neither")
+    if cache._devices != {here}:
+        raise ValueError(f"cache: on the devices {cache._devices}, but the current one is {here}")
     if q is not None:
         heads = q.shape[1]
-        qp, qs = _rows(q, heads, cache.head_dim, "q")
-        op, os_ = _rows(q_out, heads, cache.head_dim, "q_out")
+        qp, qs = _rows(q, heads, cache.head_dim, "q", here)
+        op, os_ = _rows(q_out, heads, cache.head_dim, "q_out", here)
         if q.shape[0] != T or q_out.shape[0] != T:
             raise ValueError(f"q, q_out: expected {T} tokens, got {q.shape[0]} and {q_out.shape[0]}")
     st = lib().mx_rope_kv_append(cache._address, qp, qs, heads, op, os_, kp, ks, vp, vs,
-                                 _dense(positions, torch.int32, (T,), "positions"),
-                                 _dense(rope.turns, torch.int64, (rope.rot_dim // 2,), "turns"), rope.rot_dim, rope.layout,
-                                 rope.amplitude, table, lens, starts, n, pages, T, _ptr(ws), ws.nbytes, _stream(stream))
+                                 _dense(positions, torch.int32, (T,), "positions", here),
+                                 _dense(rope.turns, torch.int64, (rope.rot_dim // 2,), "turns", here), rope.rot_dim, rope.layout,
+                                 rope.amplitude, table, lens, starts, n, pages, T, _at(ws, "ws", here), ws.nbytes, _stream(stream))
     if st:
         raise MxError(st, "mx_rope_kv_append")
 
@@ -618,12 +643,12 @@ def mx_sample(logits, u, tokens, ws, temperature=None, top_k=None, top_p=None, m
         raise ValueError(f"logits: a row is dense, got strides {logits.stride()}")
     if not logits.is_cuda:
         raise ValueError(f"expected a CUDA tensor, got one on {logits.device}")
-    _here(logits, "logits")
+    here = _here(logits, "logits")
     f32, i32, n = torch.float32, torch.int32, (T,)
-    st = lib().mx_sample(logits.data_ptr(), _type(logits), row if T > 1 else V, T, V, _dense(temperature, f32, n, "temperature"),
-                         _dense(top_k, i32, n, "top_k"), _dense(top_p, f32, n, "top_p"), _dense(min_p, f32, n, "min_p"),
-                         _dense(u, f32, n, "u"), _dense(tokens, i32, n, "tokens"), _dense(logp, f32, n, "logp"), _ptr(ws), ws.nbytes,
-                         _stream(stream))
+    st = lib().mx_sample(logits.data_ptr(), _type(logits), row if T > 1 else V, T, V, _dense(temperature, f32, n, "temperature", here),
+                         _dense(top_k, i32, n, "top_k", here), _dense(top_p, f32, n, "top_p", here), _dense(min_p, f32, n, "min_p", here),
+                         _dense(u, f32, n, "u", here), _dense(tokens, i32, n, "tokens", here), _dense(logp, f32, n, "logp", here),
+                         _at(ws, "ws", here), ws.nbytes, _stream(stream))
     if st:
         raise MxError(st, "mx_sample")
 

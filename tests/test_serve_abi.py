@@ -202,3 +202,86 @@ def test_capture_refusals(L):
         assert L.mx_exchange_capture_mode(ctypes.addressof(ctypes.c_int(bad))) == 1
     if not torch.cuda.is_available():
         assert mx.current_capture() == 0
+
+
+class Gpu(torch.Tensor):
+    """Host memory that says it lies on a GPU: for calls that are refused before they read it."""
+    is_cuda = property(lambda t: True)
+
+    def get_device(self):
+        return self.gpu
+
+
+def _gpu(shape, dtype=torch.float32, gpu=0):
+    t = torch.zeros(shape, dtype=dtype).as_subclass(Gpu)
+    t.gpu = gpu
+    return t
+
+
+BF16, U8, I32 = torch.bfloat16, torch.uint8, torch.int32
+
+
+def _linear_call(mx, at):
+    w = object.__new__(mx.LinearWeights)
+    w.fmt, w.N, w.K, w.data = 0, 128, 256, at("w", (1024,), U8)
+    return lambda: mx.mx_linear(w, at("out", (4, 128)), at("ws", (4096,), U8), codes=at("codes", (4, 256), U8), scales=at("scales", (4, 8), U8),
+                                bias=at("bias", (128,)))
+
+
+def _linear_x_call(mx, at):
+    w = object.__new__(mx.LinearWeights)
+    w.fmt, w.N, w.K, w.data = 0, 128, 256, at("w", (1024,), U8)
+    return lambda: mx.mx_linear(w, at("out", (4, 128)), at("ws", (4096,), U8), x=at("x", (4, 256), BF16))
+
+
+def _weights_call(mx, at):
+    return lambda: mx.LinearWeights(at("codes", (128, 256), U8), at("scales", (128, 8), U8), "e4m3")
+
+
+def _sandwich_call(mx, at):
+    return lambda: mx.mx_sandwich_rmsnorm(at("x", (4, 64)), at("post_weight", (64,)), 1e-6, at("residual", (4, 64)), at("residual_out", (4, 64)),
+                                          gate=at("gate", (64,)), weight=at("weight", (64,)), y=at("y", (4, 64), BF16), codes=at("codes", (4, 64), U8),
+                                          scales=at("scales", (4, 2), U8))
+
+
+def _rope_call(mx, at):
+    cache = mx.KVCache.of(*(at("cache", (8, 2, 16, n), U8) for n in (64, 2, 64, 2)), 64)
+    rope = mx.Rope(64, device="cpu")
+    rope.turns = at("turns", (32,), torch.int64)
+    return lambda: mx.mx_rope_kv_append(cache, rope, at("q", (4, 8, 64), BF16), at("k", (4, 2, 64), BF16), at("v", (4, 2, 64), BF16),
+                                        at("block_table", (2, 4), I32), at("kv_lens", (2,), I32), at("q_starts", (3,), I32), at("ws", (256,), U8),
+                                        q_out=at("q_out", (4, 8, 64), BF16), positions=at("positions", (4,), I32))
+
+
+def _sample_call(mx, at):
+    return lambda: mx.mx_sample(at("logits", (4, 50)), at("u", (4,)), at("tokens", (4,), I32), at("ws", (256,), U8), temperature=at("temperature", (4,)),
+                                top_k=at("top_k", (4,), I32), top_p=at("top_p", (4,)), min_p=at("min_p", (4,)), logp=at("logp", (4,)))
+
+
+@pytest.mark.parametrize("call", [_linear_call, _linear_x_call, _weights_call, _sandwich_call, _rope_call, _sample_call])
+def test_binding_refuses_every_tensor_of_another_device(L, monkeypatch, call):
+    from block_scaled_mx_gb300 import mxmoe as mx
+
+    class NoLibrary:
+        def __getattr__(self, name):
+            def called(*a):
+                raise AssertionError(f"{name} was called")
+
+            return called
+
+    def run(gpu_of):
+        names = []
+        with monkeypatch.context() as m:
+            m.setattr(mx, "_current_device", lambda: 0)
+            m.setattr(mx, "_current_raw_stream", lambda device: 0)
+            make = call(mx, lambda name, *a: names.append(name) or _gpu(*a, gpu=gpu_of(name)))
+            m.setattr(mx, "lib", NoLibrary)
+            make()
+        return names
+
+    names = []
+    with pytest.raises(AssertionError, match="was called"):     # all in place: on to the library
+        run(lambda name: names.append(name) or 0)
+    for other in sorted(set(names)):
+        with pytest.raises(ValueError, match=f"^{other}: on .* but the current"):
+            run(lambda name: int(name == other))
