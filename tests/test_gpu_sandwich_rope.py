@@ -304,3 +304,20 @@ def test_rope_in_a_graph_on_another_stream():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(o, p) and torch.equal(want.k_codes, got.k_codes) and torch.equal(want.v_codes, got.v_codes)
+
+
+@pytest.mark.parametrize("kind", ["channel", "token", "full"])
+@pytest.mark.parametrize("gt", ["bf16", "f32"])
+def test_sigmoid_of_far_gates_in_fp32(kind, gt):
+    """A residual of zeros in fp32 leaves act(gate) x alone: the sigmoid has to be as good as
+    fp32 wherever its gate lies."""
+    T, H = 401, 128
+    x = torch.ones(T, H) * 0.75
+    far = torch.linspace(-86.0, 20.0, T)   # the result is a normal number for all of them
+    gate = {"channel": torch.linspace(-86.0, 20.0, H), "token": far[:, None], "full": far[:, None] + torch.linspace(-1, 1, H)}[kind].to(DT[gt])
+    res, ro = torch.zeros(T, H, device="cuda"), torch.empty(T, H, device="cuda")
+    mx.mx_sandwich_rmsnorm(x.cuda(), None, 1e-6, res, ro, gate=gate.cuda(), gate_act="sigmoid")
+    want = torch.sigmoid(gate.double()) * x.double()
+    # the exponential (a power of two, 2 ulp: 2^-22, and its correction, 2^-24), a sum (2^-24), a
+    # division (2 ulp: 2^-22), two products (2^-24 each)
+    assert torch.all((ro.cpu().double() - want).abs() <= (2 * 2.0 ** -22 + 4 * 2.0 ** -24) * want)
