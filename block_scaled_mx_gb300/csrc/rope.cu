@@ -6,7 +6,9 @@
 // for the pairs (i, i + R/2) or (2i, 2i + 1).  Angles of far positions lose their
 // fraction of a turn in fp32, so f_i is kept as the 64-bit fraction of a turn a
 // position, p * f_i is a product modulo 2^64, which is exact but for f_i's own rounding
-// (2^-53), and its upper 32 bits are the angle in [-1/2, 1/2) turns (2^-33 of a turn off).
+// (2^-52 turns a position), and its upper 32 bits are the angle in [-1/2, 1/2) turns (2^-32
+// of a turn off).  Sines are fp32 (sincospif, an ulp or two), and so are the products: some
+// 2^-21 of |a| + |b| off, where bf16 rounds by 2^-9 and E4M3 by 2^-4 of the result.
 //
 // Memory-bound: every input is read once and every output written once.  A warp takes a
 // token, or a part of one: its lanes find the angles' sines, each once, and go through the

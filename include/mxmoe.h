@@ -509,12 +509,13 @@ MX_API int mx_rope_table(int rot_dim, double base, int scaling, double factor, d
  *     with the same stride, and else does not overlap q, k or v.
  *   positions [T] int32 or NULL: the angles' positions; without them a token's place in
  *     its sequence.  They do not move the place that is written.
- *   turns [rot_dim / 2] on the device, amplitude: mx_rope_table's.  An angle is exact
- *     to 2^-32 turns at any position.
+ *   turns [rot_dim / 2] on the device, amplitude: mx_rope_table's.  An angle is exact to
+ *     2^-32 turns for the table's frequencies, which are f_i in 64-bit arithmetic: another
+ *     2^-52 turns a position (2^-32 at position 2^20), more for BANDS with low next to high.
  * Tokens that are skipped leave their rows of q_out as they were.
  * Errors: as mx_kv_append (with q, q_out and their strides), plus MX_ERR_INVALID_ARG (an
  * unknown layout, rot_dim < 0 or > head_dim, amplitude not finite, q without q_out) and
- * MX_ERR_UNSUPPORTED (rot_dim % 16, head_dim > 256). */
+ * MX_ERR_UNSUPPORTED (rot_dim % 16, head_dim > 256, n_q_heads * head_dim > 2^20). */
 MX_API int mx_rope_kv_append(const mx_kv_cache* cache, const void* q, int64_t q_stride, int n_q_heads, void* q_out,
                              int64_t q_out_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                              const int32_t* positions, const uint64_t* turns, int rot_dim, int layout,

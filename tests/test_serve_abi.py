@@ -1,6 +1,7 @@
 """Host-side argument checks of the operators that close a decoding step: every call
 below is refused, or has nothing to do, before any device work (no GPU needed)."""
 import ctypes
+import decimal
 import math
 
 import pytest
@@ -285,3 +286,43 @@ def test_binding_refuses_every_tensor_of_another_device(L, monkeypatch, call):
     for other in sorted(set(names)):
         with pytest.raises(ValueError, match=f"^{other}: on .* but the current"):
             run(lambda name: int(name == other))
+
+
+def _dec_turns(R, base, scaling, factor, low, high, length):
+    """The table's formulas in 60 decimal digits: turns a position of each pair."""
+    D = decimal.Decimal
+    pi = D("3.14159265358979323846264338327950288419716939937510582097494")
+    base, factor, low, high, length = D(base), D(factor), D(low), D(high), D(length)
+    if scaling == "ntk":
+        base *= factor ** (D(R) / (R - 2))
+    out = []
+    at = {t: R * (length / (2 * pi * t)).ln() / (2 * base.ln()) for t in (low, high)}
+    first, last = max(math.floor(at[high]), 0), min(math.ceil(at[low]), R - 1)
+    for i in range(R // 2):
+        f, slow = base ** (D(-2 * i) / R), D(0)
+        if scaling == "linear":
+            slow = D(1)
+        elif scaling == "yarn":
+            slow = D(i - first) / max(D(last - first), D("0.001"))
+        elif scaling == "bands":
+            slow = 1 - (length * f / (2 * pi) - low) / (high - low)
+        slow = min(max(slow, D(0)), D(1))
+        out.append((f / factor * slow + f * (1 - slow)) / (2 * pi))
+    return out
+
+
+@pytest.mark.parametrize("scaling", ["none", "linear", "ntk", "yarn", "bands"])
+@pytest.mark.parametrize("R,base,factor,length,low,high", [(16, 10000.0, 2.0, 4096, 1.0, 32.0), (64, 1e6, 3.0, 8192, 1.0, 4.0),
+                                                           (128, 500000.0, 16.0, 32768, 0.5, 2.0), (256, 1.5, 1.0, 100, 1.0, 8.0), (256, 1e9, 7.0, 2048, 1.0, 32.0)])
+def test_rope_table_is_near_enough_for_far_positions(L, scaling, R, base, factor, length, low, high):
+    """What the header says of an angle: the table is at most 2^-52 turns a position off."""
+    with decimal.localcontext() as c:
+        c.prec = 60
+        st, turns, _ = _table(L, R, base, ["none", "linear", "ntk", "yarn", "bands"].index(scaling), factor, low, high, length)
+        want = _dec_turns(R, base, scaling, factor, low, high, length)
+        assert st == 0
+        # in units of 2^-53 of f_i <= 1: the power (2: an ulp), its exponent's rounding (x log(base)
+        # base^-x <= 1 / e of one), its base's (ntk: 3), the mix (3, and 6 half f_i for a ramp with
+        # high / (high - low) <= 4 / 3), 2 pi and the division by it (2): 10 at most in one scaling,
+        # 10 / (2 pi) 2^-53 < 2^-52 turns, and what is cut off behind 2^-64
+        assert max(abs(decimal.Decimal(t) / 2 ** 64 - w) for t, w in zip(turns, want)) <= decimal.Decimal(2) ** -52
