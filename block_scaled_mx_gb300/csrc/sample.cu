@@ -18,7 +18,8 @@
 // are exact in any order (no atomic changes a result) and two calls agree.  A draw next
 // to a token's border is decided by the weights' own rounding: e^x is taken in two floats
 // with a table of 2^(j/64), 2^-31 off where one float's exponential would be 2^-22, as a
-// vocabulary has 10^5 borders.  Weights below 2^-44 of the largest are zero.
+// vocabulary has 10^5 borders (table-driven reduction, P. T. P. Tang 1989, and the Taylor series
+// of 2^f).  Weights below 2^-43 of the largest are zero.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <climits>
@@ -106,7 +107,6 @@ struct Control {
   unsigned long long slice_mass[2][kMaxCluster];
   Found found;
   End end;
-  uint32_t key_min[kMaxCluster], key_max[kMaxCluster];
   uint32_t n;  // candidates (rank 0)
   uint32_t local_n, local_base, local_at[kCandidates];  // this CTA's
   uint32_t gathered[kMaxCluster];

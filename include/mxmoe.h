@@ -594,14 +594,15 @@ MX_API size_t mx_sample_workspace_size(int T, int V);
  *   logits [T, V] bf16 or fp32 (type), row t at t * stride elements.
  *   temperature, top_p, min_p fp32, top_k int32: [T] each, or NULL for 1, 1, 0, 0.
  *   u [T] fp32 in [0, 1) (held to it, a NaN counts as 0).  tokens [T] int32, logp [T] fp32 or NULL.
- * Weights are held as whole multiples of 2^-43 (those below 2^-44 are never drawn),
- * 2^-30 off (those of bf16 logits below 2^-16 of the largest 2^-22), and summed exactly: the same call gives the same tokens, and one next to a
- * border may differ from exact arithmetic.  Logits of -inf are never drawn; of +inf, the
+ * Weights are held as whole multiples of 2^-43 (those below 2^-44 are never drawn), 2^-30 off
+ * (those of bf16 logits below 2^-16 of the largest 2^-22), and summed exactly: the same call
+ * gives the same tokens, and one next to a border may differ from exact arithmetic.  In logp a
+ * logit's distance from the maximum is in fp32.  Logits of -inf are never drawn; of +inf, the
  * only ones drawn.  A row with a NaN, without a finite or infinite maximum, with a negative
  * temperature or a NaN among its rules gives token -1 and logp NaN and sets
  * MX_ERR_DEVICE_ARG in the workspace status.
  * Errors: MX_ERR_INVALID_ARG (null, T < 0, V <= 0, an unknown type, stride < V),
- * MX_ERR_UNSUPPORTED (V > 800000 in bf16, V > 400000 in fp32), MX_ERR_ALIGNMENT (a tensor
+ * MX_ERR_UNSUPPORTED (V > 800000 in bf16, V > 400000 in fp32, T >= 2^27), MX_ERR_ALIGNMENT (a tensor
  * not aligned to its elements, ws), MX_ERR_WORKSPACE, MX_ERR_CUDA. */
 MX_API int mx_sample(const void* logits, int type, int64_t stride, int T, int V, const float* temperature,
                      const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* tokens,
