@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = cluster.num_blocks(), R = cluster.block_rank();
   const int t = blockIdx.x / C;
-  cluster.barrier_arrive();  // waited for ahead of the first store to a peer, which has to have started by then
+  cluster_arrive_relaxed();  // waited for ahead of the first store to a peer, which has to have started by then
   uint4* const seg = reinterpret_cast<uint4*>(smem);
   const int per = chunk * kWarps;  // 16-byte pieces of a CTA: a run of `chunk` a warp
   Control& ctl = *reinterpret_cast<Control*>(smem + static_cast<size_t>(per) * 16);
@@ -864,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
   for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
   if (lane == 0) ctl.red[warp] = __float_as_uint(mx);
   __syncthreads();
-  cluster.barrier_wait();
+  cluster_wait();
   if (tid < C) {
     for (int i = 0; i < kWarps; ++i) mx = fmaxf(mx, __uint_as_float(ctl.red[i]));
     Control* peer = cluster.map_shared_rank(&ctl, tid);
